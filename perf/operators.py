@@ -170,9 +170,10 @@ def work(case):
 def _codes(x, kind):
     """Codes and scales of rows (the last axis), 32 bits until the code."""
     a = x.abs().amax(-1).clamp(min=TINY)
-    y = x * (TOP[kind] / a).unsqueeze(-1)
+    top = torch.full_like(a, TOP[kind])   # (a quotient with a number would go by its reciprocal)
+    y = x * (top / a).unsqueeze(-1)
     code = y.round().to(torch.int8) if kind == "int8" else y.to(torch.float8_e4m3fn)
-    return code, a / TOP[kind]
+    return code, a / top
 
 
 def prepare(case, seed):
