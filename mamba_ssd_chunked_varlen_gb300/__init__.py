@@ -1,9 +1,18 @@
 """GB300-native (sm_103a) Mamba-2 SSD varlen forward prefill scan.
 
 The compute path is the CUDA library libssd_scan.so (C ABI in
-include/ssd_scan.h); ``binding`` is its thin Python front end and
+include/ssd_scan.h and include/ssd_attn.h); ``binding`` (the scan) and
+``attention`` (the paged key/value cache and the attention over it, for the
+attention layers of a hybrid model) are its thin Python front ends and
 ``workloads`` the seeded synthetic inputs.
 """
+from .attention import (  # noqa: F401
+    alloc_attn_workspace,
+    ssd_attn_varlen_fwd,
+    ssd_attn_varlen_workspace_size,
+    ssd_kv_cache_read,
+    ssd_kv_cache_write,
+)
 from .binding import (  # noqa: F401
     EXPORTED_SYMBOLS,
     SSDError,

@@ -3,7 +3,7 @@
 Each translation unit under csrc/ is compiled in parallel with nvcc
 (-gencode arch=compute_103a,code=sm_103a, -lineinfo, static CUDA runtime)
 and linked into one shared library exporting the C ABI of
-include/ssd_scan.h.  Only nvcc and a host compiler are needed; no GPU.
+include/ssd_scan.h and include/ssd_attn.h.  Only nvcc and a host compiler are needed; no GPU.
 """
 from __future__ import annotations
 
@@ -34,7 +34,8 @@ def sources():
 
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hs.append(os.path.join(ROOT, "include", "ssd_scan.h"))
+    inc = os.path.join(ROOT, "include")
+    hs += [os.path.join(inc, f) for f in os.listdir(inc) if f.endswith(".h")]
     return hs
 
 
