@@ -60,8 +60,8 @@ typedef enum {
  * holds (a read zeroes them); attention computes and writes nothing. */
 #define SSD_DEVERR_BAD_KV_LEN 0x8u  /* kv_lens[b] < 0 or more than table_width pages hold: the
                                        sequence counts as having no token in the cache */
-#define SSD_DEVERR_BAD_PAGE   0x10u /* a page index outside [0, num_pages): not written, read
-                                       back as zeros, seen by no query */
+#define SSD_DEVERR_BAD_PAGE   0x10u /* a page index outside [0, num_pages): not written; its
+                                       keys and values read as zeros */
 
 /* Writes the new tokens' keys and values into the cache.
  *

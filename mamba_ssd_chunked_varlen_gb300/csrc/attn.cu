@@ -1,90 +1,258 @@
-// Causal grouped-query attention of a ragged batch's new tokens over a paged
-// cache: one warp per (row, query head), one pass over the keys with the
-// running maximum and sum of the softmax.
+// Attention over the paged cache: the plan of a call, the join of split rows,
+// and the C ABI (argument checks, tensor maps, launches).
 #include <cmath>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+#include <mutex>
 
-#include "attn_common.cuh"
+#include "attn.cuh"
+#include "kernels.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kWarps = 4;
+// ---------------------------------------------------------------- plan
+// One CTA cuts the call into units (AttnUnit), in the order of the rows, and
+// counts their key tiles.
+constexpr int kPlanThreads = 1024;
 
-struct AttnParams {
-    KvView c;
-    __nv_bfloat16 *o;
-    const __nv_bfloat16 *q;
-    float *lse;
-    int64_t o_stride, q_stride;
-    int32_t heads, window;
-    float scale;
-};
-
-__device__ __forceinline__ float cache_value(const KvView &c, const void *base, int64_t i)
+// Inclusive sum over the CTA's threads; `total` gets the sum of all.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64_t *total)
 {
-    if (c.type == SSD_KV_BF16)
-        return __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[i]);
-    if (c.type == SSD_KV_INT8)
-        return static_cast<const int8_t *>(base)[i];
-    return __half2float(
-        __half(__nv_cvt_fp8_to_halfraw(static_cast<const __nv_fp8_storage_t *>(base)[i], __NV_E4M3)));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t incl = warp_inclusive_scan(v);
+    __syncthreads();
+    if (lane == 31)
+        scratch[warp] = incl;
+    __syncthreads();
+    if (warp == 0)
+        scratch[lane] = warp_inclusive_scan(scratch[lane]);
+    __syncthreads();
+    *total = scratch[31];
+    return incl + (warp ? scratch[warp - 1] : 0);
 }
 
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p)
+{
+    __shared__ int64_t scratch[32];
+    const KvView &c = p.c;
+    const int tid = threadIdx.x;
+    const int unit_tokens = 2 * p.tile_tokens;
+    pdl_launch_dependents();
+    int64_t units = 0;
+    int bad = 0;
+    for (int base = 0; base < c.batch; base += kPlanThreads) {
+        const int b = base + tid;
+        int64_t n = 0;
+        if (b < c.batch) {
+            const int32_t start = c.qsl[b], end = c.qsl[b + 1];
+            if (end < start || (b == 0 && start != 0) || (b == c.batch - 1 && end != c.total_len))
+                bad = 1;
+            else
+                n = (static_cast<int64_t>(end) - start + unit_tokens - 1) / unit_tokens;
+        }
+        int64_t all;
+        const int64_t incl = block_scan(n, scratch, &all);
+        if (b < c.batch)
+            p.seq_units[b] = static_cast<int32_t>(min(units + incl - n, static_cast<int64_t>(INT32_MAX)));
+        units += all;
+    }
+    // (a query_start_loc that fails may count any number of units: none is written)
+    bad = __syncthreads_or(bad);
+    if (bad) {
+        if (tid == 0) {
+            kv_error(c, SSD_DEVERR_BAD_QUERY_START_LOC);
+            p.hdr->total = 0;
+            p.hdr->units = 0;
+        }
+        return;
+    }
+    int64_t tiles = 0;
+    for (int64_t base = 0; base < units; base += kPlanThreads) {
+        const int64_t u = base + tid;
+        AttnUnit e = {};
+        if (u < units) {
+            // the last sequence whose units begin at or before u (the sequences
+            // without rows that begin there as well come before it)
+            int lo = 0, hi = c.batch - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (p.seq_units[mid] <= u)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int32_t start = c.qsl[lo], rows = c.qsl[lo + 1] - start;
+            const int32_t first = static_cast<int32_t>(u - p.seq_units[lo]) * unit_tokens;
+            e.seq = lo;
+            e.row0 = start + first;
+            e.tokens = min(unit_tokens, rows - first);
+            e.kv_len = kv_len_of(c, lo);
+            e.pos0 = e.kv_len - rows + first;
+            const int32_t keys = max(e.pos0 + e.tokens, 0);
+            e.tile0 = p.window > 0 ? max(e.pos0 - p.window + 1, 0) / kTileKeys : 0;
+            e.tiles = max((keys + kTileKeys - 1) / kTileKeys - e.tile0, 1);
+        }
+        int64_t all;
+        const int64_t incl = block_scan(e.tiles, scratch, &all);
+        if (u < units) {
+            p.units[u] = e;
+            p.cum[u] = tiles + incl - e.tiles;
+        }
+        tiles += all;
+    }
+    if (tid == 0) {
+        p.cum[units] = tiles;
+        p.hdr->total = tiles * c.heads;
+        p.hdr->units = static_cast<int32_t>(units);
+    }
+}
+
+// ---------------------------------------------------------------- join
+// Rows whose keys were split over several pieces: with M the largest of the
+// pieces' references m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// CTA (i, y) looks at the boundary before piece i + 1 and, when it is the first
+// boundary inside its (unit, kv head) pair, joins the pair's rows y, y + 8, ...
+// of every eight; the pieces are summed in their order.
+constexpr int kJoinWarps = 8, kJoinParts = 8;
+
 template <int kDim>
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(AttnParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnParams p)
 {
     constexpr int kE = kDim / 32;
-    const KvView &c = p.c;
+    pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    int bad = 0;
-    for (int b = threadIdx.x; b < c.batch; b += kWarps * 32)
-        bad |= c.qsl[b + 1] < c.qsl[b] || (b == 0 && c.qsl[0] != 0) ||
-               (b == c.batch - 1 && c.qsl[c.batch] != c.total_len);
-    if (__syncthreads_or(bad)) {
-        kv_error(c, SSD_DEVERR_BAD_QUERY_START_LOC);
+    const int64_t total = p.hdr->total;
+    if (total == 0)
         return;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) + 1, s = attn_piece_begin(total, i);
+    int u = 0, n = p.hdr->units;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const bool below = at < n && p.cum[u + at] * p.c.heads <= s;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
+        u += k * step;
+        n = min(step, n - k * step);
     }
-    if (item >= c.total_len * p.heads)
+    const AttnUnit e = p.units[u];
+    const int64_t r = s - p.cum[u] * p.c.heads;
+    const int h = static_cast<int>(r / e.tiles);
+    const int64_t begin = s - (r - static_cast<int64_t>(h) * e.tiles);
+    if (s >= total || begin == s)
         return;
-    const int64_t t = item / p.heads;
-    const int h = static_cast<int>(item % p.heads), kvh = h / (p.heads / c.heads);
-    const int b = warp_sequence_of(c, t);
-    if (b < 0)
+    const int64_t first = attn_piece_of(total, begin), last = attn_piece_of(total, begin + e.tiles - 1);
+    if (first != i - 1)
         return;
-    const int64_t at = kv_len_of(c, b) - static_cast<int64_t>(c.qsl[b + 1]) + t;
-    const int64_t lo = p.window > 0 && at - p.window + 1 > 0 ? at - p.window + 1 : 0;
-    float q[kE], o[kE], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < kE; ++e) {
-        q[e] = __bfloat162float(p.q[t * p.q_stride + h * kDim + e * 32 + lane]);
-        o[e] = 0.f;
+    const int rows = e.tokens * p.group;
+    for (int x = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); x < rows; x += kJoinWarps * kJoinParts) {
+        const int tok = x / p.group, sub = x % p.group;
+        const int st = tok / p.tile_tokens;
+        const int prow = st * 128 + (tok - st * p.tile_tokens) * p.group + sub;
+        // every lane takes a piece's (m, l)
+        float top = -INFINITY, sum = 0.f;
+        bool nan = false;
+        for (int64_t base = first; base <= last; base += 32) {
+            const int64_t k = base + lane;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (k <= last && attn_piece_begin(total, k) < attn_piece_begin(total, k + 1))
+                ml = p.part_ml[attn_slot(k, k == first) * 256 + prow];
+            nan = nan || ml.x != ml.x;
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float nt = fmaxf(top, m);
+            float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - nt) * ml.y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                w += __shfl_xor_sync(0xffffffffu, w, o);
+            sum = (top == -INFINITY ? 0.f : sum * exp2f(top - nt)) + w;
+            top = nt;
+        }
+        float acc[kE];
+#pragma unroll
+        for (int j = 0; j < kE; ++j)
+            acc[j] = 0.f;
+        for (int64_t k = first; k <= last; ++k) {
+            if (attn_piece_begin(total, k) == attn_piece_begin(total, k + 1))
+                continue;
+            const int64_t at = attn_slot(k, k == first) * 256 + prow;
+            const float m = p.part_ml[at].x;
+            const float w = m == -INFINITY ? 0.f : exp2f(m - top);
+            const float *src = p.part_o + at * kDim + lane * kE;
+#pragma unroll
+            for (int j = 0; j < kE; ++j)
+                acc[j] += w == 0.f ? 0.f : w * src[j];
+        }
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        const int64_t row = e.row0 + tok;
+        const int head = h * p.group + sub;
+        __nv_bfloat16 *dst = p.o + row * p.o_stride + static_cast<int64_t>(head) * kDim + lane * kE;
+#pragma unroll
+        for (int j = 0; j < kE; j += 2)
+            *reinterpret_cast<uint32_t *>(dst + j) = pack_bf16(acc[j] * inv, acc[j + 1] * inv);
+        if (p.lse && lane == 0)
+            p.lse[row * p.heads + head] =
+                sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
-    for (int64_t j = lo; j <= at; ++j) {
-        const int64_t page = kv_page_of(c, b, static_cast<int32_t>(j));
-        if (page < 0)
-            continue;
-        const int64_t row = kv_row(c, page, kvh, static_cast<int32_t>(j));
-        float s = 0.f;
-        for (int e = 0; e < kE; ++e)
-            s += q[e] * cache_value(c, c.k, row * kDim + e * 32 + lane);
-        for (int w = 16; w; w >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= p.scale * (c.k_scale ? c.k_scale[row] : 1.f);
-        const float mn = fmaxf(m, s);
-        const float a = m == -INFINITY ? 0.f : expf(m - mn), w = expf(s - mn);
-        l = l * a + w;
-        const float wv = w * (c.v_scale ? c.v_scale[row] : 1.f);
-        for (int e = 0; e < kE; ++e)
-            o[e] = o[e] * a + wv * cache_value(c, c.v, row * kDim + e * 32 + lane);
-        m = mn;
-    }
-    for (int e = 0; e < kE; ++e)
-        p.o[t * p.o_stride + h * kDim + e * 32 + lane] =
-            __float2bfloat16_rn(m == -INFINITY ? 0.f : o[e] / l);
-    if (p.lse && lane == 0)
-        p.lse[item] = m == -INFINITY ? -INFINITY : m + logf(l);
+}
+
+// ---------------------------------------------------------------- host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// Three-dimensional tensor map; what lies outside reads as zeros.
+bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t d0, uint64_t d1,
+              uint64_t d2, uint64_t pitch1, uint64_t pitch2, uint32_t b0, uint32_t b1, uint32_t b2,
+              CUtensorMapSwizzle swizzle)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[3] = {d0, d1, d2};
+    const cuuint64_t strides[2] = {pitch1, pitch2};
+    const cuuint32_t box[3] = {b0, b1, b2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, type, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool sizes_ok(int64_t total_len, int32_t batch, int32_t nheads, int32_t nheads_kv, int32_t head_dim)
+{
+    return total_len >= 0 && total_len <= INT32_MAX / 2 && batch >= 0 && batch <= INT32_MAX / 2 &&
+           nheads > 0 && nheads_kv > 0 && nheads % nheads_kv == 0 && nheads / nheads_kv <= kTileRows &&
+           (head_dim == 64 || head_dim == 128);
+}
+
+template <typename... Args>
+cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
 }  // namespace
@@ -95,10 +263,9 @@ extern "C" {
 size_t ssd_attn_varlen_workspace_size(int64_t total_len, int32_t batch, int32_t nheads,
                                       int32_t nheads_kv, int32_t head_dim)
 {
-    if (total_len < 0 || total_len > INT32_MAX / 2 || batch < 0 || nheads <= 0 || nheads_kv <= 0 || nheads % nheads_kv != 0 ||
-        nheads / nheads_kv > 128 || (head_dim != 64 && head_dim != 128))
+    if (!ssd::sizes_ok(total_len, batch, nheads, nheads_kv, head_dim))
         return 0;
-    return 256;
+    return ssd::attn_layout(total_len, batch, nheads / nheads_kv, head_dim).total;
 }
 
 ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void *k_cache,
@@ -113,7 +280,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
                                  ssd_stream_t stream_)
 {
     using namespace ssd;
-    AttnParams p;
+    AttnParams p = {};
     const ssd_status_t st =
         kv_check(&p.c, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, block_table,
                  total_len, batch, nheads_kv, head_dim, num_pages, page_size, table_width,
@@ -122,7 +289,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
         return st;
     if (nheads <= 0 || nheads % nheads_kv != 0 || window < 0 || !std::isfinite(softmax_scale))
         return SSD_ERR_INVALID_ARG;
-    if (nheads / nheads_kv > 128)
+    if (!sizes_ok(total_len, batch, nheads, nheads_kv, head_dim))
         return SSD_ERR_UNSUPPORTED;
     const int64_t row = static_cast<int64_t>(nheads) * head_dim;
     if (!kv_pitch(&o_stride, row) || !kv_pitch(&q_stride, row))
@@ -131,24 +298,63 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
         return SSD_OK;
     if (batch == 0 || !o || !q || !kv_aligned16(o) || !kv_aligned16(q))
         return SSD_ERR_INVALID_ARG;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-        workspace_bytes < ssd_attn_varlen_workspace_size(total_len, batch, nheads, nheads_kv, head_dim))
+    const int group = nheads / nheads_kv;
+    const AttnLayout L = attn_layout(total_len, batch, group, head_dim);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < L.total)
         return SSD_ERR_WORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.lse = lse;
     p.o_stride = o_stride;
-    p.q_stride = q_stride;
     p.heads = nheads;
+    p.group = group;
+    p.tile_tokens = kTileRows / group;
     p.window = window;
-    p.scale = softmax_scale;
+    // a scale of zero still has to leave the hidden keys' -infinity as it is
+    p.scale_log2 = std::fmax(std::fabs(softmax_scale) * 1.4426950408889634f, 0x1p-120f);
+    p.negate = softmax_scale < 0.f;
+    p.hdr = reinterpret_cast<AttnHeader *>(ws + L.header);
+    p.seq_units = reinterpret_cast<int32_t *>(ws + L.seq_units);
+    p.units = reinterpret_cast<AttnUnit *>(ws + L.units);
+    p.cum = reinterpret_cast<int64_t *>(ws + L.cum);
+    p.part_o = reinterpret_cast<float *>(ws + L.part_o);
+    p.part_ml = reinterpret_cast<float2 *>(ws + L.part_ml);
+
+    AttnMaps m = {};
+    const uint64_t D = head_dim, rows = static_cast<uint64_t>(num_pages) * nheads_kv;
+    const uint32_t box = page_size < kTileKeys ? page_size : kTileKeys;
+    bool ok = make_map(&m.Q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, D, nheads, total_len, D * 2,
+                       q_stride * 2, 64, group, p.tile_tokens, CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int kv = 0; kv < 2 && ok; ++kv) {
+        CUtensorMap *t = kv ? &m.V : &m.K;
+        const void *base = kv ? v_cache : k_cache;
+        if (cache_type == SSD_KV_BF16) {
+            ok = make_map(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, D, page_size, rows, D * 2,
+                          D * 2 * page_size, 64, box, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+        } else {
+            ok = make_map(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, D, page_size, rows, D,
+                          D * page_size, head_dim, box, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+        }
+    }
+    if (!ok)
+        return SSD_ERR_CUDA;
+
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    const unsigned grid = static_cast<unsigned>((total_len * nheads + kWarps - 1) / kWarps);
-    if (head_dim == 128)
-        attn_kernel<128><<<grid, kWarps * 32, 0, stream>>>(p);
-    else
-        attn_kernel<64><<<grid, kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess)
+        return SSD_ERR_CUDA;
+    const cudaError_t e = cache_type == SSD_KV_BF16       ? launch_attn_bf16(p, m, stream)
+                          : cache_type == SSD_KV_FP8_E4M3 ? launch_attn_fp8(p, m, stream)
+                                                          : launch_attn_int8(p, m, stream);
+    if (e != cudaSuccess)
+        return SSD_ERR_CUDA;
+    const dim3 grid(kAttnCtas - 1, kJoinParts);
+    if ((head_dim == 128 ? launch_pdl(attn_join_kernel<128>, grid, kJoinWarps * 32, stream, p)
+                         : launch_pdl(attn_join_kernel<64>, grid, kJoinWarps * 32, stream, p)) !=
+        cudaSuccess)
+        return SSD_ERR_CUDA;
+    return SSD_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,11 @@
+// The attention kernel over a bf16 cache.
+#include "attn_kernel.cuh"
+
+namespace ssd {
+
+cudaError_t launch_attn_bf16(const AttnParams &p, const AttnMaps &m, cudaStream_t s)
+{
+    return launch_type<SSD_KV_BF16>(p, m, s);
+}
+
+}  // namespace ssd

@@ -1,0 +1,11 @@
+// The attention kernel over a int8 cache.
+#include "attn_kernel.cuh"
+
+namespace ssd {
+
+cudaError_t launch_attn_int8(const AttnParams &p, const AttnMaps &m, cudaStream_t s)
+{
+    return launch_type<SSD_KV_INT8>(p, m, s);
+}
+
+}  // namespace ssd

@@ -1,0 +1,733 @@
+// The attention kernel, for one cache type and head_dim.
+//
+// For the query rows of a unit (whole tokens with the query heads of one kv
+// head, packed into one or two 128-row tiles, "streams") and its key tiles of
+// 128 keys:
+//
+//   S = Q K^T                       (tcgen05, both operands in shared memory)
+//   m' = max(m, max_j S_j),  P = 2^(c S - c m'),  l = l 2^(c m - c m') + sum P
+//   O = O 2^(c m - c m') + P V      (tcgen05, P in tensor memory, V in shared memory)
+//
+// with c = softmax_scale log2(e): one pass over the keys with the running
+// maximum and sum of the softmax.  O keeps an old reference m until a maximum
+// exceeds it by 2^8, so that it is rescaled a few times per row and not per
+// tile; a probability then is at most 2^8, which neither the fp32 sums nor the
+// bf16 operand feel.
+//
+// One CTA per SM, 16 warps.  The two streams share every key tile, which halves
+// the reads of K and V per query row, and take turns: while one stream's warps
+// exponentiate, the tensor cores run the other's products.
+//   warps 0-3, 4-7   softmax and output of stream 0 and 1: a thread per row,
+//                    all 128 scores of the row in registers
+//   warps 8-11       bf16: clean the V tiles that hold rows nobody may see;
+//                    8-bit: widen codes to bf16 tiles (exact: 8 bits at most)
+//   warp 12          TMA producer: Q, K and V page by page
+//   warp 13          tcgen05 issuer
+#pragma once
+
+#include "attn.cuh"
+#include "attn_ptx.cuh"
+#include "kernels.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kBlk = kTileKeys * 128;      // 128 rows of 64 bf16: one swizzled block
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSlots8 = 4;                 // scale tiles in flight (8-bit caches)
+constexpr float kRescaleLog2 = 8.f;
+
+template <int kType, int kDim>
+struct Cfg {
+    static constexpr bool kQuant = kType != SSD_KV_BF16;
+    static constexpr int kBlocks = kDim / 64;
+    static constexpr int kTile = kBlocks * kBlk;             // a bf16 tile of 128 rows
+    static constexpr int kRaw = kTileKeys * kDim;            // the same in 8-bit codes
+    static constexpr int kStages = (kQuant ? 3 : 5) * (128 / kDim) - (kQuant || kDim == 128 ? 0 : 2);
+    static constexpr int kRawStages = kQuant ? 3 * (128 / kDim) : 0;
+    // shared memory, from a 1024-byte boundary
+    static constexpr int kQOff = 0;
+    static constexpr int kKvOff = kQOff + 2 * kTile;
+    static constexpr int kRawOff = kKvOff + kStages * kTile;
+    static constexpr int kScaleOff = kRawOff + kRawStages * kRaw;
+    static constexpr int kBarOff = kScaleOff + (kQuant ? kSlots8 * 2 * kTileKeys * 4 : 0);
+    static constexpr int kBytes = kBarOff + 512 + 1024;
+    // tensor memory: per stream 128 columns of S (P in the first 64) and kDim of O
+    static constexpr uint32_t kColO = 256;
+};
+
+// Barriers, in 8-byte words from kBarOff.
+enum Bar {
+    kQFull = 0,
+    kQEmpty,
+    kSFull,              // [2] scores of a stream's tile are in tensor memory
+    kPFull = kSFull + 2, // [2] its probabilities are
+    kOFull = kPFull + 2, // [2] a segment's last product is
+    kFixReq = kOFull + 2,
+    kFixDone,
+    kDrain,
+    kKvFull,                      // [8]
+    kKvEmpty = kKvFull + 8,       // [8]
+    kRawFull = kKvEmpty + 8,      // [6]
+    kRawEmpty = kRawFull + 6,     // [6]
+    kScFull = kRawEmpty + 6,      // [4]
+    kScEmpty = kScFull + kSlots8, // [4]
+    kNumBars = kScEmpty + kSlots8,
+};
+static_assert(kNumBars * 8 + 16 <= 512, "barrier space");
+
+// The CTA's piece of the line of tiles, segment by segment: a segment is the
+// part of one (unit, kv head) pair that lies in the piece.
+struct Walk {
+    const AttnParams &p;
+    int64_t pos, end;
+    int32_t u, h, ta, tb;
+    AttnUnit e;
+    bool starts, whole;      // the segment begins its pair / is all of it
+
+    __device__ __forceinline__ explicit Walk(const AttnParams &p_) : p(p_)
+    {
+        const int64_t total = p.hdr->total;
+        pos = total > 0 ? attn_piece_begin(total, blockIdx.x) : 0;
+        end = total > 0 ? attn_piece_begin(total, blockIdx.x + 1) : 0;
+        h = -1;
+        tb = 0;
+        u = 0;
+        if (pos >= end)
+            return;
+        // the last unit whose tiles begin at or before pos, 32 probes at a time
+        const int lane = threadIdx.x & 31;
+        int n = p.hdr->units;
+        while (n > 1) {
+            const int step = (n + 31) / 32, at = lane * step;
+            const bool below = at < n && p.cum[u + at] * p.c.heads <= pos;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
+            u += k * step;
+            n = min(step, n - k * step);
+        }
+        e = p.units[u];
+        const int64_t r = pos - p.cum[u] * p.c.heads;
+        h = static_cast<int32_t>(r / e.tiles);
+        ta = static_cast<int32_t>(r - static_cast<int64_t>(h) * e.tiles);
+        set();
+    }
+    __device__ __forceinline__ void set()
+    {
+        const int64_t left = end - pos;
+        tb = left < e.tiles - ta ? ta + static_cast<int32_t>(left) : e.tiles;
+        starts = ta == 0;
+        whole = starts && tb == e.tiles;
+    }
+    __device__ __forceinline__ bool more() const { return pos < end; }
+    __device__ __forceinline__ void next()
+    {
+        pos += tb - ta;
+        if (pos >= end)
+            return;
+        ta = 0;
+        if (++h == p.c.heads) {
+            h = 0;
+            e = p.units[++u];
+        }
+        set();
+    }
+    __device__ __forceinline__ int streams() const { return e.tokens > p.tile_tokens ? 2 : 1; }
+    // Whether some row of tokens [first, last] of the unit does not see all of key tile t.
+    __device__ __forceinline__ bool partial(int t, int first, int last) const
+    {
+        const int k0 = (e.tile0 + t) * kTileKeys;
+        return k0 + kTileKeys > e.pos0 + first + 1 ||
+               (p.window > 0 && k0 < e.pos0 + last - p.window + 1);
+    }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Codes to bf16 pairs (both exact).  int8: with the low seven bits put into
+// bf16's mantissa at 128 = 0x4300, code = (128 + low7) - (128 or 256 with the sign bit).
+__device__ __forceinline__ uint32_t int8_pair(uint32_t two)   // codes in bytes 0 and 2
+{
+    const uint32_t a = (two & 0x007f007fu) | 0x43004300u, b = (two & 0x00800080u) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+template <int kType>
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t *out)
+{
+    if constexpr (kType == SSD_KV_INT8) {
+        out[0] = int8_pair(__byte_perm(codes, 0, 0x4140));
+        out[1] = int8_pair(__byte_perm(codes, 0, 0x4342));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t h2;
+            const uint16_t pair = static_cast<uint16_t>(codes >> (16 * i));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(pair));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+            out[i] = pack_bf16(f.x, f.y);
+        }
+    }
+}
+
+template <int kType, int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ AttnMaps maps, AttnParams p)
+{
+    using C = Cfg<kType, kDim>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem + C::kQOff, *sKv = smem + C::kKvOff, *sRaw = smem + C::kRawOff;
+    float *sScale = reinterpret_cast<float *>(smem + C::kScaleOff);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *s_nonfinite = s_abort + 1;   // V rows of the current segment were cleaned
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        ptx::prefetch_tensormap(&maps.Q);
+        ptx::prefetch_tensormap(&maps.K);
+        ptx::prefetch_tensormap(&maps.V);
+        for (int k = 0; k < kNumBars; ++k) {
+            const bool many = k == kPFull || k == kPFull + 1 || k == kFixDone ||
+                              (k >= kRawEmpty && k < kScFull) ||
+                              (C::kQuant && k >= kKvFull && k < kKvEmpty);
+            ptx::mbar_init(bars + k, many ? 128 : 1);
+        }
+        ptx::fence_barrier_init();
+        *s_abort = 0;
+        *s_nonfinite = 0;
+    }
+    if (warp == 13) {
+        ptx::tmem_alloc(tmem_slot, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();                                // the plan
+    const int g = p.group, tt = p.tile_tokens;
+    bool ok = true;
+    auto wait = [&](int bar, uint32_t parity) {
+        ok = ok && ptx::mbar_wait(bars + bar, parity & 1, kWaitTimeoutNs) && !*s_abort;
+        ok = __all_sync(0xffffffffu, ok);   // the warp leaves its loops together
+        return ok;
+    };
+
+    // 512 threads at 128 registers: 2 x 128 x (184 + 72) again
+    if (warp == 12) {
+        ptx::setmaxnreg_dec<72>();
+        // ------------------------------------------------------------ producer
+        uint32_t it = 0, qit = 0, sit = 0;     // tiles, segments, key tiles so far
+        constexpr int kRing = C::kQuant ? C::kRawStages : C::kStages;
+        constexpr int kFull = C::kQuant ? kRawFull : kKvFull, kEmpty = C::kQuant ? kRawEmpty : kKvEmpty;
+        const int shift = p.c.page_shift;
+        const int boxes = shift >= 7 ? 1 : kTileKeys >> shift;    // pages of a tile
+        for (Walk w(p); w.more() && ok; w.next(), ++qit) {
+            const int ns = w.streams();
+            if (qit > 0 && !wait(kQEmpty, qit - 1))
+                break;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bars + kQFull, ns * g * tt * kDim * 2);
+                for (int st = 0; st < ns; ++st)
+                    for (int b = 0; b < C::kBlocks; ++b)
+                        ptx::tma_load_3d(sQ + st * C::kTile + b * kBlk, &maps.Q, bars + kQFull,
+                                         b * 64, w.h * g, w.e.row0 + st * tt);
+            }
+            for (int t = w.ta; t < w.tb && ok; ++t, ++sit) {
+                // this lane's page of the tile; beyond the sequence's keys, or with
+                // an index out of range, one past the cache: it reads as zeros
+                const int j0 = (w.e.tile0 + t) * kTileKeys + (lane << shift);
+                int64_t page = p.c.num_pages;
+                if (lane < boxes && j0 < w.e.kv_len) {
+                    const int64_t got = kv_page_of(p.c, w.e.seq, j0);
+                    page = got < 0 ? page : got;
+                }
+                const int z = static_cast<int>(page * p.c.heads) + w.h;
+                const int y = shift > 7 ? j0 & (p.c.page - 1) : 0;
+                if constexpr (C::kQuant) {
+                    const int slot = sit % kSlots8;
+                    if (sit >= kSlots8 && !wait(kScEmpty + slot, sit / kSlots8 - 1))
+                        break;
+                    // untiled copies (a page's scales may be 64 bytes, less than a tiled
+                    // copy's alignment), so zeros are written here
+                    const bool there = lane < boxes && page < p.c.num_pages;
+                    const uint32_t bytes = min(p.c.page, kTileKeys) * 4;
+                    float *dst = sScale + slot * 2 * kTileKeys + (lane << shift);
+                    if (lane < boxes && !there) {
+                        for (int k = 0; k < static_cast<int>(bytes) / 4; ++k)
+                            dst[k] = dst[kTileKeys + k] = 0.f;
+                        ptx::fence_proxy_async_smem();
+                    }
+                    const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(bars + kScFull + slot, n * 2 * bytes);
+                    __syncwarp();
+                    if (there) {
+                        const int64_t at = static_cast<int64_t>(z) * p.c.page + y;
+                        ptx::bulk_load(dst, p.c.k_scale + at, bytes, bars + kScFull + slot);
+                        ptx::bulk_load(dst + kTileKeys, p.c.v_scale + at, bytes, bars + kScFull + slot);
+                    }
+                }
+                for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+                    const int s = it % kRing;
+                    if (it >= kRing && !wait(kEmpty + s, it / kRing - 1))
+                        break;
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(bars + kFull + s, C::kQuant ? C::kRaw : C::kTile);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const CUtensorMap *m = kv ? &maps.V : &maps.K;
+                        if constexpr (C::kQuant) {
+                            ptx::tma_load_3d(sRaw + s * C::kRaw + ((lane << shift) * kDim), m,
+                                             bars + kFull + s, 0, y, z);
+                        } else {
+                            for (int b = 0; b < C::kBlocks; ++b)
+                                ptx::tma_load_3d(sKv + s * C::kTile + b * kBlk + (lane << shift) * 128,
+                                                 m, bars + kFull + s, b * 64, y, z);
+                        }
+                    }
+                }
+            }
+        }
+        if (!ok)
+            *s_abort = 1;
+        // copies still in flight must land before the CTA exits
+        if (qit > 0)
+            ptx::mbar_wait(bars + kQFull, (qit - 1) & 1, kWaitTimeoutNs);
+        if (!ok && lane == 0)
+            ptx::mbar_wait(bars + kQFull, qit & 1, kWaitTimeoutNs);
+        for (uint32_t k = it > kRing ? it - kRing : 0; k < it; ++k)
+            ptx::mbar_wait(bars + kFull + k % kRing, (k / kRing) & 1, kWaitTimeoutNs);
+        if constexpr (C::kQuant)
+            for (uint32_t k = sit > kSlots8 ? sit - kSlots8 : 0; k < sit; ++k)
+                ptx::mbar_wait(bars + kScFull + k % kSlots8, (k / kSlots8) & 1, kWaitTimeoutNs);
+    } else if (warp == 13) {
+        ptx::setmaxnreg_dec<72>();
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t id_s = ptx::idesc_bf16_f32(128, kTileKeys, 0, 0);
+        const uint32_t id_o = ptx::idesc_bf16_f32(128, kDim, 0, 1);
+        uint32_t it = 0, qit = 0, sit = 0, fit = 0;
+        uint32_t pit0 = 0, pit1 = 0;
+        auto scores = [&](int st, int stage) {
+            if (lane == 0) {
+                const uint64_t a = ptx::sdesc_sw128(ptx::smem_u32(sQ + st * C::kTile), 16, 1024);
+                const uint64_t b = ptx::sdesc_sw128(ptx::smem_u32(sKv + stage * C::kTile), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < kDim / 16; ++k)
+                    ptx::mma_bf16_ss(tmem + st * 128, ptx::sdesc_add(a, (k / 4) * kBlk + (k % 4) * 32),
+                                     ptx::sdesc_add(b, (k / 4) * kBlk + (k % 4) * 32), id_s, k != 0);
+                ptx::mma_commit(bars + kSFull + st);
+            }
+        };
+        for (Walk w(p); w.more() && ok; w.next(), ++qit) {
+            const int ns = w.streams(), n = w.tb - w.ta;
+            if (!wait(kQFull, qit) || !wait(kKvFull + it % C::kStages, it / C::kStages))
+                break;
+            ptx::tc_fence_after_sync();
+            for (int st = 0; st < ns; ++st)
+                scores(st, it % C::kStages);
+            if (lane == 0) {
+                ptx::mma_commit(bars + kKvEmpty + it % C::kStages);
+                if (n == 1)
+                    ptx::mma_commit(bars + kQEmpty);
+            }
+            for (int t = 0; t < n && ok; ++t, ++sit) {
+                // ring order: K0 V0 K1 V1 ...; V of this tile, K of the next
+                const uint32_t vi = it + 2 * t + 1, ki = vi + 1;
+                const int vs = vi % C::kStages, ks = ki % C::kStages;
+                if (!wait(kKvFull + vs, vi / C::kStages))
+                    break;
+                if constexpr (!C::kQuant) {
+                    if (w.partial(w.ta + t, 0, w.e.tokens - 1)) {
+                        if (lane == 0)
+                            ptx::mbar_arrive(bars + kFixReq);
+                        if (!wait(kFixDone, fit++))
+                            break;
+                    }
+                }
+                for (int st = 0; st < ns && ok; ++st) {
+                    uint32_t &pit = st ? pit1 : pit0;
+                    if (!wait(kPFull + st, pit++))
+                        break;
+                    if (st == 0 && t + 1 < n && !wait(kKvFull + ks, ki / C::kStages))
+                        break;
+                    ptx::tc_fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t b =
+                            ptx::sdesc_sw128(ptx::smem_u32(sKv + vs * C::kTile), kBlk, 1024);
+#pragma unroll
+                        for (int k = 0; k < kTileKeys / 16; ++k)
+                            ptx::mma_bf16_ts(tmem + C::kColO + st * kDim, tmem + st * 128 + k * 8,
+                                             ptx::sdesc_add(b, k * 2048), id_o, t > 0 || k != 0);
+                        if (t + 1 == n)
+                            ptx::mma_commit(bars + kOFull + st);
+                    }
+                    if (t + 1 < n)
+                        scores(st, ks);
+                }
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    if constexpr (C::kQuant)   // both streams have read the scales
+                        ptx::mbar_arrive(bars + kScEmpty + sit % kSlots8);
+                    ptx::mma_commit(bars + kKvEmpty + vs);
+                    if (t + 1 < n)
+                        ptx::mma_commit(bars + kKvEmpty + ks);
+                    if (t + 2 == n)
+                        ptx::mma_commit(bars + kQEmpty);
+                }
+            }
+            it += 2 * n;
+        }
+        if (!ok)
+            *s_abort = 1;
+        // every MMA issued must finish before tensor memory is released
+        if (lane == 0) {
+            ptx::mma_commit(bars + kDrain);
+            ptx::mbar_wait(bars + kDrain, 0, kWaitTimeoutNs);
+        }
+        __syncwarp();
+    } else if (warp >= 14) {
+        ptx::setmaxnreg_dec<72>();
+    } else if (warp >= 8) {
+        ptx::setmaxnreg_dec<72>();
+        const int ht = tid - 256;              // 0..127
+        if constexpr (!C::kQuant) {
+            // -------------------------------------------------------- V cleaner
+            // A key tile that some row may not see all of: rows past the last
+            // key (whatever the page holds there) become zeros, and so do
+            // infinities and NaN, whose product with a probability of zero
+            // would reach rows that do not see them; the output adds them
+            // back for the rows that do.
+            uint32_t it = 0, fit = 0;
+            for (Walk w(p); w.more() && ok; w.next()) {
+                for (int t = w.ta; t < w.tb && ok; ++t, it += 2) {
+                    if (!w.partial(t, 0, w.e.tokens - 1))
+                        continue;
+                    if (!wait(kFixReq, fit++))
+                        break;
+                    uint8_t *v = sKv + ((it + 1) % C::kStages) * C::kTile;
+                    const int keys = w.e.kv_len - (w.e.tile0 + t) * kTileKeys;
+                    bool found = false;
+                    for (int i = ht; i < C::kTile / 16; i += 128) {
+                        uint4 *at = reinterpret_cast<uint4 *>(v + i * 16);
+                        if (((i >> 3) & (kTileKeys - 1)) >= keys) {
+                            *at = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint4 x = *at;
+                        uint32_t *x4 = &x.x;
+                        bool bad = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((x4[k] & 0x7f80u) == 0x7f80u) {
+                                x4[k] &= 0xffff0000u;
+                                bad = true;
+                            }
+                            if ((x4[k] & 0x7f800000u) == 0x7f800000u) {
+                                x4[k] &= 0xffffu;
+                                bad = true;
+                            }
+                        }
+                        if (bad) {
+                            *at = x;
+                            found = true;
+                        }
+                    }
+                    if (found)
+                        *s_nonfinite = 1;
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive(bars + kFixDone);
+                }
+            }
+        } else {
+            // -------------------------------------------------------- converter
+            constexpr int kUnits = kDim / 16;  // 16-code pieces of a row
+            uint32_t it = 0;
+            for (Walk w(p); w.more() && ok; w.next())
+                for (int t = w.ta; t < w.tb && ok; ++t)
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+                        const int rs = it % C::kRawStages, s = it % C::kStages;
+                        if (!wait(kRawFull + rs, it / C::kRawStages))
+                            break;
+                        if (it >= C::kStages && !wait(kKvEmpty + s, it / C::kStages - 1))
+                            break;
+                        const int keys = w.e.kv_len - (w.e.tile0 + t) * kTileKeys;
+                        const uint8_t *src = sRaw + rs * C::kRaw;
+                        uint8_t *dst = sKv + s * C::kTile;
+#pragma unroll 4
+                        for (int i = ht; i < kTileKeys * kUnits; i += 128) {
+                            const int row = i / kUnits, c = i % kUnits;
+                            uint4 x = *reinterpret_cast<const uint4 *>(src + i * 16);
+                            if (row >= keys)
+                                x = make_uint4(0, 0, 0, 0);
+                            uint32_t o[8];
+                            widen4<kType>(x.x, o);
+                            widen4<kType>(x.y, o + 2);
+                            widen4<kType>(x.z, o + 4);
+                            widen4<kType>(x.w, o + 6);
+                            uint8_t *line = dst + (c >> 2) * kBlk + row * 128;
+                            const int c16 = (c & 3) * 2;
+                            // pieces of the second block write their halves in the other
+                            // order: eight lanes then meet all eight 16-byte banks
+                            const int f = c >> 2;
+                            *reinterpret_cast<uint4 *>(line + (((c16 + f) ^ (row & 7)) << 4)) =
+                                f ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(line + (((c16 + 1 - f) ^ (row & 7)) << 4)) =
+                                f ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        ptx::mbar_arrive(bars + kRawEmpty + rs);
+                        ptx::mbar_arrive(bars + kKvFull + s);
+                    }
+        }
+    } else {
+        ptx::setmaxnreg_inc<184>();
+        // ------------------------------------------------------------ softmax
+        const int st = warp >> 2, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t colS = tmem + st * 128 + lanes, colO = tmem + C::kColO + st * kDim + lanes;
+        const int my_tok = row / g, my_head = row % g;
+        const float c2 = p.scale_log2;
+        uint32_t it = 0, sit = 0, oit = 0;
+        for (Walk w(p); w.more() && ok; w.next()) {
+            if (w.streams() <= st) {
+                sit += w.tb - w.ta;
+                continue;
+            }
+            const int tok0 = st * tt;
+            const int ntok = min(tt, w.e.tokens - tok0);        // tokens of this stream
+            const bool mine = my_tok < ntok;
+            const int pos = w.e.pos0 + tok0 + (mine ? my_tok : ntok - 1);
+            const int hi = pos + 1;
+            const int lo = p.window > 0 ? pos - p.window + 1 : INT32_MIN / 2;
+            float m = -INFINITY;      // reference, times c
+            float l = 0.f;
+            for (int t = w.ta; t < w.tb && ok; ++t, ++it, ++sit) {
+                if (!wait(kSFull + st, it))
+                    break;
+                const float *sc = sScale + (sit % kSlots8) * 2 * kTileKeys;
+                if constexpr (C::kQuant) {
+                    if (!wait(kScFull + sit % kSlots8, sit / kSlots8))
+                        break;
+                }
+                ptx::tc_fence_after_sync();
+                uint32_t s[128];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    ptx::tmem_ld32_nowait(colS + k * 32, s + k * 32);
+                ptx::tmem_wait_ld();
+                if (p.negate) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        s[k] ^= 0x80000000u;
+                }
+                if constexpr (C::kQuant) {
+#pragma unroll
+                    for (int k = 0; k < 128; k += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sc + k);
+                        s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
+                        s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
+                        s[k + 2] = __float_as_uint(__uint_as_float(s[k + 2]) * f.z);
+                        s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
+                    }
+                }
+                const bool partial = w.partial(t, tok0, tok0 + ntok - 1);
+                if (partial) {
+                    const int k0 = (w.e.tile0 + t) * kTileKeys;
+                    const int a = lo - k0, b = hi - k0;
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        if (k < a || k >= b)
+                            s[k] = 0xff800000u;
+                }
+                float x0 = __uint_as_float(s[0]), x1 = __uint_as_float(s[1]);
+#pragma unroll
+                for (int k = 2; k < 128; k += 4) {
+                    x0 = max3(x0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    if (k + 2 < 128)
+                        x1 = max3(x1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                }
+                const float mx = fmaxf(x0, x1) * c2;
+                if (t == w.ta) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, mx > m + kRescaleLog2)) {
+                    // rare: the rows of the warp take their new references
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == m ? 1.f : ptx::ex2(m - mn);
+                    m = mn;
+                    l *= f;
+#pragma unroll
+                    for (int k = 0; k < kDim; k += 32) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32_nowait(colO + k, o);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        ptx::tmem_st32(colO + k, o);
+                    }
+                }
+                const float me = m == -INFINITY ? 0.f : m;
+                const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
+                uint64_t acc0 = ptx::pack2(0.f, 0.f), acc1 = acc0;
+                uint32_t pk[64];
+#pragma unroll
+                for (int k = 0; k < 128; k += 4) {
+                    float e0, e1, e2, e3;
+                    ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                           c22, nm), e0, e1);
+                    ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
+                                           c22, nm), e2, e3);
+                    e0 = ptx::ex2(e0);
+                    e1 = ptx::ex2(e1);
+                    e2 = ptx::ex2(e2);
+                    e3 = ptx::ex2(e3);
+                    acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
+                    acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
+                    if constexpr (C::kQuant) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + k);
+                        // (a hidden key's scale may be NaN: its weight stays zero)
+                        e0 = partial && e0 == 0.f ? 0.f : e0 * f.x;
+                        e1 = partial && e1 == 0.f ? 0.f : e1 * f.y;
+                        e2 = partial && e2 == 0.f ? 0.f : e2 * f.z;
+                        e3 = partial && e3 == 0.f ? 0.f : e3 * f.w;
+                    }
+                    pk[k / 2] = pack_bf16(e0, e1);
+                    pk[k / 2 + 1] = pack_bf16(e2, e3);
+                    if (k % 64 == 60)
+                        ptx::tmem_st32(colS + (k / 64) * 32, pk + (k / 64) * 32);
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(bars + kPFull + st);
+                float a0, a1;
+                ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
+                l += a0 + a1;
+            }
+            if (!ok || !wait(kOFull + st, oit++))
+                break;
+            ptx::tc_fence_after_sync();
+            // ---- output: the segment's rows, or their partial sums ----
+            const bool nonfinite = !C::kQuant && *s_nonfinite;
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            const int64_t grow = w.e.row0 + tok0 + my_tok;
+            const int head = w.h * g + my_head;
+            const int slot = attn_slot(blockIdx.x, w.starts);
+            const int prow = slot * 256 + st * 128 + row;
+            __nv_bfloat16 *dst = p.o + grow * p.o_stride + static_cast<int64_t>(head) * kDim;
+            float *part = p.part_o + static_cast<int64_t>(prow) * kDim;
+#pragma unroll
+            for (int k = 0; k < kDim; k += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                ptx::tmem_ld32_nowait(colO + k, o);
+                ptx::tmem_wait_ld();
+                if (nonfinite && mine) {
+                    // the cleaned values of the keys that this row sees
+                    for (int t = w.ta; t < w.tb; ++t) {
+                        if (!w.partial(t, 0, w.e.tokens - 1))
+                            continue;
+                        const int k0 = (w.e.tile0 + t) * kTileKeys;
+                        for (int j = max(k0, max(lo, 0)); j < min(k0 + kTileKeys, hi); ++j) {
+                            const int64_t page = kv_page_of(p.c, w.e.seq, j);
+                            if (page < 0)
+                                continue;
+                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.c.v) +
+                                                     kv_row(p.c, page, w.h, j) * kDim + k;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float x = __bfloat162float(v[i]);
+                                if (!(fabsf(x) <= 3.4e38f))
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                            }
+                        }
+                    }
+                }
+                if (mine && w.whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 v;
+                        v.x = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+                        v.y = pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                        v.z = pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+                        v.w = pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + k + i) = v;
+                    }
+                } else if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4 *>(part + k + i) =
+                            make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+            if (mine) {
+                if (!w.whole)
+                    p.part_ml[prow] = make_float2(m, l);
+                else if (p.lse)
+                    p.lse[grow * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            }
+            // (the next segment's first product waits for this warp's next P)
+            ptx::tc_fence_before_sync();
+        }
+    }
+
+    if (!ok)
+        *s_abort = 1;
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && *s_abort)
+        kv_error(p.c, SSD_DEVERR_TIMEOUT);
+    if (warp == 13) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int kType, int kDim>
+cudaError_t launch_one(const AttnParams &p, const AttnMaps &m, cudaStream_t stream)
+{
+    using C = Cfg<kType, kDim>;
+    static_assert(C::kBytes <= kMaxSmemPerBlock, "shared memory");
+    static_assert(C::kStages <= 8 && C::kRawStages <= 6, "barriers");
+    static SmemOptIn opted;
+    const void *fn = reinterpret_cast<const void *>(attn_kernel<kType, kDim>);
+    cudaError_t e = ensure_max_smem(fn, opted);
+    if (e != cudaSuccess)
+        return e;
+    // the register split inside the kernel adds up to 128 registers a thread: with
+    // fewer at launch it would wait forever, so such a build is refused
+    static const bool regs_ok = [fn] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, fn) == cudaSuccess && a.numRegs == 128;
+    }();
+    if (!regs_ok)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kAttnCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_kernel<kType, kDim>, m, p);
+}
+
+template <int kType>
+cudaError_t launch_type(const AttnParams &p, const AttnMaps &m, cudaStream_t stream)
+{
+    return p.c.dim == 128 ? launch_one<kType, 128>(p, m, stream) : launch_one<kType, 64>(p, m, stream);
+}
+
+}  // namespace
+}  // namespace ssd

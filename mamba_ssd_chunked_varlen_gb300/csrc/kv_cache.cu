@@ -17,7 +17,7 @@ ssd_status_t kv_check(KvView *c, const void *k_cache, const void *v_cache, const
                       int32_t table_width, int64_t table_stride, int32_t cache_type,
                       uint32_t *errors)
 {
-    if (total_len < 0 || batch < 0 || nheads_kv <= 0 || head_dim <= 0 || num_pages < 0 ||
+    if (total_len < 0 || batch < 0 || nheads_kv <= 0 || head_dim <= 0 || num_pages <= 0 ||
         page_size <= 0 || table_width < 0)
         return SSD_ERR_INVALID_ARG;
     if (cache_type != SSD_KV_BF16 && cache_type != SSD_KV_FP8_E4M3 && cache_type != SSD_KV_INT8)
@@ -31,15 +31,15 @@ ssd_status_t kv_check(KvView *c, const void *k_cache, const void *v_cache, const
         table_stride = table_width;
     if (table_stride < table_width)
         return SSD_ERR_INVALID_ARG;
-    if (total_len > INT32_MAX / 2 || batch > INT32_MAX / 2 || num_pages > INT32_MAX ||
+    if (total_len > INT32_MAX / 2 || batch > INT32_MAX / 2 || num_pages > INT32_MAX / 2 / nheads_kv ||
         static_cast<int64_t>(table_width) * page_size > INT32_MAX / 2 || nheads_kv > 65535)
         return SSD_ERR_UNSUPPORTED;
     if (total_len > 0 && batch > 0) {
         if (!qsl || !kv_lens || (table_width > 0 && !block_table))
             return SSD_ERR_INVALID_ARG;
-        if (num_pages > 0 && (!k_cache || !v_cache))
+        if (!k_cache || !v_cache)
             return SSD_ERR_INVALID_ARG;
-        if (cache_type != SSD_KV_BF16 && num_pages > 0 && (!k_scale || !v_scale))
+        if (cache_type != SSD_KV_BF16 && (!k_scale || !v_scale))
             return SSD_ERR_INVALID_ARG;
     }
     if (!kv_aligned16(k_cache) || !kv_aligned16(v_cache) || !kv_aligned16(k_scale) ||

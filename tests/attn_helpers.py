@@ -1,7 +1,7 @@
 """Shared helpers of the paged-cache tests: a ragged batch with its cache, and
 the 64-bit answers on the CPU.
 
-Error bounds (u = 2^-9 is bf16's relative rounding).  A probability enters the
+Error bounds (u = 2^-8 is bf16's relative rounding: 8 significant bits).  A probability enters the
 product with v rounded to bf16 (relative error u) and the result is rounded to
 bf16 once (u of |o| <= sum p|v|); a score is a sum of head_dim products in fp32,
 so it is off by at most eps = head_dim 2^-23 scale max sum|q k|, which changes
@@ -158,16 +158,16 @@ def attend_ref(q, k, v, n, kv, scale, window):
             l = p.sum()
             o[i, h] = p @ vv / l
             lse[i, h] = m + np.log(l)
-            ob[i, h] = (2 * 2.0 ** -9 * (1 + 2.0 ** -6) + 2 * eps + 2.0 ** -20
+            ob[i, h] = (2 * 2.0 ** -8 * (1 + 2.0 ** -6) + 2 * eps + 2.0 ** -20
                         + 2 * (hi - lo) * 2.0 ** -24) * (p @ np.abs(vv) / l) \
                 + 2.0 ** -126 * np.abs(vv).sum(0)
             lb[i, h] = eps + 2.0 ** -20 + (hi - lo) * 2.0 ** -24 + 2.0 ** -22 * abs(lse[i, h])
     return o, lse, ob, lb
 
 
-def check_attend(batch: Batch, o, lse, softmax_scale=None, window=0, what=""):
+def check_attend(batch: Batch, o, lse, softmax_scale=None, window=0, what="", stored=None):
     scale = 1 / math.sqrt(batch.dim) if softmax_scale is None else softmax_scale
-    ks, vs = batch.stored()
+    ks, vs = batch.stored() if stored is None else stored
     o, q = o.float().cpu().double().numpy(), batch.q.float().cpu().double().numpy()
     lse = None if lse is None else lse.cpu().double().numpy()
     at, worst = 0, 0.0

@@ -209,23 +209,17 @@ def test_device_side_errors():
 
     b = make()
     clean, _ = b.attend()
-    # a page out of range: its keys are seen by no query, the others as before
+    # a page out of range: its keys and values are zeros
     for bad in (-1, 1 << 20):
         b = make()
         b.block_table[0, 3] = bad
         o, lse = b.attend()
         assert b.errors.item() == attention.DEVERR_BAD_PAGE
-        assert torch.equal(o[20], clean[20]) and torch.isfinite(o).all()
+        assert torch.equal(o[20], clean[20])
         ks, vs = b.stored()
-        keep = np.r_[0:48, 64:300]
-        q = b.q[:20].float().cpu().double().numpy()
-        for i in (0, 19):
-            kk = ks[0][:281 + i][keep[keep < 281 + i]][:, 0]
-            vv = vs[0][:281 + i][keep[keep < 281 + i]][:, 0]
-            s = kk @ q[i, 0] / 8
-            p = np.exp(s - s.max())
-            want, size = p @ vv / p.sum(), p @ np.abs(vv) / p.sum()
-            assert np.all(np.abs(o[i, 0].float().cpu().numpy() - want) <= 2 ** -7.9 * size)
+        for x in (ks[0], vs[0]):
+            x[48:64] = 0.0
+        check_attend(b, o, lse, what="bad page", stored=(ks, vs))
     for n in (-1, 100000):
         b = make()
         b.kv_lens[1] = n

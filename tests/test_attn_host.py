@@ -73,7 +73,7 @@ def _attn(lib, **over):
 
 REFUSED = [
     (dict(total=-1), 1), (dict(batch=-1), 1), (dict(kv_heads=0), 1), (dict(dim=0), 1),
-    (dict(page=0), 1), (dict(pages=-1), 1), (dict(kind=3), 1), (dict(kind=-1), 1),
+    (dict(page=0), 1), (dict(pages=-1), 1), (dict(pages=0), 1), (dict(kind=3), 1), (dict(kind=-1), 1),
     (dict(qsl=None), 1), (dict(kv_lens=None), 1), (dict(table=None), 1), (dict(k_cache=None), 1),
     (dict(v_cache=None), 1), (dict(kind=1), 1), (dict(kind=2, k_scale=A), 1),
     (dict(k_cache=A + 8), 1), (dict(v_cache=A + 2), 1), (dict(kind=1, k_scale=A, v_scale=A + 4), 1),
