@@ -1,5 +1,6 @@
 // Attention over the paged cache: the plan of a call, the join of split rows,
 // and the C ABI (argument checks, tensor maps, launches).
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -30,7 +31,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64
     return incl + (warp ? scratch[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p)
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnParams p)
 {
     __shared__ int64_t scratch[32];
     const KvView &c = p.c;
@@ -60,12 +61,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p)
     if (bad) {
         if (tid == 0) {
             kv_error(c, SSD_DEVERR_BAD_QUERY_START_LOC);
-            p.hdr->total = 0;
-            p.hdr->units = 0;
+            for (int k = 0; k < 2; ++k) {
+                p.hdr->total[k] = 0;
+                p.hdr->count[k] = 0;
+            }
         }
         return;
     }
-    int64_t tiles = 0;
+    int64_t tiles[2] = {0, 0}, count[2] = {0, 0};
     for (int64_t base = 0; base < units; base += kPlanThreads) {
         const int64_t u = base + tid;
         AttnUnit e = {};
@@ -91,49 +94,60 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p)
             e.tile0 = p.window > 0 ? max(e.pos0 - p.window + 1, 0) / kTileKeys : 0;
             e.tiles = max((keys + kTileKeys - 1) / kTileKeys - e.tile0, 1);
         }
-        int64_t all;
-        const int64_t incl = block_scan(e.tiles, scratch, &all);
-        if (u < units) {
-            p.units[u] = e;
-            p.cum[u] = tiles + incl - e.tiles;
+        const int kind = e.tokens * p.group <= kFewRows ? 1 : 0;
+        for (int k = 0; k < 2; ++k) {
+            const bool mine = u < units && kind == k;
+            int64_t all, all_n;
+            const int64_t incl = block_scan(mine ? e.tiles : 0, scratch, &all);
+            const int64_t n = block_scan(mine ? 1 : 0, scratch, &all_n);
+            if (mine) {
+                const int64_t at = count[k] + n - 1;
+                const_cast<AttnUnit *>(p.line[k].units)[at] = e;
+                const_cast<int64_t *>(p.line[k].cum)[at] = tiles[k] + incl - e.tiles;
+            }
+            tiles[k] += all;
+            count[k] += all_n;
         }
-        tiles += all;
     }
-    if (tid == 0) {
-        p.cum[units] = tiles;
-        p.hdr->total = tiles * c.heads;
-        p.hdr->units = static_cast<int32_t>(units);
+    if (tid < 2) {
+        const_cast<int64_t *>(p.line[tid].cum)[count[tid]] = tiles[tid];
+        p.hdr->total[tid] = tiles[tid] * c.heads;
+        p.hdr->count[tid] = static_cast<int32_t>(count[tid]);
     }
 }
 
 // ---------------------------------------------------------------- join
 // Rows whose keys were split over several pieces: with M the largest of the
 // pieces' references m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// CTA (i, y) looks at the boundary before piece i + 1 and, when it is the first
-// boundary inside its (unit, kv head) pair, joins the pair's rows y, y + 8, ...
-// of every eight; the pieces are summed in their order.
+// CTA (i, y) looks at the boundary before piece i + 1 of the line of tiles (y < 8;
+// y = 8: of few rows) and, when it is the first boundary inside its (unit, kv
+// head) pair, joins an eighth of the pair's rows (all of the few); the pieces are
+// summed in their order.
 constexpr int kJoinWarps = 8, kJoinParts = 8;
 
 template <int kDim>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int kE = kDim / 32;
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t total = p.hdr->total;
+    const int kind = blockIdx.y / kJoinParts, part = blockIdx.y % kJoinParts;
+    const AttnLine &line = p.line[kind];
+    const int part_rows = attn_part_rows(kind);
+    const int64_t total = *line.total;
     if (total == 0)
         return;
     const int64_t i = static_cast<int64_t>(blockIdx.x) + 1, s = attn_piece_begin(total, i);
-    int u = 0, n = p.hdr->units;
+    int u = 0, n = *line.count;
     while (n > 1) {
         const int step = (n + 31) / 32, at = lane * step;
-        const bool below = at < n && p.cum[u + at] * p.c.heads <= s;
+        const bool below = at < n && line.cum[u + at] * p.c.heads <= s;
         const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
         u += k * step;
         n = min(step, n - k * step);
     }
-    const AttnUnit e = p.units[u];
-    const int64_t r = s - p.cum[u] * p.c.heads;
+    const AttnUnit e = line.units[u];
+    const int64_t r = s - line.cum[u] * p.c.heads;
     const int h = static_cast<int>(r / e.tiles);
     const int64_t begin = s - (r - static_cast<int64_t>(h) * e.tiles);
     if (s >= total || begin == s)
@@ -142,25 +156,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnParams p
     if (first != i - 1)
         return;
     const int rows = e.tokens * p.group;
-    for (int x = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); x < rows; x += kJoinWarps * kJoinParts) {
+    for (int x = part * kJoinWarps + (threadIdx.x >> 5); x < rows;
+         x += kind ? kJoinWarps : kJoinWarps * kJoinParts) {
         const int tok = x / p.group, sub = x % p.group;
         const int st = tok / p.tile_tokens;
         const int prow = st * 128 + (tok - st * p.tile_tokens) * p.group + sub;
         // every lane takes a piece's (m, l)
         float top = -INFINITY, sum = 0.f;
-        bool nan = false;
         for (int64_t base = first; base <= last; base += 32) {
             const int64_t k = base + lane;
             float2 ml = make_float2(-INFINITY, 0.f);
             if (k <= last && attn_piece_begin(total, k) < attn_piece_begin(total, k + 1))
-                ml = p.part_ml[attn_slot(k, k == first) * 256 + prow];
-            nan = nan || ml.x != ml.x;
+                ml = line.part_ml[attn_slot(k, k == first) * part_rows + prow];
             float m = ml.x;
 #pragma unroll
             for (int o = 16; o; o >>= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float nt = fmaxf(top, m);
-            float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - nt) * ml.y;
+            // (a row of NaN may have no reference)
+            float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - nt) * ml.y;
 #pragma unroll
             for (int o = 16; o; o >>= 1)
                 w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -174,10 +188,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnParams p
         for (int64_t k = first; k <= last; ++k) {
             if (attn_piece_begin(total, k) == attn_piece_begin(total, k + 1))
                 continue;
-            const int64_t at = attn_slot(k, k == first) * 256 + prow;
-            const float m = p.part_ml[at].x;
+            const int64_t at = attn_slot(k, k == first) * part_rows + prow;
+            const float m = line.part_ml[at].x;
             const float w = m == -INFINITY ? 0.f : exp2f(m - top);
-            const float *src = p.part_o + at * kDim + lane * kE;
+            const float *src = line.part_o + at * kDim + lane * kE;
 #pragma unroll
             for (int j = 0; j < kE; ++j)
                 acc[j] += w == 0.f ? 0.f : w * src[j];
@@ -307,6 +321,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.lse = lse;
     p.o_stride = o_stride;
+    p.q_stride = q_stride;
     p.heads = nheads;
     p.group = group;
     p.tile_tokens = kTileRows / group;
@@ -316,10 +331,13 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     p.negate = softmax_scale < 0.f;
     p.hdr = reinterpret_cast<AttnHeader *>(ws + L.header);
     p.seq_units = reinterpret_cast<int32_t *>(ws + L.seq_units);
-    p.units = reinterpret_cast<AttnUnit *>(ws + L.units);
-    p.cum = reinterpret_cast<int64_t *>(ws + L.cum);
-    p.part_o = reinterpret_cast<float *>(ws + L.part_o);
-    p.part_ml = reinterpret_cast<float2 *>(ws + L.part_ml);
+    for (int k = 0; k < 2; ++k)
+        p.line[k] = AttnLine{reinterpret_cast<AttnUnit *>(ws + L.units[k]),
+                             reinterpret_cast<int64_t *>(ws + L.cum[k]),
+                             p.hdr->total + k,
+                             p.hdr->count + k,
+                             reinterpret_cast<float *>(ws + L.part_o[k]),
+                             reinterpret_cast<float2 *>(ws + L.part_ml[k])};
 
     AttnMaps m = {};
     const uint64_t D = head_dim, rows = static_cast<uint64_t>(num_pages) * nheads_kv;
@@ -340,21 +358,27 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     if (!ok)
         return SSD_ERR_CUDA;
 
+    // a unit has at most min(total_len, 2 tiles' tokens) tokens and at least one:
+    // what that rules out is not launched
+    const bool tiles = std::min<int64_t>(total_len, 2 * p.tile_tokens) * group > kFewRows;
+    const bool few = group <= kFewRows;
+    p.few_behind_tiles = tiles && few;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess)
-        return SSD_ERR_CUDA;
-    const cudaError_t e = cache_type == SSD_KV_BF16       ? launch_attn_bf16(p, m, stream)
-                          : cache_type == SSD_KV_FP8_E4M3 ? launch_attn_fp8(p, m, stream)
-                                                          : launch_attn_int8(p, m, stream);
-    if (e != cudaSuccess)
-        return SSD_ERR_CUDA;
-    const dim3 grid(kAttnCtas - 1, kJoinParts);
-    if ((head_dim == 128 ? launch_pdl(attn_join_kernel<128>, grid, kJoinWarps * 32, stream, p)
-                         : launch_pdl(attn_join_kernel<64>, grid, kJoinWarps * 32, stream, p)) !=
-        cudaSuccess)
-        return SSD_ERR_CUDA;
-    return SSD_OK;
+    cudaError_t e = cudaGetLastError();
+    const bool bf16 = cache_type == SSD_KV_BF16, fp8 = cache_type == SSD_KV_FP8_E4M3;
+    if (e == cudaSuccess && tiles)
+        e = bf16 ? launch_attn_bf16(p, m, stream)
+                 : fp8 ? launch_attn_fp8(p, m, stream) : launch_attn_int8(p, m, stream);
+    if (e == cudaSuccess && few)
+        e = bf16 ? launch_attn_few_bf16(p, stream)
+                 : fp8 ? launch_attn_few_fp8(p, stream) : launch_attn_few_int8(p, stream);
+    if (e == cudaSuccess) {
+        const dim3 grid(kAttnCtas - 1, kJoinParts + (few ? 1 : 0));
+        e = head_dim == 128 ? launch_pdl(attn_join_kernel<128>, grid, kJoinWarps * 32, stream, p)
+                            : launch_pdl(attn_join_kernel<64>, grid, kJoinWarps * 32, stream, p);
+    }
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -14,8 +14,11 @@ constexpr int kTileKeys = 128;    // keys of a tile
 constexpr int kTileRows = 128;    // query rows of a tile: whole tokens, each with
                                   // the query heads of one kv head
 
-// A unit: up to two tiles of query rows of one sequence, with the range of key
-// tiles that any of its rows sees.  A unit is worked on once per kv head.
+constexpr int kFewRows = 32;      // most query rows of a unit of the kind "few"
+
+// A unit: query rows of one sequence, up to two tiles of them, with the range of
+// key tiles that any of its rows sees.  A unit is worked on once per kv head.
+// Units of at most kFewRows rows go to a kernel of their own (attn_few.cuh).
 struct alignas(32) AttnUnit {
     int32_t seq, row0, tokens;    // its new tokens: rows [row0, row0 + tokens)
     int32_t pos0;                 // position of the first (negative: padding)
@@ -25,37 +28,47 @@ struct alignas(32) AttnUnit {
 };
 static_assert(sizeof(AttnUnit) == 32, "unit size");
 
+// The key tiles of all (unit, kv head) pairs of one kind, unit by unit and head
+// by head, form a line that is cut into kAttnCtas equal pieces.  A pair that
+// falls into several pieces leaves partial results, at most two per piece.
+struct AttnLine {
+    const AttnUnit *units;
+    const int64_t *cum;           // (count + 1): key tiles before each unit, one head
+    const int64_t *total;         // key tiles of all units and kv heads
+    const int32_t *count;
+    float *part_o;                // [2 kAttnCtas][rows][dim]: sums of p v
+    float2 *part_ml;              // [2 kAttnCtas][rows]: reference (log2), sum of p
+};
+
 struct AttnHeader {
-    int64_t total;                // key tiles of all units and kv heads
-    int32_t units;
-    int32_t pad[61];
+    int64_t total[2];             // per kind: 0 tiles, 1 few rows
+    int32_t count[2];
+    int32_t pad[58];
 };
 static_assert(sizeof(AttnHeader) == 256, "header size");
 
-// The key tiles of all (unit, kv head) pairs, unit by unit and head by head,
-// form one line that is cut into kAttnCtas equal pieces.  A pair that falls
-// into several pieces leaves partial results, at most two per piece.
 struct AttnParams {
     KvView c;
     __nv_bfloat16 *o;
     const __nv_bfloat16 *q;
     float *lse;                   // may be null
-    int64_t o_stride;
+    int64_t o_stride, q_stride;
     int32_t heads, group;         // query heads, of them per kv head
     int32_t tile_tokens;          // tokens of a tile: 128 / group
     int32_t window;
     float scale_log2;             // |softmax_scale| log2(e)
     int32_t negate;               // 1: softmax_scale < 0 (the scores change sign)
+    int32_t few_behind_tiles;     // 1: the kernel of few rows follows the tiles' kernel
     AttnHeader *hdr;
-    int32_t *seq_units;           // (batch + 1): units before each sequence
-    AttnUnit *units;
-    int64_t *cum;                 // (units + 1): key tiles before each unit, one head
-    float *part_o;                // [2 kAttnCtas][256][dim]: sums of p v
-    float2 *part_ml;              // [2 kAttnCtas][256]: maximum (log2), sum of p
+    int32_t *seq_units;           // (batch): units before each sequence
+    AttnLine line[2];
 };
 
+// Rows of a partial result of each kind.
+__host__ __device__ constexpr int attn_part_rows(int kind) { return kind ? kFewRows : 2 * kTileRows; }
+
 struct AttnLayout {
-    size_t header, seq_units, units, cum, part_ml, part_o, total;
+    size_t header, seq_units, units[2], cum[2], part_ml[2], part_o[2], total;
 };
 
 inline int64_t attn_max_units(int64_t total_len, int32_t batch, int32_t group)
@@ -76,10 +89,13 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
     };
     L.header = take(sizeof(AttnHeader));
     L.seq_units = take(sizeof(int32_t) * (static_cast<size_t>(batch) + 1));
-    L.units = take(sizeof(AttnUnit) * units);
-    L.cum = take(sizeof(int64_t) * (units + 1));
-    L.part_ml = take(sizeof(float2) * 2 * kAttnCtas * 256);
-    L.part_o = take(sizeof(float) * 2 * kAttnCtas * 256 * static_cast<size_t>(dim));
+    for (int k = 0; k < 2; ++k) {
+        const size_t rows = 2 * kAttnCtas * static_cast<size_t>(attn_part_rows(k));
+        L.units[k] = take(sizeof(AttnUnit) * units);
+        L.cum[k] = take(sizeof(int64_t) * (units + 1));
+        L.part_ml[k] = take(sizeof(float2) * rows);
+        L.part_o[k] = take(sizeof(float) * rows * static_cast<size_t>(dim));
+    }
     L.total = off;
     return L;
 }
@@ -101,15 +117,82 @@ __device__ __forceinline__ int attn_slot(int64_t piece, bool starts)
     return static_cast<int>(2 * piece + (starts ? 1 : 0));
 }
 
+// A CTA's piece of a line, segment by segment: a segment is the part of one
+// (unit, kv head) pair that lies in the piece.  Constructed by whole warps.
+struct AttnWalk {
+    const AttnLine &line;
+    int32_t heads;
+    int64_t pos, end;
+    int32_t u, h, ta, tb;     // unit, kv head, tiles [ta, tb) of the unit's
+    AttnUnit e;
+
+    __device__ __forceinline__ AttnWalk(const AttnLine &l, int32_t heads_) : line(l), heads(heads_)
+    {
+        const int64_t total = *line.total;
+        pos = total > 0 ? attn_piece_begin(total, blockIdx.x) : 0;
+        end = total > 0 ? attn_piece_begin(total, blockIdx.x + 1) : 0;
+        u = h = ta = tb = 0;
+        if (pos >= end)
+            return;
+        // the last unit whose tiles begin at or before pos, 32 probes at a time
+        const int lane = threadIdx.x & 31;
+        int n = *line.count;
+        while (n > 1) {
+            const int step = (n + 31) / 32, at = lane * step;
+            const bool below = at < n && line.cum[u + at] * heads <= pos;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
+            u += k * step;
+            n = min(step, n - k * step);
+        }
+        e = line.units[u];
+        const int64_t r = pos - line.cum[u] * heads;
+        h = static_cast<int32_t>(r / e.tiles);
+        ta = static_cast<int32_t>(r - static_cast<int64_t>(h) * e.tiles);
+        set();
+    }
+    __device__ __forceinline__ void set()
+    {
+        const int64_t left = end - pos;
+        tb = left < e.tiles - ta ? ta + static_cast<int32_t>(left) : e.tiles;
+    }
+    __device__ __forceinline__ bool more() const { return pos < end; }
+    __device__ __forceinline__ void next()
+    {
+        pos += tb - ta;
+        if (pos >= end)
+            return;
+        ta = 0;
+        if (++h == heads) {
+            h = 0;
+            e = line.units[++u];
+        }
+        set();
+    }
+    // whether the segment begins its pair, and is all of it
+    __device__ __forceinline__ bool starts() const { return ta == 0; }
+    __device__ __forceinline__ bool whole() const { return ta == 0 && tb == e.tiles; }
+};
+
+// Whether some row of tokens [first, last] of a unit does not see all of the n
+// keys from k0 on.
+__device__ __forceinline__ bool attn_partial(const AttnUnit &e, int window, int k0, int n, int first,
+                                             int last)
+{
+    return k0 + n > e.pos0 + first + 1 || (window > 0 && k0 < e.pos0 + last - window + 1);
+}
+
 struct AttnMaps {
     CUtensorMap Q;       // bf16 (dim, heads, rows), box {64, group, tile_tokens}, 128-byte swizzle
     CUtensorMap K, V;    // bf16: (dim, page, pages * heads), box {64, min(page, 128), 1}, swizzled;
                          // 8-bit codes: bytes, box {dim, min(page, 128), 1}, packed
 };
 
-// The kernel of one cache type (one translation unit each).
+// The two kernels of one cache type (one translation unit each).
 cudaError_t launch_attn_bf16(const AttnParams &p, const AttnMaps &m, cudaStream_t s);
 cudaError_t launch_attn_fp8(const AttnParams &p, const AttnMaps &m, cudaStream_t s);
 cudaError_t launch_attn_int8(const AttnParams &p, const AttnMaps &m, cudaStream_t s);
+cudaError_t launch_attn_few_bf16(const AttnParams &p, cudaStream_t s);
+cudaError_t launch_attn_few_fp8(const AttnParams &p, cudaStream_t s);
+cudaError_t launch_attn_few_int8(const AttnParams &p, cudaStream_t s);
 
 }  // namespace ssd

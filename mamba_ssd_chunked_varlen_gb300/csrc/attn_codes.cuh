@@ -1,0 +1,56 @@
+// Widening of 8-bit codes to bf16 pairs, for the attention kernels.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attn.cuh"
+#include "attn_ptx.cuh"
+#include "kernels.cuh"
+
+namespace ssd {
+namespace {
+
+// Codes to bf16 pairs (both exact).  int8: with the low seven bits put into
+// bf16's mantissa at 128 = 0x4300, code = (128 + low7) - (128 or 256 with the sign bit).
+__device__ __forceinline__ uint32_t int8_pair(uint32_t two)   // codes in bytes 0 and 2
+{
+    const uint32_t a = (two & 0x007f007fu) | 0x43004300u, b = (two & 0x00800080u) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+template <int kType>
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t *out)
+{
+    if constexpr (kType == SSD_KV_INT8) {
+        out[0] = int8_pair(__byte_perm(codes, 0, 0x4140));
+        out[1] = int8_pair(__byte_perm(codes, 0, 0x4342));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t h2;
+            const uint16_t pair = static_cast<uint16_t>(codes >> (16 * i));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(pair));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+            out[i] = pack_bf16(f.x, f.y);
+        }
+    }
+}
+
+// Of two registers with codes of two keys, neighbouring columns in their bytes:
+// the pairs of the two keys' codes of columns b and b + 1 (b 0 or 2).
+template <int kType, int b>
+__device__ __forceinline__ void widen_columns(uint32_t key0, uint32_t key1, uint32_t *out)
+{
+    if constexpr (kType == SSD_KV_INT8) {
+        const uint32_t x = __byte_perm(key0, key1, b ? 0x7632 : 0x5410);   // codes in bytes 0, 2 and 1, 3
+        out[0] = int8_pair(x);
+        out[1] = int8_pair(x >> 8);
+    } else {
+        widen4<kType>(__byte_perm(key0, key1, b ? 0x7362 : 0x5140), out);
+    }
+}
+
+}  // namespace
+}  // namespace ssd

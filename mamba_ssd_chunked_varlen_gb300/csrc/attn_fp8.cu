@@ -1,4 +1,5 @@
-// The attention kernel over a fp8 cache.
+// The attention kernels over a fp8 cache.
+#include "attn_few.cuh"
 #include "attn_kernel.cuh"
 
 namespace ssd {
@@ -6,6 +7,11 @@ namespace ssd {
 cudaError_t launch_attn_fp8(const AttnParams &p, const AttnMaps &m, cudaStream_t s)
 {
     return launch_type<SSD_KV_FP8_E4M3>(p, m, s);
+}
+
+cudaError_t launch_attn_few_fp8(const AttnParams &p, cudaStream_t s)
+{
+    return launch_few<SSD_KV_FP8_E4M3>(p, s);
 }
 
 }  // namespace ssd

@@ -25,8 +25,7 @@
 //   warp 13          tcgen05 issuer
 #pragma once
 
-#include "attn.cuh"
-#include "attn_ptx.cuh"
+#include "attn_codes.cuh"
 #include "kernels.cuh"
 
 namespace ssd {
@@ -77,104 +76,11 @@ enum Bar {
 };
 static_assert(kNumBars * 8 + 16 <= 512, "barrier space");
 
-// The CTA's piece of the line of tiles, segment by segment: a segment is the
-// part of one (unit, kv head) pair that lies in the piece.
-struct Walk {
-    const AttnParams &p;
-    int64_t pos, end;
-    int32_t u, h, ta, tb;
-    AttnUnit e;
-    bool starts, whole;      // the segment begins its pair / is all of it
-
-    __device__ __forceinline__ explicit Walk(const AttnParams &p_) : p(p_)
-    {
-        const int64_t total = p.hdr->total;
-        pos = total > 0 ? attn_piece_begin(total, blockIdx.x) : 0;
-        end = total > 0 ? attn_piece_begin(total, blockIdx.x + 1) : 0;
-        h = -1;
-        tb = 0;
-        u = 0;
-        if (pos >= end)
-            return;
-        // the last unit whose tiles begin at or before pos, 32 probes at a time
-        const int lane = threadIdx.x & 31;
-        int n = p.hdr->units;
-        while (n > 1) {
-            const int step = (n + 31) / 32, at = lane * step;
-            const bool below = at < n && p.cum[u + at] * p.c.heads <= pos;
-            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
-            u += k * step;
-            n = min(step, n - k * step);
-        }
-        e = p.units[u];
-        const int64_t r = pos - p.cum[u] * p.c.heads;
-        h = static_cast<int32_t>(r / e.tiles);
-        ta = static_cast<int32_t>(r - static_cast<int64_t>(h) * e.tiles);
-        set();
-    }
-    __device__ __forceinline__ void set()
-    {
-        const int64_t left = end - pos;
-        tb = left < e.tiles - ta ? ta + static_cast<int32_t>(left) : e.tiles;
-        starts = ta == 0;
-        whole = starts && tb == e.tiles;
-    }
-    __device__ __forceinline__ bool more() const { return pos < end; }
-    __device__ __forceinline__ void next()
-    {
-        pos += tb - ta;
-        if (pos >= end)
-            return;
-        ta = 0;
-        if (++h == p.c.heads) {
-            h = 0;
-            e = p.units[++u];
-        }
-        set();
-    }
-    __device__ __forceinline__ int streams() const { return e.tokens > p.tile_tokens ? 2 : 1; }
-    // Whether some row of tokens [first, last] of the unit does not see all of key tile t.
-    __device__ __forceinline__ bool partial(int t, int first, int last) const
-    {
-        const int k0 = (e.tile0 + t) * kTileKeys;
-        return k0 + kTileKeys > e.pos0 + first + 1 ||
-               (p.window > 0 && k0 < e.pos0 + last - p.window + 1);
-    }
-};
-
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-
-// Codes to bf16 pairs (both exact).  int8: with the low seven bits put into
-// bf16's mantissa at 128 = 0x4300, code = (128 + low7) - (128 or 256 with the sign bit).
-__device__ __forceinline__ uint32_t int8_pair(uint32_t two)   // codes in bytes 0 and 2
-{
-    const uint32_t a = (two & 0x007f007fu) | 0x43004300u, b = (two & 0x00800080u) | 0x43004300u;
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-template <int kType>
-__device__ __forceinline__ void widen4(uint32_t codes, uint32_t *out)
-{
-    if constexpr (kType == SSD_KV_INT8) {
-        out[0] = int8_pair(__byte_perm(codes, 0, 0x4140));
-        out[1] = int8_pair(__byte_perm(codes, 0, 0x4342));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t h2;
-            const uint16_t pair = static_cast<uint16_t>(codes >> (16 * i));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(pair));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-            out[i] = pack_bf16(f.x, f.y);
-        }
-    }
-}
 
 template <int kType, int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_kernel(const __grid_constant__ AttnMaps maps, AttnParams p)
+    attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
 {
     using C = Cfg<kType, kDim>;
     extern __shared__ uint8_t smem_raw[];
@@ -210,10 +116,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    pdl_launch_dependents();
     pdl_wait();                                // the plan
+    pdl_launch_dependents();                   // (few rows: they need nothing but the plan)
     const int g = p.group, tt = p.tile_tokens;
     bool ok = true;
+    auto streams = [&](const AttnUnit &e) { return e.tokens > tt ? 2 : 1; };
+    auto partial = [&](const AttnUnit &e, int t, int first, int last) {
+        return attn_partial(e, p.window, (e.tile0 + t) * kTileKeys, kTileKeys, first, last);
+    };
     auto wait = [&](int bar, uint32_t parity) {
         ok = ok && ptx::mbar_wait(bars + bar, parity & 1, kWaitTimeoutNs) && !*s_abort;
         ok = __all_sync(0xffffffffu, ok);   // the warp leaves its loops together
@@ -229,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kFull = C::kQuant ? kRawFull : kKvFull, kEmpty = C::kQuant ? kRawEmpty : kKvEmpty;
         const int shift = p.c.page_shift;
         const int boxes = shift >= 7 ? 1 : kTileKeys >> shift;    // pages of a tile
-        for (Walk w(p); w.more() && ok; w.next(), ++qit) {
-            const int ns = w.streams();
+        for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next(), ++qit) {
+            const int ns = streams(w.e);
             if (qit > 0 && !wait(kQEmpty, qit - 1))
                 break;
             if (lane == 0) {
@@ -326,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mma_commit(bars + kSFull + st);
             }
         };
-        for (Walk w(p); w.more() && ok; w.next(), ++qit) {
-            const int ns = w.streams(), n = w.tb - w.ta;
+        for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next(), ++qit) {
+            const int ns = streams(w.e), n = w.tb - w.ta;
             if (!wait(kQFull, qit) || !wait(kKvFull + it % C::kStages, it / C::kStages))
                 break;
             ptx::tc_fence_after_sync();
@@ -345,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(kKvFull + vs, vi / C::kStages))
                     break;
                 if constexpr (!C::kQuant) {
-                    if (w.partial(w.ta + t, 0, w.e.tokens - 1)) {
+                    if (partial(w.e, w.ta + t, 0, w.e.tokens - 1)) {
                         if (lane == 0)
                             ptx::mbar_arrive(bars + kFixReq);
                         if (!wait(kFixDone, fit++))
@@ -407,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // would reach rows that do not see them; the output adds them
             // back for the rows that do.
             uint32_t it = 0, fit = 0;
-            for (Walk w(p); w.more() && ok; w.next()) {
+            for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next()) {
                 for (int t = w.ta; t < w.tb && ok; ++t, it += 2) {
-                    if (!w.partial(t, 0, w.e.tokens - 1))
+                    if (!partial(w.e, t, 0, w.e.tokens - 1))
                         continue;
                     if (!wait(kFixReq, fit++))
                         break;
@@ -451,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- converter
             constexpr int kUnits = kDim / 16;  // 16-code pieces of a row
             uint32_t it = 0;
-            for (Walk w(p); w.more() && ok; w.next())
+            for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next())
                 for (int t = w.ta; t < w.tb && ok; ++t)
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
                         const int rs = it % C::kRawStages, s = it % C::kStages;
@@ -497,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int my_tok = row / g, my_head = row % g;
         const float c2 = p.scale_log2;
         uint32_t it = 0, sit = 0, oit = 0;
-        for (Walk w(p); w.more() && ok; w.next()) {
-            if (w.streams() <= st) {
+        for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next()) {
+            if (streams(w.e) <= st) {
                 sit += w.tb - w.ta;
                 continue;
             }
@@ -539,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
                     }
                 }
-                const bool partial = w.partial(t, tok0, tok0 + ntok - 1);
-                if (partial) {
+                const bool hides = partial(w.e, t, tok0, tok0 + ntok - 1);
+                if (hides) {
                     const int k0 = (w.e.tile0 + t) * kTileKeys;
                     const int a = lo - k0, b = hi - k0;
 #pragma unroll
@@ -595,10 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (C::kQuant) {
                         const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + k);
                         // (a hidden key's scale may be NaN: its weight stays zero)
-                        e0 = partial && e0 == 0.f ? 0.f : e0 * f.x;
-                        e1 = partial && e1 == 0.f ? 0.f : e1 * f.y;
-                        e2 = partial && e2 == 0.f ? 0.f : e2 * f.z;
-                        e3 = partial && e3 == 0.f ? 0.f : e3 * f.w;
+                        e0 = hides && e0 == 0.f ? 0.f : e0 * f.x;
+                        e1 = hides && e1 == 0.f ? 0.f : e1 * f.y;
+                        e2 = hides && e2 == 0.f ? 0.f : e2 * f.z;
+                        e3 = hides && e3 == 0.f ? 0.f : e3 * f.w;
                     }
                     pk[k / 2] = pack_bf16(e0, e1);
                     pk[k / 2 + 1] = pack_bf16(e2, e3);
@@ -620,10 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const int64_t grow = w.e.row0 + tok0 + my_tok;
             const int head = w.h * g + my_head;
-            const int slot = attn_slot(blockIdx.x, w.starts);
+            const int slot = attn_slot(blockIdx.x, w.starts());
             const int prow = slot * 256 + st * 128 + row;
             __nv_bfloat16 *dst = p.o + grow * p.o_stride + static_cast<int64_t>(head) * kDim;
-            float *part = p.part_o + static_cast<int64_t>(prow) * kDim;
+            float *part = p.line[0].part_o + static_cast<int64_t>(prow) * kDim;
 #pragma unroll
             for (int k = 0; k < kDim; k += 32) {
                 uint32_t o[32];
@@ -633,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nonfinite && mine) {
                     // the cleaned values of the keys that this row sees
                     for (int t = w.ta; t < w.tb; ++t) {
-                        if (!w.partial(t, 0, w.e.tokens - 1))
+                        if (!partial(w.e, t, 0, w.e.tokens - 1))
                             continue;
                         const int k0 = (w.e.tile0 + t) * kTileKeys;
                         for (int j = max(k0, max(lo, 0)); j < min(k0 + kTileKeys, hi); ++j) {
@@ -651,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (mine && w.whole) {
+                if (mine && w.whole()) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         uint4 v;
@@ -669,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (mine) {
-                if (!w.whole)
-                    p.part_ml[prow] = make_float2(m, l);
+                if (!w.whole())
+                    p.line[0].part_ml[prow] = make_float2(m, l);
                 else if (p.lse)
                     p.lse[grow * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             }

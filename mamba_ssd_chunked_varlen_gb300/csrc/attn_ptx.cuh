@@ -86,6 +86,42 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r)
         : "memory");
 }
 
+// Asynchronous copy of kBytes (8 or 16) to shared memory; with `there` false the
+// destination is filled with zeros and the source is not read.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool there)
+{
+    const int n = there ? kBytes : 0;
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
+                     : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Waits until at most kLeft of this thread's latest groups are in flight.
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// d (16 x 8, fp32) += a (16 x 16, bf16) b (16 x 8, bf16), by one warp.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // Registers per thread of this warpgroup, out of what the block was launched
 // with; every warp of the warpgroup executes it.
 template <int kRegs>
