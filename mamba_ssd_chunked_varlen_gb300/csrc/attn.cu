@@ -91,8 +91,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
             e.kv_len = kv_len_of(c, lo);
             e.pos0 = e.kv_len - rows + first;
             const int32_t keys = max(e.pos0 + e.tokens, 0);
-            e.tile0 = p.window > 0 ? max(e.pos0 - p.window + 1, 0) / kTileKeys : 0;
-            e.tiles = max((keys + kTileKeys - 1) / kTileKeys - e.tile0, 1);
+            const int n = e.tokens * p.group <= kFewRows ? kFewKeys : kTileKeys;
+            e.tile0 = p.window > 0 ? max(e.pos0 - p.window + 1, 0) / n : 0;
+            e.tiles = max((keys + n - 1) / n - e.tile0, 1);
         }
         const int kind = e.tokens * p.group <= kFewRows ? 1 : 0;
         for (int k = 0; k < 2; ++k) {
@@ -118,84 +119,79 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // ---------------------------------------------------------------- join
 // Rows whose keys were split over several pieces: with M the largest of the
-// pieces' references m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// CTA (i, y) looks at the boundary before piece i + 1 of the line of tiles (y < 8;
-// y = 8: of few rows) and, when it is the first boundary inside its (unit, kv
-// head) pair, joins an eighth of the pair's rows (all of the few); the pieces are
-// summed in their order.
-constexpr int kJoinWarps = 8, kJoinParts = 8;
+// pieces' references m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i,  the pieces
+// summed in a fixed order.  A CTA of four warps takes four rows of a split pair
+// of the tiles' kind, a warp each, or one row of few, its warps every fourth
+// piece (a decoding sequence's one row may lie in hundreds of pieces).
+constexpr int kJoinWarps = 4;
+constexpr int kJoinTileCtas = kAttnCtas - 1;        // x kJoinTileParts: a boundary between pieces each
+constexpr int kJoinTileParts = 2 * kTileRows / kJoinWarps;
+constexpr int kJoinFewCtas = 8 * kAttnCtas;
+
+// What pieces first, first + step, ... <= last of a row give: its sums relative to `top`.
+template <int kE>
+__device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows, int64_t first,
+                                            int64_t from, int64_t last, int step, int row, int dim,
+                                            float &top, float &sum, float (&acc)[kE])
+{
+    const int lane = threadIdx.x & 31;
+    top = -INFINITY;
+    sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kE; ++j)
+        acc[j] = 0.f;
+    for (int64_t base = from; base <= last; base += 32 * step) {
+        // a lane per piece
+        const int64_t mine = base + lane * step;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (mine <= last)
+            ml = line.part_ml[attn_slot(mine, mine == first) * part_rows + row];
+        float m = ml.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float nt = fmaxf(top, m), f = top == nt ? 1.f : exp2f(top - nt);
+        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - nt);
+        // (a row of NaN may have no reference)
+        float s = ml.x == -INFINITY ? ml.y : w * ml.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        sum = sum * f + s;
+        top = nt;
+#pragma unroll
+        for (int j = 0; j < kE; ++j)
+            acc[j] *= f;
+        const int n = static_cast<int>(min(static_cast<int64_t>(32), (last - base) / step + 1));
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const int64_t at = base + k * step;
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float *src =
+                line.part_o + (attn_slot(at, at == first) * static_cast<int64_t>(part_rows) + row) * dim +
+                lane * kE;
+#pragma unroll
+            for (int j = 0; j < kE; ++j)
+                acc[j] += wk == 0.f ? 0.f : wk * src[j];
+        }
+    }
+}
 
 template <int kDim>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int kE = kDim / 32;
+    __shared__ float s_ml[kJoinWarps][2], s_acc[kJoinWarps][kDim];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int kind = blockIdx.y / kJoinParts, part = blockIdx.y % kJoinParts;
+    const int kind = blockIdx.x < kJoinTileCtas * kJoinTileParts ? 0 : 1;
     const AttnLine &line = p.line[kind];
-    const int part_rows = attn_part_rows(kind);
     const int64_t total = *line.total;
     if (total == 0)
         return;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) + 1, s = attn_piece_begin(total, i);
-    int u = 0, n = *line.count;
-    while (n > 1) {
-        const int step = (n + 31) / 32, at = lane * step;
-        const bool below = at < n && line.cum[u + at] * p.c.heads <= s;
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
-        u += k * step;
-        n = min(step, n - k * step);
-    }
-    const AttnUnit e = line.units[u];
-    const int64_t r = s - line.cum[u] * p.c.heads;
-    const int h = static_cast<int>(r / e.tiles);
-    const int64_t begin = s - (r - static_cast<int64_t>(h) * e.tiles);
-    if (s >= total || begin == s)
-        return;
-    const int64_t first = attn_piece_of(total, begin), last = attn_piece_of(total, begin + e.tiles - 1);
-    if (first != i - 1)
-        return;
-    const int rows = e.tokens * p.group;
-    for (int x = part * kJoinWarps + (threadIdx.x >> 5); x < rows;
-         x += kind ? kJoinWarps : kJoinWarps * kJoinParts) {
-        const int tok = x / p.group, sub = x % p.group;
-        const int st = tok / p.tile_tokens;
-        const int prow = st * 128 + (tok - st * p.tile_tokens) * p.group + sub;
-        // every lane takes a piece's (m, l)
-        float top = -INFINITY, sum = 0.f;
-        for (int64_t base = first; base <= last; base += 32) {
-            const int64_t k = base + lane;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (k <= last && attn_piece_begin(total, k) < attn_piece_begin(total, k + 1))
-                ml = line.part_ml[attn_slot(k, k == first) * part_rows + prow];
-            float m = ml.x;
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float nt = fmaxf(top, m);
-            // (a row of NaN may have no reference)
-            float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - nt) * ml.y;
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                w += __shfl_xor_sync(0xffffffffu, w, o);
-            sum = (top == -INFINITY ? 0.f : sum * exp2f(top - nt)) + w;
-            top = nt;
-        }
-        float acc[kE];
-#pragma unroll
-        for (int j = 0; j < kE; ++j)
-            acc[j] = 0.f;
-        for (int64_t k = first; k <= last; ++k) {
-            if (attn_piece_begin(total, k) == attn_piece_begin(total, k + 1))
-                continue;
-            const int64_t at = attn_slot(k, k == first) * part_rows + prow;
-            const float m = line.part_ml[at].x;
-            const float w = m == -INFINITY ? 0.f : exp2f(m - top);
-            const float *src = line.part_o + at * kDim + lane * kE;
-#pragma unroll
-            for (int j = 0; j < kE; ++j)
-                acc[j] += w == 0.f ? 0.f : w * src[j];
-        }
+    const int pieces = attn_pieces(kind, total);
+    float top, sum, acc[kE];
+    auto write = [&](const AttnUnit &e, int h, int tok, int sub) {
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int64_t row = e.row0 + tok;
         const int head = h * p.group + sub;
@@ -206,6 +202,77 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
         if (p.lse && lane == 0)
             p.lse[row * p.heads + head] =
                 sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    };
+    if (kind == 0) {
+        // the boundary before piece i, if it is the first inside its pair
+        const int64_t i = blockIdx.x / kJoinTileParts + 1, s = attn_piece_begin(total, pieces, i);
+        if (s >= total)
+            return;
+        int u = 0, n = *line.count;
+        while (n > 1) {
+            const int step = (n + 31) / 32, at = lane * step;
+            const bool below = at < n && line.cum[u + at] * p.c.heads <= s;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
+            u += k * step;
+            n = min(step, n - k * step);
+        }
+        const AttnUnit e = line.units[u];
+        const int64_t r = s - line.cum[u] * p.c.heads;
+        const int h = static_cast<int>(r / e.tiles);
+        const int64_t begin = s - (r - static_cast<int64_t>(h) * e.tiles);
+        const int64_t first = attn_piece_of(total, pieces, begin);
+        const int x = blockIdx.x % kJoinTileParts * kJoinWarps + warp;
+        if (begin == s || first != i - 1 || x >= e.tokens * p.group)
+            return;
+        const int64_t last = attn_piece_of(total, pieces, begin + e.tiles - 1);
+        const int tok = x / p.group, st = tok / p.tile_tokens;
+        const int row = st * kTileRows + (tok - st * p.tile_tokens) * p.group + x % p.group;
+        join_pieces<kE>(line, attn_part_rows(0), first, first, last, 1, row, kDim, top, sum, acc);
+        write(e, h, tok, x % p.group);
+        return;
+    }
+    const int64_t items = static_cast<int64_t>(*line.count) * p.c.heads * kFewRows;
+    for (int64_t item = blockIdx.x - kJoinTileCtas * kJoinTileParts; item < items; item += kJoinFewCtas) {
+        const int row = static_cast<int>(item % kFewRows);
+        const int64_t pair = item / kFewRows;
+        const int u = static_cast<int>(pair / p.c.heads), h = static_cast<int>(pair % p.c.heads);
+        const AttnUnit e = line.units[u];
+        if (row >= e.tokens * p.group)
+            continue;
+        const int64_t begin = line.cum[u] * p.c.heads + static_cast<int64_t>(h) * e.tiles;
+        const int64_t first = attn_piece_of(total, pieces, begin);
+        const int64_t last = attn_piece_of(total, pieces, begin + e.tiles - 1);
+        if (first == last)
+            continue;
+        join_pieces<kE>(line, kFewRows, first, first + warp, last, kJoinWarps, row, kDim, top, sum, acc);
+        if (lane == 0) {
+            s_ml[warp][0] = top;
+            s_ml[warp][1] = sum;
+        }
+#pragma unroll
+        for (int j = 0; j < kE; ++j)
+            s_acc[warp][lane * kE + j] = acc[j];
+        __syncthreads();
+        if (warp == 0) {
+            top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k)
+                top = fmaxf(top, s_ml[k][0]);
+            sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < kE; ++j)
+                acc[j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                const float w = s_ml[k][0] == -INFINITY ? 0.f : exp2f(s_ml[k][0] - top);
+                sum += s_ml[k][0] == -INFINITY ? s_ml[k][1] : w * s_ml[k][1];
+#pragma unroll
+                for (int j = 0; j < kE; ++j)
+                    acc[j] += w == 0.f ? 0.f : w * s_acc[k][lane * kE + j];
+            }
+            write(e, h, row / p.group, row % p.group);
+        }
+        __syncthreads();
     }
 }
 
@@ -374,7 +441,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
         e = bf16 ? launch_attn_few_bf16(p, stream)
                  : fp8 ? launch_attn_few_fp8(p, stream) : launch_attn_few_int8(p, stream);
     if (e == cudaSuccess) {
-        const dim3 grid(kAttnCtas - 1, kJoinParts + (few ? 1 : 0));
+        const dim3 grid(kJoinTileCtas * kJoinTileParts + (few ? kJoinFewCtas : 0));
         e = head_dim == 128 ? launch_pdl(attn_join_kernel<128>, grid, kJoinWarps * 32, stream, p)
                             : launch_pdl(attn_join_kernel<64>, grid, kJoinWarps * 32, stream, p);
     }

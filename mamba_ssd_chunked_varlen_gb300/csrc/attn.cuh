@@ -8,37 +8,54 @@
 
 namespace ssd {
 
-// One CTA per SM of a GB300; the work is split over exactly this many.
+// One CTA per SM of a GB300.
 constexpr int kAttnCtas = 152;
 constexpr int kTileKeys = 128;    // keys of a tile
 constexpr int kTileRows = 128;    // query rows of a tile: whole tokens, each with
                                   // the query heads of one kv head
 
-constexpr int kFewRows = 32;      // most query rows of a unit of the kind "few"
+constexpr int kFewRows = 16;      // most query rows of a unit of the kind "few"
+constexpr int kFewKeys = 16;      // keys of such a unit's tile
+constexpr int kFewWarps = 12;     // warps of a CTA of its kernel
 
-// A unit: query rows of one sequence, up to two tiles of them, with the range of
-// key tiles that any of its rows sees.  A unit is worked on once per kv head.
-// Units of at most kFewRows rows go to a kernel of their own (attn_few.cuh).
+// A unit: query rows of one sequence with the range of key tiles that any of its
+// rows sees.  A unit is worked on once per kv head.  Kind 0: up to two tiles of
+// rows, for the tensor cores; kind 1: at most kFewRows rows (attn_few.cuh).
 struct alignas(32) AttnUnit {
     int32_t seq, row0, tokens;    // its new tokens: rows [row0, row0 + tokens)
     int32_t pos0;                 // position of the first (negative: padding)
-    int32_t tile0, tiles;         // key tiles [tile0, tile0 + tiles), at least one
+    int32_t tile0, tiles;         // key tiles of its kind [tile0, tile0 + tiles), at least one
     int32_t kv_len;
     int32_t pad;
 };
 static_assert(sizeof(AttnUnit) == 32, "unit size");
 
 // The key tiles of all (unit, kv head) pairs of one kind, unit by unit and head
-// by head, form a line that is cut into kAttnCtas equal pieces.  A pair that
-// falls into several pieces leaves partial results, at most two per piece.
+// by head, form a line that is cut into equal pieces: a piece per CTA (kind 0), or
+// per warp (kind 1; fewer pieces when the line is short).  A pair that falls
+// into several pieces leaves partial results, at most two per piece.
 struct AttnLine {
     const AttnUnit *units;
     const int64_t *cum;           // (count + 1): key tiles before each unit, one head
     const int64_t *total;         // key tiles of all units and kv heads
     const int32_t *count;
-    float *part_o;                // [2 kAttnCtas][rows][dim]: sums of p v
-    float2 *part_ml;              // [2 kAttnCtas][rows]: reference (log2), sum of p
+    float *part_o;                // [2 pieces][rows][dim]: sums of p v
+    float2 *part_ml;              // [2 pieces][rows]: reference (log2), sum of p
 };
+
+// Most pieces of each kind, and the fewest tiles of one (every piece has a tile).
+__host__ __device__ constexpr int attn_max_pieces(int kind)
+{
+    return kind ? kAttnCtas * kFewWarps : kAttnCtas;
+}
+constexpr int kFewPieceTiles = 4;
+
+__host__ __device__ inline int attn_pieces(int kind, int64_t total)
+{
+    const int most = attn_max_pieces(kind);
+    const int64_t n = kind ? (total + kFewPieceTiles - 1) / kFewPieceTiles : total;
+    return n < most ? static_cast<int>(n) : most;
+}
 
 struct AttnHeader {
     int64_t total[2];             // per kind: 0 tiles, 1 few rows
@@ -90,7 +107,7 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
     L.header = take(sizeof(AttnHeader));
     L.seq_units = take(sizeof(int32_t) * (static_cast<size_t>(batch) + 1));
     for (int k = 0; k < 2; ++k) {
-        const size_t rows = 2 * kAttnCtas * static_cast<size_t>(attn_part_rows(k));
+        const size_t rows = 2 * static_cast<size_t>(attn_max_pieces(k)) * attn_part_rows(k);
         L.units[k] = take(sizeof(AttnUnit) * units);
         L.cum[k] = take(sizeof(int64_t) * (units + 1));
         L.part_ml[k] = take(sizeof(float2) * rows);
@@ -100,14 +117,15 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
     return L;
 }
 
-// First tile of piece i of the line of `total` tiles, and the piece of tile t.
-__host__ __device__ inline int64_t attn_piece_begin(int64_t total, int64_t i)
+// First tile of piece i of a line of `total` tiles in n pieces, and the piece of
+// tile t.
+__host__ __device__ inline int64_t attn_piece_begin(int64_t total, int n, int64_t i)
 {
-    return total * i / kAttnCtas;
+    return total * i / n;
 }
-__host__ __device__ inline int64_t attn_piece_of(int64_t total, int64_t t)
+__host__ __device__ inline int64_t attn_piece_of(int64_t total, int n, int64_t t)
 {
-    return ((t + 1) * kAttnCtas + total - 1) / total - 1;
+    return ((t + 1) * n + total - 1) / total - 1;
 }
 
 // Partial-result slot of a piece: its first segment (one that does not start
@@ -117,7 +135,7 @@ __device__ __forceinline__ int attn_slot(int64_t piece, bool starts)
     return static_cast<int>(2 * piece + (starts ? 1 : 0));
 }
 
-// A CTA's piece of a line, segment by segment: a segment is the part of one
+// A piece of a line, segment by segment: a segment is the part of one
 // (unit, kv head) pair that lies in the piece.  Constructed by whole warps.
 struct AttnWalk {
     const AttnLine &line;
@@ -126,11 +144,13 @@ struct AttnWalk {
     int32_t u, h, ta, tb;     // unit, kv head, tiles [ta, tb) of the unit's
     AttnUnit e;
 
-    __device__ __forceinline__ AttnWalk(const AttnLine &l, int32_t heads_) : line(l), heads(heads_)
+    __device__ __forceinline__ AttnWalk(const AttnLine &l, int32_t heads_, int kind, int piece)
+        : line(l), heads(heads_)
     {
         const int64_t total = *line.total;
-        pos = total > 0 ? attn_piece_begin(total, blockIdx.x) : 0;
-        end = total > 0 ? attn_piece_begin(total, blockIdx.x + 1) : 0;
+        const int n_pieces = attn_pieces(kind, total);
+        pos = piece < n_pieces ? attn_piece_begin(total, n_pieces, piece) : 0;
+        end = piece < n_pieces ? attn_piece_begin(total, n_pieces, piece + 1) : 0;
         u = h = ta = tb = 0;
         if (pos >= end)
             return;

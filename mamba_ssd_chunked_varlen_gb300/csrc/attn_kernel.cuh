@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kFull = C::kQuant ? kRawFull : kKvFull, kEmpty = C::kQuant ? kRawEmpty : kKvEmpty;
         const int shift = p.c.page_shift;
         const int boxes = shift >= 7 ? 1 : kTileKeys >> shift;    // pages of a tile
-        for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next(), ++qit) {
+        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next(), ++qit) {
             const int ns = streams(w.e);
             if (qit > 0 && !wait(kQEmpty, qit - 1))
                 break;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mma_commit(bars + kSFull + st);
             }
         };
-        for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next(), ++qit) {
+        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next(), ++qit) {
             const int ns = streams(w.e), n = w.tb - w.ta;
             if (!wait(kQFull, qit) || !wait(kKvFull + it % C::kStages, it / C::kStages))
                 break;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // would reach rows that do not see them; the output adds them
             // back for the rows that do.
             uint32_t it = 0, fit = 0;
-            for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next()) {
+            for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
                 for (int t = w.ta; t < w.tb && ok; ++t, it += 2) {
                     if (!partial(w.e, t, 0, w.e.tokens - 1))
                         continue;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- converter
             constexpr int kUnits = kDim / 16;  // 16-code pieces of a row
             uint32_t it = 0;
-            for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next())
+            for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next())
                 for (int t = w.ta; t < w.tb && ok; ++t)
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
                         const int rs = it % C::kRawStages, s = it % C::kStages;
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int my_tok = row / g, my_head = row % g;
         const float c2 = p.scale_log2;
         uint32_t it = 0, sit = 0, oit = 0;
-        for (AttnWalk w(p.line[0], p.c.heads); w.more() && ok; w.next()) {
+        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
             if (streams(w.e) <= st) {
                 sit += w.tb - w.ta;
                 continue;

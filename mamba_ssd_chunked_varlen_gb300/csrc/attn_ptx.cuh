@@ -122,6 +122,15 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t *a, uint
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The transpose of an 8x8 tile of 16-bit elements that a warp holds (lane l: row
+// l / 4, columns 2 (l % 4) and the next).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
 // Registers per thread of this warpgroup, out of what the block was launched
 // with; every warp of the warpgroup executes it.
 template <int kRegs>
