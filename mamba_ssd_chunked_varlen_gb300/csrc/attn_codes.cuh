@@ -38,8 +38,40 @@ __device__ __forceinline__ void widen4(uint32_t codes, uint32_t *out)
     }
 }
 
+// Codes to fp16 pairs (both exact): half the instructions of bf16, for products
+// whose other operand is kept in fp16's range.  int8: code + 128 in the mantissa of
+// 1024 = 0x6400, minus 1152.
+__device__ __forceinline__ uint32_t int8_half(uint32_t plus1152)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(plus1152), "r"(0x64806480u));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_half(uint32_t two)   // codes in the low bytes
+{
+    uint32_t r;
+    const uint16_t pair = static_cast<uint16_t>(two);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(pair));
+    return r;
+}
+
+// Four codes to two pairs of neighbours.
+template <int kType>
+__device__ __forceinline__ void half4(uint32_t codes, uint32_t *out)
+{
+    if constexpr (kType == SSD_KV_INT8) {
+        const uint32_t u = codes ^ 0x80808080u;
+        out[0] = int8_half(__byte_perm(u, 0x64646464u, 0x4140));
+        out[1] = int8_half(__byte_perm(u, 0x64646464u, 0x4342));
+    } else {
+        out[0] = e4m3_half(codes);
+        out[1] = e4m3_half(codes >> 16);
+    }
+}
+
 // Of two registers with codes of two keys, neighbouring columns in their bytes:
-// the pairs of the two keys' codes of columns b and b + 1 (b 0 or 2).
+// the pairs (bf16) of the two keys' codes of columns b and b + 1 (b 0 or 2).
 template <int kType, int b>
 __device__ __forceinline__ void widen_columns(uint32_t key0, uint32_t key1, uint32_t *out)
 {

@@ -21,6 +21,11 @@
 // products serves as long as Q has the same, and a lane then holds neighbouring
 // columns of the output.  Copies of keys past the context's end are filled with
 // zeros, so nothing is read that no sequence owns.
+//
+// 8-bit codes are widened in registers, which is exact: K's to fp16 (the cheaper
+// way; a row of Q is scaled by a power of two to fit fp16's range, exact but for
+// elements below 2^-32 of the row's largest), V's to bf16, because a weight times
+// its key's scale needs the range.
 #pragma once
 
 #include "attn_codes.cuh"
@@ -76,21 +81,58 @@ struct FewLoad {
     using C = FewCfg<kType, kDim>;
     const AttnParams &p;
     AttnWalk w;
-    uint32_t ring;               // shared-memory address of the warp's slots
-    int put, t, ahead, my_page;  // slot, tile; lane l has the page of tile t - ahead + l
-    bool v_next;
-    int64_t page;
+    uint32_t dst0;               // shared-memory address of the warp's slots
+    int put, t, ahead, my_page;  // slot's offset, tile; lane l has the page of tile t - ahead + l
+    bool v_next, there;
+    int64_t row;                 // cache row of the tile's first key
+    uint32_t k_off, v_off;       // this lane's first piece in a tile of K and of V
 
-    __device__ __forceinline__ FewLoad(const AttnParams &p_, int piece, uint32_t ring_)
-        : p(p_), w(p_.line[1], p_.c.heads, 1, piece), ring(ring_), put(0), t(w.ta), ahead(32),
-          my_page(-1), v_next(false), page(-1)
+    __device__ __forceinline__ FewLoad(const AttnParams &p_, int piece, uint32_t ring)
+        : p(p_), w(p_.line[1], p_.c.heads, 1, piece), dst0(ring), put(0), t(w.ta), ahead(32),
+          my_page(-1), v_next(false), there(false), row(0)
     {
+        const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
+        k_off = i * C::kRowBytes + q * 16;
+        v_off = q * 2 * C::kRowBytes + i * C::kVPiece;
+    }
+
+    // kAll: all sixteen keys are there
+    template <bool kAll>
+    __device__ __forceinline__ void copy(int left)
+    {
+        const KvView &c = p.c;
+        const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
+        const uint32_t dst = dst0 + put;
+        if (!v_next) {
+            const uint8_t *src = static_cast<const uint8_t *>(c.k) + row * C::kRowBytes + k_off;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int k = 0; k < C::kKPieces; ++k)
+                    ptx::cp_async<16>(dst + lane * 16 + (n * C::kKPieces + k) * 512,
+                                      src + n * 8 * C::kRowBytes + k * 64, kAll || n * 8 + i < left);
+        } else {
+            const uint8_t *src = static_cast<const uint8_t *>(c.v) + row * C::kRowBytes + v_off;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int key = (n & 1) + (n >> 1) * 8;
+#pragma unroll
+                for (int k = 0; k < C::kVPieces; ++k)
+                    ptx::cp_async<C::kVPiece>(
+                        dst + lane * C::kVPiece + (n * C::kVPieces + k) * 32 * C::kVPiece,
+                        src + key * C::kRowBytes + k * 8 * C::kVPiece, kAll || q * 2 + key < left);
+            }
+        }
+        if constexpr (C::kQuant) {
+            if (lane < 4)
+                ptx::cp_async<16>(dst + 32 * C::kLaneBytes + lane * 16,
+                                  (v_next ? c.v_scale : c.k_scale) + row + lane * 4, kAll || left > 0);
+        }
     }
 
     __device__ __forceinline__ void next()
     {
-        const KvView &c = p.c;
-        const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
+        const int lane = threadIdx.x & 31;
         if (w.more()) {
             const int j0 = (w.e.tile0 + t) * kFewKeys;
             if (!v_next) {
@@ -99,38 +141,17 @@ struct FewLoad {
                     const int j = j0 + lane * kFewKeys;
                     my_page = -1;
                     if (t + lane < w.tb && j < w.e.kv_len)
-                        my_page = static_cast<int>(kv_page_of(c, w.e.seq, j));
+                        my_page = static_cast<int>(kv_page_of(p.c, w.e.seq, j));
                 }
-                page = __shfl_sync(0xffffffffu, my_page, ahead++);
+                const int page = __shfl_sync(0xffffffffu, my_page, ahead++);
+                there = page >= 0;
+                row = there ? kv_row(p.c, page, w.h, j0) : 0;
             }
-            const int left = page < 0 ? 0 : w.e.kv_len - j0;    // keys that are there
-            const int64_t row = page < 0 ? 0 : kv_row(c, page, w.h, j0);
-            const uint8_t *src = static_cast<const uint8_t *>(v_next ? c.v : c.k) + row * C::kRowBytes;
-            const uint32_t dst = ring + put * C::kSlot;
-            if (!v_next) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int k = 0; k < C::kKPieces; ++k)
-                        ptx::cp_async<16>(dst + ((n * C::kKPieces + k) * 32 + lane) * 16,
-                                          src + (n * 8 + i) * C::kRowBytes + (k * 4 + q) * 16,
-                                          n * 8 + i < left);
-            } else {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int key = q * 2 + (n & 1) + (n >> 1) * 8;
-#pragma unroll
-                    for (int k = 0; k < C::kVPieces; ++k)
-                        ptx::cp_async<C::kVPiece>(dst + ((n * C::kVPieces + k) * 32 + lane) * C::kVPiece,
-                                                  src + key * C::kRowBytes + (k * 8 + i) * C::kVPiece,
-                                                  key < left);
-                }
-            }
-            if constexpr (C::kQuant) {
-                if (lane < 4)
-                    ptx::cp_async<16>(dst + 32 * C::kLaneBytes + lane * 16,
-                                      (v_next ? c.v_scale : c.k_scale) + row + lane * 4, left > 0);
-            }
+            const int left = there ? w.e.kv_len - j0 : 0;    // keys that are there
+            if (left >= kFewKeys)
+                copy<true>(left);
+            else
+                copy<false>(left);
             if (v_next && ++t == w.tb) {
                 w.next();
                 t = w.ta;
@@ -139,7 +160,7 @@ struct FewLoad {
             v_next = !v_next;
         }
         ptx::cp_async_commit();
-        put = put + 1 == C::kSlots ? 0 : put + 1;
+        put = put + C::kSlot == C::kRing ? 0 : put + C::kSlot;
     }
 };
 
@@ -154,6 +175,7 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
     const int g = p.group, rows = e.tokens * g;
     const float c2 = p.scale_log2;
     uint32_t qb[kN][kDim / 16][2];
+    float cr[kN][2];             // what turns a score into log2 units, for rows 2q and 2q + 1
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
         const int row = n * 8 + i, tok = row / g;
@@ -171,6 +193,34 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
             qb[n][2 * k][1] = v.y ^ flip;
             qb[n][2 * k + 1][0] = v.z ^ flip;
             qb[n][2 * k + 1][1] = v.w ^ flip;
+        }
+        cr[n][0] = cr[n][1] = c2;
+        if constexpr (C::kQuant) {
+            // the row's largest magnitude to [2^7, 2^8)
+            float top = 0.f;
+#pragma unroll
+            for (int s = 0; s < kDim / 16; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qb[n][s][k] << 16)),
+                                           fabsf(__uint_as_float(qb[n][s][k] & 0xffff0000u))));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+            const int shift = ex == 0 || ex == 255 ? 0 : min(134 - ex, 100);
+            const float up = pow2i(shift);
+#pragma unroll
+            for (int s = 0; s < kDim / 16; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const __half2 h = __floats2half2_rn(__uint_as_float(qb[n][s][k] << 16) * up,
+                                                        __uint_as_float(qb[n][s][k] & 0xffff0000u) * up);
+                    qb[n][s][k] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            const float back = c2 * pow2i(-shift);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                cr[n][r] = __shfl_sync(0xffffffffu, back, (q * 2 + r) * 4);
         }
     }
     float o[kN][kDim / 16][4];
@@ -193,8 +243,8 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
         // ---- scores: keys i and i + 8, rows 2q and 2q + 1 of each eight ----
         ptx::cp_async_wait<C::kSlots - 2>();
         __syncwarp();                            // the other lanes' copies of the scales
-        const uint8_t *slot = slots + got * C::kSlot;
-        got = got + 1 == C::kSlots ? 0 : got + 1;
+        const uint8_t *slot = slots + got;
+        got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
         load.next();
         float x[kN][4];
 #pragma unroll
@@ -212,12 +262,12 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     uint32_t a[2], b[2];
-                    widen4<kType>(a4[s], a);
-                    widen4<kType>(b4[s], b);
+                    half4<kType>(a4[s], a);
+                    half4<kType>(b4[s], b);
                     const uint32_t f[4] = {a[0], b[0], a[1], b[1]};
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
-                        ptx::mma_16816(x[n], f, qb[n][k * 4 + s][0], qb[n][k * 4 + s][1]);
+                        ptx::mma_16816_f16(x[n], f, qb[n][k * 4 + s][0], qb[n][k * 4 + s][1]);
                 }
             } else {
 #pragma unroll
@@ -229,16 +279,16 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                 }
             }
         }
-        if constexpr (C::kQuant) {
-            const float *sc = reinterpret_cast<const float *>(slot + 32 * C::kLaneBytes);
-            const float s0 = sc[i], s1 = sc[i + 8];
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                x[n][0] *= s0;
-                x[n][1] *= s0;
-                x[n][2] *= s1;
-                x[n][3] *= s1;
-            }
+        for (int k = 0; k < 2; ++k) {
+            float ks = 1.f;
+            if constexpr (C::kQuant)
+                ks = reinterpret_cast<const float *>(slot + 32 * C::kLaneBytes)[i + 8 * k];
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    x[n][2 * k + r] *= C::kQuant ? ks * cr[n][r] : c2;
         }
         if (hides) {
 #pragma unroll
@@ -261,13 +311,13 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
         for (int n = 0; n < kN; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                up = up || fmaxf(x[n][r], x[n][2 + r]) * c2 > m[n][r] + kFewRescale;
+                up = up || fmaxf(x[n][r], x[n][2 + r]) > m[n][r] + kFewRescale;
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
             for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float v = fmaxf(x[n][r], x[n][2 + r]) * c2;
+                    float v = fmaxf(x[n][r], x[n][2 + r]);
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -287,35 +337,35 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const float nm = m[n][r] == -INFINITY ? 0.f : -m[n][r];
-                x[n][r] = ptx::ex2(fmaf(x[n][r], c2, nm));
-                x[n][2 + r] = ptx::ex2(fmaf(x[n][2 + r], c2, nm));
-                l[n][r] += x[n][r] + x[n][2 + r];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float &v = x[n][2 * k + r];
+                    v = ptx::ex2(v + nm);
+                    l[n][r] += v;
+                }
             }
         // ---- V^T P ----
         ptx::cp_async_wait<C::kSlots - 2>();
         __syncwarp();
-        slot = slots + got * C::kSlot;
-        got = got + 1 == C::kSlots ? 0 : got + 1;
+        slot = slots + got;
+        got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
         load.next();
         uint32_t pb[kN][2];
-        float s0 = 1.f, s1 = 1.f;
-        if constexpr (C::kQuant) {
-            const float *sc = reinterpret_cast<const float *>(slot + 32 * C::kLaneBytes);
-            s0 = sc[i];
-            s1 = sc[i + 8];
-        }
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            if constexpr (C::kQuant) {
+        for (int k = 0; k < 2; ++k) {
+            float vs = 1.f;
+            if constexpr (C::kQuant)
+                vs = reinterpret_cast<const float *>(slot + 32 * C::kLaneBytes)[i + 8 * k];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+            for (int n = 0; n < kN; ++n) {
+                float a = x[n][2 * k], b = x[n][2 * k + 1];
+                if constexpr (C::kQuant) {
                     // (a hidden key's scale may be NaN: its weight stays zero)
-                    const float v = x[n][k] * (k < 2 ? s0 : s1);
-                    x[n][k] = hides && x[n][k] == 0.f ? 0.f : v;
+                    a = hides && a == 0.f ? 0.f : a * vs;
+                    b = hides && b == 0.f ? 0.f : b * vs;
                 }
+                pb[n][k] = ptx::transpose8(pack_bf16(a, b));
             }
-            pb[n][0] = ptx::transpose8(pack_bf16(x[n][0], x[n][1]));
-            pb[n][1] = ptx::transpose8(pack_bf16(x[n][2], x[n][3]));
         }
 #pragma unroll
         for (int k = 0; k < C::kVPieces; ++k) {
@@ -339,19 +389,18 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
             if constexpr (C::kQuant) {
 #pragma unroll
                 for (int s = 0; s < kWords; ++s) {
-                    uint32_t a[2], b[2];
+                    uint32_t a[4], b[4];
                     widen_columns<kType, 0>(v[0][s], v[1][s], a);
+                    widen_columns<kType, 2>(v[0][s], v[1][s], a + 2);
                     widen_columns<kType, 0>(v[2][s], v[3][s], b);
-                    const uint32_t f0[4] = {a[0], a[1], b[0], b[1]};
+                    widen_columns<kType, 2>(v[2][s], v[3][s], b + 2);
 #pragma unroll
-                    for (int n = 0; n < kN; ++n)
-                        ptx::mma_16816(o[n][s * 2], f0, pb[n][0], pb[n][1]);
-                    widen_columns<kType, 2>(v[0][s], v[1][s], a);
-                    widen_columns<kType, 2>(v[2][s], v[3][s], b);
-                    const uint32_t f1[4] = {a[0], a[1], b[0], b[1]};
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t f[4] = {a[2 * j], a[2 * j + 1], b[2 * j], b[2 * j + 1]};
 #pragma unroll
-                    for (int n = 0; n < kN; ++n)
-                        ptx::mma_16816(o[n][s * 2 + 1], f1, pb[n][0], pb[n][1]);
+                        for (int n = 0; n < kN; ++n)
+                            ptx::mma_16816(o[n][s * 2 + j], f, pb[n][0], pb[n][1]);
+                    }
                 }
             } else {
                 if (hides) {
