@@ -14,125 +14,141 @@ namespace {
 // One CTA cuts the call into units (AttnUnit), in the order of the rows, and
 // counts their key tiles.
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanBatch = 4096;    // up to so many sequences, their first units stay on chip
 
-// Inclusive sum over the CTA's threads; `total` gets the sum of all.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64_t *total)
+// Inclusive sums of kN values over the CTA's threads; `total` gets the sums of all.
+template <int kN>
+__device__ __forceinline__ void block_scan(int64_t (&v)[kN], int64_t (*scratch)[32], int64_t (&total)[kN])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t incl = warp_inclusive_scan(v);
+#pragma unroll
+    for (int k = 0; k < kN; ++k)
+        v[k] = warp_inclusive_scan(v[k]);
     __syncthreads();
-    if (lane == 31)
-        scratch[warp] = incl;
+    if (lane == 31) {
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+            scratch[k][warp] = v[k];
+    }
     __syncthreads();
-    if (warp == 0)
-        scratch[lane] = warp_inclusive_scan(scratch[lane]);
+    if (warp < kN)
+        scratch[warp][lane] = warp_inclusive_scan(scratch[warp][lane]);
     __syncthreads();
-    *total = scratch[31];
-    return incl + (warp ? scratch[warp - 1] : 0);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        total[k] = scratch[k][31];
+        v[k] += warp ? scratch[k][warp - 1] : 0;
+    }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ int64_t scratch[32];
+    __shared__ int64_t scratch[4][32];
+    __shared__ int32_t s_units[kPlanBatch];
     const KvView &c = p.c;
     const int tid = threadIdx.x;
     const int unit_tokens = 2 * p.tile_tokens;
+    int32_t *seq_units = c.batch <= kPlanBatch ? s_units : p.seq_units;
     pdl_launch_dependents();
     int64_t units = 0;
     int bad = 0;
     for (int base = 0; base < c.batch; base += kPlanThreads) {
         const int b = base + tid;
-        int64_t n = 0;
+        int64_t n[1] = {0}, all[1];
         if (b < c.batch) {
             const int32_t start = c.qsl[b], end = c.qsl[b + 1];
             if (end < start || (b == 0 && start != 0) || (b == c.batch - 1 && end != c.total_len))
                 bad = 1;
             else
-                n = (static_cast<int64_t>(end) - start + unit_tokens - 1) / unit_tokens;
+                n[0] = (static_cast<int64_t>(end) - start + unit_tokens - 1) / unit_tokens;
         }
-        int64_t all;
-        const int64_t incl = block_scan(n, scratch, &all);
+        const int64_t mine = n[0];
+        block_scan(n, scratch, all);
         if (b < c.batch)
-            p.seq_units[b] = static_cast<int32_t>(min(units + incl - n, static_cast<int64_t>(INT32_MAX)));
-        units += all;
+            seq_units[b] = static_cast<int32_t>(min(units + n[0] - mine, static_cast<int64_t>(INT32_MAX)));
+        units += all[0];
     }
     // (a query_start_loc that fails may count any number of units: none is written)
     bad = __syncthreads_or(bad);
     if (bad) {
-        if (tid == 0) {
-            kv_error(c, SSD_DEVERR_BAD_QUERY_START_LOC);
-            for (int k = 0; k < 2; ++k) {
-                p.hdr->total[k] = 0;
-                p.hdr->count[k] = 0;
-            }
+        if (tid < 2) {
+            p.hdr->total[tid] = 0;
+            p.hdr->count[tid] = 0;
+            p.hdr->splits[tid][0] = p.hdr->splits[tid][1] = 0;
         }
+        if (tid == 0)
+            kv_error(c, SSD_DEVERR_BAD_QUERY_START_LOC);
         return;
     }
     int64_t tiles[2] = {0, 0}, count[2] = {0, 0};
     for (int64_t base = 0; base < units; base += kPlanThreads) {
         const int64_t u = base + tid;
         AttnUnit e = {};
+        int kind = 0;
         if (u < units) {
             // the last sequence whose units begin at or before u (the sequences
             // without rows that begin there as well come before it)
             int lo = 0, hi = c.batch - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
-                if (p.seq_units[mid] <= u)
+                if (seq_units[mid] <= u)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
             const int32_t start = c.qsl[lo], rows = c.qsl[lo + 1] - start;
-            const int32_t first = static_cast<int32_t>(u - p.seq_units[lo]) * unit_tokens;
+            const int32_t first = static_cast<int32_t>(u - seq_units[lo]) * unit_tokens;
             e.seq = lo;
             e.row0 = start + first;
             e.tokens = min(unit_tokens, rows - first);
             e.kv_len = kv_len_of(c, lo);
             e.pos0 = e.kv_len - rows + first;
+            kind = e.tokens * p.group <= kFewRows;
+            const int n = kind ? kFewKeys : kTileKeys;
             const int32_t keys = max(e.pos0 + e.tokens, 0);
-            const int n = e.tokens * p.group <= kFewRows ? kFewKeys : kTileKeys;
             e.tile0 = p.window > 0 ? max(e.pos0 - p.window + 1, 0) / n : 0;
             e.tiles = max((keys + n - 1) / n - e.tile0, 1);
         }
-        const int kind = e.tokens * p.group <= kFewRows ? 1 : 0;
+        int64_t v[4], all[4];
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const bool mine = u < units && kind == k;
-            int64_t all, all_n;
-            const int64_t incl = block_scan(mine ? e.tiles : 0, scratch, &all);
-            const int64_t n = block_scan(mine ? 1 : 0, scratch, &all_n);
-            if (mine) {
-                const int64_t at = count[k] + n - 1;
-                const_cast<AttnUnit *>(p.line[k].units)[at] = e;
-                const_cast<int64_t *>(p.line[k].cum)[at] = tiles[k] + incl - e.tiles;
-            }
-            tiles[k] += all;
-            count[k] += all_n;
+            v[2 * k] = u < units && kind == k ? e.tiles : 0;
+            v[2 * k + 1] = u < units && kind == k;
+        }
+        block_scan(v, scratch, all);
+        if (u < units) {
+            const int64_t at = count[kind] + (kind ? v[3] : v[1]) - 1;
+            const_cast<AttnUnit *>(p.line[kind].units)[at] = e;
+            const_cast<int64_t *>(p.line[kind].cum)[at] = tiles[kind] + (kind ? v[2] : v[0]) - e.tiles;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            tiles[k] += all[2 * k];
+            count[k] += all[2 * k + 1];
         }
     }
     if (tid < 2) {
         const_cast<int64_t *>(p.line[tid].cum)[count[tid]] = tiles[tid];
         p.hdr->total[tid] = tiles[tid] * c.heads;
         p.hdr->count[tid] = static_cast<int32_t>(count[tid]);
+        p.hdr->splits[tid][0] = p.hdr->splits[tid][1] = 0;
     }
 }
 
 // ---------------------------------------------------------------- join
 // Rows whose keys were split over several pieces: with M the largest of the
 // pieces' references m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i,  the pieces
-// summed in a fixed order.  A CTA of four warps takes four rows of a split pair
-// of the tiles' kind, a warp each, or one row of few, its warps every fourth
-// piece (a decoding sequence's one row may lie in hundreds of pieces).
-constexpr int kJoinWarps = 4;
-constexpr int kJoinTileCtas = kAttnCtas - 1;        // x kJoinTileParts: a boundary between pieces each
-constexpr int kJoinTileParts = 2 * kTileRows / kJoinWarps;
-constexpr int kJoinFewCtas = 8 * kAttnCtas;
+// summed in a fixed order.  Two CTAs of 16 warps an SM go through the listed pairs:
+// a warp takes four rows of the tiles' kind or a row of few; a row of more than
+// kJoinWide pieces (a decoding sequence alone on the GPU) takes a CTA.
+constexpr int kJoinWarps = 16;
+constexpr int kJoinCtas = 2 * kAttnCtas;
 
-// What pieces first, first + step, ... <= last of a row give: its sums relative to `top`.
+// Adds up pieces from, from + step, ... <= last of a row: its sums relative to `top`.
 template <int kE>
-__device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows, int64_t first,
-                                            int64_t from, int64_t last, int step, int row, int dim,
-                                            float &top, float &sum, float (&acc)[kE])
+__device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows, int first, int from,
+                                            int last, int step, int row, float &top, float &sum,
+                                            float (&acc)[kE])
 {
     const int lane = threadIdx.x & 31;
     top = -INFINITY;
@@ -140,9 +156,9 @@ __device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows,
 #pragma unroll
     for (int j = 0; j < kE; ++j)
         acc[j] = 0.f;
-    for (int64_t base = from; base <= last; base += 32 * step) {
+    for (int base = from; base <= last; base += 32 * step) {
         // a lane per piece
-        const int64_t mine = base + lane * step;
+        const int mine = base + lane * step;
         float2 ml = make_float2(-INFINITY, 0.f);
         if (mine <= last)
             ml = line.part_ml[attn_slot(mine, mine == first) * part_rows + row];
@@ -162,39 +178,48 @@ __device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows,
 #pragma unroll
         for (int j = 0; j < kE; ++j)
             acc[j] *= f;
-        const int n = static_cast<int>(min(static_cast<int64_t>(32), (last - base) / step + 1));
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const int64_t at = base + k * step;
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float *src =
-                line.part_o + (attn_slot(at, at == first) * static_cast<int64_t>(part_rows) + row) * dim +
-                lane * kE;
+        // eight pieces' loads at a time; those past the last have the weight zero and
+        // are not read
+        const int n = min(32, (last - base) / step + 1);
+        for (int k0 = 0; k0 < n; k0 += 8) {
+            float v[8][kE];
 #pragma unroll
-            for (int j = 0; j < kE; ++j)
-                acc[j] += wk == 0.f ? 0.f : wk * src[j];
+            for (int k = 0; k < 8; ++k) {
+                const int at = base + (k0 + k) * step;
+                const float *src = line.part_o +
+                                   (attn_slot(at, at == first) * static_cast<int64_t>(part_rows) + row) *
+                                       (32 * kE) +
+                                   lane * kE;
+#pragma unroll
+                for (int j = 0; j < kE; ++j)
+                    v[k][j] = at <= last ? src[j] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+#pragma unroll
+                for (int j = 0; j < kE; ++j)
+                    acc[j] += wk == 0.f ? 0.f : wk * v[k][j];
+            }
         }
     }
 }
 
 template <int kDim>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32, 2)
+    attn_join_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int kE = kDim / 32;
     __shared__ float s_ml[kJoinWarps][2], s_acc[kJoinWarps][kDim];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ int s_wide[attn_max_pieces(1) / kJoinWide + 1], s_n;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = p.group;
     pdl_wait();
-    const int kind = blockIdx.x < kJoinTileCtas * kJoinTileParts ? 0 : 1;
-    const AttnLine &line = p.line[kind];
-    const int64_t total = *line.total;
-    if (total == 0)
-        return;
-    const int pieces = attn_pieces(kind, total);
-    float top, sum, acc[kE];
-    auto write = [&](const AttnUnit &e, int h, int tok, int sub) {
+    const int n0 = p.hdr->splits[0][0], n1 = p.hdr->splits[1][0], wide = p.hdr->splits[1][1];
+    auto write = [&](const int4 &e, int x, float top, float sum, const float (&acc)[kE]) {
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-        const int64_t row = e.row0 + tok;
-        const int head = h * p.group + sub;
+        const int64_t row = e.x + x / g;
+        const int head = (e.y >> 9) * g + x % g;
         __nv_bfloat16 *dst = p.o + row * p.o_stride + static_cast<int64_t>(head) * kDim + lane * kE;
 #pragma unroll
         for (int j = 0; j < kE; j += 2)
@@ -203,76 +228,127 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
             p.lse[row * p.heads + head] =
                 sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     };
-    if (kind == 0) {
-        // the boundary before piece i, if it is the first inside its pair
-        const int64_t i = blockIdx.x / kJoinTileParts + 1, s = attn_piece_begin(total, pieces, i);
-        if (s >= total)
-            return;
-        int u = 0, n = *line.count;
-        while (n > 1) {
-            const int step = (n + 31) / 32, at = lane * step;
-            const bool below = at < n && line.cum[u + at] * p.c.heads <= s;
-            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
-            u += k * step;
-            n = min(step, n - k * step);
-        }
-        const AttnUnit e = line.units[u];
-        const int64_t r = s - line.cum[u] * p.c.heads;
-        const int h = static_cast<int>(r / e.tiles);
-        const int64_t begin = s - (r - static_cast<int64_t>(h) * e.tiles);
-        const int64_t first = attn_piece_of(total, pieces, begin);
-        const int x = blockIdx.x % kJoinTileParts * kJoinWarps + warp;
-        if (begin == s || first != i - 1 || x >= e.tokens * p.group)
-            return;
-        const int64_t last = attn_piece_of(total, pieces, begin + e.tiles - 1);
-        const int tok = x / p.group, st = tok / p.tile_tokens;
-        const int row = st * kTileRows + (tok - st * p.tile_tokens) * p.group + x % p.group;
-        join_pieces<kE>(line, attn_part_rows(0), first, first, last, 1, row, kDim, top, sum, acc);
-        write(e, h, tok, x % p.group);
-        return;
-    }
-    const int64_t items = static_cast<int64_t>(*line.count) * p.c.heads * kFewRows;
-    for (int64_t item = blockIdx.x - kJoinTileCtas * kJoinTileParts; item < items; item += kJoinFewCtas) {
-        const int row = static_cast<int>(item % kFewRows);
-        const int64_t pair = item / kFewRows;
-        const int u = static_cast<int>(pair / p.c.heads), h = static_cast<int>(pair % p.c.heads);
-        const AttnUnit e = line.units[u];
-        if (row >= e.tokens * p.group)
+    const int me = blockIdx.x + warp * kJoinCtas, warps = kJoinWarps * kJoinCtas;
+
+    // ---- tiles: items of four rows of a pair ----
+    const AttnLine &tl = p.line[0];
+    constexpr int kQuads = 2 * kTileRows / 4;
+    for (int item = me; item < n0 * kQuads; item += warps) {
+        const int4 e = tl.split[item / kQuads];
+        const int x0 = item % kQuads * 4, rows = (e.y & 511) * g;
+        if (x0 >= rows)
             continue;
-        const int64_t begin = line.cum[u] * p.c.heads + static_cast<int64_t>(h) * e.tiles;
-        const int64_t first = attn_piece_of(total, pieces, begin);
-        const int64_t last = attn_piece_of(total, pieces, begin + e.tiles - 1);
-        if (first == last)
+        auto part_row = [&](int x) {
+            const int tok = x / g, st = tok / p.tile_tokens;
+            return st * kTileRows + (tok - st * p.tile_tokens) * g + x % g;
+        };
+        if (e.w - e.z >= 8) {
+            for (int x = x0; x < min(x0 + 4, rows); ++x) {
+                float top, sum, acc[kE];
+                join_pieces<kE>(tl, attn_part_rows(0), e.z, e.z, e.w, 1, part_row(x), top, sum, acc);
+                write(e, x, top, sum, acc);
+            }
             continue;
-        join_pieces<kE>(line, kFewRows, first, first + warp, last, kJoinWarps, row, kDim, top, sum, acc);
-        if (lane == 0) {
-            s_ml[warp][0] = top;
-            s_ml[warp][1] = sum;
         }
+        // up to eight pieces: lane 8 r + k has piece k of row r
+        const int r = lane >> 3, k = lane & 7, x = min(x0 + r, rows - 1);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        const int my_row = attn_slot(e.z + k, k == 0) * attn_part_rows(0) + part_row(x);
+        if (e.z + k <= e.w)
+            ml = tl.part_ml[my_row];
+        float top = ml.x;
 #pragma unroll
-        for (int j = 0; j < kE; ++j)
-            s_acc[warp][lane * kE + j] = acc[j];
-        __syncthreads();
-        if (warp == 0) {
-            top = -INFINITY;
+        for (int o = 4; o; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+        float sum = ml.x == -INFINITY ? ml.y : w * ml.y;
 #pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k)
-                top = fmaxf(top, s_ml[k][0]);
-            sum = 0.f;
+        for (int o = 4; o; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        float acc[4][kE];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < kE; ++j)
-                acc[j] = 0.f;
+                acc[i][j] = 0.f;
+#pragma unroll 2
+        for (int n = 0; n <= e.w - e.z; ++n) {
 #pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k) {
-                const float w = s_ml[k][0] == -INFINITY ? 0.f : exp2f(s_ml[k][0] - top);
-                sum += s_ml[k][0] == -INFINITY ? s_ml[k][1] : w * s_ml[k][1];
+            for (int i = 0; i < 4; ++i) {
+                const float wn = __shfl_sync(0xffffffffu, w, i * 8 + n);
+                const int64_t at = __shfl_sync(0xffffffffu, my_row, i * 8 + n);
+                const float *src = tl.part_o + at * kDim + lane * kE;
+#pragma unroll
+                for (int j = 0; j < kE; ++j) {
+                    const float v = src[j];
+                    acc[i][j] += wn == 0.f ? 0.f : wn * v;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float ti = __shfl_sync(0xffffffffu, top, i * 8), si = __shfl_sync(0xffffffffu, sum, i * 8);
+            if (x0 + i < rows)
+                write(e, x0 + i, ti, si, acc[i]);
+        }
+    }
+
+    // ---- few rows: items of a row of a pair ----
+    const AttnLine &fl = p.line[1];
+    for (int item = me; item < n1 * kFewRows; item += warps) {
+        const int row = item / n1;
+        const int4 e = fl.split[item - row * n1];
+        if (row >= (e.y & 511) * g || e.w - e.z >= kJoinWide)
+            continue;
+        float top, sum, acc[kE];
+        join_pieces<kE>(fl, kFewRows, e.z, e.z, e.w, 1, row, top, sum, acc);
+        write(e, row, top, sum, acc);
+    }
+    if (wide == 0)
+        return;
+    if (tid == 0)
+        s_n = 0;
+    __syncthreads();
+    for (int k = tid; k < n1; k += kJoinWarps * 32) {
+        const int4 e = fl.split[k];
+        if (e.w - e.z >= kJoinWide)
+            s_wide[atomicAdd(&s_n, 1)] = k;
+    }
+    __syncthreads();
+    for (int i = 0; i < s_n; ++i) {
+        const int4 e = fl.split[s_wide[i]];
+        const int rows = (e.y & 511) * g;
+        // (the CTAs may hold the list in different orders: a pair's rows go by the pair)
+        for (int row = (blockIdx.x + kJoinCtas - e.z % kJoinCtas) % kJoinCtas; row < rows; row += kJoinCtas) {
+            float top, sum, acc[kE];
+            join_pieces<kE>(fl, kFewRows, e.z, e.z + warp, e.w, kJoinWarps, row, top, sum, acc);
+            if (lane == 0) {
+                s_ml[warp][0] = top;
+                s_ml[warp][1] = sum;
+            }
+#pragma unroll
+            for (int j = 0; j < kE; ++j)
+                s_acc[warp][lane * kE + j] = acc[j];
+            __syncthreads();
+            if (warp == 0) {
+                top = -INFINITY;
+                for (int w = 0; w < kJoinWarps; ++w)
+                    top = fmaxf(top, s_ml[w][0]);
+                sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < kE; ++j)
-                    acc[j] += w == 0.f ? 0.f : w * s_acc[k][lane * kE + j];
+                    acc[j] = 0.f;
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    const float m = s_ml[w][0], f = m == -INFINITY ? 0.f : exp2f(m - top);
+                    sum += m == -INFINITY ? s_ml[w][1] : f * s_ml[w][1];
+#pragma unroll
+                    for (int j = 0; j < kE; ++j)
+                        acc[j] += f == 0.f ? 0.f : f * s_acc[w][lane * kE + j];
+                }
+                write(e, row, top, sum, acc);
             }
-            write(e, h, row / p.group, row % p.group);
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -404,7 +480,9 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
                              p.hdr->total + k,
                              p.hdr->count + k,
                              reinterpret_cast<float *>(ws + L.part_o[k]),
-                             reinterpret_cast<float2 *>(ws + L.part_ml[k])};
+                             reinterpret_cast<float2 *>(ws + L.part_ml[k]),
+                             reinterpret_cast<int4 *>(ws + L.split[k]),
+                             p.hdr->splits[k]};
 
     AttnMaps m = {};
     const uint64_t D = head_dim, rows = static_cast<uint64_t>(num_pages) * nheads_kv;
@@ -441,7 +519,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
         e = bf16 ? launch_attn_few_bf16(p, stream)
                  : fp8 ? launch_attn_few_fp8(p, stream) : launch_attn_few_int8(p, stream);
     if (e == cudaSuccess) {
-        const dim3 grid(kJoinTileCtas * kJoinTileParts + (few ? kJoinFewCtas : 0));
+        const dim3 grid(kJoinCtas);
         e = head_dim == 128 ? launch_pdl(attn_join_kernel<128>, grid, kJoinWarps * 32, stream, p)
                             : launch_pdl(attn_join_kernel<64>, grid, kJoinWarps * 32, stream, p);
     }

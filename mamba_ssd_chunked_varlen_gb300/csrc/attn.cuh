@@ -41,6 +41,9 @@ struct AttnLine {
     const int32_t *count;
     float *part_o;                // [2 pieces][rows][dim]: sums of p v
     float2 *part_ml;              // [2 pieces][rows]: reference (log2), sum of p
+    int4 *split;                  // [pieces] the pairs with partial results, in any order:
+                                  // {row0, tokens + (kv head << 9), first piece, last piece}
+    int32_t *splits;              // how many: [0], of them over more than kJoinWide pieces: [1]
 };
 
 // Most pieces of each kind, and the fewest tiles of one (every piece has a tile).
@@ -48,7 +51,7 @@ __host__ __device__ constexpr int attn_max_pieces(int kind)
 {
     return kind ? kAttnCtas * kFewWarps : kAttnCtas;
 }
-constexpr int kFewPieceTiles = 4;
+constexpr int kFewPieceTiles = 2;
 
 __host__ __device__ inline int attn_pieces(int kind, int64_t total)
 {
@@ -57,10 +60,13 @@ __host__ __device__ inline int attn_pieces(int kind, int64_t total)
     return n < most ? static_cast<int>(n) : most;
 }
 
+constexpr int kJoinWide = 128;    // pieces of a row that one warp of the join adds up
+
 struct AttnHeader {
     int64_t total[2];             // per kind: 0 tiles, 1 few rows
     int32_t count[2];
-    int32_t pad[58];
+    int32_t splits[2][2];
+    int32_t pad[54];
 };
 static_assert(sizeof(AttnHeader) == 256, "header size");
 
@@ -85,7 +91,7 @@ struct AttnParams {
 __host__ __device__ constexpr int attn_part_rows(int kind) { return kind ? kFewRows : 2 * kTileRows; }
 
 struct AttnLayout {
-    size_t header, seq_units, units[2], cum[2], part_ml[2], part_o[2], total;
+    size_t header, seq_units, units[2], cum[2], split[2], part_ml[2], part_o[2], total;
 };
 
 inline int64_t attn_max_units(int64_t total_len, int32_t batch, int32_t group)
@@ -110,6 +116,7 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
         const size_t rows = 2 * static_cast<size_t>(attn_max_pieces(k)) * attn_part_rows(k);
         L.units[k] = take(sizeof(AttnUnit) * units);
         L.cum[k] = take(sizeof(int64_t) * (units + 1));
+        L.split[k] = take(sizeof(int4) * static_cast<size_t>(attn_max_pieces(k)));
         L.part_ml[k] = take(sizeof(float2) * rows);
         L.part_o[k] = take(sizeof(float) * rows * static_cast<size_t>(dim));
     }
@@ -176,6 +183,18 @@ struct AttnWalk {
         tb = left < e.tiles - ta ? ta + static_cast<int32_t>(left) : e.tiles;
     }
     __device__ __forceinline__ bool more() const { return pos < end; }
+    // Lists the pair of a segment that begins it and does not end it; by one lane.
+    __device__ __forceinline__ void note_split(int kind, int piece) const
+    {
+        if (ta != 0 || tb == e.tiles)
+            return;
+        const int64_t total = *line.total;
+        const int last =
+            static_cast<int>(attn_piece_of(total, attn_pieces(kind, total), pos + e.tiles - 1));
+        line.split[atomicAdd(line.splits, 1)] = make_int4(e.row0, e.tokens + (h << 9), piece, last);
+        if (last - piece >= kJoinWide)
+            atomicAdd(line.splits + 1, 1);
+    }
     __device__ __forceinline__ void next()
     {
         pos += tb - ta;

@@ -503,6 +503,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         for (int k = 0; k < C::kSlots - 1; ++k)
             load.next();
         for (; w.more(); w.next()) {
+            if ((threadIdx.x & 31) == 0)
+                w.note_split(1, piece);
             if (w.e.tokens * p.group <= 8)
                 few_segment<kType, kDim, 1>(p, w, piece, slots, got, load);
             else

@@ -141,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int boxes = shift >= 7 ? 1 : kTileKeys >> shift;    // pages of a tile
         for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next(), ++qit) {
             const int ns = streams(w.e);
+            if (lane == 0)
+                w.note_split(0, blockIdx.x);
             if (qit > 0 && !wait(kQEmpty, qit - 1))
                 break;
             if (lane == 0) {
