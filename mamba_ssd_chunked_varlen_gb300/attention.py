@@ -51,7 +51,10 @@ class _Functions:
         self.bf16, self.f32, self.i32, self.u8 = (torch.bfloat16, torch.float32, torch.int32,
                                                   torch.uint8)
         self.u32 = torch.uint32
-        self.current_stream = torch.cuda.current_stream
+        # the current stream's handle alone, where torch has that (an order of
+        # magnitude less time than a Stream object)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _functions() -> _Functions:
@@ -61,88 +64,121 @@ def _functions() -> _Functions:
     return _fn
 
 
-def _ptr(t, what: str, dtype, device):
-    """Address of a contiguous tensor of that type on that device."""
+def _tensor(t, what: str, dtype, device: int, contiguous: bool = True):
+    """Raise what is wrong with a tensor that should be of that type and device."""
     if t.dtype != dtype:
         raise ValueError(f"{what} must have dtype {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on device {device}, got {t.get_device()}")
+    if contiguous and not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
 
 
-def _rows(t, what: str, f, device):
-    """Address and row pitch (elements) of a (rows, heads, head_dim) bf16 tensor
-    whose rows are contiguous."""
-    if t.dtype != f.bf16:
-        raise ValueError(f"{what} must have dtype {f.bf16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
-    n, h, d = t.shape
-    s = t.stride()
-    if (s[2] != 1 and d != 1) or (s[1] != d and h != 1):
-        raise ValueError(f"{what}: each token's row must be contiguous")
-    return t.data_ptr(), (s[0] if n > 1 else h * d)
-
-
-def _cache(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, block_table, device):
-    """The arguments that all calls share: (nine pointers' tail, sizes)."""
-    kind = f.types.get(k_cache.dtype)
-    if kind is None:
+def _refuse(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, block_table, errors):
+    """Raise what is wrong with the arguments that all calls share."""
+    if k_cache.dtype not in f.types:
         raise ValueError(f"k_cache must be bfloat16, float8_e4m3fn or int8, got {k_cache.dtype}")
     if not k_cache.is_cuda:
         raise ValueError("k_cache must be a CUDA tensor")
-    shape = k_cache.shape
+    device, shape = k_cache.get_device(), k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both have shape "
                          "(num_pages, nheads_kv, page_size, head_dim)")
-    ks = vs = None
-    if kind:
+    _tensor(k_cache, "k_cache", k_cache.dtype, device)
+    _tensor(v_cache, "v_cache", k_cache.dtype, device)
+    if f.types[k_cache.dtype]:
         if k_scale is None or v_scale is None:
             raise ValueError("an 8-bit cache needs k_scale and v_scale")
-        if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
-            raise ValueError(f"k_scale and v_scale must have shape {tuple(shape[:3])}")
-        ks, vs = _ptr(k_scale, "k_scale", f.f32, device), _ptr(v_scale, "v_scale", f.f32, device)
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.shape != shape[:3]:
+                raise ValueError(f"{what} must have shape {tuple(shape[:3])}")
+            _tensor(t, what, f.f32, device)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("a bfloat16 cache has no scales")
+    _tensor(query_start_loc, "query_start_loc", f.i32, device)
+    _tensor(kv_lens, "kv_lens", f.i32, device)
     batch = query_start_loc.shape[0] - 1
     if kv_lens.shape != (batch,):
         raise ValueError(f"kv_lens must have shape ({batch},)")
-    if block_table.dtype != f.i32 or block_table.device != device or block_table.dim() != 2 \
-            or block_table.shape[0] != batch:
-        raise ValueError(f"block_table must be an int32 tensor ({batch}, pages) on {device}")
-    width = block_table.shape[1]
-    if width > 1 and block_table.stride(1) != 1:
+    _tensor(block_table, "block_table", f.i32, device, contiguous=False)
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must have shape ({batch}, pages)")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table: each sequence's entries must be contiguous")
-    stride = block_table.stride(0) if batch > 1 else width
-    return ((_ptr(k_cache, "k_cache", k_cache.dtype, device),
-             _ptr(v_cache, "v_cache", k_cache.dtype, device), ks, vs,
-             _ptr(query_start_loc, "query_start_loc", f.i32, device),
-             _ptr(kv_lens, "kv_lens", f.i32, device), block_table.data_ptr()),
-            batch, shape[1], shape[3], (shape[0], shape[2], width, stride, kind))
+    if errors is not None:
+        if errors.numel() < 1 or errors.dtype not in (f.i32, f.u32):
+            raise ValueError("errors must be an int32 or uint32 tensor of one element")
+        _tensor(errors, "errors", errors.dtype, device)
+    raise ValueError("invalid arguments")
 
 
-def _errors(f, errors, device):
-    if errors is None:
-        return None
-    if errors.dtype not in (f.i32, f.u32) or errors.device != device or errors.numel() < 1:
-        raise ValueError(f"errors must be an int32 or uint32 tensor on {device}")
-    return errors.data_ptr()
+def _cache(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, block_table, errors):
+    """The arguments that all calls share: pointers, batch, nheads_kv, head_dim, sizes,
+    the errors' pointer and the device.  One pass of cheap tests; what fails one
+    is looked at again for its message."""
+    shape, dtype, device, i32 = k_cache.shape, k_cache.dtype, k_cache.get_device(), f.i32
+    kind = f.types.get(dtype)
+    tshape, ks, vs, pe = block_table.shape, None, None, None
+    good = (kind is not None and device >= 0 and len(shape) == 4 and v_cache.shape == shape
+            and v_cache.dtype is dtype and v_cache.get_device() == device
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and query_start_loc.dtype is i32 and query_start_loc.get_device() == device
+            and query_start_loc.is_contiguous()
+            and kv_lens.dtype is i32 and kv_lens.get_device() == device and kv_lens.is_contiguous()
+            and block_table.dtype is i32 and block_table.get_device() == device
+            and len(tshape) == 2)
+    if good:
+        batch, width = tshape
+        tstride = block_table.stride()
+        good = (query_start_loc.shape == (batch + 1,) and kv_lens.shape == (batch,)
+                and (tstride[1] == 1 or width <= 1))
+    if good and kind:
+        if k_scale is None or v_scale is None:
+            good = False
+        else:
+            ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+            good = (k_scale.dtype is f.f32 and v_scale.dtype is f.f32
+                    and k_scale.shape == shape[:3] and v_scale.shape == shape[:3]
+                    and k_scale.get_device() == device and v_scale.get_device() == device
+                    and k_scale.is_contiguous() and v_scale.is_contiguous())
+    elif k_scale is not None or v_scale is not None:
+        good = False
+    if good and errors is not None:
+        pe = errors.data_ptr()
+        good = ((errors.dtype is i32 or errors.dtype is f.u32) and errors.get_device() == device
+                and errors.numel() >= 1)
+    if not good:
+        _refuse(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, block_table, errors)
+    return ((k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, query_start_loc.data_ptr(),
+             kv_lens.data_ptr(), block_table.data_ptr()),
+            batch, shape[1], shape[3],
+            (shape[0], shape[2], width, tstride[0] if batch > 1 else width, kind), pe, device)
+
+
+def _pitch(t, what: str, f, device: int):
+    """Row pitch (elements) of a (rows, heads, head_dim) bf16 tensor whose rows are
+    contiguous."""
+    n, h, d = t.shape
+    s = t.stride()
+    if t.dtype is not f.bf16 or t.get_device() != device:
+        _tensor(t, what, f.bf16, device, contiguous=False)
+    if (s[2] != 1 and d != 1) or (s[1] != d and h != 1):
+        raise ValueError(f"{what}: each token's row must be contiguous")
+    return s[0] if n > 1 else h * d
 
 
 def _copy(f, fn, what, k, v, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens,
           block_table, errors, stream):
-    device = k_cache.device
-    ptrs, batch, heads, dim, sizes = _cache(f, k_cache, v_cache, k_scale, v_scale,
-                                            query_start_loc, kv_lens, block_table, device)
-    if k.shape != v.shape or len(k.shape) != 3 or k.shape[1:] != (heads, dim):
+    ptrs, batch, heads, dim, sizes, pe, device = _cache(f, k_cache, v_cache, k_scale, v_scale,
+                                                        query_start_loc, kv_lens, block_table, errors)
+    shape = k.shape
+    if v.shape != shape or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"k and v must both have shape (rows, {heads}, {dim})")
-    pk, k_stride = _rows(k, "k", f, device)
-    pv, v_stride = _rows(v, "v", f, device)
-    s = f.current_stream(device) if stream is None else stream
-    st = fn(pk, pv, *ptrs, k.shape[0], batch, heads, dim, *sizes, k_stride, v_stride,
-            _errors(f, errors, device), s.cuda_stream)
+    st = fn(k.data_ptr(), v.data_ptr(), *ptrs, shape[0], batch, heads, dim, *sizes,
+            _pitch(k, "k", f, device), _pitch(v, "v", f, device), pe,
+            f.raw_stream(device) if stream is None else stream.cuda_stream)
     if st != SSD_OK:
         raise SSDError(st, what)
 
@@ -200,24 +236,28 @@ def ssd_attn_varlen_fwd(o, lse, q, k_cache, v_cache, k_scale, v_scale, query_sta
     sees; workspace: a uint8 tensor of at least ssd_attn_varlen_workspace_size
     bytes (alloc_attn_workspace)."""
     f = _functions()
-    device = k_cache.device
-    ptrs, batch, heads_kv, dim, sizes = _cache(f, k_cache, v_cache, k_scale, v_scale,
-                                               query_start_loc, kv_lens, block_table, device)
-    if o.shape != q.shape or len(q.shape) != 3 or q.shape[2] != dim:
+    ptrs, batch, heads_kv, dim, sizes, pe, device = _cache(f, k_cache, v_cache, k_scale, v_scale,
+                                                           query_start_loc, kv_lens, block_table,
+                                                           errors)
+    shape = q.shape
+    if o.shape != shape or len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"o and q must both have shape (rows, nheads, {dim})")
-    total, heads = q.shape[0], q.shape[1]
+    total, heads, _ = shape
     if workspace is None:
         raise ValueError("workspace is required (see alloc_attn_workspace)")
+    if workspace.dtype is not f.u8 or workspace.get_device() != device \
+            or not workspace.is_contiguous():
+        _tensor(workspace, "workspace", f.u8, device)
     plse = None
     if lse is not None:
         if lse.shape != (total, heads):
             raise ValueError(f"lse must have shape ({total}, {heads})")
-        plse = _ptr(lse, "lse", f.f32, device)
-    po, o_stride = _rows(o, "o", f, device)
-    pq, q_stride = _rows(q, "q", f, device)
-    s = f.current_stream(device) if stream is None else stream
-    st = f.attn(po, plse, pq, *ptrs, total, batch, heads, heads_kv, dim, *sizes, o_stride, q_stride,
-                softmax_scale, window, _ptr(workspace, "workspace", f.u8, device),
-                workspace.numel(), _errors(f, errors, device), s.cuda_stream)
+        if lse.dtype is not f.f32 or lse.get_device() != device or not lse.is_contiguous():
+            _tensor(lse, "lse", f.f32, device)
+        plse = lse.data_ptr()
+    st = f.attn(o.data_ptr(), plse, q.data_ptr(), *ptrs, total, batch, heads, heads_kv, dim, *sizes,
+                _pitch(o, "o", f, device), _pitch(q, "q", f, device), softmax_scale, window,
+                workspace.data_ptr(), workspace.numel(), pe,
+                f.raw_stream(device) if stream is None else stream.cuda_stream)
     if st != SSD_OK:
         raise SSDError(st, "ssd_attn_varlen_fwd")
