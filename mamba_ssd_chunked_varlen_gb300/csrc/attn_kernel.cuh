@@ -61,7 +61,8 @@ enum Bar {
     kQFull = 0,
     kQEmpty,
     kSFull,              // [2] scores of a stream's tile are in tensor memory
-    kPFull = kSFull + 2, // [2] its probabilities are
+    kPHalf = kSFull + 2, // [2] the probabilities of its first 64 keys are
+    kPFull = kPHalf + 2, // [2] all of its probabilities are
     kOFull = kPFull + 2, // [2] a segment's last product is
     kFixReq = kOFull + 2,
     kFixDone,
@@ -75,6 +76,11 @@ enum Bar {
     kNumBars = kScEmpty + kSlots8,
 };
 static_assert(kNumBars * 8 + 16 <= 512, "barrier space");
+
+template <int k>
+struct Int {
+    __device__ constexpr int operator()() const { return k; }
+};
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
@@ -92,17 +98,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *s_nonfinite = s_abort + 1;   // V rows of the current segment were cleaned
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // the same in every lane
 
     if (tid == 0) {
         ptx::prefetch_tensormap(&maps.Q);
         ptx::prefetch_tensormap(&maps.K);
         ptx::prefetch_tensormap(&maps.V);
         for (int k = 0; k < kNumBars; ++k) {
-            const bool many = k == kPFull || k == kPFull + 1 || k == kFixDone ||
-                              (k >= kRawEmpty && k < kScFull) ||
+            const bool many = k == kFixDone || (k >= kRawEmpty && k < kScFull) ||
                               (C::kQuant && k >= kKvFull && k < kKvEmpty);
-            ptx::mbar_init(bars + k, many ? 128 : 1);
+            const bool warps = k >= kPHalf && k < kOFull;
+            ptx::mbar_init(bars + k, many ? 128 : warps ? 4 : 1);
         }
         ptx::fence_barrier_init();
         *s_abort = 0;
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     pdl_wait();                                // the plan
     pdl_launch_dependents();                   // (few rows: they need nothing but the plan)
     const int g = p.group, tt = p.tile_tokens;
@@ -125,14 +132,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         return attn_partial(e, p.window, (e.tile0 + t) * kTileKeys, kTileKeys, first, last);
     };
     auto wait = [&](int bar, uint32_t parity) {
+        // the warp leaves its loops together; the first try answers most waits
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(ptx::smem_u32(bars + bar), parity & 1)))
+            return ok;
         ok = ok && ptx::mbar_wait(bars + bar, parity & 1, kWaitTimeoutNs) && !*s_abort;
-        ok = __all_sync(0xffffffffu, ok);   // the warp leaves its loops together
+        ok = __all_sync(0xffffffffu, ok);
         return ok;
     };
 
-    // 512 threads at 128 registers: 2 x 128 x (184 + 72) again
+    // 512 threads at 128 registers: 2 x 128 x (168 + 88) again
     if (warp == 12) {
-        ptx::setmaxnreg_dec<72>();
+        ptx::setmaxnreg_dec<88>();
         // ------------------------------------------------------------ producer
         uint32_t it = 0, qit = 0, sit = 0;     // tiles, segments, key tiles so far
         constexpr int kRing = C::kQuant ? C::kRawStages : C::kStages;
@@ -221,95 +231,115 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = sit > kSlots8 ? sit - kSlots8 : 0; k < sit; ++k)
                 ptx::mbar_wait(bars + kScFull + k % kSlots8, (k / kSlots8) & 1, kWaitTimeoutNs);
     } else if (warp == 13) {
-        ptx::setmaxnreg_dec<72>();
+        ptx::setmaxnreg_dec<88>();
         // ------------------------------------------------------------ MMA issuer
-        const uint32_t id_s = ptx::idesc_bf16_f32(128, kTileKeys, 0, 0);
-        const uint32_t id_o = ptx::idesc_bf16_f32(128, kDim, 0, 1);
-        uint32_t it = 0, qit = 0, sit = 0, fit = 0;
-        uint32_t pit0 = 0, pit1 = 0;
-        auto scores = [&](int st, int stage) {
-            if (lane == 0) {
-                const uint64_t a = ptx::sdesc_sw128(ptx::smem_u32(sQ + st * C::kTile), 16, 1024);
-                const uint64_t b = ptx::sdesc_sw128(ptx::smem_u32(sKv + stage * C::kTile), 16, 1024);
-#pragma unroll
-                for (int k = 0; k < kDim / 16; ++k)
-                    ptx::mma_bf16_ss(tmem + st * 128, ptx::sdesc_add(a, (k / 4) * kBlk + (k % 4) * 32),
-                                     ptx::sdesc_add(b, (k / 4) * kBlk + (k % 4) * 32), id_s, k != 0);
-                ptx::mma_commit(bars + kSFull + st);
+        constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, kTileKeys, 0, 0);
+        constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, kDim, 0, 1);
+        const uint64_t desc_q = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
+        const uint64_t desc_k = ptx::sdesc_sw128(ptx::smem_u32(sKv), 16, 1024);
+        const uint64_t desc_v = ptx::sdesc_sw128(ptx::smem_u32(sKv), kBlk, 1024);
+        // the ring's position: tiles come as K0 V0 K1 V1 ...
+        int s = 0;
+        uint32_t phase = 0, q_phase = 0, f_phase = 0, p_phase[2] = {0, 0};
+        int slot = 0;
+        auto advance = [&] {
+            if (++s == C::kStages) {
+                s = 0;
+                phase ^= 1;
             }
         };
-        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next(), ++qit) {
-            const int ns = streams(w.e), n = w.tb - w.ta;
-            if (!wait(kQFull, qit) || !wait(kKvFull + it % C::kStages, it / C::kStages))
+        auto scores = [&](auto st, int stage) {
+            const uint64_t a = desc_q + st() * (C::kTile >> 4), b = ptx::sdesc_add(desc_k, stage * C::kTile);
+#pragma unroll
+            for (int k = 0; k < kDim / 16; ++k)
+                ptx::elect_mma_ss(tmem + st() * 128, ptx::sdesc_add(a, (k / 4) * kBlk + (k % 4) * 32),
+                                  ptx::sdesc_add(b, (k / 4) * kBlk + (k % 4) * 32), id_s, k != 0);
+            ptx::elect_commit(bars + kSFull + st());
+        };
+        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
+            const int ns = streams(w.e), n = __shfl_sync(0xffffffffu, w.tb - w.ta, 0);
+            if (!wait(kQFull, q_phase) || !wait(kKvFull + s, phase))
                 break;
+            q_phase ^= 1;
             ptx::tc_fence_after_sync();
-            for (int st = 0; st < ns; ++st)
-                scores(st, it % C::kStages);
-            if (lane == 0) {
-                ptx::mma_commit(bars + kKvEmpty + it % C::kStages);
-                if (n == 1)
-                    ptx::mma_commit(bars + kQEmpty);
-            }
-            for (int t = 0; t < n && ok; ++t, ++sit) {
-                // ring order: K0 V0 K1 V1 ...; V of this tile, K of the next
-                const uint32_t vi = it + 2 * t + 1, ki = vi + 1;
-                const int vs = vi % C::kStages, ks = ki % C::kStages;
-                if (!wait(kKvFull + vs, vi / C::kStages))
+            scores(Int<0>{}, s);
+            if (ns == 2)
+                scores(Int<1>{}, s);
+            ptx::elect_commit(bars + kKvEmpty + s);
+            if (n == 1)
+                ptx::elect_commit(bars + kQEmpty);
+            advance();
+            for (int t = 0; t < n && ok; ++t) {
+                const int vs = s;               // this tile's V, then the next one's K
+                if (!wait(kKvFull + vs, phase))
                     break;
+                advance();
+                const int ks = s;
+                const uint32_t k_phase = phase;
+                const bool more = t + 1 < n;
+                if (more)
+                    advance();
                 if constexpr (!C::kQuant) {
                     if (partial(w.e, w.ta + t, 0, w.e.tokens - 1)) {
-                        if (lane == 0)
-                            ptx::mbar_arrive(bars + kFixReq);
-                        if (!wait(kFixDone, fit++))
+                        ptx::elect_arrive(bars + kFixReq);
+                        if (!wait(kFixDone, f_phase))
                             break;
+                        f_phase ^= 1;
                     }
                 }
-                for (int st = 0; st < ns && ok; ++st) {
-                    uint32_t &pit = st ? pit1 : pit0;
-                    if (!wait(kPFull + st, pit++))
-                        break;
-                    if (st == 0 && t + 1 < n && !wait(kKvFull + ks, ki / C::kStages))
-                        break;
-                    ptx::tc_fence_after_sync();
-                    if (lane == 0) {
-                        const uint64_t b =
-                            ptx::sdesc_sw128(ptx::smem_u32(sKv + vs * C::kTile), kBlk, 1024);
+                const uint64_t b = ptx::sdesc_add(desc_v, vs * C::kTile);
+                // a stream's P V as its probabilities come, and its next scores in their place
+                auto products = [&](auto st) {
+                    auto half = [&](auto h) {
+                        ptx::tc_fence_after_sync();
 #pragma unroll
-                        for (int k = 0; k < kTileKeys / 16; ++k)
-                            ptx::mma_bf16_ts(tmem + C::kColO + st * kDim, tmem + st * 128 + k * 8,
-                                             ptx::sdesc_add(b, k * 2048), id_o, t > 0 || k != 0);
-                        if (t + 1 == n)
-                            ptx::mma_commit(bars + kOFull + st);
-                    }
-                    if (t + 1 < n)
+                        for (int k = 0; k < kTileKeys / 32; ++k) {
+                            const int i = h() * (kTileKeys / 32) + k;
+                            ptx::elect_mma_ts(tmem + C::kColO + st() * kDim, tmem + st() * 128 + i * 8,
+                                              ptx::sdesc_add(b, i * 2048), id_o, t > 0 || i != 0);
+                        }
+                    };
+                    if (!wait(kPHalf + st(), p_phase[st()]))
+                        return;
+                    half(Int<0>{});
+                    if (!wait(kPFull + st(), p_phase[st()]))
+                        return;
+                    p_phase[st()] ^= 1;
+                    half(Int<1>{});
+                    if (more) {
+                        if (st() == 0 && !wait(kKvFull + ks, k_phase))
+                            return;
+                        ptx::tc_fence_after_sync();
                         scores(st, ks);
-                }
+                    } else {
+                        ptx::elect_commit(bars + kOFull + st());
+                    }
+                };
+                products(Int<0>{});
+                if (ns == 2 && ok)
+                    products(Int<1>{});
                 if (!ok)
                     break;
-                if (lane == 0) {
-                    if constexpr (C::kQuant)   // both streams have read the scales
-                        ptx::mbar_arrive(bars + kScEmpty + sit % kSlots8);
-                    ptx::mma_commit(bars + kKvEmpty + vs);
-                    if (t + 1 < n)
-                        ptx::mma_commit(bars + kKvEmpty + ks);
-                    if (t + 2 == n)
-                        ptx::mma_commit(bars + kQEmpty);
+                if constexpr (C::kQuant) {      // both streams have read the scales
+                    ptx::elect_arrive(bars + kScEmpty + slot);
+                    slot = slot + 1 == kSlots8 ? 0 : slot + 1;
                 }
+                ptx::elect_commit(bars + kKvEmpty + vs);
+                if (more)
+                    ptx::elect_commit(bars + kKvEmpty + ks);
+                if (t + 2 == n)
+                    ptx::elect_commit(bars + kQEmpty);
             }
-            it += 2 * n;
         }
         if (!ok)
             *s_abort = 1;
         // every MMA issued must finish before tensor memory is released
-        if (lane == 0) {
-            ptx::mma_commit(bars + kDrain);
-            ptx::mbar_wait(bars + kDrain, 0, kWaitTimeoutNs);
-        }
-        __syncwarp();
+        ptx::elect_commit(bars + kDrain);
+        ptx::mbar_wait(bars + kDrain, 0, kWaitTimeoutNs);
     } else if (warp >= 14) {
-        ptx::setmaxnreg_dec<72>();
+        ptx::setmaxnreg_dec<88>();
     } else if (warp >= 8) {
-        ptx::setmaxnreg_dec<72>();
+        ptx::setmaxnreg_dec<88>();
         const int ht = tid - 256;              // 0..127
         if constexpr (!C::kQuant) {
             // -------------------------------------------------------- V cleaner
@@ -401,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
         }
     } else {
-        ptx::setmaxnreg_inc<184>();
+        ptx::setmaxnreg_inc<168>();
         // ------------------------------------------------------------ softmax
         const int st = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -431,42 +461,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                 }
                 ptx::tc_fence_after_sync();
-                uint32_t s[128];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    ptx::tmem_ld32_nowait(colS + k * 32, s + k * 32);
-                ptx::tmem_wait_ld();
-                if (p.negate) {
-#pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        s[k] ^= 0x80000000u;
-                }
-                if constexpr (C::kQuant) {
-#pragma unroll
-                    for (int k = 0; k < 128; k += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(sc + k);
-                        s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
-                        s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
-                        s[k + 2] = __float_as_uint(__uint_as_float(s[k + 2]) * f.z);
-                        s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
-                    }
-                }
                 const bool hides = partial(w.e, t, tok0, tok0 + ntok - 1);
-                if (hides) {
-                    const int k0 = (w.e.tile0 + t) * kTileKeys;
-                    const int a = lo - k0, b = hi - k0;
+                const int k0 = (w.e.tile0 + t) * kTileKeys;
+                // 32 scores of the row: sign, K's scales, hidden keys
+                auto prepare = [&](uint32_t (&s)[32], int col) {
+                    if (p.negate) {
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k < a || k >= b)
-                            s[k] = 0xff800000u;
-                }
-                float x0 = __uint_as_float(s[0]), x1 = __uint_as_float(s[1]);
+                        for (int k = 0; k < 32; ++k)
+                            s[k] ^= 0x80000000u;
+                    }
+                    if constexpr (C::kQuant) {
 #pragma unroll
-                for (int k = 2; k < 128; k += 4) {
-                    x0 = max3(x0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                    if (k + 2 < 128)
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sc + col + k);
+                            s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
+                            s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
+                            s[k + 2] = __float_as_uint(__uint_as_float(s[k + 2]) * f.z);
+                            s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
+                        }
+                    }
+                    if (hides) {
+                        const int a = lo - k0 - col, b = hi - k0 - col;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (k < a || k >= b)
+                                s[k] = 0xff800000u;
+                    }
+                };
+                float x0 = -INFINITY, x1 = -INFINITY;
+                auto maximum = [&](const uint32_t (&s)[32]) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        x0 = max3(x0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
                         x1 = max3(x1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-                }
+                    }
+                };
+                // the maximum over the four quarters; the upper two are read again later,
+                // which costs less than 128 registers
+                uint32_t a[32], b[32];
+                ptx::tmem_ld32_nowait(colS + 64, a);
+                ptx::tmem_ld32_nowait(colS + 96, b);
+                ptx::tmem_wait_ld();
+                prepare(a, 64);
+                maximum(a);
+                ptx::tmem_ld32_nowait(colS, a);
+                prepare(b, 96);
+                maximum(b);
+                ptx::tmem_ld32_nowait(colS + 32, b);
+                ptx::tmem_wait_ld();
+                prepare(a, 0);
+                maximum(a);
+                prepare(b, 32);
+                maximum(b);
                 const float mx = fmaxf(x0, x1) * c2;
                 if (t == w.ta) {
                     m = mx;
@@ -477,49 +523,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = mn;
                     l *= f;
 #pragma unroll
-                    for (int k = 0; k < kDim; k += 32) {
-                        uint32_t o[32];
-                        ptx::tmem_ld32_nowait(colO + k, o);
-                        ptx::tmem_wait_ld();
+                    for (int k = 0; k < kDim; k += 16) {
+                        float o[16];
+                        uint32_t r[16];
+                        ptx::tmem_ld16(colO + k, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        ptx::tmem_st32(colO + k, o);
+                        for (int i = 0; i < 16; ++i)
+                            r[i] = __float_as_uint(o[i] * f);
+                        ptx::tmem_st16(colO + k, r);
                     }
                 }
                 const float me = m == -INFINITY ? 0.f : m;
                 const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
                 uint64_t acc0 = ptx::pack2(0.f, 0.f), acc1 = acc0;
-                uint32_t pk[64];
+                // 32 probabilities, as bf16 pairs in the place of scores already read
+                auto probabilities = [&](const uint32_t (&s)[32], int col) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int k = 0; k < 128; k += 4) {
-                    float e0, e1, e2, e3;
-                    ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
-                                           c22, nm), e0, e1);
-                    ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
-                                           c22, nm), e2, e3);
-                    e0 = ptx::ex2(e0);
-                    e1 = ptx::ex2(e1);
-                    e2 = ptx::ex2(e2);
-                    e3 = ptx::ex2(e3);
-                    acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
-                    acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
-                    if constexpr (C::kQuant) {
-                        const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + k);
-                        // (a hidden key's scale may be NaN: its weight stays zero)
-                        e0 = hides && e0 == 0.f ? 0.f : e0 * f.x;
-                        e1 = hides && e1 == 0.f ? 0.f : e1 * f.y;
-                        e2 = hides && e2 == 0.f ? 0.f : e2 * f.z;
-                        e3 = hides && e3 == 0.f ? 0.f : e3 * f.w;
+                    for (int k = 0; k < 32; k += 4) {
+                        float e0, e1, e2, e3;
+                        ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                               c22, nm), e0, e1);
+                        ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
+                                               c22, nm), e2, e3);
+                        e0 = ptx::ex2(e0);
+                        e1 = ptx::ex2(e1);
+                        e2 = ptx::ex2(e2);
+                        e3 = ptx::ex2(e3);
+                        acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
+                        acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
+                        if constexpr (C::kQuant) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + col + k);
+                            // (a hidden key's scale may be NaN: its weight stays zero)
+                            e0 = hides && e0 == 0.f ? 0.f : e0 * f.x;
+                            e1 = hides && e1 == 0.f ? 0.f : e1 * f.y;
+                            e2 = hides && e2 == 0.f ? 0.f : e2 * f.z;
+                            e3 = hides && e3 == 0.f ? 0.f : e3 * f.w;
+                        }
+                        pk[k / 2] = pack_bf16(e0, e1);
+                        pk[k / 2 + 1] = pack_bf16(e2, e3);
                     }
-                    pk[k / 2] = pack_bf16(e0, e1);
-                    pk[k / 2 + 1] = pack_bf16(e2, e3);
-                    if (k % 64 == 60)
-                        ptx::tmem_st32(colS + (k / 64) * 32, pk + (k / 64) * 32);
-                }
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(bars + kPFull + st);
+                    ptx::tmem_st16(colS + col / 2, pk);
+                };
+                auto ready = [&](int bar) {
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(bars + bar + st);
+                };
+                probabilities(a, 0);
+                ptx::tmem_ld32_nowait(colS + 64, a);
+                probabilities(b, 32);
+                ptx::tmem_ld32_nowait(colS + 96, b);
+                ready(kPHalf);             // the product with the first 64 keys may begin
+                ptx::tmem_wait_ld();
+                prepare(a, 64);
+                probabilities(a, 64);
+                prepare(b, 96);
+                probabilities(b, 96);
+                ready(kPFull);
                 float a0, a1;
                 ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
                 l += a0 + a1;
