@@ -10,9 +10,10 @@
 //
 // with c = softmax_scale log2(e): one pass over the keys with the running
 // maximum and sum of the softmax.  O keeps an old reference m until a maximum
-// exceeds it by 2^8, so that it is rescaled a few times per row and not per
-// tile; a probability then is at most 2^8, which neither the fp32 sums nor the
-// bf16 operand feel.
+// exceeds it by 2^16, so that it is rescaled a few times per row and not per
+// tile; a probability then is at most 2^16, which neither the fp32 sums nor the
+// bf16 operand feel.  So the probabilities are computed at once with the
+// reference at hand, and only then is it known whether it served.
 //
 // One CTA per SM, 16 warps.  The two streams share every key tile, which halves
 // the reads of K and V per query row, and take turns: while one stream's warps
@@ -35,7 +36,7 @@ constexpr int kThreads = 512;
 constexpr int kBlk = kTileKeys * 128;      // 128 rows of 64 bf16: one swizzled block
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSlots8 = 4;                 // scale tiles in flight (8-bit caches)
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kRescaleLog2 = 16.f;
 
 template <int kType, int kDim>
 struct Cfg {
@@ -63,7 +64,8 @@ enum Bar {
     kSFull,              // [2] scores of a stream's tile are in tensor memory
     kPHalf = kSFull + 2, // [2] the probabilities of its first 64 keys are
     kPFull = kPHalf + 2, // [2] all of its probabilities are
-    kOFull = kPFull + 2, // [2] a segment's last product is
+    kHalfDone = kPFull + 2, // [2] the product with them is done
+    kOFull = kHalfDone + 2, // [2] a segment's last product is
     kFixReq = kOFull + 2,
     kFixDone,
     kDrain,
@@ -82,7 +84,12 @@ struct Int {
     __device__ constexpr int operator()() const { return k; }
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 template <int kType, int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -108,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kNumBars; ++k) {
             const bool many = k == kFixDone || (k >= kRawEmpty && k < kScFull) ||
                               (C::kQuant && k >= kKvFull && k < kKvEmpty);
-            const bool warps = k >= kPHalf && k < kOFull;
+            const bool warps = k >= kPHalf && k < kHalfDone;
             ptx::mbar_init(bars + k, many ? 128 : warps ? 4 : 1);
         }
         ptx::fence_barrier_init();
@@ -302,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(kPHalf + st(), p_phase[st()]))
                         return;
                     half(Int<0>{});
+                    ptx::elect_commit(bars + kHalfDone + st());
                     if (!wait(kPFull + st(), p_phase[st()]))
                         return;
                     p_phase[st()] ^= 1;
@@ -463,16 +471,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after_sync();
                 const bool hides = partial(w.e, t, tok0, tok0 + ntok - 1);
                 const int k0 = (w.e.tile0 + t) * kTileKeys;
-                // 32 scores of the row: sign, K's scales, hidden keys
-                auto prepare = [&](uint32_t (&s)[32], int col) {
+                // scores from column col on: sign, K's scales, hidden keys
+                auto prepare = [&](auto &s, int col) {
+                    constexpr int n = sizeof s / 4;
                     if (p.negate) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
+                        for (int k = 0; k < n; ++k)
                             s[k] ^= 0x80000000u;
                     }
                     if constexpr (C::kQuant) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
+                        for (int k = 0; k < n; k += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(sc + col + k);
                             s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
                             s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
@@ -483,64 +492,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (hides) {
                         const int a = lo - k0 - col, b = hi - k0 - col;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
+                        for (int k = 0; k < n; ++k)
                             if (k < a || k >= b)
                                 s[k] = 0xff800000u;
                     }
                 };
-                float x0 = -INFINITY, x1 = -INFINITY;
-                auto maximum = [&](const uint32_t (&s)[32]) {
+                float x0, x1;
+                auto maximum = [&](const auto &s) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
+                    for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
                         x0 = max3(x0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
                         x1 = max3(x1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
                     }
                 };
-                // the maximum over the four quarters; the upper two are read again later,
-                // which costs less than 128 registers
-                uint32_t a[32], b[32];
-                ptx::tmem_ld32_nowait(colS + 64, a);
-                ptx::tmem_ld32_nowait(colS + 96, b);
-                ptx::tmem_wait_ld();
-                prepare(a, 64);
-                maximum(a);
-                ptx::tmem_ld32_nowait(colS, a);
-                prepare(b, 96);
-                maximum(b);
-                ptx::tmem_ld32_nowait(colS + 32, b);
-                ptx::tmem_wait_ld();
-                prepare(a, 0);
-                maximum(a);
-                prepare(b, 32);
-                maximum(b);
-                const float mx = fmaxf(x0, x1) * c2;
-                if (t == w.ta) {
-                    m = mx;
-                } else if (__any_sync(0xffffffffu, mx > m + kRescaleLog2)) {
-                    // rare: the rows of the warp take their new references
-                    const float mn = fmaxf(m, mx);
-                    const float f = mn == m ? 1.f : ptx::ex2(m - mn);
-                    m = mn;
-                    l *= f;
+                uint64_t acc0, acc1;           // sums of probabilities
+                auto probabilities = [&](const auto &s, int col, uint32_t *pk) {
+                    const float me = m == -INFINITY ? 0.f : m;
+                    const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
 #pragma unroll
-                    for (int k = 0; k < kDim; k += 16) {
-                        float o[16];
-                        uint32_t r[16];
-                        ptx::tmem_ld16(colO + k, o);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            r[i] = __float_as_uint(o[i] * f);
-                        ptx::tmem_st16(colO + k, r);
-                    }
-                }
-                const float me = m == -INFINITY ? 0.f : m;
-                const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
-                uint64_t acc0 = ptx::pack2(0.f, 0.f), acc1 = acc0;
-                // 32 probabilities, as bf16 pairs in the place of scores already read
-                auto probabilities = [&](const uint32_t (&s)[32], int col) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
+                    for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
                         float e0, e1, e2, e3;
                         ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
                                                c22, nm), e0, e1);
@@ -563,29 +533,98 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[k / 2] = pack_bf16(e0, e1);
                         pk[k / 2 + 1] = pack_bf16(e2, e3);
                     }
-                    ptx::tmem_st16(colS + col / 2, pk);
                 };
-                auto ready = [&](int bar) {
+                // ---- the rare parts, 16 scores at a time ----
+                auto row_maximum = [&] {
+                    x0 = x1 = -INFINITY;
+#pragma unroll 1
+                    for (int col = 0; col < kTileKeys; col += 16) {
+                        uint32_t s[16];
+                        __syncwarp();
+                        ptx::tmem_ld16_nowait(colS + col, s);
+                        ptx::tmem_wait_ld();
+                        prepare(s, col);
+                        maximum(s);
+                    }
+                    return fmaxf(x0, x1) * c2;
+                };
+                // the rows of the warp take new references, at least `mx`
+                auto rescale = [&](float mx) {
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == m ? 1.f : ptx::ex2(m - mn);
+                    m = mn;
+                    l *= f;
+#pragma unroll 1
+                    for (int k = 0; k < kDim; k += 16) {
+                        float o[16];
+                        uint32_t r[16];
+                        __syncwarp();
+                        ptx::tmem_ld16(colO + k, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            r[i] = __float_as_uint(o[i] * f);
+                        ptx::tmem_st16(colO + k, r);
+                    }
+                };
+                auto again = [&](int first) {   // 64 probabilities with the new reference
+                    acc0 = acc1 = ptx::pack2(0.f, 0.f);
+#pragma unroll 1
+                    for (int col = first; col < first + 64; col += 16) {
+                        uint32_t s[16], pk[8];
+                        __syncwarp();
+                        ptx::tmem_ld16_nowait(colS + col, s);
+                        ptx::tmem_wait_ld();
+                        prepare(s, col);
+                        probabilities(s, col, pk);
+                        ptx::tmem_st8(colS + col / 2, pk);
+                    }
+                };
+                if (t == w.ta)
+                    m = row_maximum();
+                // Half of the row at a time, with the reference as it is; where a score
+                // turns out to be far above it, again with a new one.  The second half
+                // then has to wait for the first half's product, which is under way.
+                uint32_t a[32], b[32];
+                ptx::tmem_ld32_nowait(colS, a);
+                ptx::tmem_ld32_nowait(colS + 32, b);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+                    ptx::tmem_wait_ld();
+                    x0 = x1 = -INFINITY;
+                    acc0 = acc1 = ptx::pack2(0.f, 0.f);
+                    prepare(a, half * 64);
+                    probabilities(a, half * 64, pk);
+                    maximum(a);
+                    prepare(b, half * 64 + 32);
+                    probabilities(b, half * 64 + 32, pk + 16);
+                    maximum(b);
+                    if (__any_sync(0xffffffffu, fmaxf(x0, x1) * c2 > m + kRescaleLog2)) {
+                        if (half == 0) {
+                            rescale(row_maximum());
+                            again(0);
+                        } else if (wait(kHalfDone + st, it)) {
+                            rescale(fmaxf(x0, x1) * c2);
+                            again(64);
+                        }
+                    } else {
+                        // (in the place of scores already read)
+                        ptx::tmem_st16(colS + half * 32, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
+                        ptx::tmem_st16(colS + half * 32 + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
+                    }
+                    if (half == 0) {
+                        ptx::tmem_ld32_nowait(colS + 64, a);
+                        ptx::tmem_ld32_nowait(colS + 96, b);
+                    }
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0)
-                        ptx::mbar_arrive(bars + bar + st);
-                };
-                probabilities(a, 0);
-                ptx::tmem_ld32_nowait(colS + 64, a);
-                probabilities(b, 32);
-                ptx::tmem_ld32_nowait(colS + 96, b);
-                ready(kPHalf);             // the product with the first 64 keys may begin
-                ptx::tmem_wait_ld();
-                prepare(a, 64);
-                probabilities(a, 64);
-                prepare(b, 96);
-                probabilities(b, 96);
-                ready(kPFull);
-                float a0, a1;
-                ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
-                l += a0 + a1;
+                        ptx::mbar_arrive(bars + (half ? kPFull : kPHalf) + st);
+                    float a0, a1;
+                    ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
+                    l += a0 + a1;
+                }
             }
             if (!ok || !wait(kOFull + st, oit++))
                 break;
