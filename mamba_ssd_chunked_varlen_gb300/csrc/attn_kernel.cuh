@@ -256,11 +256,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         auto scores = [&](auto st, int stage) {
-            const uint64_t a = desc_q + st() * (C::kTile >> 4), b = ptx::sdesc_add(desc_k, stage * C::kTile);
+            uint64_t a = desc_q + st() * (C::kTile >> 4), b = ptx::sdesc_add(desc_k, stage * C::kTile);
+#pragma unroll 1
+            for (int k = 0; k < C::kBlocks; ++k) {      // (rolled: short code stays fetched)
 #pragma unroll
-            for (int k = 0; k < kDim / 16; ++k)
-                ptx::elect_mma_ss(tmem + st() * 128, ptx::sdesc_add(a, (k / 4) * kBlk + (k % 4) * 32),
-                                  ptx::sdesc_add(b, (k / 4) * kBlk + (k % 4) * 32), id_s, k != 0);
+                for (int i = 0; i < 4; ++i)
+                    ptx::elect_mma_ss(tmem + st() * 128, ptx::sdesc_add(a, i * 32), ptx::sdesc_add(b, i * 32),
+                                      id_s, k + i != 0);
+                a = ptx::sdesc_add(a, kBlk);
+                b = ptx::sdesc_add(b, kBlk);
+            }
             ptx::elect_commit(bars + kSFull + st());
         };
         for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             // -------------------------------------------------------- converter
             constexpr int kUnits = kDim / 16;  // 16-code pieces of a row
-            uint32_t it = 0;
+            uint32_t it = 0, sit = 0;
             for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next())
                 for (int t = w.ta; t < w.tb && ok; ++t)
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
@@ -410,6 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (it >= C::kStages && !wait(kKvEmpty + s, it / C::kStages - 1))
                             break;
                         const int keys = w.e.kv_len - (w.e.tile0 + t) * kTileKeys;
+                        float *f = sScale + (sit % kSlots8) * 2 * kTileKeys;
+                        if (kv == 0 && !wait(kScFull + sit % kSlots8, sit / kSlots8))
+                            break;
+                        sit += kv;
                         const uint8_t *src = sRaw + rs * C::kRaw;
                         uint8_t *dst = sKv + s * C::kTile;
 #pragma unroll 4
@@ -423,6 +432,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             widen4<kType>(x.y, o + 2);
                             widen4<kType>(x.z, o + 4);
                             widen4<kType>(x.w, o + 6);
+                            if (kv == 0 && c == 0) {
+                                // the row's scales: a row that is not finite gets them finite
+                                // and a NaN among its codes, so that scores hidden from a
+                                // query stay hidden, and one past the last key any
+                                const float ks = f[row], vs = f[kTileKeys + row];
+                                const bool bad = !(fabsf(ks) <= 3.4e38f && fabsf(vs) <= 3.4e38f);
+                                if (bad || row >= keys) {
+                                    f[row] = 1.f;
+                                    f[kTileKeys + row] = 0.f;
+                                    if (row < keys)
+                                        o[0] = 0x7fff7fffu;
+                                }
+                            }
                             uint8_t *line = dst + (c >> 2) * kBlk + row * 128;
                             const int c16 = (c & 3) * 2;
                             // pieces of the second block write their halves in the other
@@ -463,38 +485,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = w.ta; t < w.tb && ok; ++t, ++it, ++sit) {
                 if (!wait(kSFull + st, it))
                     break;
+                // (the converter has seen the scales land)
                 const float *sc = sScale + (sit % kSlots8) * 2 * kTileKeys;
-                if constexpr (C::kQuant) {
-                    if (!wait(kScFull + sit % kSlots8, sit / kSlots8))
-                        break;
-                }
                 ptx::tc_fence_after_sync();
                 const bool hides = partial(w.e, t, tok0, tok0 + ntok - 1);
                 const int k0 = (w.e.tile0 + t) * kTileKeys;
-                // scores from column col on: sign, K's scales, hidden keys
-                auto prepare = [&](auto &s, int col) {
-                    constexpr int n = sizeof s / 4;
-                    if (p.negate) {
+                if (hides || p.negate) {
+                    // hidden keys and a negative softmax_scale, in a pass of its own that
+                    // keeps the usual one short
+#pragma unroll 1
+                    for (int col = 0; col < kTileKeys; col += 16) {
+                        uint32_t s[16];
+                        __syncwarp();
+                        ptx::tmem_ld16_nowait(colS + col, s);
+                        ptx::tmem_wait_ld();
+                        const int a = hides ? lo - k0 - col : 0, b = hides ? hi - k0 - col : 16;
 #pragma unroll
-                        for (int k = 0; k < n; ++k)
-                            s[k] ^= 0x80000000u;
+                        for (int k = 0; k < 16; ++k) {
+                            const uint32_t v = p.negate ? s[k] ^ 0x80000000u : s[k];
+                            s[k] = k < a || k >= b ? 0xff800000u : v;
+                        }
+                        ptx::tmem_st16(colS + col, s);
                     }
+                    ptx::tmem_wait_st();
+                }
+                auto prepare = [&](auto &s, int col) {     // scores from column col on: K's scales
                     if constexpr (C::kQuant) {
 #pragma unroll
-                        for (int k = 0; k < n; k += 4) {
+                        for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(sc + col + k);
                             s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
                             s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
                             s[k + 2] = __float_as_uint(__uint_as_float(s[k + 2]) * f.z);
                             s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
                         }
-                    }
-                    if (hides) {
-                        const int a = lo - k0 - col, b = hi - k0 - col;
-#pragma unroll
-                        for (int k = 0; k < n; ++k)
-                            if (k < a || k >= b)
-                                s[k] = 0xff800000u;
                     }
                 };
                 float x0, x1;
@@ -524,11 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
                         if constexpr (C::kQuant) {
                             const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + col + k);
-                            // (a hidden key's scale may be NaN: its weight stays zero)
-                            e0 = hides && e0 == 0.f ? 0.f : e0 * f.x;
-                            e1 = hides && e1 == 0.f ? 0.f : e1 * f.y;
-                            e2 = hides && e2 == 0.f ? 0.f : e2 * f.z;
-                            e3 = hides && e3 == 0.f ? 0.f : e3 * f.w;
+                            e0 *= f.x;
+                            e1 *= f.y;
+                            e2 *= f.z;
+                            e3 *= f.w;
                         }
                         pk[k / 2] = pack_bf16(e0, e1);
                         pk[k / 2 + 1] = pack_bf16(e2, e3);
@@ -584,12 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Half of the row at a time, with the reference as it is; where a score
                 // turns out to be far above it, again with a new one.  The second half
                 // then has to wait for the first half's product, which is under way.
-                uint32_t a[32], b[32];
-                ptx::tmem_ld32_nowait(colS, a);
-                ptx::tmem_ld32_nowait(colS + 32, b);
-#pragma unroll
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[32];
+                    uint32_t a[32], b[32], pk[32];
+                    ptx::tmem_ld32_nowait(colS + half * 64, a);
+                    ptx::tmem_ld32_nowait(colS + half * 64 + 32, b);
                     ptx::tmem_wait_ld();
                     x0 = x1 = -INFINITY;
                     acc0 = acc1 = ptx::pack2(0.f, 0.f);
@@ -611,10 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // (in the place of scores already read)
                         ptx::tmem_st16(colS + half * 32, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
                         ptx::tmem_st16(colS + half * 32 + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
-                    }
-                    if (half == 0) {
-                        ptx::tmem_ld32_nowait(colS + 64, a);
-                        ptx::tmem_ld32_nowait(colS + 96, b);
                     }
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before_sync();
