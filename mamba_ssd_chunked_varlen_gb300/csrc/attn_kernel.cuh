@@ -23,7 +23,7 @@
 //   warps 8-11       bf16: clean the V tiles that hold rows nobody may see;
 //                    8-bit: widen codes to bf16 tiles (exact: 8 bits at most)
 //   warp 12          TMA producer: Q, K and V page by page
-//   warp 13          tcgen05 issuer
+//   warps 13, 14     tcgen05 issuers of stream 0 and 1
 #pragma once
 
 #include "attn_codes.cuh"
@@ -68,8 +68,9 @@ enum Bar {
     kOFull = kHalfDone + 2, // [2] a segment's last product is
     kFixReq = kOFull + 2,
     kFixDone,
-    kDrain,
-    kKvFull,                      // [8]
+    kTurn,                        // [2] the issuer's turn
+    kDrain = kTurn + 2,           // [2]
+    kKvFull = kDrain + 2,         // [8]
     kKvEmpty = kKvFull + 8,       // [8]
     kRawFull = kKvEmpty + 8,      // [6]
     kRawEmpty = kRawFull + 6,     // [6]
@@ -116,8 +117,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool many = k == kFixDone || (k >= kRawEmpty && k < kScFull) ||
                               (C::kQuant && k >= kKvFull && k < kKvEmpty);
             const bool warps = k >= kPHalf && k < kHalfDone;
-            ptx::mbar_init(bars + k, many ? 128 : warps ? 4 : 1);
+            // what both issuers release
+            const bool both = k == kQEmpty || k == kFixReq || (k >= kKvEmpty && k < kRawFull) || k >= kScEmpty;
+            ptx::mbar_init(bars + k, many ? 128 : warps ? 4 : both ? 2 : 1);
         }
+        ptx::mbar_arrive(bars + kTurn);         // stream 0 goes first
         ptx::fence_barrier_init();
         *s_abort = 0;
         *s_nonfinite = 0;
@@ -237,103 +241,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (C::kQuant)
             for (uint32_t k = sit > kSlots8 ? sit - kSlots8 : 0; k < sit; ++k)
                 ptx::mbar_wait(bars + kScFull + k % kSlots8, (k / kSlots8) & 1, kWaitTimeoutNs);
-    } else if (warp == 13) {
+    } else if (warp == 13 || warp == 14) {
         ptx::setmaxnreg_dec<88>();
-        // ------------------------------------------------------------ MMA issuer
+        // ------------------------------------------------------------ MMA issuers
+        // One warp per stream: an issuer's waits and releases take about as long as
+        // its products.  They issue in turn, a stream's P V and next scores as one, so
+        // that the streams stay half a tile apart and one's exponentials run beside
+        // the other's products.  The second issuer goes through the tiles also where
+        // it has no rows: what both read is released by both.
+        const int st = warp - 13;
         constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, kTileKeys, 0, 0);
         constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, kDim, 0, 1);
-        const uint64_t desc_q = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
+        const uint64_t desc_q = ptx::sdesc_sw128(ptx::smem_u32(sQ + st * C::kTile), 16, 1024);
         const uint64_t desc_k = ptx::sdesc_sw128(ptx::smem_u32(sKv), 16, 1024);
         const uint64_t desc_v = ptx::sdesc_sw128(ptx::smem_u32(sKv), kBlk, 1024);
+        const uint32_t col_s = tmem + st * 128, col_o = tmem + C::kColO + st * kDim;
         // the ring's position: tiles come as K0 V0 K1 V1 ...
-        int s = 0;
-        uint32_t phase = 0, q_phase = 0, f_phase = 0, p_phase[2] = {0, 0};
-        int slot = 0;
+        int s = 0, slot = 0;
+        uint32_t phase = 0, q_phase = 0, f_phase = 0, p_phase = 0, turn = 0;
         auto advance = [&] {
             if (++s == C::kStages) {
                 s = 0;
                 phase ^= 1;
             }
         };
-        auto scores = [&](auto st, int stage) {
-            uint64_t a = desc_q + st() * (C::kTile >> 4), b = ptx::sdesc_add(desc_k, stage * C::kTile);
+        auto scores = [&](int stage) {
+            uint64_t a = desc_q, b = ptx::sdesc_add(desc_k, stage * C::kTile);
 #pragma unroll 1
             for (int k = 0; k < C::kBlocks; ++k) {      // (rolled: short code stays fetched)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    ptx::elect_mma_ss(tmem + st() * 128, ptx::sdesc_add(a, i * 32), ptx::sdesc_add(b, i * 32),
-                                      id_s, k + i != 0);
+                    ptx::elect_mma_ss(col_s, ptx::sdesc_add(a, i * 32), ptx::sdesc_add(b, i * 32), id_s,
+                                      k + i != 0);
                 a = ptx::sdesc_add(a, kBlk);
                 b = ptx::sdesc_add(b, kBlk);
             }
-            ptx::elect_commit(bars + kSFull + st());
+            ptx::elect_commit(bars + kSFull + st);
         };
         for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
-            const int ns = streams(w.e), n = __shfl_sync(0xffffffffu, w.tb - w.ta, 0);
+            const bool mine = __shfl_sync(0xffffffffu, static_cast<int>(streams(w.e) > st), 0) != 0;
+            const int n = __shfl_sync(0xffffffffu, w.tb - w.ta, 0);
             if (!wait(kQFull, q_phase) || !wait(kKvFull + s, phase))
                 break;
             q_phase ^= 1;
             ptx::tc_fence_after_sync();
-            scores(Int<0>{}, s);
-            if (ns == 2)
-                scores(Int<1>{}, s);
+            if (mine)
+                scores(s);
             ptx::elect_commit(bars + kKvEmpty + s);
             if (n == 1)
                 ptx::elect_commit(bars + kQEmpty);
             advance();
-            for (int t = 0; t < n && ok; ++t) {
+            for (int t = 0; t < n; ++t) {
                 const int vs = s;               // this tile's V, then the next one's K
                 if (!wait(kKvFull + vs, phase))
                     break;
                 advance();
                 const int ks = s;
-                const uint32_t k_phase = phase;
                 const bool more = t + 1 < n;
-                if (more)
-                    advance();
                 if constexpr (!C::kQuant) {
                     if (partial(w.e, w.ta + t, 0, w.e.tokens - 1)) {
+                        // (both ask, so that neither can be two answers behind)
                         ptx::elect_arrive(bars + kFixReq);
                         if (!wait(kFixDone, f_phase))
                             break;
                         f_phase ^= 1;
                     }
                 }
-                const uint64_t b = ptx::sdesc_add(desc_v, vs * C::kTile);
-                // a stream's P V as its probabilities come, and its next scores in their place
-                auto products = [&](auto st) {
-                    auto half = [&](auto h) {
+                if (more) {
+                    if (!wait(kKvFull + ks, phase))
+                        break;
+                    advance();
+                }
+                // P V as the probabilities come, then the next scores in their place
+                if (mine && !wait(kPHalf + st, p_phase))
+                    break;
+                if (!wait(kTurn + st, turn))
+                    break;
+                turn ^= 1;
+                if (mine) {
+                    const uint64_t b = ptx::sdesc_add(desc_v, vs * C::kTile);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        if (half && !wait(kPFull + st, p_phase))
+                            break;
                         ptx::tc_fence_after_sync();
 #pragma unroll
                         for (int k = 0; k < kTileKeys / 32; ++k) {
-                            const int i = h() * (kTileKeys / 32) + k;
-                            ptx::elect_mma_ts(tmem + C::kColO + st() * kDim, tmem + st() * 128 + i * 8,
-                                              ptx::sdesc_add(b, i * 2048), id_o, t > 0 || i != 0);
+                            const int i = half * (kTileKeys / 32) + k;
+                            ptx::elect_mma_ts(col_o, col_s + i * 8, ptx::sdesc_add(b, i * 2048), id_o, t + i != 0);
                         }
-                    };
-                    if (!wait(kPHalf + st(), p_phase[st()]))
-                        return;
-                    half(Int<0>{});
-                    ptx::elect_commit(bars + kHalfDone + st());
-                    if (!wait(kPFull + st(), p_phase[st()]))
-                        return;
-                    p_phase[st()] ^= 1;
-                    half(Int<1>{});
-                    if (more) {
-                        if (st() == 0 && !wait(kKvFull + ks, k_phase))
-                            return;
-                        ptx::tc_fence_after_sync();
-                        scores(st, ks);
-                    } else {
-                        ptx::elect_commit(bars + kOFull + st());
+                        if (half == 0 || !more)
+                            ptx::elect_commit(bars + (half == 0 ? kHalfDone : kOFull) + st);
                     }
-                };
-                products(Int<0>{});
-                if (ns == 2 && ok)
-                    products(Int<1>{});
-                if (!ok)
-                    break;
-                if constexpr (C::kQuant) {      // both streams have read the scales
+                    if (!ok)
+                        break;
+                    p_phase ^= 1;
+                    if (more)
+                        scores(ks);
+                }
+                ptx::elect_arrive(bars + kTurn + (st ^ 1));
+                if constexpr (C::kQuant) {      // the stream has read the scales
                     ptx::elect_arrive(bars + kScEmpty + slot);
                     slot = slot + 1 == kSlots8 ? 0 : slot + 1;
                 }
@@ -347,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok)
             *s_abort = 1;
         // every MMA issued must finish before tensor memory is released
-        ptx::elect_commit(bars + kDrain);
-        ptx::mbar_wait(bars + kDrain, 0, kWaitTimeoutNs);
-    } else if (warp >= 14) {
+        ptx::elect_commit(bars + kDrain + st);
+        ptx::mbar_wait(bars + kDrain + st, 0, kWaitTimeoutNs);
+    } else if (warp == 15) {
         ptx::setmaxnreg_dec<88>();
     } else if (warp >= 8) {
         ptx::setmaxnreg_dec<88>();
@@ -415,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (it >= C::kStages && !wait(kKvEmpty + s, it / C::kStages - 1))
                             break;
                         const int keys = w.e.kv_len - (w.e.tile0 + t) * kTileKeys;
-                        float *f = sScale + (sit % kSlots8) * 2 * kTileKeys;
+                        float *scale = sScale + (sit % kSlots8) * 2 * kTileKeys;
                         if (kv == 0 && !wait(kScFull + sit % kSlots8, sit / kSlots8))
                             break;
                         sit += kv;
@@ -436,11 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 // the row's scales: a row that is not finite gets them finite
                                 // and a NaN among its codes, so that scores hidden from a
                                 // query stay hidden, and one past the last key any
-                                const float ks = f[row], vs = f[kTileKeys + row];
+                                const float ks = scale[row], vs = scale[kTileKeys + row];
                                 const bool bad = !(fabsf(ks) <= 3.4e38f && fabsf(vs) <= 3.4e38f);
                                 if (bad || row >= keys) {
-                                    f[row] = 1.f;
-                                    f[kTileKeys + row] = 0.f;
+                                    scale[row] = 1.f;
+                                    scale[kTileKeys + row] = 0.f;
                                     if (row < keys)
                                         o[0] = 0x7fff7fffu;
                                 }
