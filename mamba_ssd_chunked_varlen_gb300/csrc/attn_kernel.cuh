@@ -265,10 +265,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 phase ^= 1;
             }
         };
-        auto scores = [&](int stage) {
+        // (rolled loops here and below: short code stays fetched)
+        auto scores = [&](int stage, bool pass) {
             uint64_t a = desc_q, b = ptx::sdesc_add(desc_k, stage * C::kTile);
 #pragma unroll 1
-            for (int k = 0; k < C::kBlocks; ++k) {      // (rolled: short code stays fetched)
+            for (int k = 0; k < C::kBlocks; ++k) {
+                // the other's turn while the last four are under way
+                if (pass && k == C::kBlocks - 1)
+                    ptx::elect_arrive(bars + kTurn + (st ^ 1));
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     ptx::elect_mma_ss(col_s, ptx::sdesc_add(a, i * 32), ptx::sdesc_add(b, i * 32), id_s,
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_phase ^= 1;
             ptx::tc_fence_after_sync();
             if (mine)
-                scores(s);
+                scores(s, false);
             ptx::elect_commit(bars + kKvEmpty + s);
             if (n == 1)
                 ptx::elect_commit(bars + kQEmpty);
@@ -319,27 +323,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 turn ^= 1;
                 if (mine) {
+                    // all of P is there when products bound the loop; else half by half
                     const uint64_t b = ptx::sdesc_add(desc_v, vs * C::kTile);
+                    const bool full = __all_sync(
+                        0xffffffffu, ptx::mbar_test(ptx::smem_u32(bars + kPFull + st), p_phase));
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        if (half && !wait(kPFull + st, p_phase))
-                            break;
+                    for (int i = 0; i < kTileKeys / 16; i += 4) {
+                        if (i == kTileKeys / 32 && !full) {
+                            ptx::elect_commit(bars + kHalfDone + st);
+                            if (!wait(kPFull + st, p_phase))
+                                break;
+                        }
                         ptx::tc_fence_after_sync();
 #pragma unroll
-                        for (int k = 0; k < kTileKeys / 32; ++k) {
-                            const int i = half * (kTileKeys / 32) + k;
-                            ptx::elect_mma_ts(col_o, col_s + i * 8, ptx::sdesc_add(b, i * 2048), id_o, t + i != 0);
-                        }
-                        if (half == 0 || !more)
-                            ptx::elect_commit(bars + (half == 0 ? kHalfDone : kOFull) + st);
+                        for (int k = 0; k < 4; ++k)
+                            ptx::elect_mma_ts(col_o, col_s + (i + k) * 8, ptx::sdesc_add(b, (i + k) * 2048),
+                                              id_o, t + i + k != 0);
                     }
                     if (!ok)
                         break;
+                    if (full)
+                        ptx::elect_commit(bars + kHalfDone + st);
                     p_phase ^= 1;
                     if (more)
-                        scores(ks);
+                        scores(ks, true);
+                    else
+                        ptx::elect_commit(bars + kOFull + st);
                 }
-                ptx::elect_arrive(bars + kTurn + (st ^ 1));
+                if (!mine || !more)
+                    ptx::elect_arrive(bars + kTurn + (st ^ 1));
                 if constexpr (C::kQuant) {      // the stream has read the scales
                     ptx::elect_arrive(bars + kScEmpty + slot);
                     slot = slot + 1 == kSlots8 ? 0 : slot + 1;
