@@ -15,15 +15,15 @@
 // bf16 operand feel.  So the probabilities are computed at once with the
 // reference at hand, and only then is it known whether it served.
 //
-// One CTA per SM, 16 warps.  The two streams share every key tile, which halves
+// One CTA per SM, 16 warps (8-bit caches: 20).  The two streams share every key tile, which halves
 // the reads of K and V per query row, and take turns: while one stream's warps
 // exponentiate, the tensor cores run the other's products.
 //   warps 0-3, 4-7   softmax and output of stream 0 and 1: a thread per row,
 //                    all 128 scores of the row in registers
-//   warps 8-11       bf16: clean the V tiles that hold rows nobody may see;
-//                    8-bit: widen codes to bf16 tiles (exact: 8 bits at most)
-//   warp 12          TMA producer: Q, K and V page by page
-//   warps 13, 14     tcgen05 issuers of stream 0 and 1
+//   four warps more  bf16: clean the V tiles that hold rows nobody may see;
+//   (8-bit: eight)   8-bit: widen codes to bf16 tiles (exact: 8 bits at most)
+//   one              TMA producer: Q, K and V page by page
+//   two              tcgen05 issuers of stream 0 and 1
 #pragma once
 
 #include "attn_codes.cuh"
@@ -32,15 +32,23 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kBlk = kTileKeys * 128;      // 128 rows of 64 bf16: one swizzled block
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSlots8 = 4;                 // scale tiles in flight (8-bit caches)
-constexpr float kRescaleLog2 = 16.f;
+constexpr float kRescale = 65536.f;      // a half tile's sum of probabilities that asks for it
 
 template <int kType, int kDim>
 struct Cfg {
     static constexpr bool kQuant = kType != SSD_KV_BF16;
+    // warps: 8 of softmax, the helpers, producer, two issuers, one idle; registers a
+    // thread at launch, and after the split
+    static constexpr int kHelpers = kQuant ? 8 : 4;
+    static constexpr int kProducer = 8 + kHelpers, kIssuer = kProducer + 1;
+    static constexpr int kThreads = (kProducer + 4) * 32;
+    static constexpr int kLaunchRegs = kQuant ? 96 : 128;
+    static constexpr int kSoftmaxRegs = kQuant ? 144 : 168, kOtherRegs = kQuant ? 64 : 88;
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs &&
+                  kThreads * kLaunchRegs <= 65536, "registers");
     static constexpr int kBlocks = kDim / 64;
     static constexpr int kTile = kBlocks * kBlk;             // a bf16 tile of 128 rows
     static constexpr int kRaw = kTileKeys * kDim;            // the same in 8-bit codes
@@ -57,19 +65,17 @@ struct Cfg {
     static constexpr uint32_t kColO = 256;
 };
 
-// Barriers, in 8-byte words from kBarOff.
+// Barriers, in 8-byte words from kBarOff.  [2][2]: stream, then half of a key tile.
 enum Bar {
     kQFull = 0,
     kQEmpty,
-    kSFull,              // [2] scores of a stream's tile are in tensor memory
-    kPHalf = kSFull + 2, // [2] the probabilities of its first 64 keys are
-    kPFull = kPHalf + 2, // [2] all of its probabilities are
-    kHalfDone = kPFull + 2, // [2] the product with them is done
-    kOFull = kHalfDone + 2, // [2] a segment's last product is
+    kSFull,              // [2][2] scores are in tensor memory
+    kPFull = kSFull + 4, // [2][2] probabilities are
+    kPvDone = kPFull + 4, // [2][2] their product is done
+    kOFull = kPvDone + 4, // [2] a segment's last product is
     kFixReq = kOFull + 2,
     kFixDone,
-    kTurn,                        // [2] the issuer's turn
-    kDrain = kTurn + 2,           // [2]
+    kDrain,                       // [2]
     kKvFull = kDrain + 2,         // [8]
     kKvEmpty = kKvFull + 8,       // [8]
     kRawFull = kKvEmpty + 8,      // [6]
@@ -93,7 +99,7 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 }
 
 template <int kType, int kDim>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
     attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
 {
     using C = Cfg<kType, kDim>;
@@ -115,18 +121,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tensormap(&maps.V);
         for (int k = 0; k < kNumBars; ++k) {
             const bool many = k == kFixDone || (k >= kRawEmpty && k < kScFull) ||
-                              (C::kQuant && k >= kKvFull && k < kKvEmpty);
-            const bool warps = k >= kPHalf && k < kHalfDone;
+                              (C::kQuant && k >= kKvFull && k < kKvEmpty);   // the helpers
+            const bool warps = k >= kPFull && k < kPvDone;
             // what both issuers release
             const bool both = k == kQEmpty || k == kFixReq || (k >= kKvEmpty && k < kRawFull) || k >= kScEmpty;
-            ptx::mbar_init(bars + k, many ? 128 : warps ? 4 : both ? 2 : 1);
+            ptx::mbar_init(bars + k, many ? C::kHelpers * 32 : warps ? 4 : both ? 2 : 1);
         }
-        ptx::mbar_arrive(bars + kTurn);         // stream 0 goes first
         ptx::fence_barrier_init();
         *s_abort = 0;
         *s_nonfinite = 0;
     }
-    if (warp == 13) {
+    if (warp == C::kIssuer) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
     }
@@ -142,18 +147,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto partial = [&](const AttnUnit &e, int t, int first, int last) {
         return attn_partial(e, p.window, (e.tile0 + t) * kTileKeys, kTileKeys, first, last);
     };
-    auto wait = [&](int bar, uint32_t parity) {
-        // the warp leaves its loops together; the first try answers most waits
-        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(ptx::smem_u32(bars + bar), parity & 1)))
-            return ok;
+    // Waits, after which the warp goes on together or leaves its loops together.  (A
+    // test answers sooner where the barrier is through already, 56 against 86 cycles;
+    // polling with it took more issue slots than it won: 782 against 756 us for 2048
+    // tokens over 32,768 keys.)
+    auto lazy_wait = [&](int bar, uint32_t parity) {
         ok = ok && ptx::mbar_wait(bars + bar, parity & 1, kWaitTimeoutNs) && !*s_abort;
         ok = __all_sync(0xffffffffu, ok);
         return ok;
     };
+    auto wait = [&](int bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, ptx::mbar_test(ptx::smem_u32(bars + bar), parity & 1)))
+            return ok;
+        return lazy_wait(bar, parity);
+    };
 
-    // 512 threads at 128 registers: 2 x 128 x (168 + 88) again
-    if (warp == 12) {
-        ptx::setmaxnreg_dec<88>();
+    if (warp == C::kProducer) {
+        ptx::setmaxnreg_dec<C::kOtherRegs>();
         // ------------------------------------------------------------ producer
         uint32_t it = 0, qit = 0, sit = 0;     // tiles, segments, key tiles so far
         constexpr int kRing = C::kQuant ? C::kRawStages : C::kStages;
@@ -164,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ns = streams(w.e);
             if (lane == 0)
                 w.note_split(0, blockIdx.x);
-            if (qit > 0 && !wait(kQEmpty, qit - 1))
+            if (qit > 0 && !lazy_wait(kQEmpty, qit - 1))
                 break;
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(bars + kQFull, ns * g * tt * kDim * 2);
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int y = shift > 7 ? j0 & (p.c.page - 1) : 0;
                 if constexpr (C::kQuant) {
                     const int slot = sit % kSlots8;
-                    if (sit >= kSlots8 && !wait(kScEmpty + slot, sit / kSlots8 - 1))
+                    if (sit >= kSlots8 && !lazy_wait(kScEmpty + slot, sit / kSlots8 - 1))
                         break;
                     // untiled copies (a page's scales may be 64 bytes, less than a tiled
                     // copy's alignment), so zeros are written here
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
                     const int s = it % kRing;
-                    if (it >= kRing && !wait(kEmpty + s, it / kRing - 1))
+                    if (it >= kRing && !lazy_wait(kEmpty + s, it / kRing - 1))
                         break;
                     if (lane == 0)
                         ptx::mbar_arrive_expect_tx(bars + kFull + s, C::kQuant ? C::kRaw : C::kTile);
@@ -241,16 +251,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (C::kQuant)
             for (uint32_t k = sit > kSlots8 ? sit - kSlots8 : 0; k < sit; ++k)
                 ptx::mbar_wait(bars + kScFull + k % kSlots8, (k / kSlots8) & 1, kWaitTimeoutNs);
-    } else if (warp == 13 || warp == 14) {
-        ptx::setmaxnreg_dec<88>();
+    } else if (warp == C::kIssuer || warp == C::kIssuer + 1) {
+        ptx::setmaxnreg_dec<C::kOtherRegs>();
         // ------------------------------------------------------------ MMA issuers
-        // One warp per stream: an issuer's waits and releases take about as long as
-        // its products.  They issue in turn, a stream's P V and next scores as one, so
-        // that the streams stay half a tile apart and one's exponentials run beside
-        // the other's products.  The second issuer goes through the tiles also where
-        // it has no rows: what both read is released by both.
-        const int st = warp - 13;
-        constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, kTileKeys, 0, 0);
+        // One warp per stream.  A key tile goes in halves of 64 keys with scores of
+        // their own, so that the tensor cores have one half's products while the
+        // other half's scores are exponentiated.  The second issuer goes through
+        // the tiles also where it has no rows: what both read is released by both.
+        const int st = warp - C::kIssuer;
+        constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, kTileKeys / 2, 0, 0);
         constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, kDim, 0, 1);
         const uint64_t desc_q = ptx::sdesc_sw128(ptx::smem_u32(sQ + st * C::kTile), 16, 1024);
         const uint64_t desc_k = ptx::sdesc_sw128(ptx::smem_u32(sKv), 16, 1024);
@@ -258,29 +267,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t col_s = tmem + st * 128, col_o = tmem + C::kColO + st * kDim;
         // the ring's position: tiles come as K0 V0 K1 V1 ...
         int s = 0, slot = 0;
-        uint32_t phase = 0, q_phase = 0, f_phase = 0, p_phase = 0, turn = 0;
+        uint32_t phase = 0, q_phase = 0, f_phase = 0, p_phase = 0;
         auto advance = [&] {
             if (++s == C::kStages) {
                 s = 0;
                 phase ^= 1;
             }
         };
-        // (rolled loops here and below: short code stays fetched)
-        auto scores = [&](int stage, bool pass) {
-            uint64_t a = desc_q, b = ptx::sdesc_add(desc_k, stage * C::kTile);
-#pragma unroll 1
-            for (int k = 0; k < C::kBlocks; ++k) {
-                // the other's turn while the last four are under way
-                if (pass && k == C::kBlocks - 1)
-                    ptx::elect_arrive(bars + kTurn + (st ^ 1));
+        auto scores = [&](int stage, int half) {
+            const uint64_t b = ptx::sdesc_add(desc_k, stage * C::kTile + half * (kBlk / 2));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ptx::elect_mma_ss(col_s, ptx::sdesc_add(a, i * 32), ptx::sdesc_add(b, i * 32), id_s,
-                                      k + i != 0);
-                a = ptx::sdesc_add(a, kBlk);
-                b = ptx::sdesc_add(b, kBlk);
-            }
-            ptx::elect_commit(bars + kSFull + st);
+            for (int k = 0; k < kDim / 16; ++k)
+                ptx::elect_mma_ss(col_s + half * 64, ptx::sdesc_add(desc_q, (k / 4) * kBlk + (k % 4) * 32),
+                                  ptx::sdesc_add(b, (k / 4) * kBlk + (k % 4) * 32), id_s, k != 0);
+            ptx::elect_commit(bars + kSFull + st * 2 + half);
         };
         for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
             const bool mine = __shfl_sync(0xffffffffu, static_cast<int>(streams(w.e) > st), 0) != 0;
@@ -289,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             q_phase ^= 1;
             ptx::tc_fence_after_sync();
-            if (mine)
-                scores(s, false);
+            if (mine) {
+                scores(s, 0);
+                scores(s, 1);
+            }
             ptx::elect_commit(bars + kKvEmpty + s);
             if (n == 1)
                 ptx::elect_commit(bars + kQEmpty);
@@ -316,42 +318,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     advance();
                 }
-                // P V as the probabilities come, then the next scores in their place
-                if (mine && !wait(kPHalf + st, p_phase))
-                    break;
-                if (!wait(kTurn + st, turn))
-                    break;
-                turn ^= 1;
                 if (mine) {
-                    // all of P is there when products bound the loop; else half by half
-                    const uint64_t b = ptx::sdesc_add(desc_v, vs * C::kTile);
-                    const bool full = __all_sync(
-                        0xffffffffu, ptx::mbar_test(ptx::smem_u32(bars + kPFull + st), p_phase));
 #pragma unroll 1
-                    for (int i = 0; i < kTileKeys / 16; i += 4) {
-                        if (i == kTileKeys / 32 && !full) {
-                            ptx::elect_commit(bars + kHalfDone + st);
-                            if (!wait(kPFull + st, p_phase))
-                                break;
-                        }
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        // P V, then the next tile's scores in P's place
+                        wait(kPFull + st * 2 + half, p_phase);
                         ptx::tc_fence_after_sync();
+                        const uint64_t b = ptx::sdesc_add(desc_v, vs * C::kTile + half * (kBlk / 2));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::elect_mma_ts(col_o, col_s + (i + k) * 8, ptx::sdesc_add(b, (i + k) * 2048),
-                                              id_o, t + i + k != 0);
+                        for (int k = 0; k < kTileKeys / 32; ++k)
+                            ptx::elect_mma_ts(col_o, col_s + half * 64 + k * 8, ptx::sdesc_add(b, k * 2048),
+                                              id_o, t + half + k != 0);
+                        ptx::elect_commit(bars + kPvDone + st * 2 + half);
+                        if (more)
+                            scores(ks, half);
                     }
                     if (!ok)
                         break;
-                    if (full)
-                        ptx::elect_commit(bars + kHalfDone + st);
                     p_phase ^= 1;
-                    if (more)
-                        scores(ks, true);
-                    else
+                    if (!more)
                         ptx::elect_commit(bars + kOFull + st);
                 }
-                if (!mine || !more)
-                    ptx::elect_arrive(bars + kTurn + (st ^ 1));
                 if constexpr (C::kQuant) {      // the stream has read the scales
                     ptx::elect_arrive(bars + kScEmpty + slot);
                     slot = slot + 1 == kSlots8 ? 0 : slot + 1;
@@ -368,11 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every MMA issued must finish before tensor memory is released
         ptx::elect_commit(bars + kDrain + st);
         ptx::mbar_wait(bars + kDrain + st, 0, kWaitTimeoutNs);
-    } else if (warp == 15) {
-        ptx::setmaxnreg_dec<88>();
+    } else if (warp == C::kIssuer + 2) {
+        ptx::setmaxnreg_dec<C::kOtherRegs>();
     } else if (warp >= 8) {
-        ptx::setmaxnreg_dec<88>();
-        const int ht = tid - 256;              // 0..127
+        ptx::setmaxnreg_dec<C::kOtherRegs>();
+        const int ht = tid - 256;
         if constexpr (!C::kQuant) {
             // -------------------------------------------------------- V cleaner
             // A key tile that some row may not see all of: rows past the last
@@ -385,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = w.ta; t < w.tb && ok; ++t, it += 2) {
                     if (!partial(w.e, t, 0, w.e.tokens - 1))
                         continue;
-                    if (!wait(kFixReq, fit++))
+                    if (!lazy_wait(kFixReq, fit++))
                         break;
                     uint8_t *v = sKv + ((it + 1) % C::kStages) * C::kTile;
                     const int keys = w.e.kv_len - (w.e.tile0 + t) * kTileKeys;
@@ -423,7 +410,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
             // -------------------------------------------------------- converter
-            constexpr int kUnits = kDim / 16;  // 16-code pieces of a row
+            // a thread has one 16-code piece of every kRows-th row: rows alike mod 8, so
+            // that its places in the swizzled tile are the same distance apart
+            constexpr int kUnits = kDim / 16, kRows = C::kHelpers * 32 / kUnits;
+            static_assert(kRows % 8 == 0 && kTileKeys % kRows == 0, "rows of a thread");
+            const int row0 = ht / kUnits, c = ht % kUnits;
+            const int f = (c >> 2) & 1, c16 = (c & 3) * 2;
+            const uint32_t from = row0 * kDim + c * 16;
+            // pieces of the second block write their halves in the other order: eight
+            // lanes then meet all eight 16-byte banks
+            const uint32_t line = (c >> 2) * kBlk + row0 * 128;
+            const uint32_t to0 = line + (((c16 + f) ^ (row0 & 7)) << 4);
+            const uint32_t to1 = line + (((c16 + 1 - f) ^ (row0 & 7)) << 4);
             uint32_t it = 0, sit = 0;
             for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next())
                 for (int t = w.ta; t < w.tb && ok; ++t)
@@ -438,41 +436,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kv == 0 && !wait(kScFull + sit % kSlots8, sit / kSlots8))
                             break;
                         sit += kv;
-                        const uint8_t *src = sRaw + rs * C::kRaw;
+                        const uint8_t *src = sRaw + rs * C::kRaw + from;
                         uint8_t *dst = sKv + s * C::kTile;
-#pragma unroll 4
-                        for (int i = ht; i < kTileKeys * kUnits; i += 128) {
-                            const int row = i / kUnits, c = i % kUnits;
-                            uint4 x = *reinterpret_cast<const uint4 *>(src + i * 16);
-                            if (row >= keys)
-                                x = make_uint4(0, 0, 0, 0);
+                        uint4 x[kTileKeys / kRows];
+#pragma unroll
+                        for (int k = 0; k < kTileKeys / kRows; ++k)
+                            x[k] = *reinterpret_cast<const uint4 *>(src + k * kRows * kDim);
+                        if (keys < kTileKeys) {
+#pragma unroll
+                            for (int k = 0; k < kTileKeys / kRows; ++k)
+                                if (row0 + k * kRows >= keys)
+                                    x[k] = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int k = 0; k < kTileKeys / kRows; ++k) {
                             uint32_t o[8];
-                            widen4<kType>(x.x, o);
-                            widen4<kType>(x.y, o + 2);
-                            widen4<kType>(x.z, o + 4);
-                            widen4<kType>(x.w, o + 6);
-                            if (kv == 0 && c == 0) {
-                                // the row's scales: a row that is not finite gets them finite
-                                // and a NaN among its codes, so that scores hidden from a
-                                // query stay hidden, and one past the last key any
+                            widen4<kType>(x[k].x, o);
+                            widen4<kType>(x[k].y, o + 2);
+                            widen4<kType>(x[k].z, o + 4);
+                            widen4<kType>(x[k].w, o + 6);
+                            *reinterpret_cast<uint4 *>(dst + to0 + k * kRows * 128) =
+                                f ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + to1 + k * kRows * 128) =
+                                f ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                        if (kv == 0 && c == 0) {
+                            // the rows' scales: a row that is not finite gets them finite and
+                            // a NaN among its codes, so that scores hidden from a query stay
+                            // hidden, and one past the last key any
+#pragma unroll 1
+                            for (int row = row0; row < kTileKeys; row += kRows) {
                                 const float ks = scale[row], vs = scale[kTileKeys + row];
                                 const bool bad = !(fabsf(ks) <= 3.4e38f && fabsf(vs) <= 3.4e38f);
                                 if (bad || row >= keys) {
                                     scale[row] = 1.f;
                                     scale[kTileKeys + row] = 0.f;
                                     if (row < keys)
-                                        o[0] = 0x7fff7fffu;
+                                        *reinterpret_cast<uint32_t *>(dst + to0 + (row - row0) * 128) =
+                                            0x7fff7fffu;
                                 }
                             }
-                            uint8_t *line = dst + (c >> 2) * kBlk + row * 128;
-                            const int c16 = (c & 3) * 2;
-                            // pieces of the second block write their halves in the other
-                            // order: eight lanes then meet all eight 16-byte banks
-                            const int f = c >> 2;
-                            *reinterpret_cast<uint4 *>(line + (((c16 + f) ^ (row & 7)) << 4)) =
-                                f ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(line + (((c16 + 1 - f) ^ (row & 7)) << 4)) =
-                                f ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         ptx::fence_proxy_async_smem();
                         ptx::mbar_arrive(bars + kRawEmpty + rs);
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
         }
     } else {
-        ptx::setmaxnreg_inc<168>();
+        ptx::setmaxnreg_inc<C::kSoftmaxRegs>();
         // ------------------------------------------------------------ softmax
         const int st = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -499,168 +502,159 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = w.e.pos0 + tok0 + (mine ? my_tok : ntok - 1);
             const int hi = pos + 1;
             const int lo = p.window > 0 ? pos - p.window + 1 : INT32_MIN / 2;
-            float m = -INFINITY;      // reference, times c
+            // reference, times c (a row that is none has one, and asks for no other)
+            float m = mine ? -INFINITY : 0.f;
             float l = 0.f;
             for (int t = w.ta; t < w.tb && ok; ++t, ++it, ++sit) {
-                if (!wait(kSFull + st, it))
-                    break;
                 // (the converter has seen the scales land)
                 const float *sc = sScale + (sit % kSlots8) * 2 * kTileKeys;
-                ptx::tc_fence_after_sync();
                 const bool hides = partial(w.e, t, tok0, tok0 + ntok - 1);
-                const int k0 = (w.e.tile0 + t) * kTileKeys;
-                if (hides || p.negate) {
-                    // hidden keys and a negative softmax_scale, in a pass of its own that
-                    // keeps the usual one short
 #pragma unroll 1
-                    for (int col = 0; col < kTileKeys; col += 16) {
-                        uint32_t s[16];
-                        __syncwarp();
-                        ptx::tmem_ld16_nowait(colS + col, s);
-                        ptx::tmem_wait_ld();
-                        const int a = hides ? lo - k0 - col : 0, b = hides ? hi - k0 - col : 16;
+                for (int half = 0; half < 2; ++half, sc += 64) {
+                    const uint32_t col = colS + half * 64;
+                    if (!wait(kSFull + st * 2 + half, it))
+                        break;
+                    ptx::tc_fence_after_sync();
+                    if (hides || p.negate) {
+                        // hidden keys and a negative softmax_scale, in a pass of its own
+                        // that keeps the usual one short
+                        const int k0 = (w.e.tile0 + t) * kTileKeys + half * 64;
+#pragma unroll 1
+                        for (int k = 0; k < 64; k += 16) {
+                            uint32_t s[16];
+                            ptx::tmem_ld16_nowait(col + k, s);
+                            ptx::tmem_wait_ld();
+                            const int a = hides ? lo - k0 - k : 0, b = hides ? hi - k0 - k : 16;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const uint32_t v = p.negate ? s[k] ^ 0x80000000u : s[k];
-                            s[k] = k < a || k >= b ? 0xff800000u : v;
+                            for (int i = 0; i < 16; ++i) {
+                                const uint32_t v = p.negate ? s[i] ^ 0x80000000u : s[i];
+                                s[i] = i < a || i >= b ? 0xff800000u : v;
+                            }
+                            ptx::tmem_st16(col + k, s);
                         }
-                        ptx::tmem_st16(colS + col, s);
+                        ptx::tmem_wait_st();
                     }
-                    ptx::tmem_wait_st();
-                }
-                auto prepare = [&](auto &s, int col) {     // scores from column col on: K's scales
-                    if constexpr (C::kQuant) {
+                    auto prepare = [&](auto &s, int k0) {      // K's scales
+                        if constexpr (C::kQuant) {
+#pragma unroll
+                            for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(sc + k0 + k);
+                                s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
+                                s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
+                                s[k + 2] = __float_as_uint(__uint_as_float(s[k + 2]) * f.z);
+                                s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
+                            }
+                        }
+                    };
+                    uint64_t acc0, acc1;       // sums of probabilities
+                    auto probabilities = [&](const auto &s, int k0, uint32_t *pk) {
+                        const float me = m == -INFINITY ? 0.f : m;
+                        const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
 #pragma unroll
                         for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sc + col + k);
-                            s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
-                            s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
-                            s[k + 2] = __float_as_uint(__uint_as_float(s[k + 2]) * f.z);
-                            s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
+                            float e0, e1, e2, e3;
+                            ptx::unpack2(
+                                ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c22, nm),
+                                e0, e1);
+                            ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]),
+                                                              __uint_as_float(s[k + 3])), c22, nm),
+                                         e2, e3);
+                            e0 = ptx::ex2(e0);
+                            e1 = ptx::ex2(e1);
+                            e2 = ptx::ex2(e2);
+                            e3 = ptx::ex2(e3);
+                            acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
+                            acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
+                            if constexpr (C::kQuant) {
+                                const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + k0 + k);
+                                e0 *= f.x;
+                                e1 *= f.y;
+                                e2 *= f.z;
+                                e3 *= f.w;
+                            }
+                            pk[k / 2] = pack_bf16(e0, e1);
+                            pk[k / 2 + 1] = pack_bf16(e2, e3);
                         }
-                    }
-                };
-                float x0, x1;
-                auto maximum = [&](const auto &s) {
+                    };
+                    // ---- the rare parts, 16 scores at a time ----
+                    auto maximum = [&] {
+                        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll 1
+                        for (int k0 = 0; k0 < 64; k0 += 16) {
+                            uint32_t s[16];
+                            ptx::tmem_ld16_nowait(col + k0, s);
+                            ptx::tmem_wait_ld();
+                            prepare(s, k0);
 #pragma unroll
-                    for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
-                        x0 = max3(x0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                        x1 = max3(x1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-                    }
-                };
-                uint64_t acc0, acc1;           // sums of probabilities
-                auto probabilities = [&](const auto &s, int col, uint32_t *pk) {
-                    const float me = m == -INFINITY ? 0.f : m;
-                    const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
-#pragma unroll
-                    for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
-                        float e0, e1, e2, e3;
-                        ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
-                                               c22, nm), e0, e1);
-                        ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
-                                               c22, nm), e2, e3);
-                        e0 = ptx::ex2(e0);
-                        e1 = ptx::ex2(e1);
-                        e2 = ptx::ex2(e2);
-                        e3 = ptx::ex2(e3);
-                        acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
-                        acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
-                        if constexpr (C::kQuant) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + col + k);
-                            e0 *= f.x;
-                            e1 *= f.y;
-                            e2 *= f.z;
-                            e3 *= f.w;
+                            for (int k = 0; k < 16; k += 4) {
+                                x0 = max3(x0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                                x1 = max3(x1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                            }
                         }
-                        pk[k / 2] = pack_bf16(e0, e1);
-                        pk[k / 2 + 1] = pack_bf16(e2, e3);
+                        return fmaxf(x0, x1) * c2;
+                    };
+                    // rows that have seen no key take the half's maximum as reference (a
+                    // row's first keys; O and l are zero)
+                    if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                        const float mx = maximum();
+                        m = m == -INFINITY ? mx : m;
                     }
-                };
-                // ---- the rare parts, 16 scores at a time ----
-                auto row_maximum = [&] {
-                    x0 = x1 = -INFINITY;
-#pragma unroll 1
-                    for (int col = 0; col < kTileKeys; col += 16) {
-                        uint32_t s[16];
-                        __syncwarp();
-                        ptx::tmem_ld16_nowait(colS + col, s);
-                        ptx::tmem_wait_ld();
-                        prepare(s, col);
-                        maximum(s);
-                    }
-                    return fmaxf(x0, x1) * c2;
-                };
-                // the rows of the warp take new references, at least `mx`
-                auto rescale = [&](float mx) {
-                    const float mn = fmaxf(m, mx);
-                    const float f = mn == m ? 1.f : ptx::ex2(m - mn);
-                    m = mn;
-                    l *= f;
-#pragma unroll 1
-                    for (int k = 0; k < kDim; k += 16) {
-                        float o[16];
-                        uint32_t r[16];
-                        __syncwarp();
-                        ptx::tmem_ld16(colO + k, o);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            r[i] = __float_as_uint(o[i] * f);
-                        ptx::tmem_st16(colO + k, r);
-                    }
-                };
-                auto again = [&](int first) {   // 64 probabilities with the new reference
-                    acc0 = acc1 = ptx::pack2(0.f, 0.f);
-#pragma unroll 1
-                    for (int col = first; col < first + 64; col += 16) {
-                        uint32_t s[16], pk[8];
-                        __syncwarp();
-                        ptx::tmem_ld16_nowait(colS + col, s);
-                        ptx::tmem_wait_ld();
-                        prepare(s, col);
-                        probabilities(s, col, pk);
-                        ptx::tmem_st8(colS + col / 2, pk);
-                    }
-                };
-                if (t == w.ta)
-                    m = row_maximum();
-                // Half of the row at a time, with the reference as it is; where a score
-                // turns out to be far above it, again with a new one.  The second half
-                // then has to wait for the first half's product, which is under way.
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
                     uint32_t a[32], b[32], pk[32];
-                    ptx::tmem_ld32_nowait(colS + half * 64, a);
-                    ptx::tmem_ld32_nowait(colS + half * 64 + 32, b);
+                    ptx::tmem_ld32_nowait(col, a);
+                    ptx::tmem_ld32_nowait(col + 32, b);
                     ptx::tmem_wait_ld();
-                    x0 = x1 = -INFINITY;
                     acc0 = acc1 = ptx::pack2(0.f, 0.f);
-                    prepare(a, half * 64);
-                    probabilities(a, half * 64, pk);
-                    maximum(a);
-                    prepare(b, half * 64 + 32);
-                    probabilities(b, half * 64 + 32, pk + 16);
-                    maximum(b);
-                    if (__any_sync(0xffffffffu, fmaxf(x0, x1) * c2 > m + kRescaleLog2)) {
-                        if (half == 0) {
-                            rescale(row_maximum());
-                            again(0);
-                        } else if (wait(kHalfDone + st, it)) {
-                            rescale(fmaxf(x0, x1) * c2);
-                            again(64);
+                    prepare(a, 0);
+                    probabilities(a, 0, pk);
+                    prepare(b, 32);
+                    probabilities(b, 32, pk + 16);
+                    float a0, a1;
+                    ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
+                    if (__any_sync(0xffffffffu, mine && !(a0 + a1 <= kRescale))) {
+                        // scores far above the reference: once the product under way is
+                        // done, the rows of the warp take new ones
+                        if ((half || t > w.ta) &&
+                            !wait(kPvDone + st * 2 + (half ^ 1), half ? it : it - 1))
+                            break;
+                        ptx::tc_fence_after_sync();
+                        const float mn = fmaxf(m, maximum());
+                        const float f = mn == m ? 1.f : ptx::ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (half || t > w.ta) {
+#pragma unroll 1
+                            for (int k = 0; k < kDim; k += 16) {
+                                float o[16];
+                                uint32_t r[16];
+                                ptx::tmem_ld16(colO + k, o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    r[i] = __float_as_uint(o[i] * f);
+                                ptx::tmem_st16(colO + k, r);
+                            }
                         }
+                        acc0 = acc1 = ptx::pack2(0.f, 0.f);
+#pragma unroll 1
+                        for (int k0 = 0; k0 < 64; k0 += 16) {
+                            uint32_t s[16], pk16[8];
+                            ptx::tmem_ld16_nowait(col + k0, s);
+                            ptx::tmem_wait_ld();
+                            prepare(s, k0);
+                            probabilities(s, k0, pk16);
+                            ptx::tmem_st8(col + k0 / 2, pk16);
+                        }
+                        ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
                     } else {
                         // (in the place of scores already read)
-                        ptx::tmem_st16(colS + half * 32, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
-                        ptx::tmem_st16(colS + half * 32 + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
+                        ptx::tmem_st16(col, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
+                        ptx::tmem_st16(col + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
                     }
+                    l += a0 + a1;
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0)
-                        ptx::mbar_arrive(bars + (half ? kPFull : kPHalf) + st);
-                    float a0, a1;
-                    ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
-                    l += a0 + a1;
+                        ptx::mbar_arrive(bars + kPFull + st * 2 + half);
                 }
             }
             if (!ok || !wait(kOFull + st, oit++))
@@ -736,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (tid == 0 && *s_abort)
         kv_error(p.c, SSD_DEVERR_TIMEOUT);
-    if (warp == 13) {
+    if (warp == C::kIssuer) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }
@@ -753,17 +747,17 @@ cudaError_t launch_one(const AttnParams &p, const AttnMaps &m, cudaStream_t stre
     cudaError_t e = ensure_max_smem(fn, opted);
     if (e != cudaSuccess)
         return e;
-    // the register split inside the kernel adds up to 128 registers a thread: with
-    // fewer at launch it would wait forever, so such a build is refused
+    // with fewer registers at launch the split inside the kernel would wait forever:
+    // such a build is refused
     static const bool regs_ok = [fn] {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, fn) == cudaSuccess && a.numRegs == 128;
+        return cudaFuncGetAttributes(&a, fn) == cudaSuccess && a.numRegs == C::kLaunchRegs;
     }();
     if (!regs_ok)
         return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kAttnCtas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
