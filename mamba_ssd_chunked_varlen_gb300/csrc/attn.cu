@@ -14,7 +14,8 @@ namespace {
 // One CTA cuts the call into units (AttnUnit), in the order of the rows, and
 // counts their key tiles.
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanBatch = 4096;    // up to so many sequences, their first units stay on chip
+constexpr int kPlanBatch = 4096;    // up to so many sequences, their first units stay on chip,
+constexpr int kPlanUnits = 1024;    // and so many units of a kind, their first tiles
 
 // Inclusive sums of kN values over the CTA's threads; `total` gets the sums of all.
 template <int kN>
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 {
     __shared__ int64_t scratch[4][32];
     __shared__ int32_t s_units[kPlanBatch];
+    __shared__ int64_t s_cum[2][kPlanUnits];
     const KvView &c = p.c;
     const int tid = threadIdx.x;
     const int unit_tokens = 2 * p.tile_tokens;
@@ -73,9 +75,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     if (bad) {
         if (tid < 2) {
             p.hdr->total[tid] = 0;
-            p.hdr->count[tid] = 0;
             p.hdr->splits[tid][0] = p.hdr->splits[tid][1] = 0;
         }
+        for (int k = 0; k < 2; ++k)
+            for (int i = tid; i < attn_max_pieces(k); i += kPlanThreads)
+                const_cast<AttnPiece *>(p.line[k].pieces)[i] = AttnPiece{};
         if (tid == 0)
             kv_error(c, SSD_DEVERR_BAD_QUERY_START_LOC);
         return;
@@ -119,7 +123,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         if (u < units) {
             const int64_t at = count[kind] + (kind ? v[3] : v[1]) - 1;
             const_cast<AttnUnit *>(p.line[kind].units)[at] = e;
-            const_cast<int64_t *>(p.line[kind].cum)[at] = tiles[kind] + (kind ? v[2] : v[0]) - e.tiles;
+            const int64_t before = tiles[kind] + (kind ? v[2] : v[0]) - e.tiles;
+            p.line[kind].cum[at] = before;
+            if (at < kPlanUnits)
+                s_cum[kind][at] = before;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -128,10 +135,38 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         }
     }
     if (tid < 2) {
-        const_cast<int64_t *>(p.line[tid].cum)[count[tid]] = tiles[tid];
         p.hdr->total[tid] = tiles[tid] * c.heads;
-        p.hdr->count[tid] = static_cast<int32_t>(count[tid]);
         p.hdr->splits[tid][0] = p.hdr->splits[tid][1] = 0;
+    }
+    __syncthreads();
+    // where every piece begins
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int64_t total = tiles[k] * c.heads;
+        const int pieces = attn_pieces(k, total);
+        const int64_t *cum = count[k] <= kPlanUnits ? s_cum[k] : p.line[k].cum;
+        for (int i = tid; i < attn_max_pieces(k); i += kPlanThreads) {
+            AttnPiece pc = {};
+            if (i < pieces) {
+                pc.pos = attn_piece_begin(total, pieces, i);
+                pc.end = attn_piece_begin(total, pieces, i + 1);
+                int lo = 0, hi = static_cast<int>(count[k]) - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) / 2;
+                    if (cum[mid] * c.heads <= pc.pos)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                const int64_t r = pc.pos - cum[lo] * c.heads;
+                const int n = p.line[k].units[lo].tiles;
+                pc.u = lo;
+                // (tiles and heads are below 2^23 and 2^16)
+                pc.h = r >> 31 ? static_cast<int32_t>(r / n) : static_cast<int32_t>(r) / n;
+                pc.ta = static_cast<int32_t>(r - static_cast<int64_t>(pc.h) * n);
+            }
+            const_cast<AttnPiece *>(p.line[k].pieces)[i] = pc;
+        }
     }
 }
 
@@ -476,9 +511,9 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     p.seq_units = reinterpret_cast<int32_t *>(ws + L.seq_units);
     for (int k = 0; k < 2; ++k)
         p.line[k] = AttnLine{reinterpret_cast<AttnUnit *>(ws + L.units[k]),
-                             reinterpret_cast<int64_t *>(ws + L.cum[k]),
+                             reinterpret_cast<AttnPiece *>(ws + L.pieces[k]),
                              p.hdr->total + k,
-                             p.hdr->count + k,
+                             reinterpret_cast<int64_t *>(ws + L.cum[k]),
                              reinterpret_cast<float *>(ws + L.part_o[k]),
                              reinterpret_cast<float2 *>(ws + L.part_ml[k]),
                              reinterpret_cast<int4 *>(ws + L.split[k]),

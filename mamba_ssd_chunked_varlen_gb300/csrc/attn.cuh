@@ -34,11 +34,17 @@ static_assert(sizeof(AttnUnit) == 32, "unit size");
 // by head, form a line that is cut into equal pieces: a piece per CTA (kind 0), or
 // per warp (kind 1; fewer pieces when the line is short).  A pair that falls
 // into several pieces leaves partial results, at most two per piece.
+struct alignas(32) AttnPiece {
+    int64_t pos, end;             // its tiles of the line: [pos, end), none past the last piece
+    int32_t u, h, ta;             // unit, kv head and tile of the unit where it begins
+    int32_t pad;
+};
+
 struct AttnLine {
     const AttnUnit *units;
-    const int64_t *cum;           // (count + 1): key tiles before each unit, one head
+    const AttnPiece *pieces;
     const int64_t *total;         // key tiles of all units and kv heads
-    const int32_t *count;
+    int64_t *cum;                 // (units): key tiles before each unit, one head (the plan's)
     float *part_o;                // [2 pieces][rows][dim]: sums of p v
     float2 *part_ml;              // [2 pieces][rows]: reference (log2), sum of p
     int4 *split;                  // [pieces] the pairs with partial results, in any order:
@@ -64,9 +70,8 @@ constexpr int kJoinWide = 128;    // pieces of a row that one warp of the join a
 
 struct AttnHeader {
     int64_t total[2];             // per kind: 0 tiles, 1 few rows
-    int32_t count[2];
     int32_t splits[2][2];
-    int32_t pad[54];
+    int32_t pad[56];
 };
 static_assert(sizeof(AttnHeader) == 256, "header size");
 
@@ -91,7 +96,7 @@ struct AttnParams {
 __host__ __device__ constexpr int attn_part_rows(int kind) { return kind ? kFewRows : 2 * kTileRows; }
 
 struct AttnLayout {
-    size_t header, seq_units, units[2], cum[2], split[2], part_ml[2], part_o[2], total;
+    size_t header, seq_units, units[2], pieces[2], cum[2], split[2], part_ml[2], part_o[2], total;
 };
 
 inline int64_t attn_max_units(int64_t total_len, int32_t batch, int32_t group)
@@ -115,7 +120,8 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
     for (int k = 0; k < 2; ++k) {
         const size_t rows = 2 * static_cast<size_t>(attn_max_pieces(k)) * attn_part_rows(k);
         L.units[k] = take(sizeof(AttnUnit) * units);
-        L.cum[k] = take(sizeof(int64_t) * (units + 1));
+        L.pieces[k] = take(sizeof(AttnPiece) * static_cast<size_t>(attn_max_pieces(k)));
+        L.cum[k] = take(sizeof(int64_t) * units);
         L.split[k] = take(sizeof(int4) * static_cast<size_t>(attn_max_pieces(k)));
         L.part_ml[k] = take(sizeof(float2) * rows);
         L.part_o[k] = take(sizeof(float) * rows * static_cast<size_t>(dim));
@@ -124,15 +130,16 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
     return L;
 }
 
-// First tile of piece i of a line of `total` tiles in n pieces, and the piece of
-// tile t.
-__host__ __device__ inline int64_t attn_piece_begin(int64_t total, int n, int64_t i)
+// First tile of piece i of a line of `total` tiles in n pieces, floor(total i / n),
+// and the piece of tile t.
+__host__ __device__ inline int64_t attn_piece_begin(int64_t total, int n, int i)
 {
-    return total * i / n;
+    const int64_t q = total / n;
+    return q * i + static_cast<int>(total - q * n) * i / n;
 }
-__host__ __device__ inline int64_t attn_piece_of(int64_t total, int n, int64_t t)
+__host__ __device__ inline int attn_piece_of(int64_t total, int n, int64_t t)
 {
-    return ((t + 1) * n + total - 1) / total - 1;
+    return static_cast<int>(((t + 1) * n + total - 1) / total - 1);
 }
 
 // Partial-result slot of a piece: its first segment (one that does not start
@@ -142,70 +149,52 @@ __device__ __forceinline__ int attn_slot(int64_t piece, bool starts)
     return static_cast<int>(2 * piece + (starts ? 1 : 0));
 }
 
-// A piece of a line, segment by segment: a segment is the part of one
-// (unit, kv head) pair that lies in the piece.  Constructed by whole warps.
+// A piece of a line, segment by segment: a segment is the part of one (unit, kv
+// head) pair that lies in the piece.
 struct AttnWalk {
     const AttnLine &line;
     int32_t heads;
-    int64_t pos, end;
+    int32_t left;             // tiles of the piece from the segment's first on
     int32_t u, h, ta, tb;     // unit, kv head, tiles [ta, tb) of the unit's
     AttnUnit e;
 
-    __device__ __forceinline__ AttnWalk(const AttnLine &l, int32_t heads_, int kind, int piece)
+    __device__ __forceinline__ AttnWalk(const AttnLine &l, int32_t heads_, int piece)
         : line(l), heads(heads_)
     {
-        const int64_t total = *line.total;
-        const int n_pieces = attn_pieces(kind, total);
-        pos = piece < n_pieces ? attn_piece_begin(total, n_pieces, piece) : 0;
-        end = piece < n_pieces ? attn_piece_begin(total, n_pieces, piece + 1) : 0;
-        u = h = ta = tb = 0;
-        if (pos >= end)
-            return;
-        // the last unit whose tiles begin at or before pos, 32 probes at a time
-        const int lane = threadIdx.x & 31;
-        int n = *line.count;
-        while (n > 1) {
-            const int step = (n + 31) / 32, at = lane * step;
-            const bool below = at < n && line.cum[u + at] * heads <= pos;
-            const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
-            u += k * step;
-            n = min(step, n - k * step);
+        const AttnPiece pc = line.pieces[piece];
+        left = static_cast<int32_t>(pc.end - pc.pos);
+        u = pc.u;
+        h = pc.h;
+        ta = pc.ta;
+        tb = ta;
+        if (left > 0) {
+            e = line.units[u];
+            tb = min(ta + left, e.tiles);
         }
-        e = line.units[u];
-        const int64_t r = pos - line.cum[u] * heads;
-        h = static_cast<int32_t>(r / e.tiles);
-        ta = static_cast<int32_t>(r - static_cast<int64_t>(h) * e.tiles);
-        set();
     }
-    __device__ __forceinline__ void set()
-    {
-        const int64_t left = end - pos;
-        tb = left < e.tiles - ta ? ta + static_cast<int32_t>(left) : e.tiles;
-    }
-    __device__ __forceinline__ bool more() const { return pos < end; }
+    __device__ __forceinline__ bool more() const { return left > 0; }
     // Lists the pair of a segment that begins it and does not end it; by one lane.
     __device__ __forceinline__ void note_split(int kind, int piece) const
     {
         if (ta != 0 || tb == e.tiles)
             return;
-        const int64_t total = *line.total;
-        const int last =
-            static_cast<int>(attn_piece_of(total, attn_pieces(kind, total), pos + e.tiles - 1));
+        const int64_t total = *line.total, pos = line.pieces[piece].end - left;
+        const int last = attn_piece_of(total, attn_pieces(kind, total), pos + e.tiles - 1);
         line.split[atomicAdd(line.splits, 1)] = make_int4(e.row0, e.tokens + (h << 9), piece, last);
         if (last - piece >= kJoinWide)
             atomicAdd(line.splits + 1, 1);
     }
     __device__ __forceinline__ void next()
     {
-        pos += tb - ta;
-        if (pos >= end)
+        left -= tb - ta;
+        if (left <= 0)
             return;
         ta = 0;
         if (++h == heads) {
             h = 0;
             e = line.units[++u];
         }
-        set();
+        tb = min(left, e.tiles);
     }
     // whether the segment begins its pair, and is all of it
     __device__ __forceinline__ bool starts() const { return ta == 0; }

@@ -88,7 +88,7 @@ struct FewLoad {
     uint32_t k_off, v_off;       // this lane's first piece in a tile of K and of V
 
     __device__ __forceinline__ FewLoad(const AttnParams &p_, int piece, uint32_t ring)
-        : p(p_), w(p_.line[1], p_.c.heads, 1, piece), dst0(ring), put(0), t(w.ta), ahead(32),
+        : p(p_), w(p_.line[1], p_.c.heads, piece), dst0(ring), put(0), t(w.ta), ahead(32),
           my_page(-1), v_next(false), there(false), row(0)
     {
         const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;

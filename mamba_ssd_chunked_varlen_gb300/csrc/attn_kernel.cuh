@@ -98,6 +98,32 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+// Adds to 32 columns from d of a row's sums the infinities and NaN that were taken
+// out of V: those of the keys in [lo, hi) of tiles [ta, tb) that some row of the
+// unit does not see all of.
+template <int kDim>
+__device__ __noinline__ void add_nonfinite(const AttnParams &p, const AttnUnit &e, int h, int ta, int tb,
+                                           int hi, int lo, int d, float *acc)
+{
+    for (int t = ta; t < tb; ++t) {
+        const int k0 = (e.tile0 + t) * kTileKeys;
+        if (!attn_partial(e, p.window, k0, kTileKeys, 0, e.tokens - 1))
+            continue;
+        for (int j = max(k0, max(lo, 0)); j < min(k0 + kTileKeys, hi); ++j) {
+            const int64_t page = kv_page_of(p.c, e.seq, j);
+            if (page < 0)
+                continue;
+            const __nv_bfloat16 *v =
+                static_cast<const __nv_bfloat16 *>(p.c.v) + kv_row(p.c, page, h, j) * kDim + d;
+            for (int k = 0; k < 32; ++k) {
+                const float x = __bfloat162float(v[k]);
+                if (!(fabsf(x) <= 3.4e38f))
+                    acc[k] += x;
+            }
+        }
+    }
+}
+
 template <int kType, int kDim>
 __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
     attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p)
@@ -170,7 +196,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         constexpr int kFull = C::kQuant ? kRawFull : kKvFull, kEmpty = C::kQuant ? kRawEmpty : kKvEmpty;
         const int shift = p.c.page_shift;
         const int boxes = shift >= 7 ? 1 : kTileKeys >> shift;    // pages of a tile
-        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next(), ++qit) {
+        for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next(), ++qit) {
             const int ns = streams(w.e);
             if (lane == 0)
                 w.note_split(0, blockIdx.x);
@@ -282,7 +308,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                                   ptx::sdesc_add(b, (k / 4) * kBlk + (k % 4) * 32), id_s, k != 0);
             ptx::elect_commit(bars + kSFull + st * 2 + half);
         };
-        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
+        for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next()) {
             const bool mine = __shfl_sync(0xffffffffu, static_cast<int>(streams(w.e) > st), 0) != 0;
             const int n = __shfl_sync(0xffffffffu, w.tb - w.ta, 0);
             if (!wait(kQFull, q_phase) || !wait(kKvFull + s, phase))
@@ -368,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
             // would reach rows that do not see them; the output adds them
             // back for the rows that do.
             uint32_t it = 0, fit = 0;
-            for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
+            for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next()) {
                 for (int t = w.ta; t < w.tb && ok; ++t, it += 2) {
                     if (!partial(w.e, t, 0, w.e.tokens - 1))
                         continue;
@@ -423,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
             const uint32_t to0 = line + (((c16 + f) ^ (row0 & 7)) << 4);
             const uint32_t to1 = line + (((c16 + 1 - f) ^ (row0 & 7)) << 4);
             uint32_t it = 0, sit = 0;
-            for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next())
+            for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next())
                 for (int t = w.ta; t < w.tb && ok; ++t)
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
                         const int rs = it % C::kRawStages, s = it % C::kStages;
@@ -491,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         const int my_tok = row / g, my_head = row % g;
         const float c2 = p.scale_log2;
         uint32_t it = 0, sit = 0, oit = 0;
-        for (AttnWalk w(p.line[0], p.c.heads, 0, blockIdx.x); w.more() && ok; w.next()) {
+        for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next()) {
             if (streams(w.e) <= st) {
                 sit += w.tb - w.ta;
                 continue;
@@ -515,140 +541,114 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                     if (!wait(kSFull + st * 2 + half, it))
                         break;
                     ptx::tc_fence_after_sync();
-                    if (hides || p.negate) {
-                        // hidden keys and a negative softmax_scale, in a pass of its own
-                        // that keeps the usual one short
-                        const int k0 = (w.e.tile0 + t) * kTileKeys + half * 64;
+                    uint32_t a[32], b[32], pk[32];
+                    float a0, a1;
 #pragma unroll 1
-                        for (int k = 0; k < 64; k += 16) {
-                            uint32_t s[16];
-                            ptx::tmem_ld16_nowait(col + k, s);
-                            ptx::tmem_wait_ld();
-                            const int a = hides ? lo - k0 - k : 0, b = hides ? hi - k0 - k : 16;
+                    for (int pass = 0;; ++pass) {
+                        // ---- 64 scores: K's scales, sign, hidden keys ----
+                        ptx::tmem_ld32_nowait(col, a);
+                        ptx::tmem_ld32_nowait(col + 32, b);
+                        ptx::tmem_wait_ld();
+                        auto each = [&](auto f) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint32_t v = p.negate ? s[i] ^ 0x80000000u : s[i];
-                                s[i] = i < a || i >= b ? 0xff800000u : v;
-                            }
-                            ptx::tmem_st16(col + k, s);
-                        }
-                        ptx::tmem_wait_st();
-                    }
-                    auto prepare = [&](auto &s, int k0) {      // K's scales
+                            for (int k = 0; k < 32; ++k)
+                                a[k] = f(a[k], k);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                b[k] = f(b[k], 32 + k);
+                        };
                         if constexpr (C::kQuant) {
-#pragma unroll
-                            for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(sc + k0 + k);
-                                s[k] = __float_as_uint(__uint_as_float(s[k]) * f.x);
-                                s[k + 1] = __float_as_uint(__uint_as_float(s[k + 1]) * f.y);
-                                s[k + 2] = __float_as_uint(__uint_as_float(s[k + 2]) * f.z);
-                                s[k + 3] = __float_as_uint(__uint_as_float(s[k + 3]) * f.w);
-                            }
+                            float4 f;
+                            each([&](uint32_t v, int k) {
+                                if (k % 4 == 0)
+                                    f = *reinterpret_cast<const float4 *>(sc + k);
+                                return __float_as_uint(__uint_as_float(v) *
+                                                       (k % 4 == 0 ? f.x : k % 4 == 1 ? f.y : k % 4 == 2 ? f.z : f.w));
+                            });
                         }
-                    };
-                    uint64_t acc0, acc1;       // sums of probabilities
-                    auto probabilities = [&](const auto &s, int k0, uint32_t *pk) {
+                        if (p.negate)
+                            each([&](uint32_t v, int) { return v ^ 0x80000000u; });
+                        if (hides) {
+                            const int k0 = (w.e.tile0 + t) * kTileKeys + half * 64;
+                            const int from = lo - k0, to = hi - k0;
+                            each([&](uint32_t v, int k) { return k < from || k >= to ? 0xff800000u : v; });
+                        }
+                        auto maximum = [&] {
+                            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                x0 = max3(x0, __uint_as_float(a[k]), __uint_as_float(a[k + 1]));
+                                x1 = max3(x1, __uint_as_float(b[k]), __uint_as_float(b[k + 1]));
+                            }
+                            return fmaxf(x0, x1) * c2;
+                        };
+                        // rows that have seen no key take the half's maximum as reference
+                        // (O and l are zero)
+                        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                            const float mx = maximum();
+                            m = m == -INFINITY ? mx : m;
+                        }
+                        // ---- probabilities, and their sum ----
                         const float me = m == -INFINITY ? 0.f : m;
                         const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
+                        uint64_t acc0 = ptx::pack2(0.f, 0.f), acc1 = acc0;
+                        auto probabilities = [&](const uint32_t (&s)[32], int k0, uint32_t *pk) {
 #pragma unroll
-                        for (int k = 0; k < static_cast<int>(sizeof s / 4); k += 4) {
-                            float e0, e1, e2, e3;
-                            ptx::unpack2(
-                                ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c22, nm),
-                                e0, e1);
-                            ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]),
-                                                              __uint_as_float(s[k + 3])), c22, nm),
-                                         e2, e3);
-                            e0 = ptx::ex2(e0);
-                            e1 = ptx::ex2(e1);
-                            e2 = ptx::ex2(e2);
-                            e3 = ptx::ex2(e3);
-                            acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
-                            acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
-                            if constexpr (C::kQuant) {
-                                const float4 f = *reinterpret_cast<const float4 *>(sc + kTileKeys + k0 + k);
-                                e0 *= f.x;
-                                e1 *= f.y;
-                                e2 *= f.z;
-                                e3 *= f.w;
+                            for (int k = 0; k < 32; k += 4) {
+                                float e0, e1, e2, e3;
+                                ptx::unpack2(
+                                    ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c22, nm),
+                                    e0, e1);
+                                ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]),
+                                                                  __uint_as_float(s[k + 3])), c22, nm),
+                                             e2, e3);
+                                e0 = ptx::ex2(e0);
+                                e1 = ptx::ex2(e1);
+                                e2 = ptx::ex2(e2);
+                                e3 = ptx::ex2(e3);
+                                acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
+                                acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
+                                if constexpr (C::kQuant) {
+                                    const float4 f =
+                                        *reinterpret_cast<const float4 *>(sc + kTileKeys + k0 + k);
+                                    e0 *= f.x;
+                                    e1 *= f.y;
+                                    e2 *= f.z;
+                                    e3 *= f.w;
+                                }
+                                pk[k / 2] = pack_bf16(e0, e1);
+                                pk[k / 2 + 1] = pack_bf16(e2, e3);
                             }
-                            pk[k / 2] = pack_bf16(e0, e1);
-                            pk[k / 2 + 1] = pack_bf16(e2, e3);
-                        }
-                    };
-                    // ---- the rare parts, 16 scores at a time ----
-                    auto maximum = [&] {
-                        float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll 1
-                        for (int k0 = 0; k0 < 64; k0 += 16) {
-                            uint32_t s[16];
-                            ptx::tmem_ld16_nowait(col + k0, s);
-                            ptx::tmem_wait_ld();
-                            prepare(s, k0);
-#pragma unroll
-                            for (int k = 0; k < 16; k += 4) {
-                                x0 = max3(x0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                                x1 = max3(x1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-                            }
-                        }
-                        return fmaxf(x0, x1) * c2;
-                    };
-                    // rows that have seen no key take the half's maximum as reference (a
-                    // row's first keys; O and l are zero)
-                    if (__any_sync(0xffffffffu, m == -INFINITY)) {
-                        const float mx = maximum();
-                        m = m == -INFINITY ? mx : m;
-                    }
-                    uint32_t a[32], b[32], pk[32];
-                    ptx::tmem_ld32_nowait(col, a);
-                    ptx::tmem_ld32_nowait(col + 32, b);
-                    ptx::tmem_wait_ld();
-                    acc0 = acc1 = ptx::pack2(0.f, 0.f);
-                    prepare(a, 0);
-                    probabilities(a, 0, pk);
-                    prepare(b, 32);
-                    probabilities(b, 32, pk + 16);
-                    float a0, a1;
-                    ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
-                    if (__any_sync(0xffffffffu, mine && !(a0 + a1 <= kRescale))) {
-                        // scores far above the reference: once the product under way is
-                        // done, the rows of the warp take new ones
-                        if ((half || t > w.ta) &&
-                            !wait(kPvDone + st * 2 + (half ^ 1), half ? it : it - 1))
+                        };
+                        probabilities(a, 0, pk);
+                        probabilities(b, 32, pk + 16);
+                        ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
+                        if (pass || !__any_sync(0xffffffffu, mine && !(a0 + a1 <= kRescale)))
+                            break;
+                        // rare: scores far above the reference.  Once the product under way is
+                        // done, the rows of the warp take new ones, and the half is done again
+                        const bool first = !half && t == w.ta;
+                        if (!first && !wait(kPvDone + st * 2 + (half ^ 1), half ? it : it - 1))
                             break;
                         ptx::tc_fence_after_sync();
                         const float mn = fmaxf(m, maximum());
                         const float f = mn == m ? 1.f : ptx::ex2(m - mn);
                         m = mn;
                         l *= f;
-                        if (half || t > w.ta) {
 #pragma unroll 1
-                            for (int k = 0; k < kDim; k += 16) {
-                                float o[16];
-                                uint32_t r[16];
-                                ptx::tmem_ld16(colO + k, o);
+                        for (int k = 0; k < (first ? 0 : kDim); k += 16) {
+                            float o[16];
+                            uint32_t r[16];
+                            ptx::tmem_ld16(colO + k, o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    r[i] = __float_as_uint(o[i] * f);
-                                ptx::tmem_st16(colO + k, r);
-                            }
+                            for (int i = 0; i < 16; ++i)
+                                r[i] = __float_as_uint(o[i] * f);
+                            ptx::tmem_st16(colO + k, r);
                         }
-                        acc0 = acc1 = ptx::pack2(0.f, 0.f);
-#pragma unroll 1
-                        for (int k0 = 0; k0 < 64; k0 += 16) {
-                            uint32_t s[16], pk16[8];
-                            ptx::tmem_ld16_nowait(col + k0, s);
-                            ptx::tmem_wait_ld();
-                            prepare(s, k0);
-                            probabilities(s, k0, pk16);
-                            ptx::tmem_st8(col + k0 / 2, pk16);
-                        }
-                        ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
-                    } else {
-                        // (in the place of scores already read)
-                        ptx::tmem_st16(col, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
-                        ptx::tmem_st16(col + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
                     }
+                    // (in the place of scores already read)
+                    ptx::tmem_st16(col, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
+                    ptx::tmem_st16(col + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
                     l += a0 + a1;
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before_sync();
@@ -661,15 +661,14 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                 break;
             ptx::tc_fence_after_sync();
             // ---- output: the segment's rows, or their partial sums ----
-            const bool nonfinite = !C::kQuant && *s_nonfinite;
+            const bool nonfinite = !C::kQuant && *s_nonfinite, whole = w.whole();
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const int64_t grow = w.e.row0 + tok0 + my_tok;
             const int head = w.h * g + my_head;
-            const int slot = attn_slot(blockIdx.x, w.starts());
-            const int prow = slot * 256 + st * 128 + row;
+            const int prow = attn_slot(blockIdx.x, w.starts()) * 256 + st * 128 + row;
             __nv_bfloat16 *dst = p.o + grow * p.o_stride + static_cast<int64_t>(head) * kDim;
             float *part = p.line[0].part_o + static_cast<int64_t>(prow) * kDim;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < kDim; k += 32) {
                 uint32_t o[32];
                 __syncwarp();
@@ -677,26 +676,16 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                 ptx::tmem_wait_ld();
                 if (nonfinite && mine) {
                     // the cleaned values of the keys that this row sees
-                    for (int t = w.ta; t < w.tb; ++t) {
-                        if (!partial(w.e, t, 0, w.e.tokens - 1))
-                            continue;
-                        const int k0 = (w.e.tile0 + t) * kTileKeys;
-                        for (int j = max(k0, max(lo, 0)); j < min(k0 + kTileKeys, hi); ++j) {
-                            const int64_t page = kv_page_of(p.c, w.e.seq, j);
-                            if (page < 0)
-                                continue;
-                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.c.v) +
-                                                     kv_row(p.c, page, w.h, j) * kDim + k;
+                    float v[32];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float x = __bfloat162float(v[i]);
-                                if (!(fabsf(x) <= 3.4e38f))
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-                            }
-                        }
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __uint_as_float(o[i]);
+                    add_nonfinite<kDim>(p, w.e, w.h, w.ta, w.tb, hi, lo, k, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __float_as_uint(v[i]);
                 }
-                if (mine && w.whole()) {
+                if (mine && whole) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         uint4 v;
