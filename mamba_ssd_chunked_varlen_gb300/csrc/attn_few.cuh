@@ -41,7 +41,8 @@ struct FewCfg {
     static constexpr int kRowBytes = kQuant ? kDim : 2 * kDim;
     static constexpr int kLaneBytes = kRowBytes / 2;          // of 16 keys, a lane's 1 / 32
     static constexpr int kSlot = 32 * kLaneBytes + (kQuant ? 64 : 0);   // K or V of a tile, with scales
-    static constexpr int kSlots = kMaxSmemPerBlock / kFewWarps / kSlot;
+    // an odd number: with the step at which K (or V) is used, K (or V) is copied
+    static constexpr int kSlots = (kMaxSmemPerBlock / kFewWarps / kSlot - 1) / 2 * 2 + 1;
     static constexpr int kRing = kSlots * kSlot;              // bytes of a warp
     // a lane's copies: pieces of 16 bytes of two keys of K, of kVPiece bytes of four of V
     static constexpr int kKPieces = kLaneBytes / 32;
@@ -83,59 +84,64 @@ struct FewLoad {
     AttnWalk w;
     uint32_t dst0;               // shared-memory address of the warp's slots
     int put, t, ahead, my_page;  // slot's offset, tile; lane l has the page of tile t - ahead + l
-    bool v_next, there;
+    bool there;
     int64_t row;                 // cache row of the tile's first key
     uint32_t k_off, v_off;       // this lane's first piece in a tile of K and of V
 
     __device__ __forceinline__ FewLoad(const AttnParams &p_, int piece, uint32_t ring)
         : p(p_), w(p_.line[1], p_.c.heads, piece), dst0(ring), put(0), t(w.ta), ahead(32),
-          my_page(-1), v_next(false), there(false), row(0)
+          my_page(-1), there(false), row(0)
     {
         const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
         k_off = i * C::kRowBytes + q * 16;
         v_off = q * 2 * C::kRowBytes + i * C::kVPiece;
     }
 
-    // kAll: all sixteen keys are there
-    template <bool kAll>
+    // The next tile's K (kV 0) or V (1), of which `left` keys are there.
+    template <int kV>
     __device__ __forceinline__ void copy(int left)
     {
         const KvView &c = p.c;
         const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
-        const uint32_t dst = dst0 + put;
-        if (!v_next) {
-            const uint8_t *src = static_cast<const uint8_t *>(c.k) + row * C::kRowBytes + k_off;
+        constexpr int kKeys = kV ? 4 : 2, kPieces = kV ? C::kVPieces : C::kKPieces;
+        constexpr int kPiece = kV ? C::kVPiece : 16, kNext = kV ? 8 * kPiece : 64;
+        const uint32_t dst = dst0 + put + lane * kPiece;
+        const uint8_t *src = static_cast<const uint8_t *>(kV ? c.v : c.k) + row * C::kRowBytes +
+                             (kV ? v_off : k_off);
+        const int mine = kV ? q * 2 : i;
+        if (left >= kFewKeys) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < kKeys; ++n) {
+                const int key = kV ? (n & 1) + (n >> 1) * 8 : n * 8;
 #pragma unroll
-                for (int k = 0; k < C::kKPieces; ++k)
-                    ptx::cp_async<16>(dst + lane * 16 + (n * C::kKPieces + k) * 512,
-                                      src + n * 8 * C::kRowBytes + k * 64, kAll || n * 8 + i < left);
+                for (int k = 0; k < kPieces; ++k)
+                    ptx::cp_async<kPiece>(dst + (n * kPieces + k) * 32 * kPiece,
+                                          src + key * C::kRowBytes + k * kNext, true);
+            }
         } else {
-            const uint8_t *src = static_cast<const uint8_t *>(c.v) + row * C::kRowBytes + v_off;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int key = (n & 1) + (n >> 1) * 8;
-#pragma unroll
-                for (int k = 0; k < C::kVPieces; ++k)
-                    ptx::cp_async<C::kVPiece>(
-                        dst + lane * C::kVPiece + (n * C::kVPieces + k) * 32 * C::kVPiece,
-                        src + key * C::kRowBytes + k * 8 * C::kVPiece, kAll || q * 2 + key < left);
+#pragma unroll 1
+            for (int n = 0; n < kKeys; ++n) {
+                const int key = kV ? (n & 1) + (n >> 1) * 8 : n * 8;
+#pragma unroll 1
+                for (int k = 0; k < kPieces; ++k)
+                    ptx::cp_async<kPiece>(dst + (n * kPieces + k) * 32 * kPiece,
+                                          src + key * C::kRowBytes + k * kNext, mine + key < left);
             }
         }
         if constexpr (C::kQuant) {
             if (lane < 4)
-                ptx::cp_async<16>(dst + 32 * C::kLaneBytes + lane * 16,
-                                  (v_next ? c.v_scale : c.k_scale) + row + lane * 4, kAll || left > 0);
+                ptx::cp_async<16>(dst0 + put + 32 * C::kLaneBytes + lane * 16,
+                                  (kV ? c.v_scale : c.k_scale) + row + lane * 4, left > 0);
         }
     }
 
+    template <int kV>
     __device__ __forceinline__ void next()
     {
         const int lane = threadIdx.x & 31;
         if (w.more()) {
             const int j0 = (w.e.tile0 + t) * kFewKeys;
-            if (!v_next) {
+            if constexpr (kV == 0) {
                 if (ahead == 32) {
                     ahead = 0;
                     const int j = j0 + lane * kFewKeys;
@@ -147,17 +153,12 @@ struct FewLoad {
                 there = page >= 0;
                 row = there ? kv_row(p.c, page, w.h, j0) : 0;
             }
-            const int left = there ? w.e.kv_len - j0 : 0;    // keys that are there
-            if (left >= kFewKeys)
-                copy<true>(left);
-            else
-                copy<false>(left);
-            if (v_next && ++t == w.tb) {
+            copy<kV>(there ? w.e.kv_len - j0 : 0);
+            if (kV && ++t == w.tb) {
                 w.next();
                 t = w.ta;
                 ahead = 32;
             }
-            v_next = !v_next;
         }
         ptx::cp_async_commit();
         put = put + C::kSlot == C::kRing ? 0 : put + C::kSlot;
@@ -245,7 +246,7 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
         __syncwarp();                            // the other lanes' copies of the scales
         const uint8_t *slot = slots + got;
         got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
-        load.next();
+        load.template next<0>();
         float x[kN][4];
 #pragma unroll
         for (int n = 0; n < kN; ++n)
@@ -349,7 +350,7 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
         __syncwarp();
         slot = slots + got;
         got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
-        load.next();
+        load.template next<1>();
         uint32_t pb[kN][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -500,8 +501,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         AttnWalk w = load.w;
         int got = 0;
 #pragma unroll 1
-        for (int k = 0; k < C::kSlots - 1; ++k)
-            load.next();
+        for (int k = 0; k < C::kSlots - 1; k += 2) {
+            load.template next<0>();
+            load.template next<1>();
+        }
         for (; w.more(); w.next()) {
             if ((threadIdx.x & 31) == 0)
                 w.note_split(1, piece);
@@ -520,7 +523,7 @@ template <int kType, int kDim>
 cudaError_t launch_few_one(const AttnParams &p, cudaStream_t stream)
 {
     using C = FewCfg<kType, kDim>;
-    static_assert(C::kBytes <= kMaxSmemPerBlock && C::kSlots >= 4, "shared memory");
+    static_assert(C::kBytes <= kMaxSmemPerBlock && C::kSlots >= 3, "shared memory");
     static SmemOptIn opted;
     cudaError_t e =
         ensure_max_smem(reinterpret_cast<const void *>(attn_few_kernel<kType, kDim>), opted);

@@ -570,8 +570,13 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                             each([&](uint32_t v, int) { return v ^ 0x80000000u; });
                         if (hides) {
                             const int k0 = (w.e.tile0 + t) * kTileKeys + half * 64;
-                            const int from = lo - k0, to = hi - k0;
-                            each([&](uint32_t v, int k) { return k < from || k >= to ? 0xff800000u : v; });
+                            // (a bit per key: the compiler moves eight to predicates at a time)
+                            auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; };
+                            const uint32_t v0 = below(hi - k0) & ~below(lo - k0);
+                            const uint32_t v1 = below(hi - k0 - 32) & ~below(lo - k0 - 32);
+                            each([&](uint32_t v, int k) {
+                                return ((k < 32 ? v0 : v1) >> (k & 31) & 1) ? v : 0xff800000u;
+                            });
                         }
                         auto maximum = [&] {
                             float x0 = -INFINITY, x1 = -INFINITY;
