@@ -46,7 +46,7 @@ struct Cfg {
     static constexpr int kProducer = 8 + kHelpers, kIssuer = kProducer + 1;
     static constexpr int kThreads = (kProducer + 4) * 32;
     static constexpr int kLaunchRegs = kQuant ? 96 : 128;
-    static constexpr int kSoftmaxRegs = kQuant ? 144 : 168, kOtherRegs = kQuant ? 64 : 88;
+    static constexpr int kSoftmaxRegs = kQuant ? 152 : 168, kOtherRegs = kQuant ? 56 : 88;
     static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs &&
                   kThreads * kLaunchRegs <= 65536, "registers");
     static constexpr int kBlocks = kDim / 64;
@@ -487,19 +487,21 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                                 f ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         if (kv == 0 && c == 0) {
-                            // the rows' scales: a row that is not finite gets them finite and
-                            // a NaN among its codes, so that scores hidden from a query stay
-                            // hidden, and one past the last key any
-#pragma unroll 1
-                            for (int row = row0; row < kTileKeys; row += kRows) {
-                                const float ks = scale[row], vs = scale[kTileKeys + row];
+                            // the rows' scales: K's become the scores' factors (softmax_scale
+                            // log2(e) among them); a row that is not finite gets finite ones
+                            // and a NaN among its codes, so that scores hidden from a query
+                            // stay hidden, and one past the last key any
+                            const float c2 = p.negate ? -p.scale_log2 : p.scale_log2;
+#pragma unroll
+                            for (int k = 0; k < kTileKeys / kRows; ++k) {
+                                const int row = row0 + k * kRows;
+                                const float ks = scale[row] * c2, vs = scale[kTileKeys + row];
                                 const bool bad = !(fabsf(ks) <= 3.4e38f && fabsf(vs) <= 3.4e38f);
+                                scale[row] = bad || row >= keys ? c2 : ks;
                                 if (bad || row >= keys) {
-                                    scale[row] = 1.f;
                                     scale[kTileKeys + row] = 0.f;
                                     if (row < keys)
-                                        *reinterpret_cast<uint32_t *>(dst + to0 + (row - row0) * 128) =
-                                            0x7fff7fffu;
+                                        *reinterpret_cast<uint32_t *>(dst + to0 + k * kRows * 128) = 0x7fff7fffu;
                                 }
                             }
                         }
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                     float a0, a1;
 #pragma unroll 1
                     for (int pass = 0;; ++pass) {
-                        // ---- 64 scores: K's scales, sign, hidden keys ----
+                        // ---- 64 scores: sign, hidden keys ----
                         ptx::tmem_ld32_nowait(col, a);
                         ptx::tmem_ld32_nowait(col + 32, b);
                         ptx::tmem_wait_ld();
@@ -557,35 +559,45 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                             for (int k = 0; k < 32; ++k)
                                 b[k] = f(b[k], 32 + k);
                         };
-                        if constexpr (C::kQuant) {
-                            float4 f;
-                            each([&](uint32_t v, int k) {
-                                if (k % 4 == 0)
-                                    f = *reinterpret_cast<const float4 *>(sc + k);
-                                return __float_as_uint(__uint_as_float(v) *
-                                                       (k % 4 == 0 ? f.x : k % 4 == 1 ? f.y : k % 4 == 2 ? f.z : f.w));
-                            });
-                        }
-                        if (p.negate)
+                        if (!C::kQuant && p.negate)
                             each([&](uint32_t v, int) { return v ^ 0x80000000u; });
                         if (hides) {
                             const int k0 = (w.e.tile0 + t) * kTileKeys + half * 64;
-                            // (a bit per key: the compiler moves eight to predicates at a time)
+                            // (a bit per key: the compiler moves eight to predicates at a time;
+                            // the factors of an 8-bit cache's scores have the scale's sign)
                             auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; };
                             const uint32_t v0 = below(hi - k0) & ~below(lo - k0);
                             const uint32_t v1 = below(hi - k0 - 32) & ~below(lo - k0 - 32);
+                            const uint32_t hidden = C::kQuant && p.negate ? 0x7f800000u : 0xff800000u;
                             each([&](uint32_t v, int k) {
-                                return ((k < 32 ? v0 : v1) >> (k & 31) & 1) ? v : 0xff800000u;
+                                return ((k < 32 ? v0 : v1) >> (k & 31) & 1) ? v : hidden;
                             });
                         }
+                        const uint64_t c22 = ptx::pack2(c2, c2);
+                        auto factors = [&](int k) {    // of scores k .. k + 3, to log2 units
+                            if constexpr (C::kQuant)
+                                return *reinterpret_cast<const ulonglong2 *>(sc + k);
+                            else
+                                return make_ulonglong2(c22, c22);
+                        };
                         auto maximum = [&] {
                             float x0 = -INFINITY, x1 = -INFINITY;
+                            auto quarter = [&](const uint32_t (&s)[32], int k0) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                x0 = max3(x0, __uint_as_float(a[k]), __uint_as_float(a[k + 1]));
-                                x1 = max3(x1, __uint_as_float(b[k]), __uint_as_float(b[k + 1]));
-                            }
-                            return fmaxf(x0, x1) * c2;
+                                for (int k = 0; k < 32; k += 4) {
+                                    const ulonglong2 f = factors(k0 + k);
+                                    float e0, e1, e2, e3;
+                                    ptx::unpack2(ptx::mul2(ptx::pack2(__uint_as_float(s[k]),
+                                                                      __uint_as_float(s[k + 1])), f.x), e0, e1);
+                                    ptx::unpack2(ptx::mul2(ptx::pack2(__uint_as_float(s[k + 2]),
+                                                                      __uint_as_float(s[k + 3])), f.y), e2, e3);
+                                    x0 = max3(x0, e0, e1);
+                                    x1 = max3(x1, e2, e3);
+                                }
+                            };
+                            quarter(a, 0);
+                            quarter(b, 32);
+                            return fmaxf(x0, x1);
                         };
                         // rows that have seen no key take the half's maximum as reference
                         // (O and l are zero)
@@ -595,32 +607,31 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                         }
                         // ---- probabilities, and their sum ----
                         const float me = m == -INFINITY ? 0.f : m;
-                        const uint64_t c22 = ptx::pack2(c2, c2), nm = ptx::pack2(-me, -me);
+                        const uint64_t nm = ptx::pack2(-me, -me);
                         uint64_t acc0 = ptx::pack2(0.f, 0.f), acc1 = acc0;
                         auto probabilities = [&](const uint32_t (&s)[32], int k0, uint32_t *pk) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
+                                const ulonglong2 f = factors(k0 + k);
                                 float e0, e1, e2, e3;
                                 ptx::unpack2(
-                                    ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c22, nm),
+                                    ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f.x, nm),
                                     e0, e1);
                                 ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]),
-                                                                  __uint_as_float(s[k + 3])), c22, nm),
+                                                                  __uint_as_float(s[k + 3])), f.y, nm),
                                              e2, e3);
-                                e0 = ptx::ex2(e0);
-                                e1 = ptx::ex2(e1);
-                                e2 = ptx::ex2(e2);
-                                e3 = ptx::ex2(e3);
-                                acc0 = ptx::add2(acc0, ptx::pack2(e0, e1));
-                                acc1 = ptx::add2(acc1, ptx::pack2(e2, e3));
+                                uint64_t p0 = ptx::pack2(ptx::ex2(e0), ptx::ex2(e1));
+                                uint64_t p1 = ptx::pack2(ptx::ex2(e2), ptx::ex2(e3));
+                                acc0 = ptx::add2(acc0, p0);
+                                acc1 = ptx::add2(acc1, p1);
                                 if constexpr (C::kQuant) {
-                                    const float4 f =
-                                        *reinterpret_cast<const float4 *>(sc + kTileKeys + k0 + k);
-                                    e0 *= f.x;
-                                    e1 *= f.y;
-                                    e2 *= f.z;
-                                    e3 *= f.w;
+                                    const ulonglong2 v =
+                                        *reinterpret_cast<const ulonglong2 *>(sc + kTileKeys + k0 + k);
+                                    p0 = ptx::mul2(p0, v.x);
+                                    p1 = ptx::mul2(p1, v.y);
                                 }
+                                ptx::unpack2(p0, e0, e1);
+                                ptx::unpack2(p1, e2, e3);
                                 pk[k / 2] = pack_bf16(e0, e1);
                                 pk[k / 2 + 1] = pack_bf16(e2, e3);
                             }
