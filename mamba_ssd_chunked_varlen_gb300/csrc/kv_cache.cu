@@ -144,6 +144,13 @@ template <int kTokens>
 __device__ __forceinline__ int64_t place_tokens(const KvView &c, int64_t t)
 {
     int b = warp_sequence_of(c, t);
+    if constexpr (kTokens == 1) {
+        if (b < 0)
+            return -1;
+        const int64_t j = kv_len_of(c, b) - static_cast<int64_t>(c.qsl[b + 1]) + t;
+        const int64_t page = j < 0 ? -1 : kv_page_of(c, b, static_cast<int32_t>(j));
+        return page < 0 ? -1 : kv_row(c, page, 0, static_cast<int32_t>(j));
+    }
     const int lane = threadIdx.x & 31;
     const int64_t mine = t + lane;
     if (lane >= kTokens || mine >= c.total_len)
