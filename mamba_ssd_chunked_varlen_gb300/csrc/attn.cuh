@@ -15,7 +15,7 @@ constexpr int kTileRows = 128;    // query rows of a tile: whole tokens, each wi
                                   // the query heads of one kv head
 
 constexpr int kFewRows = 16;      // most query rows of a unit of the kind "few"
-constexpr int kFewKeys = 16;      // keys of such a unit's tile
+constexpr int kFewKeys = 32;      // keys of such a unit's tile
 constexpr int kFewWarps = 12;     // warps of a CTA of its kernel
 
 // A unit: query rows of one sequence with the range of key tiles that any of its
@@ -57,7 +57,7 @@ __host__ __device__ constexpr int attn_max_pieces(int kind)
 {
     return kind ? kAttnCtas * kFewWarps : kAttnCtas;
 }
-constexpr int kFewPieceTiles = 2;
+constexpr int kFewPieceTiles = 1;
 
 __host__ __device__ inline int attn_pieces(int kind, int64_t total)
 {

@@ -28,6 +28,8 @@
 // its key's scale needs the range.
 #pragma once
 
+#include <cfloat>
+
 #include "attn_codes.cuh"
 
 namespace ssd {
@@ -40,9 +42,11 @@ struct FewCfg {
     static constexpr bool kQuant = kType != SSD_KV_BF16;
     static constexpr int kRowBytes = kQuant ? kDim : 2 * kDim;
     static constexpr int kLaneBytes = kRowBytes / 2;          // of 16 keys, a lane's 1 / 32
-    static constexpr int kSlot = 32 * kLaneBytes + (kQuant ? 64 : 0);   // K or V of a tile, with scales
-    // an odd number: with the step at which K (or V) is used, K (or V) is copied
-    static constexpr int kSlots = (kMaxSmemPerBlock / kFewWarps / kSlot - 1) / 2 * 2 + 1;
+    static constexpr int kHalf = 32 * kLaneBytes;             // K or V of 16 keys
+    static constexpr int kSlot = 2 * kHalf + (kQuant ? 128 : 0);   // K or V of a tile, with scales
+    static constexpr int kSlots = kMaxSmemPerBlock / kFewWarps / kSlot;
+    // the step that uses a K copies kSlots - 1 steps on: a K (0) or a V (1)
+    static constexpr int kAhead = (kSlots - 1) % 2;
     static constexpr int kRing = kSlots * kSlot;              // bytes of a warp
     // a lane's copies: pieces of 16 bytes of two keys of K, of kVPiece bytes of four of V
     static constexpr int kKPieces = kLaneBytes / 32;
@@ -83,14 +87,15 @@ struct FewLoad {
     const AttnParams &p;
     AttnWalk w;
     uint32_t dst0;               // shared-memory address of the warp's slots
-    int put, t, ahead, my_page;  // slot's offset, tile; lane l has the page of tile t - ahead + l
-    bool there;
-    int64_t row;                 // cache row of the tile's first key
-    uint32_t k_off, v_off;       // this lane's first piece in a tile of K and of V
+    int put, t, ahead, my_page;  // slot's offset, tile; lane l has the page of the 16 keys from
+                                 // tile t - ahead on + l
+    bool there[2];               // of the tile's halves: whether they have a page,
+    int64_t row[2];              // cache row of the first key
+    uint32_t k_off, v_off;       // this lane's first piece in 16 keys of K and of V
 
     __device__ __forceinline__ FewLoad(const AttnParams &p_, int piece, uint32_t ring)
         : p(p_), w(p_.line[1], p_.c.heads, piece), dst0(ring), put(0), t(w.ta), ahead(32),
-          my_page(-1), there(false), row(0)
+          my_page(-1), there{false, false}, row{0, 0}
     {
         const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
         k_off = i * C::kRowBytes + q * 16;
@@ -105,33 +110,42 @@ struct FewLoad {
         const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
         constexpr int kKeys = kV ? 4 : 2, kPieces = kV ? C::kVPieces : C::kKPieces;
         constexpr int kPiece = kV ? C::kVPiece : 16, kNext = kV ? 8 * kPiece : 64;
+        const uint8_t *cache = static_cast<const uint8_t *>(kV ? c.v : c.k) + (kV ? v_off : k_off);
         const uint32_t dst = dst0 + put + lane * kPiece;
-        const uint8_t *src = static_cast<const uint8_t *>(kV ? c.v : c.k) + row * C::kRowBytes +
-                             (kV ? v_off : k_off);
         const int mine = kV ? q * 2 : i;
-        if (left >= kFewKeys) {
+        if (left >= kFewKeys && there[0] && there[1]) {
 #pragma unroll
-            for (int n = 0; n < kKeys; ++n) {
-                const int key = kV ? (n & 1) + (n >> 1) * 8 : n * 8;
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t *src = cache + row[u] * C::kRowBytes;
 #pragma unroll
-                for (int k = 0; k < kPieces; ++k)
-                    ptx::cp_async<kPiece>(dst + (n * kPieces + k) * 32 * kPiece,
-                                          src + key * C::kRowBytes + k * kNext, true);
+                for (int n = 0; n < kKeys; ++n) {
+                    const int key = kV ? (n & 1) + (n >> 1) * 8 : n * 8;
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k)
+                        ptx::cp_async<kPiece>(dst + u * C::kHalf + (n * kPieces + k) * 32 * kPiece,
+                                              src + key * C::kRowBytes + k * kNext, true);
+                }
             }
         } else {
 #pragma unroll 1
-            for (int n = 0; n < kKeys; ++n) {
-                const int key = kV ? (n & 1) + (n >> 1) * 8 : n * 8;
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t *src = cache + (u ? row[1] : row[0]) * C::kRowBytes;
+                const int keys = (u ? there[1] : there[0]) ? left - 16 * u : 0;
 #pragma unroll 1
-                for (int k = 0; k < kPieces; ++k)
-                    ptx::cp_async<kPiece>(dst + (n * kPieces + k) * 32 * kPiece,
-                                          src + key * C::kRowBytes + k * kNext, mine + key < left);
+                for (int n = 0; n < kKeys; ++n) {
+                    const int key = kV ? (n & 1) + (n >> 1) * 8 : n * 8;
+#pragma unroll 1
+                    for (int k = 0; k < kPieces; ++k)
+                        ptx::cp_async<kPiece>(dst + u * C::kHalf + (n * kPieces + k) * 32 * kPiece,
+                                              src + key * C::kRowBytes + k * kNext, mine + key < keys);
+                }
             }
         }
         if constexpr (C::kQuant) {
-            if (lane < 4)
-                ptx::cp_async<16>(dst0 + put + 32 * C::kLaneBytes + lane * 16,
-                                  (kV ? c.v_scale : c.k_scale) + row + lane * 4, left > 0);
+            if (lane < 8)
+                ptx::cp_async<16>(dst0 + put + 2 * C::kHalf + lane * 16,
+                                  (kV ? c.v_scale : c.k_scale) + (lane < 4 ? row[0] : row[1]) + (lane & 3) * 4,
+                                  lane < 4 ? there[0] && left > 0 : there[1] && left > 16);
         }
     }
 
@@ -144,16 +158,20 @@ struct FewLoad {
             if constexpr (kV == 0) {
                 if (ahead == 32) {
                     ahead = 0;
-                    const int j = j0 + lane * kFewKeys;
+                    const int j = j0 + lane * 16;
                     my_page = -1;
-                    if (t + lane < w.tb && j < w.e.kv_len)
+                    if (2 * t + lane < 2 * w.tb && j < w.e.kv_len)
                         my_page = static_cast<int>(kv_page_of(p.c, w.e.seq, j));
                 }
-                const int page = __shfl_sync(0xffffffffu, my_page, ahead++);
-                there = page >= 0;
-                row = there ? kv_row(p.c, page, w.h, j0) : 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int page = __shfl_sync(0xffffffffu, my_page, ahead + u);
+                    there[u] = page >= 0;
+                    row[u] = there[u] ? kv_row(p.c, page, w.h, j0 + 16 * u) : 0;
+                }
+                ahead += 2;
             }
-            copy<kV>(there ? w.e.kv_len - j0 : 0);
+            copy<kV>(w.e.kv_len - j0);
             if (kV && ++t == w.tb) {
                 w.next();
                 t = w.ta;
@@ -225,7 +243,8 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
         }
     }
     float o[kN][kDim / 16][4];
-    float m[kN][2], l[kN][2];
+    // -m: the reference begins with the least finite number, which is one like any other
+    float nm[kN][2], l[kN][2];
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
 #pragma unroll
@@ -233,7 +252,7 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 o[n][s][k] = 0.f;
-        m[n][0] = m[n][1] = -INFINITY;
+        nm[n][0] = nm[n][1] = FLT_MAX;
         l[n][0] = l[n][1] = 0.f;
     }
     bool nonfinite = false;
@@ -241,55 +260,60 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
     for (int t = w.ta; t < w.tb; ++t) {
         const int j0 = (e.tile0 + t) * kFewKeys;
         const bool hides = attn_partial(e, p.window, j0, kFewKeys, 0, e.tokens - 1);
-        // ---- scores: keys i and i + 8, rows 2q and 2q + 1 of each eight ----
+        // ---- scores: keys i, i + 8, ... (k), rows 2q and 2q + 1 of each eight ----
         ptx::cp_async_wait<C::kSlots - 2>();
         __syncwarp();                            // the other lanes' copies of the scales
         const uint8_t *slot = slots + got;
         got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
-        load.template next<0>();
-        float x[kN][4];
+        load.template next<C::kAhead>();
+        float x[2][kN][4];
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                x[n][k] = 0.f;
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int k = 0; k < C::kKPieces; ++k) {
-            const uint4 va = *reinterpret_cast<const uint4 *>(slot + (k * 32 + lane) * 16);
-            const uint4 vb =
-                *reinterpret_cast<const uint4 *>(slot + ((C::kKPieces + k) * 32 + lane) * 16);
-            const uint32_t a4[4] = {va.x, va.y, va.z, va.w}, b4[4] = {vb.x, vb.y, vb.z, vb.w};
-            if constexpr (C::kQuant) {
+                for (int k = 0; k < 4; ++k)
+                    x[u][n][k] = 0.f;
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    uint32_t a[2], b[2];
-                    half4<kType>(a4[s], a);
-                    half4<kType>(b4[s], b);
-                    const uint32_t f[4] = {a[0], b[0], a[1], b[1]};
+        for (int k = 0; k < C::kKPieces; ++k)
 #pragma unroll
-                    for (int n = 0; n < kN; ++n)
-                        ptx::mma_16816_f16(x[n], f, qb[n][k * 4 + s][0], qb[n][k * 4 + s][1]);
-                }
-            } else {
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t *src = slot + u * C::kHalf + (k * 32 + lane) * 16;
+                const uint4 va = *reinterpret_cast<const uint4 *>(src);
+                const uint4 vb = *reinterpret_cast<const uint4 *>(src + C::kKPieces * 512);
+                const uint32_t a4[4] = {va.x, va.y, va.z, va.w}, b4[4] = {vb.x, vb.y, vb.z, vb.w};
+                if constexpr (C::kQuant) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t f[4] = {a4[2 * s], b4[2 * s], a4[2 * s + 1], b4[2 * s + 1]};
+                    for (int s = 0; s < 4; ++s) {
+                        uint32_t a[2], b[2];
+                        half4<kType>(a4[s], a);
+                        half4<kType>(b4[s], b);
+                        const uint32_t f[4] = {a[0], b[0], a[1], b[1]};
 #pragma unroll
-                    for (int n = 0; n < kN; ++n)
-                        ptx::mma_16816(x[n], f, qb[n][k * 2 + s][0], qb[n][k * 2 + s][1]);
+                        for (int n = 0; n < kN; ++n)
+                            ptx::mma_16816_f16(x[u][n], f, qb[n][k * 4 + s][0], qb[n][k * 4 + s][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t f[4] = {a4[2 * s], b4[2 * s], a4[2 * s + 1], b4[2 * s + 1]};
+#pragma unroll
+                        for (int n = 0; n < kN; ++n)
+                            ptx::mma_16816(x[u][n], f, qb[n][k * 2 + s][0], qb[n][k * 2 + s][1]);
+                    }
                 }
             }
-        }
+        const float *scales = reinterpret_cast<const float *>(slot + 2 * C::kHalf) + i;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
             float ks = 1.f;
             if constexpr (C::kQuant)
-                ks = reinterpret_cast<const float *>(slot + 32 * C::kLaneBytes)[i + 8 * k];
+                ks = scales[8 * k];
 #pragma unroll
             for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    x[n][2 * k + r] *= C::kQuant ? ks * cr[n][r] : c2;
+                    x[k / 2][n][k % 2 * 2 + r] *= C::kQuant ? ks * cr[n][r] : c2;
         }
         if (hides) {
 #pragma unroll
@@ -299,32 +323,35 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                     const int pos = e.pos0 + min((n * 8 + q * 2 + r) / g, e.tokens - 1);
                     const int lo = p.window > 0 ? pos - p.window + 1 : INT32_MIN / 2;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const int j = j0 + i + k * 8;
                         if (j < lo || j > pos)
-                            x[n][2 * k + r] = -INFINITY;
+                            x[k / 2][n][k % 2 * 2 + r] = -INFINITY;
                     }
                 }
         }
         // ---- probabilities ----
-        bool up = false;
+        auto largest = [&](int n, int r) {
+            return fmaxf(fmaxf(x[0][n][r], x[0][n][2 + r]), fmaxf(x[1][n][r], x[1][n][2 + r]));
+        };
+        float over = -INFINITY;
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                up = up || fmaxf(x[n][r], x[n][2 + r]) > m[n][r] + kFewRescale;
-        if (__any_sync(0xffffffffu, up)) {
+                over = fmaxf(over, largest(n, r) + nm[n][r]);
+        if (__any_sync(0xffffffffu, over > kFewRescale)) {
 #pragma unroll
             for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float v = fmaxf(x[n][r], x[n][2 + r]);
+                    float v = largest(n, r);
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    const float mn = fmaxf(m[n][r], v);
-                    const float f = mn == m[n][r] ? 1.f : ptx::ex2(m[n][r] - mn);
-                    m[n][r] = mn;
+                    const float to = fminf(nm[n][r], -v);
+                    const float f = to == nm[n][r] ? 1.f : ptx::ex2(to - nm[n][r]);
+                    nm[n][r] = to;
                     l[n][r] *= f;
 #pragma unroll
                     for (int s = 0; s < kDim / 16; ++s) {
@@ -334,100 +361,102 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                 }
         }
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float nm = m[n][r] == -INFINITY ? 0.f : -m[n][r];
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float &v = x[n][2 * k + r];
-                    v = ptx::ex2(v + nm);
-                    l[n][r] += v;
+                for (int k = 0; k < 4; ++k) {
+                    float &v = x[u][n][k];
+                    v = ptx::ex2(v + nm[n][k & 1]);
+                    l[n][k & 1] += v;
                 }
-            }
         // ---- V^T P ----
         ptx::cp_async_wait<C::kSlots - 2>();
         __syncwarp();
         slot = slots + got;
         got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
-        load.template next<1>();
-        uint32_t pb[kN][2];
+        load.template next<1 - C::kAhead>();
+        uint32_t pb[2][kN][2];
+        scales = reinterpret_cast<const float *>(slot + 2 * C::kHalf) + i;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
             float vs = 1.f;
             if constexpr (C::kQuant)
-                vs = reinterpret_cast<const float *>(slot + 32 * C::kLaneBytes)[i + 8 * k];
+                vs = scales[8 * k];
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
-                float a = x[n][2 * k], b = x[n][2 * k + 1];
+                float a = x[k / 2][n][k % 2 * 2], b = x[k / 2][n][k % 2 * 2 + 1];
                 if constexpr (C::kQuant) {
                     // (a hidden key's scale may be NaN: its weight stays zero)
                     a = hides && a == 0.f ? 0.f : a * vs;
                     b = hides && b == 0.f ? 0.f : b * vs;
                 }
-                pb[n][k] = ptx::transpose8(pack_bf16(a, b));
+                pb[k / 2][n][k % 2] = ptx::transpose8(pack_bf16(a, b));
             }
         }
 #pragma unroll
-        for (int k = 0; k < C::kVPieces; ++k) {
-            constexpr int kWords = C::kVPiece / 4;
-            uint32_t v[4][kWords];
+        for (int k = 0; k < C::kVPieces; ++k)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const uint8_t *src = slot + ((n * C::kVPieces + k) * 32 + lane) * C::kVPiece;
-                if constexpr (kWords == 4) {
-                    const uint4 t4 = *reinterpret_cast<const uint4 *>(src);
-                    v[n][0] = t4.x;
-                    v[n][1] = t4.y;
-                    v[n][2] = t4.z;
-                    v[n][3] = t4.w;
-                } else {
-                    const uint2 t2 = *reinterpret_cast<const uint2 *>(src);
-                    v[n][0] = t2.x;
-                    v[n][1] = t2.y;
-                }
-            }
-            if constexpr (C::kQuant) {
+            for (int u = 0; u < 2; ++u) {
+                constexpr int kWords = C::kVPiece / 4;
+                uint32_t v[4][kWords];
 #pragma unroll
-                for (int s = 0; s < kWords; ++s) {
-                    uint32_t a[4], b[4];
-                    widen_columns<kType, 0>(v[0][s], v[1][s], a);
-                    widen_columns<kType, 2>(v[0][s], v[1][s], a + 2);
-                    widen_columns<kType, 0>(v[2][s], v[3][s], b);
-                    widen_columns<kType, 2>(v[2][s], v[3][s], b + 2);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t f[4] = {a[2 * j], a[2 * j + 1], b[2 * j], b[2 * j + 1]};
-#pragma unroll
-                        for (int n = 0; n < kN; ++n)
-                            ptx::mma_16816(o[n][s * 2 + j], f, pb[n][0], pb[n][1]);
+                for (int n = 0; n < 4; ++n) {
+                    const uint8_t *src =
+                        slot + u * C::kHalf + ((n * C::kVPieces + k) * 32 + lane) * C::kVPiece;
+                    if constexpr (kWords == 4) {
+                        const uint4 t4 = *reinterpret_cast<const uint4 *>(src);
+                        v[n][0] = t4.x;
+                        v[n][1] = t4.y;
+                        v[n][2] = t4.z;
+                        v[n][3] = t4.w;
+                    } else {
+                        const uint2 t2 = *reinterpret_cast<const uint2 *>(src);
+                        v[n][0] = t2.x;
+                        v[n][1] = t2.y;
                     }
                 }
-            } else {
-                if (hides) {
-                    // infinities and NaN would reach the rows that do not see them
-                    // (0 times them): they are added at the end to those that do
+                if constexpr (C::kQuant) {
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
+                    for (int s = 0; s < kWords; ++s) {
+                        uint32_t a[4], b[4];
+                        widen_columns<kType, 0>(v[0][s], v[1][s], a);
+                        widen_columns<kType, 2>(v[0][s], v[1][s], a + 2);
+                        widen_columns<kType, 0>(v[2][s], v[3][s], b);
+                        widen_columns<kType, 2>(v[2][s], v[3][s], b + 2);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            const bool a = (v[n][s] & 0x7f80u) == 0x7f80u;
-                            const bool b = (v[n][s] & 0x7f800000u) == 0x7f800000u;
-                            nonfinite = nonfinite || a || b;
-                            v[n][s] &= (a ? 0xffff0000u : 0xffffffffu) & (b ? 0xffffu : 0xffffffffu);
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t f[4] = {a[2 * j], a[2 * j + 1], b[2 * j], b[2 * j + 1]};
+#pragma unroll
+                            for (int n = 0; n < kN; ++n)
+                                ptx::mma_16816(o[n][s * 2 + j], f, pb[u][n][0], pb[u][n][1]);
                         }
-                }
+                    }
+                } else {
+                    if (hides) {
+                        // infinities and NaN would reach the rows that do not see them
+                        // (0 times them): they are added at the end to those that do
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t f[4] = {
-                        __byte_perm(v[0][s], v[1][s], 0x5410), __byte_perm(v[0][s], v[1][s], 0x7632),
-                        __byte_perm(v[2][s], v[3][s], 0x5410), __byte_perm(v[2][s], v[3][s], 0x7632)};
+                        for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int n = 0; n < kN; ++n)
-                        ptx::mma_16816(o[n][k * 4 + s], f, pb[n][0], pb[n][1]);
+                            for (int s = 0; s < 4; ++s) {
+                                const bool a = (v[n][s] & 0x7f80u) == 0x7f80u;
+                                const bool b = (v[n][s] & 0x7f800000u) == 0x7f800000u;
+                                nonfinite = nonfinite || a || b;
+                                v[n][s] &= (a ? 0xffff0000u : 0xffffffffu) & (b ? 0xffffu : 0xffffffffu);
+                            }
+                    }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t f[4] = {
+                            __byte_perm(v[0][s], v[1][s], 0x5410), __byte_perm(v[0][s], v[1][s], 0x7632),
+                            __byte_perm(v[2][s], v[3][s], 0x5410), __byte_perm(v[2][s], v[3][s], 0x7632)};
+#pragma unroll
+                        for (int n = 0; n < kN; ++n)
+                            ptx::mma_16816(o[n][k * 4 + s], f, pb[u][n][0], pb[u][n][1]);
+                    }
                 }
             }
-        }
     }
 
     // ---- output: rows 2q and 2q + 1 of each eight, the lane's columns ----
@@ -474,10 +503,10 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
             }
             if (i == 0) {
                 if (!w.whole())
-                    p.line[1].part_ml[prow] = make_float2(m[n][r], l[n][r]);
+                    p.line[1].part_ml[prow] = make_float2(-nm[n][r], l[n][r]);
                 else if (p.lse)
                     p.lse[grow * p.heads + head] =
-                        l[n][r] == 0.f ? -INFINITY : (m[n][r] + log2f(l[n][r])) * 0.6931471805599453f;
+                        l[n][r] == 0.f ? -INFINITY : (log2f(l[n][r]) - nm[n][r]) * 0.6931471805599453f;
             }
         }
 }
@@ -501,10 +530,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         AttnWalk w = load.w;
         int got = 0;
 #pragma unroll 1
-        for (int k = 0; k < C::kSlots - 1; k += 2) {
+        for (int k = 0; k < (C::kSlots - 1) / 2; ++k) {
             load.template next<0>();
             load.template next<1>();
         }
+        if constexpr (C::kAhead == 1)
+            load.template next<0>();
         for (; w.more(); w.next()) {
             if ((threadIdx.x & 31) == 0)
                 w.note_split(1, piece);
@@ -523,7 +554,7 @@ template <int kType, int kDim>
 cudaError_t launch_few_one(const AttnParams &p, cudaStream_t stream)
 {
     using C = FewCfg<kType, kDim>;
-    static_assert(C::kBytes <= kMaxSmemPerBlock && C::kSlots >= 3, "shared memory");
+    static_assert(C::kBytes <= kMaxSmemPerBlock && C::kSlots >= 2, "shared memory");
     static SmemOptIn opted;
     cudaError_t e =
         ensure_max_smem(reinterpret_cast<const void *>(attn_few_kernel<kType, kDim>), opted);
