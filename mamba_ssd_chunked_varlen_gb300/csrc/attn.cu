@@ -277,54 +277,65 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2)
             const int tok = x / g, st = tok / p.tile_tokens;
             return st * kTileRows + (tok - st * p.tile_tokens) * g + x % g;
         };
-        if (e.w - e.z >= 8) {
-            for (int x = x0; x < min(x0 + 4, rows); ++x) {
-                float top, sum, acc[kE];
-                join_pieces<kE>(tl, attn_part_rows(0), e.z, e.z, e.w, 1, part_row(x), top, sum, acc);
-                write(e, x, top, sum, acc);
-            }
-            continue;
-        }
-        // up to eight pieces: lane 8 r + k has piece k of row r
-        const int r = lane >> 3, k = lane & 7, x = min(x0 + r, rows - 1);
-        float2 ml = make_float2(-INFINITY, 0.f);
-        const int my_row = attn_slot(e.z + k, k == 0) * attn_part_rows(0) + part_row(x);
-        if (e.z + k <= e.w)
-            ml = tl.part_ml[my_row];
-        float top = ml.x;
+        // lane 4 k + r: eight pieces' references of row r; then four columns of each 32
+        const int r = lane & 3, k = lane >> 2, x = min(x0 + r, rows - 1), row = part_row(x);
+        float top = -INFINITY, sum = 0.f, acc[kE][4];
 #pragma unroll
-        for (int o = 4; o; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-        float sum = ml.x == -INFINITY ? ml.y : w * ml.y;
+        for (int j = 0; j < kE; ++j)
 #pragma unroll
-        for (int o = 4; o; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        float acc[4][kE];
+            for (int i = 0; i < 4; ++i)
+                acc[j][i] = 0.f;
+        for (int base = e.z; base <= e.w; base += 8) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (base + k <= e.w)
+                ml = tl.part_ml[attn_slot(base + k, base + k == e.z) * attn_part_rows(0) + row];
+            float m = ml.x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int o = 4; o < 32; o <<= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float nt = fmaxf(top, m), f = top == nt ? 1.f : exp2f(top - nt);
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - nt);
+            float s = ml.x == -INFINITY ? ml.y : w * ml.y;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+            sum = sum * f + s;
+            top = nt;
 #pragma unroll
             for (int j = 0; j < kE; ++j)
-                acc[i][j] = 0.f;
-#pragma unroll 2
-        for (int n = 0; n <= e.w - e.z; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float wn = __shfl_sync(0xffffffffu, w, i * 8 + n);
-                const int64_t at = __shfl_sync(0xffffffffu, my_row, i * 8 + n);
-                const float *src = tl.part_o + at * kDim + lane * kE;
+                for (int i = 0; i < 4; ++i)
+                    acc[j][i] *= f;
+            const int n = min(8, e.w - base + 1);
+#pragma unroll 2
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, 4 * i + r);
+                const float4 *src = reinterpret_cast<const float4 *>(tl.part_o) +
+                                    attn_slot(base + i, base + i == e.z) *
+                                        static_cast<int64_t>(attn_part_rows(0) * kDim / 4) +
+                                    k * attn_part_rows(0) + row;
 #pragma unroll
                 for (int j = 0; j < kE; ++j) {
-                    const float v = src[j];
-                    acc[i][j] += wn == 0.f ? 0.f : wn * v;
+                    const float4 v = src[j * 8 * attn_part_rows(0)];
+                    acc[j][0] += wi == 0.f ? 0.f : wi * v.x;
+                    acc[j][1] += wi == 0.f ? 0.f : wi * v.y;
+                    acc[j][2] += wi == 0.f ? 0.f : wi * v.z;
+                    acc[j][3] += wi == 0.f ? 0.f : wi * v.w;
                 }
             }
         }
+        if (x0 + r < rows) {
+            const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+            const int64_t orow = e.x + x / g;
+            const int head = (e.y >> 9) * g + x % g;
+            __nv_bfloat16 *dst = p.o + orow * p.o_stride + static_cast<int64_t>(head) * kDim + k * 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float ti = __shfl_sync(0xffffffffu, top, i * 8), si = __shfl_sync(0xffffffffu, sum, i * 8);
-            if (x0 + i < rows)
-                write(e, x0 + i, ti, si, acc[i]);
+            for (int j = 0; j < kE; ++j)
+                *reinterpret_cast<uint2 *>(dst + j * 32) = make_uint2(
+                    pack_bf16(acc[j][0] * inv, acc[j][1] * inv), pack_bf16(acc[j][2] * inv, acc[j][3] * inv));
+            if (p.lse && k == 0)
+                p.lse[orow * p.heads + head] =
+                    sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         }
     }
 

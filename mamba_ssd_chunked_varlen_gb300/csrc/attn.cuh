@@ -45,7 +45,8 @@ struct AttnLine {
     const AttnPiece *pieces;
     const int64_t *total;         // key tiles of all units and kv heads
     int64_t *cum;                 // (units): key tiles before each unit, one head (the plan's)
-    float *part_o;                // [2 pieces][rows][dim]: sums of p v
+    float *part_o;                // sums of p v: few [2 pieces][rows][dim], tiles
+                                  // [2 pieces][dim / 4][rows][4]
     float2 *part_ml;              // [2 pieces][rows]: reference (log2), sum of p
     int4 *split;                  // [pieces] the pairs with partial results, in any order:
                                   // {row0, tokens + (kv head << 9), first piece, last piece}

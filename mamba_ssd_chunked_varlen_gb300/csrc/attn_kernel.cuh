@@ -198,8 +198,6 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         const int boxes = shift >= 7 ? 1 : kTileKeys >> shift;    // pages of a tile
         for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next(), ++qit) {
             const int ns = streams(w.e);
-            if (lane == 0)
-                w.note_split(0, blockIdx.x);
             if (qit > 0 && !lazy_wait(kQEmpty, qit - 1))
                 break;
             if (lane == 0) {
@@ -383,6 +381,10 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         ptx::mbar_wait(bars + kDrain + st, 0, kWaitTimeoutNs);
     } else if (warp == C::kIssuer + 2) {
         ptx::setmaxnreg_dec<C::kOtherRegs>();
+        // ------------------------------------------------ the list for the join
+        for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more(); w.next())
+            if (lane == 0)
+                w.note_split(0, blockIdx.x);
     } else if (warp >= 8) {
         ptx::setmaxnreg_dec<C::kOtherRegs>();
         const int ht = tid - 256;
@@ -517,6 +519,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t colS = tmem + st * 128 + lanes, colO = tmem + C::kColO + st * kDim + lanes;
         const int my_tok = row / g, my_head = row % g;
+        const int warp_tok0 = (warp & 3) * 32 / g, warp_tok1 = ((warp & 3) * 32 + 31) / g;
         const float c2 = p.scale_log2;
         uint32_t it = 0, sit = 0, oit = 0;
         for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next()) {
@@ -530,23 +533,36 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
             const int pos = w.e.pos0 + tok0 + (mine ? my_tok : ntok - 1);
             const int hi = pos + 1;
             const int lo = p.window > 0 ? pos - p.window + 1 : INT32_MIN / 2;
+            // of the warp's rows: first and last position, or none
+            const int pos0 = w.e.pos0 + tok0 + warp_tok0;
+            const int pos1 = warp_tok0 < ntok ? w.e.pos0 + tok0 + min(warp_tok1, ntok - 1) : INT32_MIN / 2;
+            const int back = p.window > 0 ? p.window : INT32_MAX / 2;
             // reference, times c (a row that is none has one, and asks for no other)
             float m = mine ? -INFINITY : 0.f;
             float l = 0.f;
             for (int t = w.ta; t < w.tb && ok; ++t, ++it, ++sit) {
                 // (the converter has seen the scales land)
                 const float *sc = sScale + (sit % kSlots8) * 2 * kTileKeys;
-                const bool hides = partial(w.e, t, tok0, tok0 + ntok - 1);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, sc += 64) {
                     const uint32_t col = colS + half * 64;
+                    const int k0 = (w.e.tile0 + t) * kTileKeys + half * 64;
+                    // by warp and half: whether a row does not see all of the keys, and
+                    // whether any row sees any
+                    const bool hides = k0 + 63 > pos0 || k0 <= pos1 - back;
+                    const bool some = k0 <= pos1 && k0 + 63 > pos0 - back;
                     if (!wait(kSFull + st * 2 + half, it))
                         break;
                     ptx::tc_fence_after_sync();
                     uint32_t a[32], b[32], pk[32];
-                    float a0, a1;
+                    float a0 = 0.f, a1 = 0.f;
+                    if (!some) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            pk[k] = 0;
+                    }
 #pragma unroll 1
-                    for (int pass = 0;; ++pass) {
+                    for (int pass = 0; some; ++pass) {
                         // ---- 64 scores: sign, hidden keys ----
                         ptx::tmem_ld32_nowait(col, a);
                         ptx::tmem_ld32_nowait(col + 32, b);
@@ -562,7 +578,6 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                         if (!C::kQuant && p.negate)
                             each([&](uint32_t v, int) { return v ^ 0x80000000u; });
                         if (hides) {
-                            const int k0 = (w.e.tile0 + t) * kTileKeys + half * 64;
                             // (a bit per key: the compiler moves eight to predicates at a time;
                             // the factors of an 8-bit cache's scores have the scale's sign)
                             auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; };
@@ -681,9 +696,20 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const int64_t grow = w.e.row0 + tok0 + my_tok;
             const int head = w.h * g + my_head;
-            const int prow = attn_slot(blockIdx.x, w.starts()) * 256 + st * 128 + row;
+            const int64_t slot = attn_slot(blockIdx.x, w.starts());
+            // where this thread stores: of four rows (its own and its neighbours') a
+            // sixteen-byte piece each, so that four lanes fill 64 bytes of a row; a
+            // partial result lies by four columns, row by row
             __nv_bfloat16 *dst = p.o + grow * p.o_stride + static_cast<int64_t>(head) * kDim;
-            float *part = p.line[0].part_o + static_cast<int64_t>(prow) * kDim;
+            __nv_bfloat16 *to[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine ? dst : nullptr),
+                                                (lane & ~3) + j);
+                to[j] = reinterpret_cast<__nv_bfloat16 *>(at);
+            }
+            float4 *part = reinterpret_cast<float4 *>(p.line[0].part_o + slot * (2 * kTileRows * kDim)) +
+                           st * 128 + row;
 #pragma unroll 1
             for (int k = 0; k < kDim; k += 32) {
                 uint32_t o[32];
@@ -701,26 +727,41 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                     for (int i = 0; i < 32; ++i)
                         o[i] = __float_as_uint(v[i]);
                 }
-                if (mine && whole) {
+                __syncwarp();
+                if (whole) {
+                    uint32_t v[4][4];               // [piece][word], then [row][word]
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 v;
-                        v.x = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-                        v.y = pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                        v.z = pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-                        v.w = pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + k + i) = v;
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        v[i / 4][i % 4] = pack_bf16(__uint_as_float(o[2 * i]) * inv,
+                                                    __uint_as_float(o[2 * i + 1]) * inv);
+#pragma unroll
+                    for (int bit = 1; bit < 4; bit *= 2)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4 && !(j & bit); ++i) {
+                                const bool up = lane & bit;
+                                const uint32_t got = __shfl_xor_sync(
+                                    0xffffffffu, up ? v[j][i] : v[j | bit][i], bit);
+                                v[j][i] = up ? got : v[j][i];
+                                v[j | bit][i] = up ? v[j | bit][i] : got;
+                            }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (to[j])
+                            *reinterpret_cast<uint4 *>(to[j] + k + (lane & 3) * 8) =
+                                make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
                 } else if (mine) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4 *>(part + k + i) =
-                            make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        part[(k + i) / 4 * (2 * kTileRows)] =
+                            make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                                        __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
                 }
             }
             if (mine) {
                 if (!w.whole())
-                    p.line[0].part_ml[prow] = make_float2(m, l);
+                    p.line[0].part_ml[slot * (2 * kTileRows) + st * 128 + row] = make_float2(m, l);
                 else if (p.lse)
                     p.lse[grow * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             }
