@@ -14,6 +14,7 @@ namespace {
 // One CTA cuts the call into units (AttnUnit), in the order of the rows, and
 // counts their key tiles.
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCtas = 8;
 constexpr int kPlanBatch = 4096;    // up to so many sequences, their first units stay on chip,
 constexpr int kPlanUnits = 1024;    // and so many units of a kind, their first tiles
 
@@ -72,14 +73,20 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     }
     // (a query_start_loc that fails may count any number of units: none is written)
     bad = __syncthreads_or(bad);
+    // this CTA's pieces, of both kinds one after the other
+    constexpr int kEach = (attn_max_pieces(0) + attn_max_pieces(1) + kPlanCtas - 1) / kPlanCtas;
+    static_assert(kEach <= kPlanThreads, "a piece per thread");
+    const int my_piece = blockIdx.x * kEach + tid;
+    const int my_kind = my_piece < attn_max_pieces(0) ? 0 : 1;
+    const int i = my_piece - (my_kind ? attn_max_pieces(0) : 0);
+    const bool has_piece = tid < kEach && i < attn_max_pieces(my_kind);
+    AttnPiece pc = {};
+    int4 split = make_int4(0, 0, 0, 0);
     if (bad) {
-        if (tid < 2) {
-            p.hdr->total[tid] = 0;
-            p.hdr->splits[tid][0] = p.hdr->splits[tid][1] = 0;
+        if (has_piece) {
+            const_cast<AttnPiece *>(p.line[my_kind].pieces)[i] = pc;
+            p.line[my_kind].split[i] = split;
         }
-        for (int k = 0; k < 2; ++k)
-            for (int i = tid; i < attn_max_pieces(k); i += kPlanThreads)
-                const_cast<AttnPiece *>(p.line[k].pieces)[i] = AttnPiece{};
         if (tid == 0)
             kv_error(c, SSD_DEVERR_BAD_QUERY_START_LOC);
         return;
@@ -134,40 +141,52 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
             count[k] += all[2 * k + 1];
         }
     }
-    if (tid < 2) {
-        p.hdr->total[tid] = tiles[tid] * c.heads;
-        p.hdr->splits[tid][0] = p.hdr->splits[tid][1] = 0;
-    }
     __syncthreads();
-    // where every piece begins
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int64_t total = tiles[k] * c.heads;
-        const int pieces = attn_pieces(k, total);
-        const int64_t *cum = count[k] <= kPlanUnits ? s_cum[k] : p.line[k].cum;
-        for (int i = tid; i < attn_max_pieces(k); i += kPlanThreads) {
-            AttnPiece pc = {};
-            if (i < pieces) {
-                pc.pos = attn_piece_begin(total, pieces, i);
-                pc.end = attn_piece_begin(total, pieces, i + 1);
-                int lo = 0, hi = static_cast<int>(count[k]) - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) / 2;
-                    if (cum[mid] * c.heads <= pc.pos)
-                        lo = mid;
-                    else
-                        hi = mid - 1;
-                }
-                const int64_t r = pc.pos - cum[lo] * c.heads;
-                const int n = p.line[k].units[lo].tiles;
-                pc.u = lo;
-                // (tiles and heads are below 2^23 and 2^16)
-                pc.h = r >> 31 ? static_cast<int32_t>(r / n) : static_cast<int32_t>(r) / n;
-                pc.ta = static_cast<int32_t>(r - static_cast<int64_t>(pc.h) * n);
-            }
-            const_cast<AttnPiece *>(p.line[k].pieces)[i] = pc;
+    if (!has_piece)
+        return;
+    // where the piece begins; and where that is within a pair that the piece before
+    // begins, the pair is one for the join
+    const AttnLine &line = p.line[my_kind];
+    const int64_t n_units = my_kind ? count[1] : count[0];
+    const int64_t total = (my_kind ? tiles[1] : tiles[0]) * c.heads;
+    const int pieces = attn_pieces(my_kind, total);
+    if (i < pieces) {
+        const int64_t *cum = n_units <= kPlanUnits ? s_cum[my_kind] : line.cum;
+        // piece i begins at floor(total i / pieces)
+        const int64_t each = total / pieces;
+        const int rest = static_cast<int>(total - each * pieces);
+        auto begin = [&](int k) { return each * k + rest * k / pieces; };
+        const int64_t pos = begin(i);
+        pc.tiles = static_cast<int32_t>(begin(i + 1) - pos);
+        int lo = 0, hi = static_cast<int>(n_units) - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (cum[mid] * c.heads <= pos)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int64_t r = pos - cum[lo] * c.heads;
+        pc.e = line.units[lo];
+        const int n = pc.e.tiles;
+        pc.u = lo;
+        // (tiles and heads are below 2^23 and 2^16)
+        pc.h = r >> 31 ? static_cast<int32_t>(r / n) : static_cast<int32_t>(r) / n;
+        pc.ta = static_cast<int32_t>(r - static_cast<int64_t>(pc.h) * n);
+        const int64_t first = pos - pc.ta;
+        if (pc.ta > 0 && first >= begin(i - 1)) {
+            // the last piece that begins before the pair's end
+            const float rate = static_cast<float>(pieces) / static_cast<float>(total);
+            int last = min(i + static_cast<int>((n - pc.ta) * rate), pieces - 1);
+            while (last + 1 < pieces && begin(last + 1) < first + n)
+                ++last;
+            while (begin(last) >= first + n)
+                --last;
+            split = make_int4(pc.e.row0, pc.e.tokens + (pc.h << 9), i - 1, last);
         }
     }
+    const_cast<AttnPiece *>(line.pieces)[i] = pc;
+    line.split[i] = split;
 }
 
 // ---------------------------------------------------------------- join
@@ -225,9 +244,18 @@ __device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows,
                                    (attn_slot(at, at == first) * static_cast<int64_t>(part_rows) + row) *
                                        (32 * kE) +
                                    lane * kE;
-#pragma unroll
-                for (int j = 0; j < kE; ++j)
-                    v[k][j] = at <= last ? src[j] : 0.f;
+                if constexpr (kE == 4) {
+                    const float4 x =
+                        at <= last ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[k][0] = x.x;
+                    v[k][1] = x.y;
+                    v[k][2] = x.z;
+                    v[k][3] = x.w;
+                } else {
+                    const float2 x = at <= last ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
+                    v[k][0] = x.x;
+                    v[k][1] = x.y;
+                }
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -246,11 +274,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2)
 {
     constexpr int kE = kDim / 32;
     __shared__ float s_ml[kJoinWarps][2], s_acc[kJoinWarps][kDim];
+    constexpr int kThreads = kJoinWarps * 32, kFewPairs = attn_max_pieces(1);
+    constexpr int kLoads = (kFewPairs + kThreads - 1) / kThreads;
+    static_assert(attn_max_pieces(0) <= kThreads && kLoads * kJoinWarps == 64);
+    __shared__ int4 s_tiles[attn_max_pieces(0)], s_few[kFewPairs];
+    __shared__ int s_counts[kLoads + 1][kJoinWarps];
     __shared__ int s_wide[attn_max_pieces(1) / kJoinWide + 1], s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = p.group;
     pdl_wait();
-    const int n0 = p.hdr->splits[0][0], n1 = p.hdr->splits[1][0], wide = p.hdr->splits[1][1];
     auto write = [&](const int4 &e, int x, float top, float sum, const float (&acc)[kE]) {
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int64_t row = e.x + x / g;
@@ -265,11 +297,48 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2)
     };
     const int me = blockIdx.x + warp * kJoinCtas, warps = kJoinWarps * kJoinCtas;
 
+    // ---- the pairs of both kinds, closed up; those of very many pieces apart ----
+    const AttnLine &tl = p.line[0], &fl = p.line[1];
+    if (tid == 0)
+        s_n = 0;
+    int4 found[kLoads + 1];
+    uint32_t which[kLoads + 1];
+#pragma unroll
+    for (int k = 0; k <= kLoads; ++k) {
+        const int at = k < kLoads ? k * kThreads + tid : tid;
+        found[k] = make_int4(0, 0, 0, 0);
+        if (at < attn_max_pieces(k < kLoads))
+            found[k] = (k < kLoads ? fl : tl).split[at];
+    }
+#pragma unroll
+    for (int k = 0; k <= kLoads; ++k) {
+        which[k] = __ballot_sync(0xffffffffu, found[k].y != 0);
+        if (lane == 0)
+            s_counts[k][warp] = __popc(which[k]);
+    }
+    __syncthreads();
+    const int c0 = s_counts[0][2 * lane], c1 = s_counts[0][2 * lane + 1];   // (few: 64 counts)
+    const int upto = warp_inclusive_scan(c0 + c1);
+    const int upto0 = warp_inclusive_scan(lane < kJoinWarps ? s_counts[kLoads][lane] : 0);
+    const int n1 = __shfl_sync(0xffffffffu, upto, 31), n0 = __shfl_sync(0xffffffffu, upto0, 31);
+#pragma unroll
+    for (int k = 0; k <= kLoads; ++k) {
+        const int i = k * kJoinWarps + warp;
+        int at = k < kLoads ? __shfl_sync(0xffffffffu, upto - c1 - (i & 1 ? 0 : c0), i / 2 & 31)
+                            : __shfl_sync(0xffffffffu, upto0, warp) - __popc(which[k]);
+        at += __popc(which[k] & ((1u << lane) - 1));
+        if (found[k].y != 0) {
+            (k < kLoads ? s_few : s_tiles)[at] = found[k];
+            if (k < kLoads && found[k].w - found[k].z >= kJoinWide)
+                s_wide[atomicAdd(&s_n, 1)] = at;
+        }
+    }
+    __syncthreads();
+
     // ---- tiles: items of four rows of a pair ----
-    const AttnLine &tl = p.line[0];
     constexpr int kQuads = 2 * kTileRows / 4;
     for (int item = me; item < n0 * kQuads; item += warps) {
-        const int4 e = tl.split[item / kQuads];
+        const int4 e = s_tiles[item / kQuads];
         const int x0 = item % kQuads * 4, rows = (e.y & 511) * g;
         if (x0 >= rows)
             continue;
@@ -340,29 +409,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2)
     }
 
     // ---- few rows: items of a row of a pair ----
-    const AttnLine &fl = p.line[1];
     for (int item = me; item < n1 * kFewRows; item += warps) {
         const int row = item / n1;
-        const int4 e = fl.split[item - row * n1];
+        const int4 e = s_few[item - row * n1];
         if (row >= (e.y & 511) * g || e.w - e.z >= kJoinWide)
             continue;
         float top, sum, acc[kE];
         join_pieces<kE>(fl, kFewRows, e.z, e.z, e.w, 1, row, top, sum, acc);
         write(e, row, top, sum, acc);
     }
-    if (wide == 0)
-        return;
-    if (tid == 0)
-        s_n = 0;
-    __syncthreads();
-    for (int k = tid; k < n1; k += kJoinWarps * 32) {
-        const int4 e = fl.split[k];
-        if (e.w - e.z >= kJoinWide)
-            s_wide[atomicAdd(&s_n, 1)] = k;
-    }
-    __syncthreads();
     for (int i = 0; i < s_n; ++i) {
-        const int4 e = fl.split[s_wide[i]];
+        const int4 e = s_few[s_wide[i]];
         const int rows = (e.y & 511) * g;
         // (the CTAs may hold the list in different orders: a pair's rows go by the pair)
         for (int row = (blockIdx.x + kJoinCtas - e.z % kJoinCtas) % kJoinCtas; row < rows; row += kJoinCtas) {
@@ -518,17 +575,14 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     // a scale of zero still has to leave the hidden keys' -infinity as it is
     p.scale_log2 = std::fmax(std::fabs(softmax_scale) * 1.4426950408889634f, 0x1p-120f);
     p.negate = softmax_scale < 0.f;
-    p.hdr = reinterpret_cast<AttnHeader *>(ws + L.header);
     p.seq_units = reinterpret_cast<int32_t *>(ws + L.seq_units);
     for (int k = 0; k < 2; ++k)
         p.line[k] = AttnLine{reinterpret_cast<AttnUnit *>(ws + L.units[k]),
                              reinterpret_cast<AttnPiece *>(ws + L.pieces[k]),
-                             p.hdr->total + k,
                              reinterpret_cast<int64_t *>(ws + L.cum[k]),
                              reinterpret_cast<float *>(ws + L.part_o[k]),
                              reinterpret_cast<float2 *>(ws + L.part_ml[k]),
-                             reinterpret_cast<int4 *>(ws + L.split[k]),
-                             p.hdr->splits[k]};
+                             reinterpret_cast<int4 *>(ws + L.split[k])};
 
     AttnMaps m = {};
     const uint64_t D = head_dim, rows = static_cast<uint64_t>(num_pages) * nheads_kv;
@@ -555,7 +609,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     const bool few = group <= kFewRows;
     p.few_behind_tiles = tiles && few;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    attn_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     const bool bf16 = cache_type == SSD_KV_BF16, fp8 = cache_type == SSD_KV_FP8_E4M3;
     if (e == cudaSuccess && tiles)

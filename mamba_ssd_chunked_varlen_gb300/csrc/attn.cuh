@@ -35,22 +35,22 @@ static_assert(sizeof(AttnUnit) == 32, "unit size");
 // per warp (kind 1; fewer pieces when the line is short).  A pair that falls
 // into several pieces leaves partial results, at most two per piece.
 struct alignas(32) AttnPiece {
-    int64_t pos, end;             // its tiles of the line: [pos, end), none past the last piece
+    int32_t tiles;                // its tiles of the line, none past the last piece
     int32_t u, h, ta;             // unit, kv head and tile of the unit where it begins
-    int32_t pad;
+    int32_t pad[4];
+    AttnUnit e;                   // the unit
 };
 
 struct AttnLine {
     const AttnUnit *units;
     const AttnPiece *pieces;
-    const int64_t *total;         // key tiles of all units and kv heads
     int64_t *cum;                 // (units): key tiles before each unit, one head (the plan's)
     float *part_o;                // sums of p v: few [2 pieces][rows][dim], tiles
                                   // [2 pieces][dim / 4][rows][4]
     float2 *part_ml;              // [2 pieces][rows]: reference (log2), sum of p
-    int4 *split;                  // [pieces] the pairs with partial results, in any order:
-                                  // {row0, tokens + (kv head << 9), first piece, last piece}
-    int32_t *splits;              // how many: [0], of them over more than kJoinWide pieces: [1]
+    int4 *split;                  // [pieces] of a piece that begins within a pair begun by the
+                                  // one before: {row0, tokens + (kv head << 9), that piece, the
+                                  // pair's last}; zeros otherwise
 };
 
 // Most pieces of each kind, and the fewest tiles of one (every piece has a tile).
@@ -69,13 +69,6 @@ __host__ __device__ inline int attn_pieces(int kind, int64_t total)
 
 constexpr int kJoinWide = 128;    // pieces of a row that one warp of the join adds up
 
-struct AttnHeader {
-    int64_t total[2];             // per kind: 0 tiles, 1 few rows
-    int32_t splits[2][2];
-    int32_t pad[56];
-};
-static_assert(sizeof(AttnHeader) == 256, "header size");
-
 struct AttnParams {
     KvView c;
     __nv_bfloat16 *o;
@@ -88,7 +81,6 @@ struct AttnParams {
     float scale_log2;             // |softmax_scale| log2(e)
     int32_t negate;               // 1: softmax_scale < 0 (the scores change sign)
     int32_t few_behind_tiles;     // 1: the kernel of few rows follows the tiles' kernel
-    AttnHeader *hdr;
     int32_t *seq_units;           // (batch): units before each sequence
     AttnLine line[2];
 };
@@ -97,7 +89,7 @@ struct AttnParams {
 __host__ __device__ constexpr int attn_part_rows(int kind) { return kind ? kFewRows : 2 * kTileRows; }
 
 struct AttnLayout {
-    size_t header, seq_units, units[2], pieces[2], cum[2], split[2], part_ml[2], part_o[2], total;
+    size_t seq_units, units[2], pieces[2], cum[2], split[2], part_ml[2], part_o[2], total;
 };
 
 inline int64_t attn_max_units(int64_t total_len, int32_t batch, int32_t group)
@@ -116,7 +108,6 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
         off = (off + bytes + 255) & ~size_t(255);
         return at;
     };
-    L.header = take(sizeof(AttnHeader));
     L.seq_units = take(sizeof(int32_t) * (static_cast<size_t>(batch) + 1));
     for (int k = 0; k < 2; ++k) {
         const size_t rows = 2 * static_cast<size_t>(attn_max_pieces(k)) * attn_part_rows(k);
@@ -129,18 +120,6 @@ inline AttnLayout attn_layout(int64_t total_len, int32_t batch, int32_t group, i
     }
     L.total = off;
     return L;
-}
-
-// First tile of piece i of a line of `total` tiles in n pieces, floor(total i / n),
-// and the piece of tile t.
-__host__ __device__ inline int64_t attn_piece_begin(int64_t total, int n, int i)
-{
-    const int64_t q = total / n;
-    return q * i + static_cast<int>(total - q * n) * i / n;
-}
-__host__ __device__ inline int attn_piece_of(int64_t total, int n, int64_t t)
-{
-    return static_cast<int>(((t + 1) * n + total - 1) / total - 1);
 }
 
 // Partial-result slot of a piece: its first segment (one that does not start
@@ -163,28 +142,14 @@ struct AttnWalk {
         : line(l), heads(heads_)
     {
         const AttnPiece pc = line.pieces[piece];
-        left = static_cast<int32_t>(pc.end - pc.pos);
+        left = pc.tiles;
         u = pc.u;
         h = pc.h;
         ta = pc.ta;
-        tb = ta;
-        if (left > 0) {
-            e = line.units[u];
-            tb = min(ta + left, e.tiles);
-        }
+        e = pc.e;
+        tb = min(ta + left, e.tiles);
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
-    // Lists the pair of a segment that begins it and does not end it; by one lane.
-    __device__ __forceinline__ void note_split(int kind, int piece) const
-    {
-        if (ta != 0 || tb == e.tiles)
-            return;
-        const int64_t total = *line.total, pos = line.pieces[piece].end - left;
-        const int last = attn_piece_of(total, attn_pieces(kind, total), pos + e.tiles - 1);
-        line.split[atomicAdd(line.splits, 1)] = make_int4(e.row0, e.tokens + (h << 9), piece, last);
-        if (last - piece >= kJoinWide)
-            atomicAdd(line.splits + 1, 1);
-    }
     __device__ __forceinline__ void next()
     {
         left -= tb - ta;

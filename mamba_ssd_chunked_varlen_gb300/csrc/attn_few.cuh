@@ -537,8 +537,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         if constexpr (C::kAhead == 1)
             load.template next<0>();
         for (; w.more(); w.next()) {
-            if ((threadIdx.x & 31) == 0)
-                w.note_split(1, piece);
             if (w.e.tokens * p.group <= 8)
                 few_segment<kType, kDim, 1>(p, w, piece, slots, got, load);
             else

@@ -381,10 +381,6 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         ptx::mbar_wait(bars + kDrain + st, 0, kWaitTimeoutNs);
     } else if (warp == C::kIssuer + 2) {
         ptx::setmaxnreg_dec<C::kOtherRegs>();
-        // ------------------------------------------------ the list for the join
-        for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more(); w.next())
-            if (lane == 0)
-                w.note_split(0, blockIdx.x);
     } else if (warp >= 8) {
         ptx::setmaxnreg_dec<C::kOtherRegs>();
         const int ht = tid - 256;
@@ -404,30 +400,37 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                         break;
                     uint8_t *v = sKv + ((it + 1) % C::kStages) * C::kTile;
                     const int keys = w.e.kv_len - (w.e.tile0 + t) * kTileKeys;
+                    if (keys < kTileKeys) {
+#pragma unroll 1
+                        for (int i = ht; i < C::kTile / 16; i += 128)
+                            if (((i >> 3) & (kTileKeys - 1)) >= keys)
+                                *reinterpret_cast<uint4 *>(v + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    // (an exponent of ones carries into the sign's place)
                     bool found = false;
-                    for (int i = ht; i < C::kTile / 16; i += 128) {
-                        uint4 *at = reinterpret_cast<uint4 *>(v + i * 16);
-                        if (((i >> 3) & (kTileKeys - 1)) >= keys) {
-                            *at = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint4 x = *at;
-                        uint32_t *x4 = &x.x;
-                        bool bad = false;
+                    constexpr int kAtOnce = 8;
+                    static_assert(C::kTile / 16 % (128 * kAtOnce) == 0, "a thread's pieces");
+#pragma unroll 1
+                    for (int i = ht; i < C::kTile / 16; i += 128 * kAtOnce) {
+                        uint32_t any = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((x4[k] & 0x7f80u) == 0x7f80u) {
-                                x4[k] &= 0xffff0000u;
-                                bad = true;
-                            }
-                            if ((x4[k] & 0x7f800000u) == 0x7f800000u) {
-                                x4[k] &= 0xffffu;
-                                bad = true;
-                            }
+                        for (int k = 0; k < kAtOnce; ++k) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(v + (i + k * 128) * 16);
+                            any |= ((x.x & 0x7fff7fffu) + 0x00800080u) | ((x.y & 0x7fff7fffu) + 0x00800080u) |
+                                   ((x.z & 0x7fff7fffu) + 0x00800080u) | ((x.w & 0x7fff7fffu) + 0x00800080u);
                         }
-                        if (bad) {
+                        if (!(any & 0x80008000u))
+                            continue;
+                        found = true;
+#pragma unroll 1
+                        for (int k = 0; k < kAtOnce * 4; ++k) {
+                            uint32_t *at = reinterpret_cast<uint32_t *>(v + (i + k / 4 * 128) * 16) + k % 4;
+                            uint32_t x = *at;
+                            if ((x & 0x7f80u) == 0x7f80u)
+                                x &= 0xffff0000u;
+                            if ((x & 0x7f800000u) == 0x7f800000u)
+                                x &= 0xffffu;
                             *at = x;
-                            found = true;
                         }
                     }
                     if (found)
