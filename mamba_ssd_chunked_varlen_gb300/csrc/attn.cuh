@@ -53,18 +53,22 @@ struct AttnLine {
                                   // pair's last}; zeros otherwise
 };
 
-// Most pieces of each kind, and the fewest tiles of one (every piece has a tile).
+// Most pieces of each kind, and the pieces of a line of `total` tiles.  A short line
+// gets as few as leave the longest as short as it can be, because partial results
+// cost more than shorter pieces among them save (24 sequences, 2,900 tiles of few rows:
+// pieces of two 70.2 us, of one and two 72.2).  A long one gets them all: warps left
+// over would be missed (64 sequences decoding: 151.5 us, with the same rule 155.7).
 __host__ __device__ constexpr int attn_max_pieces(int kind)
 {
     return kind ? kAttnCtas * kFewWarps : kAttnCtas;
 }
-constexpr int kFewPieceTiles = 1;
-
 __host__ __device__ inline int attn_pieces(int kind, int64_t total)
 {
     const int most = attn_max_pieces(kind);
-    const int64_t n = kind ? (total + kFewPieceTiles - 1) / kFewPieceTiles : total;
-    return n < most ? static_cast<int>(n) : most;
+    const int64_t longest = (total + most - 1) / most;
+    if (longest > 4)
+        return most;
+    return total > 0 ? static_cast<int>((total + longest - 1) / longest) : 0;
 }
 
 constexpr int kJoinWide = 128;    // pieces of a row that one warp of the join adds up
