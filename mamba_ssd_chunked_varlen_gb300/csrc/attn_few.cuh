@@ -315,6 +315,7 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                 for (int r = 0; r < 2; ++r)
                     x[k / 2][n][k % 2 * 2 + r] *= C::kQuant ? ks * cr[n][r] : c2;
         }
+        uint32_t unseen = 0;     // a bit per score of the lane
         if (hides) {
 #pragma unroll
             for (int n = 0; n < kN; ++n)
@@ -325,8 +326,10 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int j = j0 + i + k * 8;
-                        if (j < lo || j > pos)
+                        if (j < lo || j > pos) {
                             x[k / 2][n][k % 2 * 2 + r] = -INFINITY;
+                            unseen |= 1u << ((k * kN + n) * 2 + r);
+                        }
                     }
                 }
         }
@@ -376,24 +379,32 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
         slot = slots + got;
         got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
         load.template next<1 - C::kAhead>();
-        uint32_t pb[2][kN][2];
-        scales = reinterpret_cast<const float *>(slot + 2 * C::kHalf) + i;
+        if constexpr (C::kQuant) {
+            scales = reinterpret_cast<const float *>(slot + 2 * C::kHalf) + i;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float vs = 1.f;
-            if constexpr (C::kQuant)
-                vs = scales[8 * k];
+            for (int k = 0; k < 4; ++k) {
+                const float vs = scales[8 * k];
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                float a = x[k / 2][n][k % 2 * 2], b = x[k / 2][n][k % 2 * 2 + 1];
-                if constexpr (C::kQuant) {
-                    // (a hidden key's scale may be NaN: its weight stays zero)
-                    a = hides && a == 0.f ? 0.f : a * vs;
-                    b = hides && b == 0.f ? 0.f : b * vs;
-                }
-                pb[k / 2][n][k % 2] = ptx::transpose8(pack_bf16(a, b));
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        // (a hidden key's scale may be NaN)
+                        float &w = x[k / 2][n][k % 2 * 2 + r];
+                        w = unseen >> ((k * kN + n) * 2 + r) & 1 ? 0.f : w * vs;
+                    }
             }
         }
+        uint32_t pb[2][kN][2], pl[2][kN][2];     // the weights as two bf16 each
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                const float a = x[k / 2][n][k % 2 * 2], b = x[k / 2][n][k % 2 * 2 + 1];
+                const uint32_t top = pack_bf16(a, b);
+                pb[k / 2][n][k % 2] = ptx::transpose8(top);
+                pl[k / 2][n][k % 2] = ptx::transpose8(pack_bf16(
+                    a - __uint_as_float(top << 16), b - __uint_as_float(top & 0xffff0000u)));
+            }
 #pragma unroll
         for (int k = 0; k < C::kVPieces; ++k)
 #pragma unroll
@@ -428,8 +439,10 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                         for (int j = 0; j < 2; ++j) {
                             const uint32_t f[4] = {a[2 * j], a[2 * j + 1], b[2 * j], b[2 * j + 1]};
 #pragma unroll
-                            for (int n = 0; n < kN; ++n)
+                            for (int n = 0; n < kN; ++n) {
                                 ptx::mma_16816(o[n][s * 2 + j], f, pb[u][n][0], pb[u][n][1]);
+                                ptx::mma_16816(o[n][s * 2 + j], f, pl[u][n][0], pl[u][n][1]);
+                            }
                         }
                     }
                 } else {
@@ -452,8 +465,10 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                             __byte_perm(v[0][s], v[1][s], 0x5410), __byte_perm(v[0][s], v[1][s], 0x7632),
                             __byte_perm(v[2][s], v[3][s], 0x5410), __byte_perm(v[2][s], v[3][s], 0x7632)};
 #pragma unroll
-                        for (int n = 0; n < kN; ++n)
+                        for (int n = 0; n < kN; ++n) {
                             ptx::mma_16816(o[n][k * 4 + s], f, pb[u][n][0], pb[u][n][1]);
+                            ptx::mma_16816(o[n][k * 4 + s], f, pl[u][n][0], pl[u][n][1]);
+                        }
                     }
                 }
             }

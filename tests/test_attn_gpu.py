@@ -149,6 +149,25 @@ def test_hidden_rows_of_quantised_cache(kind):
         assert torch.isnan(o[sees][:, 2:]).all()
 
 
+@pytest.mark.parametrize("new", [2, 40])
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+def test_nan_scale_of_negligible_key(kind, new):
+    """A value's scale of NaN reaches the rows that see it even where the key's
+    probability underflows to zero, in a tile that hides other keys."""
+    import torch
+    b = Batch([(new, 40)], 4, 2, 64, 16, kind, seed=11)
+    b.q.fill_(8.0)
+    b.k_seq[0].mul_(0.125)
+    b.k_seq[0][33] = -8.0            # its score is -512: 2^-738 next to the others
+    b.fill()
+    p, r = b.row_of(0, 33)
+    b.v_scale[p, 0, r] = float("nan")
+    o, _ = b.attend()
+    sees = torch.arange(40 - new, 40, device=o.device) >= 33
+    assert torch.isnan(o[sees][:, :2]).all()
+    assert torch.isfinite(o[~sees]).all() and torch.isfinite(o[:, 2:]).all()
+
+
 def test_strides():
     """q as a slice of a fused projection, o a slice of a wider buffer, the table
     a slice of a wider one."""
