@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     const int tid = threadIdx.x;
     const int unit_tokens = 2 * p.tile_tokens;
     int32_t *seq_units = c.batch <= kPlanBatch ? s_units : p.seq_units;
+    pdl_wait();                  // (the launch alone goes ahead of its predecessor's end)
     pdl_launch_dependents();
     int64_t units = 0;
     int bad = 0;
@@ -613,8 +614,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     const bool few = group <= kFewRows;
     p.few_behind_tiles = tiles && few;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    attn_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_pdl(attn_plan_kernel, dim3(kPlanCtas), kPlanThreads, stream, p);
     const bool bf16 = cache_type == SSD_KV_BF16, fp8 = cache_type == SSD_KV_FP8_E4M3;
     if (e == cudaSuccess && tiles)
         e = bf16 ? launch_attn_bf16(p, m, stream)
