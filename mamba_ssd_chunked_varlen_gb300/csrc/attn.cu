@@ -505,21 +505,6 @@ bool sizes_ok(int64_t total_len, int32_t batch, int32_t nheads, int32_t nheads_k
            (head_dim == 64 || head_dim == 128);
 }
 
-template <typename... Args>
-cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, args...);
-}
-
 }  // namespace
 }  // namespace ssd
 

@@ -10,6 +10,23 @@
 
 namespace ssd {
 
+// Launches a kernel that begins with pdl_wait() (or ends with it, see attn_few.cuh)
+// ahead of its predecessor's end.
+template <typename... Args>
+inline cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 // Smallest row maximum that a quantised row is scaled by: M / a and a / M stay
 // normal fp32 numbers for every row, all zeros among them.
 constexpr float kKvTiny = 8.673617379884035e-19f;   // 2^-60

@@ -8,6 +8,7 @@
 #include <cuda_fp8.h>
 
 #include "attn_common.cuh"
+#include "ssd_device.cuh"
 
 namespace ssd {
 
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     constexpr int kLanes = kDim / 8;           // lanes of a row
     constexpr int kAtOnce = 32 / kLanes;       // rows of the warp's one load
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
     const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens;
     if (blockIdx.x == 0 && blockIdx.y == 0) {   // one CTA looks the offsets over
         bool bad = false;
@@ -310,11 +312,8 @@ cudaError_t launch(const KvView &c, void *k, void *v, int64_t ks, int64_t vs, cu
     const int64_t tokens = kWarps * (many ? kMany : 1);
     const dim3 grid(static_cast<unsigned>((c.total_len + tokens - 1) / tokens), parts);
     __nv_bfloat16 *kk = static_cast<__nv_bfloat16 *>(k), *vv = static_cast<__nv_bfloat16 *>(v);
-    if (many)
-        kv_copy_kernel<kType, kDim, kWrite, kMany><<<grid, kWarps * 32, 0, stream>>>(c, kk, vv, ks, vs);
-    else
-        kv_copy_kernel<kType, kDim, kWrite, 1><<<grid, kWarps * 32, 0, stream>>>(c, kk, vv, ks, vs);
-    return cudaGetLastError();
+    return launch_pdl(many ? kv_copy_kernel<kType, kDim, kWrite, kMany> : kv_copy_kernel<kType, kDim, kWrite, 1>,
+                      grid, kWarps * 32, stream, c, kk, vv, ks, vs);
 }
 
 template <bool kWrite>
