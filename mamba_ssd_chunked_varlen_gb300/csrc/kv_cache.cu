@@ -173,8 +173,8 @@ __device__ __forceinline__ int64_t place_tokens(const KvView &c, int64_t t)
 // place takes five loads in a row.  A write loads its rows meanwhile; a read has
 // to wait, so that with many tokens a warp places four at once and has all of their
 // rows in flight together, while a few tokens are spread over warps.  Memory bounds
-// a long int8 read (403 MB of codes and rows in 67.6 us, 88 % of the copy rate; one
-// token a warp 81.8), the instructions per element a quantising write.
+// a long int8 read (403 MB of codes and rows in 65.3 us, 91 % of the copy rate; one
+// token a warp 14 us more), the instructions per element a quantising write.
 template <int kType, int kDim, bool kWrite, int kTokens>
 __global__ void __launch_bounds__(kWarps * 32)
     kv_copy_kernel(const __grid_constant__ KvView c, __nv_bfloat16 *k, __nv_bfloat16 *v, int64_t k_stride,
