@@ -20,9 +20,9 @@
 // warps exponentiate, the tensor cores run the other's products.  A tile's scores come
 // in two halves of 64 keys, so that the first half's probabilities are there before
 // the second half's scores are (830 us as a whole, 796 in halves).
-//   warps 0-3, 4-7   softmax and output of stream 0 and 1: a thread per row, a half
-//                    tile's 64 scores in registers; probabilities are rounded once, to
-//                    bf16, the operand's type, in the scores' place
+//   warps 0-3, 4-7   softmax and output of stream 0 and 1: 64 scores a thread, of one
+//                    row or of four; probabilities are rounded once, to bf16, the
+//                    operand's type, in the scores' place
 //   four warps more  bf16: clean the V tiles that hold rows nobody may see;
 //   (8-bit: eight)   8-bit: widen codes to bf16 tiles (exact: 8 bits at most)
 //   one              TMA producer: Q, K and V page by page
@@ -32,11 +32,12 @@
 // sequences of 700 to 1,111 tokens with a window of 1,024 take 73 us, 63 so.
 //
 // Measured: 2,048 tokens of 32 heads over 32,768 keys of 8 kv heads of 128, bf16:
-// 755 us, 1.41 PFLOP/s, 73 % of the burst rate of a plain matrix product; the tensor
+// 750 us, 1.42 PFLOP/s, 73 % of the burst rate of a plain matrix product; the tensor
 // pipes are busy 77 % of the time, at the board's power limit.  The same heads, two
-// sequences of 1,024 tokens over 12,001 to 16,383 fp8 keys: 544 us, 0.83 PFLOP/s; there
-// shared memory is the busiest (codes in, out and in again as bf16, beside what the
-// products read) and the way from a code to a product the longest.
+// sequences of 1,024 tokens over 12,001 to 16,383 fp8 keys: 484 us, 0.93 PFLOP/s; there
+// the softmax and the widening share the schedulers and shared memory, and the way
+// from a code to a product is long (with three tiles for products and three of codes
+// instead of four and one: 14 us more).
 #pragma once
 
 #include "attn_codes.cuh"
@@ -65,8 +66,8 @@ struct Cfg {
     static constexpr int kBlocks = kDim / 64;
     static constexpr int kTile = kBlocks * kBlk;             // a bf16 tile of 128 rows
     static constexpr int kRaw = kTileKeys * kDim;            // the same in 8-bit codes
-    static constexpr int kStages = (kQuant ? 3 : 5) * (128 / kDim) - (kQuant || kDim == 128 ? 0 : 2);
-    static constexpr int kRawStages = kQuant ? 3 * (128 / kDim) : 0;
+    static constexpr int kStages = (kQuant ? 4 : 5) * (128 / kDim) - (kQuant || kDim == 128 ? 0 : 2);
+    static constexpr int kRawStages = kQuant ? 128 / kDim : 0;
     // shared memory, from a 1024-byte boundary
     static constexpr int kQOff = 0;
     static constexpr int kKvOff = kQOff + 2 * kTile;
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kTileKeys / kRows; ++k)
                             x[k] = *reinterpret_cast<const uint4 *>(src + k * kRows * kDim);
+                        ptx::mbar_arrive(bars + kRawEmpty + rs);
                         if (keys < kTileKeys) {
 #pragma unroll
                             for (int k = 0; k < kTileKeys / kRows; ++k)
@@ -519,18 +521,41 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                             }
                         }
                         ptx::fence_proxy_async_smem();
-                        ptx::mbar_arrive(bars + kRawEmpty + rs);
                         ptx::mbar_arrive(bars + kKvFull + s);
                     }
         }
     } else {
         ptx::setmaxnreg_inc<C::kSoftmaxRegs>();
         // ------------------------------------------------------------ softmax
-        const int st = warp >> 2, row = tid & 127;
+        // bf16: a thread has all 64 scores of its row.  8-bit caches: scores come in the
+        // fragments of a matrix product, with i = lane / 4, q = lane % 4, of rows i, i + 8,
+        // i + 16 and i + 24 of the warp the columns 2q and 2q + 1 of every eight, so that
+        // a thread needs a quarter of the keys' scales.  (A row's thread needs them all:
+        // their 16-byte reads then take more of shared memory's time than the codes,
+        // 542 us instead of 484 for the chunks above.  Without scales rows are faster,
+        // 50.3 instead of 53.4 us for the windows.)
+        constexpr int kR = C::kQuant ? 4 : 1;      // a thread's rows
+        constexpr int kPairs = 32 / kR;            // pairs of a row's scores
+        const int st = warp >> 2, row = tid & 127, fi = lane >> 2, fq = kR == 4 ? lane & 3 : 0;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t colS = tmem + st * 128 + lanes, colO = tmem + C::kColO + st * kDim + lanes;
-        const int my_tok = row / g, my_head = row % g;
+        int row_tok[kR];
+#pragma unroll
+        for (int j = 0; j < kR; ++j)
+            row_tok[j] = (kR == 4 ? (warp & 3) * 32 + j * 8 + fi : row) / g;
         const int warp_tok0 = (warp & 3) * 32 / g, warp_tok1 = ((warp & 3) * 32 + 31) / g;
+        // of the rows' values, the one of row `lane`
+        auto of_row = [&](const float (&v)[kR]) {
+            float r = v[0];
+            if constexpr (kR == 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = __shfl_sync(0xffffffffu, v[j], (lane & 7) * 4);
+                    r = lane >> 3 == j ? x : r;
+                }
+            }
+            return r;
+        };
         const float c2 = p.scale_log2;
         uint32_t it = 0, sit = 0, oit = 0;
         for (AttnWalk w(p.line[0], p.c.heads, blockIdx.x); w.more() && ok; w.next()) {
@@ -540,20 +565,20 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
             }
             const int tok0 = st * tt;
             const int ntok = min(tt, w.e.tokens - tok0);        // tokens of this stream
-            const bool mine = my_tok < ntok;
-            const int pos = w.e.pos0 + tok0 + (mine ? my_tok : ntok - 1);
-            const int hi = pos + 1;
-            const int lo = p.window > 0 ? pos - p.window + 1 : INT32_MIN / 2;
             // of the warp's rows: first and last position, or none
             const int pos0 = w.e.pos0 + tok0 + warp_tok0;
             const int pos1 = warp_tok0 < ntok ? w.e.pos0 + tok0 + min(warp_tok1, ntok - 1) : INT32_MIN / 2;
             const int back = p.window > 0 ? p.window : INT32_MAX / 2;
             // reference, times c (a row that is none has one, and asks for no other)
-            float m = mine ? -INFINITY : 0.f;
-            float l = 0.f;
+            float m[kR], l[kR];
+#pragma unroll
+            for (int j = 0; j < kR; ++j) {
+                m[j] = row_tok[j] < ntok ? -INFINITY : 0.f;
+                l[j] = 0.f;
+            }
             for (int t = w.ta; t < w.tb && ok; ++t, ++it, ++sit) {
                 // (the converter has seen the scales land)
-                const float *sc = sScale + (sit % kSlots8) * 2 * kTileKeys;
+                const float *sc = sScale + (sit % kSlots8) * 2 * kTileKeys + 2 * fq;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, sc += 64) {
                     const uint32_t col = colS + half * 64;
@@ -565,107 +590,152 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                     if (!wait(kSFull + st * 2 + half, it))
                         break;
                     ptx::tc_fence_after_sync();
-                    uint32_t a[32], b[32], pk[32];
-                    float a0 = 0.f, a1 = 0.f;
+                    // a row's halves, or [rows i, i + 8 | i + 16, i + 24]
+                    uint32_t s[2][32], pk[2][16];
+                    constexpr int kAcc = kR == 4 ? 4 : 2;
+                    uint64_t acc[kAcc];
+#pragma unroll
+                    for (int j = 0; j < kAcc; ++j)
+                        acc[j] = ptx::pack2(0.f, 0.f);
                     if (!some) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            pk[k] = 0;
+                        for (int k = 0; k < 16; ++k)
+                            pk[0][k] = pk[1][k] = 0;
                     }
 #pragma unroll 1
                     for (int pass = 0; some; ++pass) {
                         // ---- 64 scores: sign, hidden keys ----
-                        ptx::tmem_ld32_nowait(col, a);
-                        ptx::tmem_ld32_nowait(col + 32, b);
+                        if constexpr (kR == 4) {
+                            ptx::tmem_ld_16x64(col, s[0]);
+                            ptx::tmem_ld_16x64(col + (16u << 16), s[1]);
+                        } else {
+                            ptx::tmem_ld32_nowait(col, s[0]);
+                            ptx::tmem_ld32_nowait(col + 32, s[1]);
+                        }
                         ptx::tmem_wait_ld();
-                        auto each = [&](auto f) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                a[k] = f(a[k], k);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                b[k] = f(b[k], 32 + k);
+                        // element e of pair k of row j, and its first column
+                        auto score = [&](int j, int k, int e) -> uint32_t & {
+                            if constexpr (kR == 4)
+                                return s[j / 2][k * 4 + j % 2 * 2 + e];
+                            else
+                                return s[k / 16][k % 16 * 2 + e];
                         };
-                        if (!C::kQuant && p.negate)
-                            each([&](uint32_t v, int) { return v ^ 0x80000000u; });
+                        constexpr int kStep = kR == 4 ? 8 : 2;
+                        if (!C::kQuant && p.negate) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                s[0][k] ^= 0x80000000u;
+                                s[1][k] ^= 0x80000000u;
+                            }
+                        }
                         if (hides) {
                             // (a bit per key: the compiler moves eight to predicates at a time;
                             // the factors of an 8-bit cache's scores have the scale's sign)
                             auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; };
-                            const uint32_t v0 = below(hi - k0) & ~below(lo - k0);
-                            const uint32_t v1 = below(hi - k0 - 32) & ~below(lo - k0 - 32);
                             const uint32_t hidden = C::kQuant && p.negate ? 0x7f800000u : 0xff800000u;
-                            each([&](uint32_t v, int k) {
-                                return ((k < 32 ? v0 : v1) >> (k & 31) & 1) ? v : hidden;
-                            });
+#pragma unroll
+                            for (int j = 0; j < kR; ++j) {
+                                const int pos = w.e.pos0 + tok0 + min(row_tok[j], ntok - 1);
+                                const int hi = pos + 1 - k0 - 2 * fq;
+                                const int lo = p.window > 0 ? hi - p.window : INT32_MIN / 2;
+                                const uint32_t v0 = below(hi) & ~below(lo);
+                                const uint32_t v1 = below(hi - 32) & ~below(lo - 32);
+#pragma unroll
+                                for (int k = 0; k < kPairs; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int at = k * kStep + e;
+                                        uint32_t &x = score(j, k, e);
+                                        x = (at < 32 ? v0 : v1) >> (at & 31) & 1 ? x : hidden;
+                                    }
+                            }
                         }
                         const uint64_t c22 = ptx::pack2(c2, c2);
-                        auto factors = [&](int k) {    // of scores k .. k + 3, to log2 units
+                        auto factors = [&](int k) -> uint64_t {    // of pair k, to log2 units
                             if constexpr (C::kQuant)
-                                return *reinterpret_cast<const ulonglong2 *>(sc + k);
+                                return *reinterpret_cast<const uint64_t *>(sc + k * 8);
                             else
-                                return make_ulonglong2(c22, c22);
+                                return c22;
                         };
-                        auto maximum = [&] {
-                            float x0 = -INFINITY, x1 = -INFINITY;
-                            auto quarter = [&](const uint32_t (&s)[32], int k0) {
+                        auto pair = [&](int j, int k) {
+                            return ptx::pack2(__uint_as_float(score(j, k, 0)), __uint_as_float(score(j, k, 1)));
+                        };
+                        auto maxima = [&](float (&x)[kR]) {
+                            float x2[kAcc];
 #pragma unroll
-                                for (int k = 0; k < 32; k += 4) {
-                                    const ulonglong2 f = factors(k0 + k);
-                                    float e0, e1, e2, e3;
-                                    ptx::unpack2(ptx::mul2(ptx::pack2(__uint_as_float(s[k]),
-                                                                      __uint_as_float(s[k + 1])), f.x), e0, e1);
-                                    ptx::unpack2(ptx::mul2(ptx::pack2(__uint_as_float(s[k + 2]),
-                                                                      __uint_as_float(s[k + 3])), f.y), e2, e3);
-                                    x0 = max3(x0, e0, e1);
-                                    x1 = max3(x1, e2, e3);
+                            for (int j = 0; j < kAcc; ++j)
+                                x2[j] = -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < kPairs; ++k) {
+                                const uint64_t f = factors(k);
+#pragma unroll
+                                for (int j = 0; j < kR; ++j) {
+                                    float e0, e1, &to = x2[kR == 4 ? j : k & 1];
+                                    ptx::unpack2(ptx::mul2(pair(j, k), f), e0, e1);
+                                    to = max3(to, e0, e1);
                                 }
-                            };
-                            quarter(a, 0);
-                            quarter(b, 32);
-                            return fmaxf(x0, x1);
+                            }
+#pragma unroll
+                            for (int j = 0; j < kR; ++j) {
+                                x[j] = kR == 4 ? x2[j] : fmaxf(x2[0], x2[1]);
+                                if constexpr (kR == 4) {
+                                    x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
+                                    x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
+                                }
+                            }
                         };
                         // rows that have seen no key take the half's maximum as reference
                         // (O and l are zero)
-                        if (__any_sync(0xffffffffu, m == -INFINITY)) {
-                            const float mx = maximum();
-                            m = m == -INFINITY ? mx : m;
+                        float least = m[0];
+#pragma unroll
+                        for (int j = 1; j < kR; ++j)
+                            least = fminf(least, m[j]);
+                        if (__any_sync(0xffffffffu, least == -INFINITY)) {
+                            float mx[kR];
+                            maxima(mx);
+#pragma unroll
+                            for (int j = 0; j < kR; ++j)
+                                m[j] = m[j] == -INFINITY ? mx[j] : m[j];
                         }
                         // ---- probabilities, and their sum ----
-                        const float me = m == -INFINITY ? 0.f : m;
-                        const uint64_t nm = ptx::pack2(-me, -me);
-                        uint64_t acc0 = ptx::pack2(0.f, 0.f), acc1 = acc0;
-                        auto probabilities = [&](const uint32_t (&s)[32], int k0, uint32_t *pk) {
+                        uint64_t nm[kR];
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                const ulonglong2 f = factors(k0 + k);
-                                float e0, e1, e2, e3;
-                                ptx::unpack2(
-                                    ptx::fma2(ptx::pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f.x, nm),
-                                    e0, e1);
-                                ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[k + 2]),
-                                                                  __uint_as_float(s[k + 3])), f.y, nm),
-                                             e2, e3);
-                                uint64_t p0 = ptx::pack2(ptx::ex2(e0), ptx::ex2(e1));
-                                uint64_t p1 = ptx::pack2(ptx::ex2(e2), ptx::ex2(e3));
-                                acc0 = ptx::add2(acc0, p0);
-                                acc1 = ptx::add2(acc1, p1);
-                                if constexpr (C::kQuant) {
-                                    const ulonglong2 v =
-                                        *reinterpret_cast<const ulonglong2 *>(sc + kTileKeys + k0 + k);
-                                    p0 = ptx::mul2(p0, v.x);
-                                    p1 = ptx::mul2(p1, v.y);
-                                }
-                                ptx::unpack2(p0, e0, e1);
-                                ptx::unpack2(p1, e2, e3);
-                                pk[k / 2] = pack_bf16(e0, e1);
-                                pk[k / 2 + 1] = pack_bf16(e2, e3);
+                        for (int j = 0; j < kR; ++j) {
+                            const float me = m[j] == -INFINITY ? 0.f : -m[j];
+                            nm[j] = ptx::pack2(me, me);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kAcc; ++j)
+                            acc[j] = ptx::pack2(0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < kPairs; ++k) {
+                            const uint64_t f = factors(k);
+#pragma unroll
+                            for (int j = 0; j < kR; ++j) {
+                                float e0, e1;
+                                ptx::unpack2(ptx::fma2(pair(j, k), f, nm[j]), e0, e1);
+                                uint64_t x = ptx::pack2(ptx::ex2(e0), ptx::ex2(e1));
+                                uint64_t &to = acc[kR == 4 ? j : k & 1];
+                                to = ptx::add2(to, x);
+                                if constexpr (C::kQuant)
+                                    x = ptx::mul2(x, *reinterpret_cast<const uint64_t *>(sc + kTileKeys + k * 8));
+                                ptx::unpack2(x, e0, e1);
+                                if constexpr (kR == 4)
+                                    pk[j / 2][k * 2 + j % 2] = pack_bf16(e0, e1);
+                                else
+                                    pk[k / 16][k % 16] = pack_bf16(e0, e1);
                             }
-                        };
-                        probabilities(a, 0, pk);
-                        probabilities(b, 32, pk + 16);
-                        ptx::unpack2(ptx::add2(acc0, acc1), a0, a1);
-                        if (pass || !__any_sync(0xffffffffu, mine && !(a0 + a1 <= kRescale)))
+                        }
+                        if constexpr (kR == 1)
+                            acc[0] = ptx::add2(acc[0], acc[1]);
+                        float most = 0.f;        // (not a number: asks as well)
+#pragma unroll
+                        for (int j = 0; j < kR; ++j) {
+                            float a0, a1;
+                            ptx::unpack2(acc[j], a0, a1);
+                            most = row_tok[j] < ntok && !(a0 + a1 <= kRescale) ? INFINITY : most;
+                        }
+                        if (pass || !__any_sync(0xffffffffu, most > 0.f))
                             break;
                         // rare: scores far above the reference.  Once the product under way is
                         // done, the rows of the warp take new ones, and the half is done again
@@ -673,10 +743,16 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                         if (!first && !wait(kPvDone + st * 2 + (half ^ 1), half ? it : it - 1))
                             break;
                         ptx::tc_fence_after_sync();
-                        const float mn = fmaxf(m, maximum());
-                        const float f = mn == m ? 1.f : ptx::ex2(m - mn);
-                        m = mn;
-                        l *= f;
+                        float f[kR], mx[kR];
+                        maxima(mx);
+#pragma unroll
+                        for (int j = 0; j < kR; ++j) {
+                            const float mn = fmaxf(m[j], mx[j]);
+                            f[j] = mn == m[j] ? 1.f : ptx::ex2(m[j] - mn);
+                            m[j] = mn;
+                            l[j] *= f[j];
+                        }
+                        const float by = of_row(f);
 #pragma unroll 1
                         for (int k = 0; k < (first ? 0 : kDim); k += 16) {
                             float o[16];
@@ -684,14 +760,24 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                             ptx::tmem_ld16(colO + k, o);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                r[i] = __float_as_uint(o[i] * f);
+                                r[i] = __float_as_uint(o[i] * by);
                             ptx::tmem_st16(colO + k, r);
                         }
                     }
                     // (in the place of scores already read)
-                    ptx::tmem_st16(col, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
-                    ptx::tmem_st16(col + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
-                    l += a0 + a1;
+                    if constexpr (kR == 4) {
+                        ptx::tmem_st_16x32(col, pk[0]);
+                        ptx::tmem_st_16x32(col + (16u << 16), pk[1]);
+                    } else {
+                        ptx::tmem_st16(col, pk[0]);
+                        ptx::tmem_st16(col + 16, pk[1]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kR; ++j) {
+                        float a0, a1;
+                        ptx::unpack2(acc[j], a0, a1);
+                        l[j] += a0 + a1;
+                    }
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before_sync();
                     __syncwarp();
@@ -704,9 +790,20 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
             ptx::tc_fence_after_sync();
             // ---- output: the segment's rows, or their partial sums ----
             const bool nonfinite = !C::kQuant && *s_nonfinite, whole = w.whole();
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            if constexpr (kR == 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
+                    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
+                }
+            }
+            // a thread per row from here on
+            const float sum = of_row(l), top = of_row(m);
+            const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+            const int my_tok = row / g;
+            const bool mine = my_tok < ntok;
             const int64_t grow = w.e.row0 + tok0 + my_tok;
-            const int head = w.h * g + my_head;
+            const int head = w.h * g + row % g;
             const int64_t slot = attn_slot(blockIdx.x, w.starts());
             // where this thread stores: of four rows (its own and its neighbours') a
             // sixteen-byte piece each, so that four lanes fill 64 bytes of a row; a
@@ -733,7 +830,9 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         v[i] = __uint_as_float(o[i]);
-                    add_nonfinite<kDim>(p, w.e, w.h, w.ta, w.tb, hi, lo, k, v);
+                    const int pos = w.e.pos0 + tok0 + my_tok;
+                    add_nonfinite<kDim>(p, w.e, w.h, w.ta, w.tb, pos + 1,
+                                        p.window > 0 ? pos - p.window + 1 : 0, k, v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         o[i] = __float_as_uint(v[i]);
@@ -772,9 +871,9 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
             }
             if (mine) {
                 if (!w.whole())
-                    p.line[0].part_ml[slot * (2 * kTileRows) + st * 128 + row] = make_float2(m, l);
+                    p.line[0].part_ml[slot * (2 * kTileRows) + st * 128 + row] = make_float2(top, sum);
                 else if (p.lse)
-                    p.lse[grow * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                    p.lse[grow * p.heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
             }
             // (the next segment's first product waits for this warp's next P)
             ptx::tc_fence_before_sync();
