@@ -33,7 +33,7 @@
 //
 // Measured: 2,048 tokens of 32 heads over 32,768 keys of 8 kv heads of 128, bf16:
 // 750 us, 1.42 PFLOP/s, 73 % of the burst rate of a plain matrix product; the tensor
-// pipes are busy 77 % of the time, at the board's power limit.  The same heads, two
+// pipes are busy 80 % of the time, at the board's power limit.  The same heads, two
 // sequences of 1,024 tokens over 12,001 to 16,383 fp8 keys: 484 us, 0.93 PFLOP/s; there
 // the softmax and the widening share the schedulers and shared memory, and the way
 // from a code to a product is long (with three tiles for products and three of codes
