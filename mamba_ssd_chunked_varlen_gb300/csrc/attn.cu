@@ -14,7 +14,8 @@ namespace {
 // Cuts the call into units (AttnUnit), in the order of the rows, lays their key tiles
 // on the two lines and finds where every piece begins.  Every CTA makes the units for
 // itself and an eighth of the pieces: one CTA for all took 10 us, eight take 6.5.
-constexpr int kPlanThreads = 1024;
+// Up to 256 sequences, 256 threads: shorter barriers (a call is 1 us shorter).
+constexpr int kPlanThreads = 1024, kPlanSmall = 256;
 constexpr int kPlanCtas = 8;
 constexpr int kPlanBatch = 4096;    // up to so many sequences, their first units stay on chip,
 constexpr int kPlanUnits = 1024;    // and so many units of a kind, their first tiles
@@ -35,7 +36,7 @@ __device__ __forceinline__ void block_scan(int64_t (&v)[kN], int64_t (*scratch)[
     }
     __syncthreads();
     if (warp < kN)
-        scratch[warp][lane] = warp_inclusive_scan(scratch[warp][lane]);
+        scratch[warp][lane] = warp_inclusive_scan(lane < blockDim.x / 32 ? scratch[warp][lane] : 0);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     pdl_launch_dependents();
     int64_t units = 0;
     int bad = 0;
-    for (int base = 0; base < c.batch; base += kPlanThreads) {
+    for (int base = 0; base < c.batch; base += blockDim.x) {
         const int b = base + tid;
         int64_t n[1] = {0}, all[1];
         if (b < c.batch) {
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     bad = __syncthreads_or(bad);
     // this CTA's pieces, of both kinds one after the other
     constexpr int kEach = (attn_max_pieces(0) + attn_max_pieces(1) + kPlanCtas - 1) / kPlanCtas;
-    static_assert(kEach <= kPlanThreads, "a piece per thread");
+    static_assert(kEach <= kPlanSmall, "a piece per thread");
     const int my_piece = blockIdx.x * kEach + tid;
     const int my_kind = my_piece < attn_max_pieces(0) ? 0 : 1;
     const int i = my_piece - (my_kind ? attn_max_pieces(0) : 0);
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         return;
     }
     int64_t tiles[2] = {0, 0}, count[2] = {0, 0};
-    for (int64_t base = 0; base < units; base += kPlanThreads) {
+    for (int64_t base = 0; base < units; base += blockDim.x) {
         const int64_t u = base + tid;
         AttnUnit e = {};
         int kind = 0;
@@ -599,7 +600,8 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     const bool few = group <= kFewRows;
     p.few_behind_tiles = tiles && few;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    cudaError_t e = launch_pdl(attn_plan_kernel, dim3(kPlanCtas), kPlanThreads, stream, p);
+    cudaError_t e = launch_pdl(attn_plan_kernel, dim3(kPlanCtas),
+                               batch <= kPlanSmall ? kPlanSmall : kPlanThreads, stream, p);
     const bool bf16 = cache_type == SSD_KV_BF16, fp8 = cache_type == SSD_KV_FP8_E4M3;
     if (e == cudaSuccess && tiles)
         e = bf16 ? launch_attn_bf16(p, m, stream)
