@@ -7,7 +7,8 @@
 // piece of the line of 32-key tiles, with its own running maximum and sum, in
 // registers.  (Tiles of the other kind from 9 rows on: 32 sequences of 15 rows 66 us
 // instead of 58.)  Keys take the 16-row side of the products and query rows the
-// 8-column side, so that eight rows (or twice eight) waste nothing:
+// 8-column side, so that eight rows (or twice eight) waste nothing (few_segment16: the
+// other way round):
 //
 //   X = c (K Q^T),  m' = max(m, max X),  P = 2^(X - m'),  l = l 2^(m - m') + sum P,
 //   O^T = O^T 2^(m - m') + V^T P
@@ -26,7 +27,7 @@
 // context's end are filled with zeros, so nothing is read that no sequence owns.
 //
 // Measured, with 32 query heads on 8 kv heads of 128: 64 sequences of up to 8,192
-// int8 keys, one token each: 137 us for 639 MB, 4.7 TB/s, 69 % of the copy rate.  Each
+// int8 keys, one token each: 137 us of the call's 149, for 639 MB, 4.7 TB/s, 69 % of the copy rate.  Each
 // scheduler has three warps, which wait for one another's widening and products
 // more than for memory (issue 51 %, integer pipe 56 %); more warps have too few
 // registers (12 warps of 168: 152 us a call, 14 of 144: 179, 16 of 128: 162).  Tiles
@@ -193,23 +194,20 @@ struct FewLoad {
     }
 };
 
-// One segment, with 8 kN rows.
+// The fragments of query rows n 8 + i: element pairs in the order of K's pieces, and
+// what turns a row's scores into log2 units.
 template <int kType, int kDim, int kN>
-__device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk &w, int piece,
-                                            const uint8_t *slots, int &got, FewLoad<kType, kDim> &load)
+__device__ __forceinline__ void few_query(const AttnParams &p, const AttnUnit &e, int h,
+                                          uint32_t (&qb)[kN][kDim / 16][2], float (&unit)[kN])
 {
     using C = FewCfg<kType, kDim>;
     const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
-    const AttnUnit &e = w.e;
     const int g = p.group, rows = e.tokens * g;
-    const float c2 = p.scale_log2;
-    uint32_t qb[kN][kDim / 16][2];
-    float cr[kN][2];             // what turns a score into log2 units, for rows 2q and 2q + 1
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
         const int row = n * 8 + i, tok = row / g;
         const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (e.row0 + tok) * p.q_stride + static_cast<int64_t>(w.h * g + row % g) * kDim);
+            p.q + (e.row0 + tok) * p.q_stride + static_cast<int64_t>(h * g + row % g) * kDim);
 #pragma unroll
         for (int k = 0; k < kDim / 32; ++k) {
             // (eight elements, in the order of K's pieces)
@@ -223,7 +221,7 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
             qb[n][2 * k + 1][0] = v.z ^ flip;
             qb[n][2 * k + 1][1] = v.w ^ flip;
         }
-        cr[n][0] = cr[n][1] = c2;
+        unit[n] = p.scale_log2;
         if constexpr (C::kQuant) {
             // the row's largest magnitude to [2^7, 2^8)
             float top = 0.f;
@@ -242,16 +240,118 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
             for (int s = 0; s < kDim / 16; ++s)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const __half2 h = __floats2half2_rn(__uint_as_float(qb[n][s][k] << 16) * up,
+                    const __half2 x = __floats2half2_rn(__uint_as_float(qb[n][s][k] << 16) * up,
                                                         __uint_as_float(qb[n][s][k] & 0xffff0000u) * up);
-                    qb[n][s][k] = *reinterpret_cast<const uint32_t *>(&h);
+                    qb[n][s][k] = *reinterpret_cast<const uint32_t *>(&x);
                 }
-            const float back = c2 * pow2i(-shift);
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                cr[n][r] = __shfl_sync(0xffffffffu, back, (q * 2 + r) * 4);
+            unit[n] *= pow2i(-shift);
         }
     }
+}
+
+// A lane's values of piece k of sixteen keys: of keys 2q, 2q + 1, 8 + 2q and 9 + 2q.
+template <int kType, int kDim, int kWords>
+__device__ __forceinline__ void few_values(const uint8_t *half, int k, uint32_t (&v)[4][kWords])
+{
+    using C = FewCfg<kType, kDim>;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const uint8_t *src = half + ((n * C::kVPieces + k) * 32 + lane) * C::kVPiece;
+        if constexpr (kWords == 4) {
+            const uint4 t4 = *reinterpret_cast<const uint4 *>(src);
+            v[n][0] = t4.x;
+            v[n][1] = t4.y;
+            v[n][2] = t4.z;
+            v[n][3] = t4.w;
+        } else {
+            const uint2 t2 = *reinterpret_cast<const uint2 *>(src);
+            v[n][0] = t2.x;
+            v[n][1] = t2.y;
+        }
+    }
+}
+
+// Takes infinities and NaN out: they would reach the rows that do not see them (0 times
+// them), and are added at the end to those that do.  Whether there were any.
+__device__ __forceinline__ bool few_clean(uint32_t (&v)[4][4])
+{
+    bool found = false;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bool a = (v[n][s] & 0x7f80u) == 0x7f80u;
+            const bool b = (v[n][s] & 0x7f800000u) == 0x7f800000u;
+            found = found || a || b;
+            v[n][s] &= (a ? 0xffff0000u : 0xffffffffu) & (b ? 0xffffu : 0xffffffffu);
+        }
+    return found;
+}
+
+// Where a row of a segment goes: to the output, or to the piece's partial results.
+struct FewRow {
+    int64_t grow, prow;
+    int tok, head;
+    float m, l, inv;
+
+    __device__ __forceinline__ FewRow(const AttnParams &p, const AttnWalk &w, int piece, int row, float m_,
+                                      float l_)
+        : prow(attn_slot(piece, w.starts()) * static_cast<int64_t>(kFewRows) + row), tok(row / p.group),
+          head(w.h * p.group + row % p.group), m(m_), l(l_), inv(l > 0.f || l != l ? 1.f / l : 0.f)
+    {
+        grow = w.e.row0 + tok;
+    }
+    template <int kDim>
+    __device__ __forceinline__ void add_nonfinite(const AttnParams &p, const AttnWalk &w, int d,
+                                                  float (&v)[8]) const
+    {
+        const int pos = w.e.pos0 + tok;
+        few_add_nonfinite<kDim, 8>(p, w.e, w.h, w.e.tile0 + w.ta, w.e.tile0 + w.tb, pos + 1,
+                                   p.window > 0 ? pos - p.window + 1 : 0, d, v);
+    }
+    // eight columns from d on
+    template <int kDim>
+    __device__ __forceinline__ void store(const AttnParams &p, const AttnWalk &w, int d,
+                                          const float (&v)[8]) const
+    {
+        if (w.whole()) {
+            *reinterpret_cast<uint4 *>(p.o + grow * p.o_stride + static_cast<int64_t>(head) * kDim + d) =
+                make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                           pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(p.line[1].part_o + prow * kDim + d);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    __device__ __forceinline__ void statistics(const AttnParams &p, const AttnWalk &w) const
+    {
+        if (!w.whole())
+            p.line[1].part_ml[prow] = make_float2(m, l);
+        else if (p.lse)
+            p.lse[grow * p.heads + head] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.6931471805599453f;
+    }
+};
+
+// One segment, with 8 kN rows (kN 2 for 8-bit caches alone, see few_segment16).
+template <int kType, int kDim, int kN>
+__device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk &w, int piece,
+                                            const uint8_t *slots, int &got, FewLoad<kType, kDim> &load)
+{
+    using C = FewCfg<kType, kDim>;
+    const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
+    const AttnUnit &e = w.e;
+    const int g = p.group, rows = e.tokens * g;
+    const float c2 = p.scale_log2;
+    uint32_t qb[kN][kDim / 16][2];
+    float unit[kN], cr[kN][2];   // (a lane's scores are of rows 2q and 2q + 1)
+    few_query<kType, kDim, kN>(p, e, w.h, qb, unit);
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            cr[n][r] = __shfl_sync(0xffffffffu, unit[n], (q * 2 + r) * 4);
     float o[kN][kDim / 16][4];
     // -m: the reference begins with the least finite number, which is one like any other
     float nm[kN][2], l[kN][2];
@@ -421,22 +521,7 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
             for (int u = 0; u < 2; ++u) {
                 constexpr int kWords = C::kVPiece / 4;
                 uint32_t v[4][kWords];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const uint8_t *src =
-                        slot + u * C::kHalf + ((n * C::kVPieces + k) * 32 + lane) * C::kVPiece;
-                    if constexpr (kWords == 4) {
-                        const uint4 t4 = *reinterpret_cast<const uint4 *>(src);
-                        v[n][0] = t4.x;
-                        v[n][1] = t4.y;
-                        v[n][2] = t4.z;
-                        v[n][3] = t4.w;
-                    } else {
-                        const uint2 t2 = *reinterpret_cast<const uint2 *>(src);
-                        v[n][0] = t2.x;
-                        v[n][1] = t2.y;
-                    }
-                }
+                few_values<kType, kDim>(slot + u * C::kHalf, k, v);
                 if constexpr (C::kQuant) {
 #pragma unroll
                     for (int s = 0; s < kWords; ++s) {
@@ -456,19 +541,8 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                         }
                     }
                 } else {
-                    if (hides) {
-                        // infinities and NaN would reach the rows that do not see them
-                        // (0 times them): they are added at the end to those that do
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) {
-                                const bool a = (v[n][s] & 0x7f80u) == 0x7f80u;
-                                const bool b = (v[n][s] & 0x7f800000u) == 0x7f800000u;
-                                nonfinite = nonfinite || a || b;
-                                v[n][s] &= (a ? 0xffff0000u : 0xffffffffu) & (b ? 0xffffu : 0xffffffffu);
-                            }
-                    }
+                    if (hides)
+                        nonfinite = few_clean(v) || nonfinite;
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         const uint32_t f[4] = {
@@ -493,13 +567,10 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
             l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], 4);
             l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], 8);
             l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], 16);
-            const int row = n * 8 + q * 2 + r, tok = row / g;
+            const int row = n * 8 + q * 2 + r;
             if (row >= rows)
                 continue;
-            const int64_t grow = e.row0 + tok;
-            const int head = w.h * g + row % g;
-            const float inv = l[n][r] > 0.f || l[n][r] != l[n][r] ? 1.f / l[n][r] : 0.f;
-            const int64_t prow = attn_slot(piece, w.starts()) * kFewRows + row;
+            const FewRow out(p, w, piece, row, -nm[n][r], l[n][r]);
             // runs of eight neighbouring columns: products s .. s + 3 with both of theirs
 #pragma unroll
             for (int s = 0; s < kDim / 16; s += 4) {
@@ -510,30 +581,188 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                     v[2 * k] = o[n][s + k][r];
                     v[2 * k + 1] = o[n][s + k][2 + r];
                 }
-                if (!clean) {
-                    const int pos = e.pos0 + tok;
-                    few_add_nonfinite<kDim, 8>(p, e, w.h, e.tile0 + w.ta, e.tile0 + w.tb, pos + 1,
-                                               p.window > 0 ? pos - p.window + 1 : 0, d, v);
-                }
-                if (w.whole()) {
-                    *reinterpret_cast<uint4 *>(p.o + grow * p.o_stride +
-                                               static_cast<int64_t>(head) * kDim + d) =
-                        make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                                   pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.line[1].part_o + prow * kDim + d);
-                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                if (!clean)
+                    out.add_nonfinite<kDim>(p, w, d, v);
+                out.store<kDim>(p, w, d, v);
+            }
+            if (i == 0)
+                out.statistics(p, w);
+        }
+}
+
+// One segment of a bf16 cache with 9 to 16 rows: query rows take the 16-row side, keys
+// the 8-column side, so that the scores' fragments are the weights' without a transpose
+// (32 sequences of 15 rows: 51.5 us, with few_segment 53.0.  For 8-bit caches its
+// registers do not suffice beside what widens the codes, and cost the units of fewer
+// rows as well: 64 sequences decoding 149 us -> 163).
+template <int kDim>
+__device__ __forceinline__ void few_segment16(const AttnParams &p, const AttnWalk &w, int piece,
+                                              const uint8_t *slots, int &got,
+                                              FewLoad<SSD_KV_BF16, kDim> &load)
+{
+    using C = FewCfg<SSD_KV_BF16, kDim>;
+    const int lane = threadIdx.x & 31, i = lane >> 2, q = lane & 3;
+    const AttnUnit &e = w.e;
+    const int g = p.group, rows = e.tokens * g;
+    uint32_t qb[2][kDim / 16][2];
+    float unit[2];               // (of rows i and i + 8: the scale)
+    few_query<SSD_KV_BF16, kDim, 2>(p, e, w.h, qb, unit);
+    // product 8 k + t: columns 8 (8 k + n) + t, n its column
+    float o[kDim / 8][4];
+    float nm[2], l[2];           // (see few_segment)
+#pragma unroll
+    for (int t = 0; t < kDim / 8; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[t][k] = 0.f;
+    nm[0] = nm[1] = FLT_MAX;
+    l[0] = l[1] = 0.f;
+    bool nonfinite = false;
+
+    for (int t = w.ta; t < w.tb; ++t) {
+        const int j0 = (e.tile0 + t) * kFewKeys;
+        const bool hides = attn_partial(e, p.window, j0, kFewKeys, 0, e.tokens - 1);
+        // ---- scores of eight keys each: rows i and i + 8, keys 2q and 2q + 1 ----
+        ptx::cp_async_wait<C::kSlots - 2>();
+        __syncwarp();
+        const uint8_t *slot = slots + got;
+        got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
+        load.template next<C::kAhead>();
+        float x[4][4];           // [eight keys][row i: two keys, row i + 8: two keys]
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[k][r] = 0.f;
+#pragma unroll
+        for (int k = 0; k < C::kKPieces; ++k)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(
+                    slot + u / 2 * C::kHalf + ((u % 2 * C::kKPieces + k) * 32 + lane) * 16);
+                const uint32_t v4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t(&a)[2] = qb[0][k * 2 + s], (&b)[2] = qb[1][k * 2 + s];
+                    const uint32_t rows4[4] = {a[0], b[0], a[1], b[1]};
+                    ptx::mma_16816(x[u], rows4, v4[2 * s], v4[2 * s + 1]);
                 }
             }
-            if (i == 0) {
-                if (!w.whole())
-                    p.line[1].part_ml[prow] = make_float2(-nm[n][r], l[n][r]);
-                else if (p.lse)
-                    p.lse[grow * p.heads + head] =
-                        l[n][r] == 0.f ? -INFINITY : (log2f(l[n][r]) - nm[n][r]) * 0.6931471805599453f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[k][r] *= unit[r / 2];
+        if (hides) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int pos = e.pos0 + min((r * 8 + i) / g, e.tokens - 1);
+                const int lo = p.window > 0 ? pos - p.window + 1 : INT32_MIN / 2;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int j = j0 + k / 2 * 8 + 2 * q + k % 2;
+                    if (j < lo || j > pos)
+                        x[k / 2][2 * r + k % 2] = -INFINITY;
+                }
             }
         }
+        // ---- probabilities ----
+        auto largest = [&](int r) {
+            float v = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                v = fmaxf(v, fmaxf(x[k][2 * r], x[k][2 * r + 1]));
+            return v;
+        };
+        if (__any_sync(0xffffffffu, fmaxf(largest(0) + nm[0], largest(1) + nm[1]) > kFewRescale)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float v = largest(r);
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                const float to = fminf(nm[r], -v);
+                const float f = to == nm[r] ? 1.f : ptx::ex2(to - nm[r]);
+                nm[r] = to;
+                l[r] *= f;
+#pragma unroll
+                for (int s = 0; s < kDim / 8; ++s) {
+                    o[s][2 * r] *= f;
+                    o[s][2 * r + 1] *= f;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[k][r] = ptx::ex2(x[k][r] + nm[r / 2]);
+                l[r / 2] += x[k][r];
+            }
+        // ---- P V ----
+        ptx::cp_async_wait<C::kSlots - 2>();
+        __syncwarp();
+        slot = slots + got;
+        got = got + C::kSlot == C::kRing ? 0 : got + C::kSlot;
+        load.template next<1 - C::kAhead>();
+        uint32_t pa[2][4], pl[2][4];             // the weights as two bf16 each
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float a = x[k][2 * r], b = x[k][2 * r + 1];
+                const uint32_t top = pack_bf16(a, b);
+                pa[k / 2][k % 2 * 2 + r] = top;
+                pl[k / 2][k % 2 * 2 + r] =
+                    pack_bf16(a - __uint_as_float(top << 16), b - __uint_as_float(top & 0xffff0000u));
+            }
+#pragma unroll
+        for (int k = 0; k < C::kVPieces; ++k)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t v[4][4];
+                few_values<SSD_KV_BF16, kDim>(slot + u * C::kHalf, k, v);
+                if (hides)
+                    nonfinite = few_clean(v) || nonfinite;
+                auto product = [&](int s, uint32_t b0, uint32_t b1) {
+                    ptx::mma_16816(o[s], pa[u], b0, b1);
+                    ptx::mma_16816(o[s], pl[u], b0, b1);
+                };
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    product(k * 8 + 2 * s, __byte_perm(v[0][s], v[1][s], 0x5410),
+                            __byte_perm(v[2][s], v[3][s], 0x5410));
+                    product(k * 8 + 2 * s + 1, __byte_perm(v[0][s], v[1][s], 0x7632),
+                            __byte_perm(v[2][s], v[3][s], 0x7632));
+                }
+            }
+    }
+
+    // ---- output: rows i and i + 8, runs of eight neighbouring columns ----
+    const bool clean = !__any_sync(0xffffffffu, nonfinite);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        const int row = r * 8 + i;
+        if (row >= rows)
+            continue;
+        const FewRow out(p, w, piece, row, -nm[r], l[r]);
+#pragma unroll
+        for (int s = 0; s < kDim / 8; s += 8)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int d = (s + 2 * q + c) * 8;
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = o[s + k][2 * r + c];
+                if (!clean)
+                    out.add_nonfinite<kDim>(p, w, d, v);
+                out.store<kDim>(p, w, d, v);
+            }
+        if (q == 0)
+            out.statistics(p, w);
+    }
 }
 
 template <int kType, int kDim>
@@ -564,8 +793,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         for (; w.more(); w.next()) {
             if (w.e.tokens * p.group <= 8)
                 few_segment<kType, kDim, 1>(p, w, piece, slots, got, load);
-            else
+            else if constexpr (C::kQuant)
                 few_segment<kType, kDim, 2>(p, w, piece, slots, got, load);
+            else
+                few_segment16<kDim>(p, w, piece, slots, got, load);
         }
         ptx::cp_async_wait<0>();
     }
