@@ -107,6 +107,9 @@ def _refuse(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, blo
         raise ValueError(f"block_table must have shape ({batch}, pages)")
     if block_table.shape[1] > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table: each sequence's entries must be contiguous")
+    if block_table.stride(0) < block_table.shape[1] and batch > 1:
+        raise ValueError("block_table: sequences' rows must not overlap (an expanded table has to "
+                         "be made contiguous)")
     if errors is not None:
         if errors.numel() < 1 or errors.dtype not in (f.i32, f.u32):
             raise ValueError("errors must be an int32 or uint32 tensor of one element")
@@ -133,7 +136,7 @@ def _cache(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, bloc
         batch, width = tshape
         tstride = block_table.stride()
         good = (query_start_loc.shape == (batch + 1,) and kv_lens.shape == (batch,)
-                and (tstride[1] == 1 or width <= 1))
+                and (tstride[1] == 1 or width <= 1) and (tstride[0] >= width or batch <= 1))
     if good and kind:
         if k_scale is None or v_scale is None:
             good = False
@@ -159,14 +162,20 @@ def _cache(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, bloc
 
 def _pitch(t, what: str, f, device: int):
     """Row pitch (elements) of a (rows, heads, head_dim) bf16 tensor whose rows are
-    contiguous."""
+    contiguous and do not overlap (an expanded tensor's do: its pitch of 0 would
+    say "contiguous" in the C ABI)."""
     n, h, d = t.shape
     s = t.stride()
     if t.dtype is not f.bf16 or t.get_device() != device:
         _tensor(t, what, f.bf16, device, contiguous=False)
     if (s[2] != 1 and d != 1) or (s[1] != d and h != 1):
         raise ValueError(f"{what}: each token's row must be contiguous")
-    return s[0] if n > 1 else h * d
+    if n <= 1:
+        return h * d
+    if s[0] < h * d:
+        raise ValueError(f"{what}: tokens' rows must not overlap (an expanded tensor has to be "
+                         "made contiguous)")
+    return s[0]
 
 
 def _copy(f, fn, what, k, v, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens,

@@ -1,0 +1,101 @@
+"""Host-side checks of the paged cache's and the attention's edges (no GPU): views
+that the C ABI cannot express are refused by the binding."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from mamba_ssd_chunked_varlen_gb300 import attention
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on device 0: for checks that come before any launch."""
+
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 0
+
+
+def on_device(t):
+    return t.as_subclass(OnDevice)
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """The binding with entry points that must not be reached."""
+    f = attention._Functions()
+
+    def launched(*args):
+        raise AssertionError("a refused call was launched")
+
+    f.write = f.read = f.attn = launched
+    f.raw_stream = lambda device: 0
+    monkeypatch.setattr(attention, "_fn", f)
+    return f
+
+
+def batch_of(n=2, rows=5, heads=2, dim=64, page=16, width=3):
+    """Arguments of a call of `n` sequences that passes every check."""
+    i32 = dict(dtype=torch.int32)
+    shape = (4, heads, page, dim)
+    return dict(x=on_device(torch.zeros(rows, heads, dim, dtype=torch.bfloat16)),
+                cache=(on_device(torch.zeros(shape, dtype=torch.bfloat16)),
+                       on_device(torch.zeros(shape, dtype=torch.bfloat16)), None, None),
+                qsl=on_device(torch.zeros(n + 1, **i32)), lens=on_device(torch.zeros(n, **i32)),
+                table=on_device(torch.zeros(n, width, **i32)),
+                ws=on_device(torch.zeros(1024, dtype=torch.uint8)))
+
+
+def calls(a, k=None, v=None, table=None, which=("write", "read", "attn")):
+    """The three calls with `k` and `v` (attention: q and o) and `table` in place of the usual ones."""
+    k, v = a["x"] if k is None else k, a["x"] if v is None else v
+    where = (a["qsl"], a["lens"], a["table"] if table is None else table)
+    made = dict(
+        write=lambda: attention.ssd_kv_cache_write(k, v, *a["cache"], *where),
+        read=lambda: attention.ssd_kv_cache_read(k, v, *a["cache"], *where),
+        attn=lambda: attention.ssd_attn_varlen_fwd(v, None, k, *a["cache"], *where, softmax_scale=1.0,
+                                                   workspace=a["ws"]))
+    return [made[w] for w in which]
+
+
+def test_the_usual_call_passes_the_checks(no_launch):
+    for call in calls(batch_of()):
+        with pytest.raises(AssertionError, match="launched"):
+            call()
+
+
+def overlapping(rows=5, heads=2, dim=64):
+    one = torch.zeros(1, heads, dim, dtype=torch.bfloat16).expand(rows, heads, dim)
+    half = torch.zeros(rows * heads * dim, dtype=torch.bfloat16).as_strided(
+        (rows, heads, dim), (heads * dim // 2, dim, 1))
+    return [on_device(one), on_device(half)]
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_overlapping_rows_are_refused(no_launch, which):
+    """An expanded tensor has a row pitch of 0, which the C ABI takes as contiguous: the
+    call would read, or write, rows past the tensor's end."""
+    bad = overlapping()[which]
+    for kw in (dict(k=bad), dict(v=bad)):
+        for call in calls(batch_of(), **kw):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+
+
+def test_overlapping_table_is_refused(no_launch):
+    row = torch.zeros(1, 3, dtype=torch.int32)
+    for table in (row.expand(2, 3), torch.zeros(8, dtype=torch.int32).as_strided((2, 3), (2, 1)),
+                  torch.zeros(1, 1, dtype=torch.int32).expand(2, 1)):
+        for call in calls(batch_of(), table=on_device(table)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+
+
+def test_one_row_may_have_any_pitch(no_launch):
+    """A single row, or a single sequence's table, has nothing to overlap with."""
+    one = on_device(torch.zeros(1, 2, 64, dtype=torch.bfloat16).as_strided((1, 2, 64), (0, 64, 1)))
+    table = on_device(torch.zeros(3, dtype=torch.int32).as_strided((1, 3), (0, 1)))
+    for call in calls(batch_of(n=1, rows=1), k=one, v=one, table=table):
+        with pytest.raises(AssertionError, match="launched"):
+            call()
