@@ -263,7 +263,8 @@ def ssd_scan_varlen_fwd_states(y, x, dt, A, B, C, D, dt_bias, initial_states,
 
 def _token_major(t, what: str, dtype, inner: int):
     """Pointer and token stride of a token-major view whose rows (the trailing
-    `inner` elements) are contiguous."""
+    `inner` elements) are contiguous and do not overlap (an expanded view's do: its
+    stride of 0 would say "contiguous" in the C ABI)."""
     if t is None:
         raise ValueError(f"{what} is required")
     if not t.is_cuda:
@@ -272,6 +273,9 @@ def _token_major(t, what: str, dtype, inner: int):
         raise ValueError(f"{what} must have dtype {dtype}, got {t.dtype}")
     if t.dim() < 2 or t[0].numel() != inner or (t.shape[0] > 0 and not t[0].is_contiguous()):
         raise ValueError(f"{what}: each token's row must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < inner:
+        raise ValueError(f"{what}: tokens' rows must not overlap (an expanded tensor has to be "
+                         "made contiguous)")
     return ctypes.c_void_p(t.data_ptr()), t.stride(0)
 
 
