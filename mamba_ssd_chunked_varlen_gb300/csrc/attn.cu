@@ -562,7 +562,9 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     p.heads = nheads;
     p.group = group;
     p.tile_tokens = kTileRows / group;
-    p.window = window;
+    // no context is longer than its block table: such a window hides nothing, and those
+    // left are below 2^30, so that a position less a window stays in 32 bits
+    p.window = window >= static_cast<int64_t>(table_width) * page_size ? 0 : window;
     // a scale of zero still has to leave the hidden keys' -infinity as it is
     p.scale_log2 = std::fmax(std::fabs(softmax_scale) * 1.4426950408889634f, 0x1p-120f);
     p.negate = softmax_scale < 0.f;

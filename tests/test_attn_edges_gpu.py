@@ -1,0 +1,43 @@
+"""Edges of the attention over the paged cache, on the GPU, against the 64-bit
+answer with the bounds that attn_helpers derives (or its own, where stated)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from attn_helpers import Batch, check_attend
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["bf16", "fp8", "int8"]
+
+
+def padded(lens, kv, *args, **kw):
+    """A batch of `lens` whose kv_lens are then set to `kv`: rows at negative positions."""
+    import torch
+    b = Batch(lens, *args, **kw).fill()
+    b.kv_lens.copy_(torch.tensor(kv))
+    b.lens = [(n, k) for (n, _), k in zip(lens, kv)]
+    return b
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 64, 2 ** 30, 2 ** 30 - 1])
+def test_window_of_no_limit(kind, window):
+    """A window wider than any context is none, beside padding rows as well (their
+    positions are negative: less a window of 2^31 they leave 32 bits)."""
+    import torch
+    lens, kv = [(6, 6), (130, 130), (40, 40), (1, 1)], [2, 3, 33, 1]
+    b = padded(lens, kv, 4, 2, 64, 16, kind, seed=21)
+    o, lse = b.attend(window=0)
+    check_attend(b, o, lse, what="padding")
+    o2, lse2 = b.attend(window=window)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and b.errors.item() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [1, 3, 40])
+def test_window_and_padding(kind, window):
+    b = padded([(6, 6), (130, 130), (40, 60), (3, 1)], [4, 70, 60, 1], 4, 2, 64, 16, kind, seed=22)
+    o, lse = b.attend(window=window)
+    check_attend(b, o, lse, window=window, what="padding")
