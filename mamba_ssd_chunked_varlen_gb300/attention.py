@@ -244,6 +244,8 @@ def ssd_attn_varlen_fwd(o, lse, q, k_cache, v_cache, k_scale, v_scale, query_sta
     the batch as for ssd_kv_cache_write; window 0 or the number of keys a query
     sees; workspace: a uint8 tensor of at least ssd_attn_varlen_workspace_size
     bytes (alloc_attn_workspace)."""
+    if not 0 <= window <= 0x7fffffff:    # (ctypes would cut it to 32 bits)
+        raise ValueError(f"window must be in [0, 2^31), got {window}")
     f = _functions()
     ptrs, batch, heads_kv, dim, sizes, pe, device = _cache(f, k_cache, v_cache, k_scale, v_scale,
                                                            query_start_loc, kv_lens, block_table,

@@ -99,3 +99,12 @@ def test_one_row_may_have_any_pitch(no_launch):
     for call in calls(batch_of(n=1, rows=1), k=one, v=one, table=table):
         with pytest.raises(AssertionError, match="launched"):
             call()
+
+
+@pytest.mark.parametrize("window", [-1, 2 ** 31, 2 ** 32, 2 ** 32 + 5])
+def test_window_out_of_range_is_refused(no_launch, window):
+    """A window is 32 bits in the C ABI: 2^32 + 5 must not become 5."""
+    a = batch_of()
+    with pytest.raises(ValueError, match="window"):
+        attention.ssd_attn_varlen_fwd(a["x"], None, a["x"], *a["cache"], a["qsl"], a["lens"], a["table"],
+                                      softmax_scale=1.0, window=window, workspace=a["ws"])
