@@ -600,7 +600,6 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     // what that rules out is not launched
     const bool tiles = std::min<int64_t>(total_len, 2 * p.tile_tokens) * group > kFewRows;
     const bool few = group <= kFewRows;
-    p.few_behind_tiles = tiles && few;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     cudaError_t e = launch_pdl(attn_plan_kernel, dim3(kPlanCtas),
                                batch <= kPlanSmall ? kPlanSmall : kPlanThreads, stream, p);

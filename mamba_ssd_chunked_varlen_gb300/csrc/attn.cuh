@@ -84,7 +84,6 @@ struct AttnParams {
     int32_t window;
     float scale_log2;             // |softmax_scale| log2(e)
     int32_t negate;               // 1: softmax_scale < 0 (the scores change sign)
-    int32_t few_behind_tiles;     // 1: the kernel of few rows follows the tiles' kernel
     int32_t *seq_units;           // (batch): units before each sequence
     AttnLine line[2];
 };

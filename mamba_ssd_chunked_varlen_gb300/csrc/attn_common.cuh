@@ -10,8 +10,7 @@
 
 namespace ssd {
 
-// Launches a kernel that begins with pdl_wait() (or ends with it, see attn_few.cuh)
-// ahead of its predecessor's end.
+// Launches a kernel that begins with pdl_wait() ahead of its predecessor's end.
 template <typename... Args>
 inline cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args)
 {

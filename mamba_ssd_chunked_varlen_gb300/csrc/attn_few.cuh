@@ -774,10 +774,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     const int warp = threadIdx.x >> 5;
     const int piece = blockIdx.x + warp * kAttnCtas;    // short lines: a piece per CTA first
     pdl_launch_dependents();
-    // the plan; behind the tiles' kernel, whose CTAs let this one start only after
-    // they have seen the plan, nothing more is needed before the end
-    if (!p.few_behind_tiles)
-        pdl_wait();
+    // the plan (behind the tiles' kernel the plan's grid has long ended, but only this
+    // grid's own wait makes its writes visible here)
+    pdl_wait();
     const uint8_t *slots = smem + warp * C::kRing;
     FewLoad<kType, kDim> load(p, piece, ptx::smem_u32(slots));
     if (load.w.more()) {
@@ -800,8 +799,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         }
         ptx::cp_async_wait<0>();
     }
-    // this grid ends after its predecessors, so that the join may rely on them all
-    pdl_wait();
 }
 
 template <int kType, int kDim>

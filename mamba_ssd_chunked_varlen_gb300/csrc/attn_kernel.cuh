@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     pdl_wait();                                // the plan
-    pdl_launch_dependents();                   // (few rows: they need nothing but the plan)
+    pdl_launch_dependents();                   // (its CTAs start as these end, and wait)
     const int g = p.group, tt = p.tile_tokens;
     bool ok = true;
     auto streams = [&](const AttnUnit &e) { return e.tokens > tt ? 2 : 1; };

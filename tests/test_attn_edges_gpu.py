@@ -41,3 +41,30 @@ def test_window_and_padding(kind, window):
     b = padded([(6, 6), (130, 130), (40, 60), (3, 1)], [4, 70, 60, 1], 4, 2, 64, 16, kind, seed=22)
     o, lse = b.attend(window=window)
     check_attend(b, o, lse, window=window, what="padding")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_calls_in_a_row_have_plans_of_their_own(kind):
+    """Batches of both kinds of unit in turn, in one workspace and without a stop between: each
+    call's kernels go by its own plan, also where they start ahead of their predecessor's
+    end."""
+    import torch
+    import mamba_ssd_chunked_varlen_gb300 as pkg
+    made = []
+    for seed, lens in enumerate([[(1, 900), (90, 300), (1, 33)] * 4, [(70, 70), (1, 2000), (130, 131)],
+                                 [(1, 50)] * 60 + [(33, 700)], [(1, 5)], [(40, 40)]]):
+        b = Batch(lens, 4, 2, 64, 16, kind, seed=30 + seed).fill()
+        o, lse = b.attend()
+        check_attend(b, o, lse, what=f"batch {seed}")
+        made.append((b, o, lse, torch.empty_like(o), torch.empty_like(lse)))
+    ws = pkg.alloc_attn_workspace(max(b.total for b, *_ in made), 64, 4, 2, 64)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(20):
+        for b, o, lse, o2, lse2 in made:
+            pkg.ssd_attn_varlen_fwd(o2, lse2, b.q, *b.cache, *b.where, softmax_scale=0.125,
+                                    workspace=ws, errors=b.errors)
+        for b, o, lse, o2, lse2 in made:
+            wrong += (o != o2).sum() + (lse != lse2).sum()
+            o2.zero_()
+            lse2.zero_()
+    assert wrong.item() == 0 and all(b.errors.item() == 0 for b, *_ in made)
