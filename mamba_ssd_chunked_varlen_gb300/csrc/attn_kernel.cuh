@@ -73,7 +73,8 @@ struct Cfg {
     static constexpr int kKvOff = kQOff + 2 * kTile;
     static constexpr int kRawOff = kKvOff + kStages * kTile;
     static constexpr int kScaleOff = kRawOff + kRawStages * kRaw;
-    static constexpr int kBarOff = kScaleOff + (kQuant ? kSlots8 * 2 * kTileKeys * 4 : 0);
+    static constexpr int kOnesOff = kScaleOff + (kQuant ? kSlots8 * 2 * kTileKeys * 4 : 0);
+    static constexpr int kBarOff = kOnesOff + (kQuant ? kTileKeys / 2 * 4 : 0);
     static constexpr int kBytes = kBarOff + 512 + 1024;
     // tensor memory: per stream 128 columns of S (P in the first 64) and kDim of O
     static constexpr uint32_t kColO = 256;
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem + C::kQOff, *sKv = smem + C::kKvOff, *sRaw = smem + C::kRawOff;
     float *sScale = reinterpret_cast<float *>(smem + C::kScaleOff);
+    float *sOnes = reinterpret_cast<float *>(smem + C::kOnesOff);   // factors of scores that have theirs
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -166,6 +168,8 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
         *s_abort = 0;
         *s_nonfinite = 0;
     }
+    if (C::kQuant && tid < kTileKeys / 2)
+        sOnes[tid] = 1.f;
     if (warp == C::kIssuer) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
@@ -628,11 +632,29 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                                 s[1][k] ^= 0x80000000u;
                             }
                         }
+                        const uint64_t c22 = ptx::pack2(c2, c2);
+                        const float *fs = hides ? sOnes + 2 * fq : sc;
+                        auto pair = [&](int j, int k) {
+                            return ptx::pack2(__uint_as_float(score(j, k, 0)), __uint_as_float(score(j, k, 1)));
+                        };
                         if (hides) {
-                            // (a bit per key: the compiler moves eight to predicates at a time;
-                            // the factors of an 8-bit cache's scores have the scale's sign)
+                            if constexpr (C::kQuant) {
+                                // to log2 units first: a key's factor may be zero (its page is out
+                                // of range) or have any sign, and hidden it is -infinity
+#pragma unroll
+                                for (int k = 0; k < kPairs; ++k) {
+                                    const uint64_t f = *reinterpret_cast<const uint64_t *>(sc + k * 8);
+#pragma unroll
+                                    for (int j = 0; j < kR; ++j) {
+                                        float e0, e1;
+                                        ptx::unpack2(ptx::mul2(pair(j, k), f), e0, e1);
+                                        score(j, k, 0) = __float_as_uint(e0);
+                                        score(j, k, 1) = __float_as_uint(e1);
+                                    }
+                                }
+                            }
+                            // (a bit per key: the compiler moves eight to predicates at a time)
                             auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; };
-                            const uint32_t hidden = C::kQuant && p.negate ? 0x7f800000u : 0xff800000u;
 #pragma unroll
                             for (int j = 0; j < kR; ++j) {
                                 const int pos = w.e.pos0 + tok0 + min(row_tok[j], ntok - 1);
@@ -646,19 +668,15 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                                     for (int e = 0; e < 2; ++e) {
                                         const int at = k * kStep + e;
                                         uint32_t &x = score(j, k, e);
-                                        x = (at < 32 ? v0 : v1) >> (at & 31) & 1 ? x : hidden;
+                                        x = (at < 32 ? v0 : v1) >> (at & 31) & 1 ? x : 0xff800000u;
                                     }
                             }
                         }
-                        const uint64_t c22 = ptx::pack2(c2, c2);
                         auto factors = [&](int k) -> uint64_t {    // of pair k, to log2 units
                             if constexpr (C::kQuant)
-                                return *reinterpret_cast<const uint64_t *>(sc + k * 8);
+                                return *reinterpret_cast<const uint64_t *>(fs + k * 8);
                             else
                                 return c22;
-                        };
-                        auto pair = [&](int j, int k) {
-                            return ptx::pack2(__uint_as_float(score(j, k, 0)), __uint_as_float(score(j, k, 1)));
                         };
                         auto maxima = [&](float (&x)[kR]) {
                             float x2[kAcc];

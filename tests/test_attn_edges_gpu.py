@@ -68,3 +68,52 @@ def test_calls_in_a_row_have_plans_of_their_own(kind):
             o2.zero_()
             lse2.zero_()
     assert wrong.item() == 0 and all(b.errors.item() == 0 for b, *_ in made)
+
+
+def spoil(b, what):
+    """Keys that rows of the batch do not see, and some that they do, get a factor of zero, or
+    a negative one: what `stored` then gives for them is what the definition says."""
+    import torch
+    ks, vs = None, None
+    if what == "bad page":
+        b.block_table[0, 3] = -1
+        b.block_table[0, 18] = 1 << 20
+        ks, vs = b.stored()
+        for x in (ks[0], vs[0]):
+            x[48:64] = 0.0
+            x[288:300] = 0.0
+        return ks, vs
+    for j in (5, 60, 283, 290, 299):
+        p, r = b.row_of(0, j)
+        b.k_scale[p, :, r] *= 0.0 if what == "zero scale" else -1.0
+    return b.stored()
+
+
+@pytest.mark.parametrize("softmax_scale", [None, -0.1])
+@pytest.mark.parametrize("new", [3, 20])
+@pytest.mark.parametrize("what", ["bad page", "zero scale", "negative scale"])
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+def test_hidden_keys_of_any_factor(kind, what, new, softmax_scale):
+    """A key whose scale is zero or negative, or whose page is out of range (it reads as zeros),
+    is hidden from the rows before it like any other."""
+    from mamba_ssd_chunked_varlen_gb300 import attention
+    b = Batch([(new, 300), (1, 90)], 4, 2, 64, 16, kind, seed=23).fill()
+    stored = spoil(b, what)
+    o, lse = b.attend(softmax_scale=softmax_scale)
+    check_attend(b, o, lse, softmax_scale=softmax_scale, what=what, stored=stored)
+    assert b.errors.item() == (attention.DEVERR_BAD_PAGE if what == "bad page" else 0)
+
+
+@pytest.mark.parametrize("new", [2, 40])
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("softmax_scale", [0.0, 1e-30, -0.1])
+def test_softmax_scale_of_quantised_cache(softmax_scale, kind, new):
+    """A softmax_scale of zero gives means also where the product with a key's scale is below
+    fp32's numbers: small keys, and rows of zeros."""
+    b = Batch([(new, 300), (20, 20)], 4, 2, 64, 16, kind, seed=24)
+    for k in b.k_seq:
+        k[::3] *= 2.0 ** -50
+        k[1::7] = 0.0
+    b.fill()
+    o, lse = b.attend(softmax_scale=softmax_scale)
+    check_attend(b, o, lse, softmax_scale=softmax_scale, what="scale")
