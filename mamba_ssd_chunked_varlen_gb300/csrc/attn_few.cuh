@@ -66,15 +66,22 @@ struct FewCfg {
     static constexpr int kBytes = kFewWarps * kRing;
 };
 
-// Adds to kN columns from d of a row's sums the infinities and NaN that were
-// taken out of V: those of the keys in [lo, hi) of tiles [ta, tb) that some row
-// does not see all of.
+// Puts the infinities and NaN of V into kN columns from d of a row's sums: those of the
+// keys in [lo, hi) of tiles [ta, tb).  In tiles that some row does not see all of they were
+// taken out; in the others they are in the sums, as NaN where an infinity met a weight's
+// second part, so that sums that are not finite are looked up over all tiles.
 template <int kDim, int kN>
 __device__ __noinline__ void few_add_nonfinite(const AttnParams &p, const AttnUnit &e, int h, int ta,
                                                int tb, int hi, int lo, int d, float *acc)
 {
+    float found[kN];
+    bool all = false;
+    for (int k = 0; k < kN; ++k) {
+        found[k] = 0.f;
+        all = all || !(fabsf(acc[k]) <= FLT_MAX);
+    }
     for (int t = ta; t < tb; ++t) {
-        if (!attn_partial(e, p.window, t * kFewKeys, kFewKeys, 0, e.tokens - 1))
+        if (!all && !attn_partial(e, p.window, t * kFewKeys, kFewKeys, 0, e.tokens - 1))
             continue;
         for (int j = max(t * kFewKeys, max(lo, 0)); j < min((t + 1) * kFewKeys, hi); ++j) {
             const int64_t page = kv_page_of(p.c, e.seq, j);
@@ -84,11 +91,13 @@ __device__ __noinline__ void few_add_nonfinite(const AttnParams &p, const AttnUn
                 static_cast<const __nv_bfloat16 *>(p.c.v) + kv_row(p.c, page, h, j) * kDim + d;
             for (int k = 0; k < kN; ++k) {
                 const float x = __bfloat162float(v[k]);
-                if (!(fabsf(x) <= 3.4e38f))
-                    acc[k] += x;
+                if (!(fabsf(x) <= FLT_MAX))
+                    found[k] += x;
             }
         }
     }
+    for (int k = 0; k < kN; ++k)
+        acc[k] = found[k] == 0.f ? acc[k] : found[k];
 }
 
 // The copies of a warp: tile by tile of its piece, K then V, slot by slot.
@@ -302,10 +311,18 @@ struct FewRow {
     {
         grow = w.e.row0 + tok;
     }
+    // Of eight columns from d on, infinities and NaN as the definition has them (a row
+    // whose probabilities are NaN is NaN whatever its sums are).
     template <int kDim>
-    __device__ __forceinline__ void add_nonfinite(const AttnParams &p, const AttnWalk &w, int d,
+    __device__ __forceinline__ void add_nonfinite(const AttnParams &p, const AttnWalk &w, bool clean, int d,
                                                   float (&v)[8]) const
     {
+        float most = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            most += fabsf(v[k]);     // (one that is not finite shows)
+        if ((clean && most <= FLT_MAX) || l != l)
+            return;
         const int pos = w.e.pos0 + tok;
         few_add_nonfinite<kDim, 8>(p, w.e, w.h, w.e.tile0 + w.ta, w.e.tile0 + w.tb, pos + 1,
                                    p.window > 0 ? pos - p.window + 1 : 0, d, v);
@@ -581,8 +598,8 @@ __device__ __forceinline__ void few_segment(const AttnParams &p, const AttnWalk 
                     v[2 * k] = o[n][s + k][r];
                     v[2 * k + 1] = o[n][s + k][2 + r];
                 }
-                if (!clean)
-                    out.add_nonfinite<kDim>(p, w, d, v);
+                if constexpr (!C::kQuant)
+                    out.add_nonfinite<kDim>(p, w, clean, d, v);
                 out.store<kDim>(p, w, d, v);
             }
             if (i == 0)
@@ -756,8 +773,7 @@ __device__ __forceinline__ void few_segment16(const AttnParams &p, const AttnWal
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     v[k] = o[s + k][2 * r + c];
-                if (!clean)
-                    out.add_nonfinite<kDim>(p, w, d, v);
+                out.add_nonfinite<kDim>(p, w, clean, d, v);
                 out.store<kDim>(p, w, d, v);
             }
         if (q == 0)

@@ -117,3 +117,44 @@ def test_softmax_scale_of_quantised_cache(softmax_scale, kind, new):
     b.fill()
     o, lse = b.attend(softmax_scale=softmax_scale)
     check_attend(b, o, lse, softmax_scale=softmax_scale, what="scale")
+
+
+@pytest.mark.parametrize("kv,new,dim,window",
+                         [(kv, new, dim, window) for kv in (310, 5000) for new in (1, 4, 6, 8, 40)
+                          for dim in (64, 128) for window in (0, 290)]
+                         + [(120001, new, dim, 0) for new in (1, 6) for dim in (64, 128)])
+def test_infinite_values(kv, new, dim, window):
+    """An infinity in V is the result of every row that sees it, with its sign, in the keys'
+    first tiles as in the last; so is NaN, and so is NaN where both infinities meet.  The
+    other columns, and the rows that do not see it, are as they were."""
+    import torch
+    # (a second sequence, so that the first is cut in several ways)
+    b = Batch([(new, kv), (1, 64)], 4, 2, dim, 16, "bf16", seed=25).fill()
+    clean, clean_lse = b.attend(window=window)
+    inf = float("inf")
+    keys = [kv - 289, kv - 200, kv - 2 if new > 1 else kv - 1]
+    for j, (up, down) in zip(keys, ((3, 9), (17, 30), (40, 57))):
+        p, r = b.row_of(0, j)
+        b.v_cache[p, 0, r, up] = inf
+        b.v_cache[p, 0, r, down] = -inf
+        b.v_cache[p, 1, r, up] = float("nan")
+        b.v_cache[p, 0, r, 60] = inf
+        p, r = b.row_of(0, j - 5)
+        b.v_cache[p, 0, r, 61] = -inf
+        b.v_cache[p, 1, r, 62] = inf
+        b.v_cache[p, 1, r, 63] = -inf
+    p, r = b.row_of(0, kv - 250)
+    b.v_cache[p, 1, r, 62] = -inf
+    o, lse = b.attend(window=window)
+    # by the definition, column by column: sums of what a row sees
+    _, vs = b.stored()
+    want = clean.float().cpu().numpy()
+    for i in range(new):
+        at = kv - new + i
+        lo = max(0, at - window + 1) if window else 0
+        with np.errstate(invalid="ignore"):      # (both infinities)
+            seen = np.where(np.isfinite(vs[0]), 0.0, vs[0])[lo:at + 1].sum(0)  # (kv heads, dim)
+        for h in range(4):
+            want[i, h] = np.where(seen[h // 2] == 0, want[i, h], seen[h // 2])
+    assert np.array_equal(o.float().cpu().numpy(), want, equal_nan=True)
+    assert torch.equal(lse, clean_lse)
