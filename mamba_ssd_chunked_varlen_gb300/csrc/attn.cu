@@ -204,6 +204,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 constexpr int kJoinWarps = 16;
 constexpr int kJoinCtas = 2 * kAttnCtas;
 
+// A sum v of a piece by its weight w: an infinity stays one (and NaN is NaN) where the
+// weight has underflowed, so that what a row sees does not depend on how it was cut.
+__device__ __forceinline__ float weighted(float w, float v)
+{
+    return fabsf(v) == INFINITY ? v : w * v;
+}
+
 // Adds up pieces from, from + step, ... <= last of a row: its sums relative to `top`.
 template <int kE>
 __device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows, int first, int from,
@@ -237,9 +244,8 @@ __device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows,
         top = nt;
 #pragma unroll
         for (int j = 0; j < kE; ++j)
-            acc[j] *= f;
-        // eight pieces' loads at a time; those past the last have the weight zero and
-        // are not read
+            acc[j] = weighted(f, acc[j]);
+        // eight pieces' loads at a time; those past the last are not read, but zeros
         const int n = min(32, (last - base) / step + 1);
         for (int k0 = 0; k0 < n; k0 += 8) {
             float v[8][kE];
@@ -268,7 +274,7 @@ __device__ __forceinline__ void join_pieces(const AttnLine &line, int part_rows,
                 const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
 #pragma unroll
                 for (int j = 0; j < kE; ++j)
-                    acc[j] += wk == 0.f ? 0.f : wk * v[k][j];
+                    acc[j] += weighted(wk, v[k][j]);
             }
         }
     }
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2)
             for (int j = 0; j < kE; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[j][i] *= f;
+                    acc[j][i] = weighted(f, acc[j][i]);
             const int n = min(8, e.w - base + 1);
 #pragma unroll 2
             for (int i = 0; i < n; ++i) {
@@ -392,10 +398,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2)
 #pragma unroll
                 for (int j = 0; j < kE; ++j) {
                     const float4 v = src[j * 8 * attn_part_rows(0)];
-                    acc[j][0] += wi == 0.f ? 0.f : wi * v.x;
-                    acc[j][1] += wi == 0.f ? 0.f : wi * v.y;
-                    acc[j][2] += wi == 0.f ? 0.f : wi * v.z;
-                    acc[j][3] += wi == 0.f ? 0.f : wi * v.w;
+                    acc[j][0] += weighted(wi, v.x);
+                    acc[j][1] += weighted(wi, v.y);
+                    acc[j][2] += weighted(wi, v.z);
+                    acc[j][3] += weighted(wi, v.w);
                 }
             }
         }
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2)
                     sum += m == -INFINITY ? s_ml[w][1] : f * s_ml[w][1];
 #pragma unroll
                     for (int j = 0; j < kE; ++j)
-                        acc[j] += f == 0.f ? 0.f : f * s_acc[w][lane * kE + j];
+                        acc[j] += weighted(f, s_acc[w][lane * kE + j]);
                 }
                 write(e, row, top, sum, acc);
             }

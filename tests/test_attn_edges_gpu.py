@@ -158,3 +158,36 @@ def test_infinite_values(kv, new, dim, window):
             want[i, h] = np.where(seen[h // 2] == 0, want[i, h], seen[h // 2])
     assert np.array_equal(o.float().cpu().numpy(), want, equal_nan=True)
     assert torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("case", ["few", "few16", "tiles", "wide"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_values_of_a_negligible_piece(kind, case):
+    """NaN (bf16: and infinities) in V reach the rows that see them also where all keys of the
+    piece that they lie in have probabilities of 2^-738, and no column or row but theirs."""
+    import torch
+    new, kv, lo, hi, at = {"few": (1, 400, 32, 64, 40), "few16": (5, 400, 32, 64, 40),
+                           "tiles": (40, 700, 128, 256, 200), "wide": (1, 70000, 32000, 32320, 32160)}[case]
+    b = Batch([(new, kv)], 4, 2, 64, 16, kind, seed=26) if case != "wide" else \
+        Batch([(new, kv)], 2, 1, 64, 16, kind, seed=26)
+    b.q.fill_(8.0)
+    b.k_seq[0].mul_(0.125)
+    b.k_seq[0][lo:hi] = -8.0
+    b.fill()
+    clean, clean_lse = b.attend()
+    p, r = b.row_of(0, at)
+    if kind == "bf16":
+        b.v_cache[p, 0, r, 7] = float("nan")
+        b.v_cache[p, 0, r, 8] = float("inf")
+        b.v_cache[p, 0, r, 9] = -float("inf")
+    else:
+        b.v_scale[p, 0, r] = float("nan")
+    o, lse = b.attend()
+    if kind == "bf16":
+        assert torch.isnan(o[:, :2, 7]).all()
+        assert (o[:, :2, 8] == float("inf")).all() and (o[:, :2, 9] == -float("inf")).all()
+        o[:, :2, 7:10] = clean[:, :2, 7:10]
+    else:
+        assert torch.isnan(o[:, :2]).all()
+        o[:, :2] = clean[:, :2]
+    assert torch.equal(o, clean) and (kind != "bf16" or torch.equal(lse, clean_lse))
