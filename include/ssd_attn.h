@@ -90,9 +90,10 @@ SSD_API ssd_status_t ssd_kv_cache_read(
     int64_t table_stride, int32_t cache_type, int64_t k_stride, int64_t v_stride,
     uint32_t *errors, ssd_stream_t stream);
 
-/* Bytes of device scratch that ssd_attn_varlen_fwd needs for these sizes, or 0
- * when they are invalid or unsupported.  It does not depend on the contexts'
- * lengths. */
+/* Bytes of device scratch that ssd_attn_varlen_fwd needs for these sizes, and
+ * enough for every call that is not larger in any of them (fewer kv heads, as in
+ * another layer, among them), whatever the contexts' lengths; or 0 when they are
+ * invalid or unsupported. */
 SSD_API size_t ssd_attn_varlen_workspace_size(int64_t total_len, int32_t batch, int32_t nheads,
                                               int32_t nheads_kv, int32_t head_dim);
 

@@ -522,7 +522,9 @@ size_t ssd_attn_varlen_workspace_size(int64_t total_len, int32_t batch, int32_t 
 {
     if (!ssd::sizes_ok(total_len, batch, nheads, nheads_kv, head_dim))
         return 0;
-    return ssd::attn_layout(total_len, batch, nheads / nheads_kv, head_dim).total;
+    // for the largest group that so many query heads can have (it needs the most units), so
+    // that calls of fewer kv heads fit as well
+    return ssd::attn_layout(total_len, batch, std::min(nheads, ssd::kTileRows), head_dim).total;
 }
 
 ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void *k_cache,

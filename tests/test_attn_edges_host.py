@@ -108,3 +108,19 @@ def test_window_out_of_range_is_refused(no_launch, window):
     with pytest.raises(ValueError, match="window"):
         attention.ssd_attn_varlen_fwd(a["x"], None, a["x"], *a["cache"], a["qsl"], a["lens"], a["table"],
                                       softmax_scale=1.0, window=window, workspace=a["ws"])
+
+
+def test_workspace_serves_every_smaller_call():
+    """Of two calls' sizes of which none of the second is larger, the second needs no more:
+    one workspace serves layers of different head counts."""
+    ws = attention.ssd_attn_varlen_workspace_size
+    sizes = [(total, batch, heads, kv_heads, dim)
+             for total in (1, 100, 4096) for batch in (1, 64) for dim in (64, 128)
+             for heads, kv_heads in ((1, 1), (32, 1), (32, 4), (32, 8), (32, 32), (128, 1), (256, 2),
+                                     (24, 8), (24, 1))]
+    need = {s: ws(*s) for s in sizes}
+    assert all(need.values())
+    for large in sizes:
+        for small in sizes:
+            if all(a <= b for a, b in zip(small, large)):
+                assert need[small] <= need[large], (small, large)
