@@ -115,7 +115,8 @@ SSD_API size_t ssd_attn_varlen_workspace_size(int64_t total_len, int32_t batch, 
  * Sums and softmax statistics are fp32; probabilities (times v's scale) enter the
  * product with v as one bf16 each, or as two where a sequence has at most 16 query
  * rows a kv head.  Supported as above, nheads a multiple of nheads_kv, at most 128
- * query heads a kv head; window >= 0; softmax_scale finite. */
+ * query heads a kv head; window >= 0; softmax_scale finite, and so
+ * is its product with log2(e). */
 SSD_API ssd_status_t ssd_attn_varlen_fwd(
     void *o, float *lse, const void *q, const void *k_cache, const void *v_cache,
     const float *k_scale, const float *v_scale, const int32_t *query_start_loc,

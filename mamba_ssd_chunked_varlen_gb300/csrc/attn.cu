@@ -546,7 +546,8 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
                  table_stride, cache_type, errors);
     if (st != SSD_OK)
         return st;
-    if (nheads <= 0 || nheads % nheads_kv != 0 || window < 0 || !std::isfinite(softmax_scale))
+    const float scale_log2 = std::fabs(softmax_scale) * 1.4426950408889634f;
+    if (nheads <= 0 || nheads % nheads_kv != 0 || window < 0 || !std::isfinite(scale_log2))
         return SSD_ERR_INVALID_ARG;
     if (!sizes_ok(total_len, batch, nheads, nheads_kv, head_dim))
         return SSD_ERR_UNSUPPORTED;
@@ -574,7 +575,7 @@ ssd_status_t ssd_attn_varlen_fwd(void *o, float *lse, const void *q, const void 
     // left are below 2^30, so that a position less a window stays in 32 bits
     p.window = window >= static_cast<int64_t>(table_width) * page_size ? 0 : window;
     // a scale of zero still has to leave the hidden keys' -infinity as it is
-    p.scale_log2 = std::fmax(std::fabs(softmax_scale) * 1.4426950408889634f, 0x1p-120f);
+    p.scale_log2 = std::fmax(scale_log2, 0x1p-120f);
     p.negate = softmax_scale < 0.f;
     p.seq_units = reinterpret_cast<int32_t *>(ws + L.seq_units);
     for (int k = 0; k < 2; ++k)

@@ -124,3 +124,13 @@ def test_workspace_serves_every_smaller_call():
         for small in sizes:
             if all(a <= b for a, b in zip(small, large)):
                 assert need[small] <= need[large], (small, large)
+
+
+@pytest.mark.parametrize("scale", [2.5e38, -3.4e38])
+def test_softmax_scale_that_overflows_is_refused(scale):
+    """Scores are in units of log2: a scale whose product with log2(e) is infinite is none."""
+    import ctypes
+    lib = attention._functions()
+    p = ctypes.c_void_p(1 << 12)
+    assert lib.attn(p, None, p, p, p, None, None, p, p, p, 10, 2, 4, 2, 64, 8, 16, 4, 4, 0, 0, 0, scale, 0,
+                    p, 1 << 40, None, None) == 1
