@@ -69,8 +69,8 @@ typedef enum {
  *              v_stride elements apart (0: contiguous), e.g. column slices of
  *              a fused projection; strides multiples of 8, 16-byte aligned
  *
- * Supported: head_dim 64 or 128; page_size 16, 32, 64, 128 or 256.  Cache
- * pointers 16-byte aligned.  Two rows of one call must not share a cache row. */
+ * Supported: head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; at most
+ * 65,535 kv heads.  Cache pointers 16-byte aligned.  Two rows of one call must not share a cache row. */
 SSD_API ssd_status_t ssd_kv_cache_write(
     const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
     const int32_t *query_start_loc, const int32_t *kv_lens, const int32_t *block_table,

@@ -508,8 +508,8 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64
 bool sizes_ok(int64_t total_len, int32_t batch, int32_t nheads, int32_t nheads_kv, int32_t head_dim)
 {
     return total_len >= 0 && total_len <= INT32_MAX / 2 && batch >= 0 && batch <= INT32_MAX / 2 &&
-           nheads > 0 && nheads_kv > 0 && nheads % nheads_kv == 0 && nheads / nheads_kv <= kTileRows &&
-           (head_dim == 64 || head_dim == 128);
+           nheads > 0 && nheads_kv > 0 && nheads_kv <= kKvMaxHeads && nheads % nheads_kv == 0 &&
+           nheads / nheads_kv <= kTileRows && (head_dim == 64 || head_dim == 128);
 }
 
 }  // namespace

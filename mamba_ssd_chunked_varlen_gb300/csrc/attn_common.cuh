@@ -30,6 +30,8 @@ inline cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaS
 // normal fp32 numbers for every row, all zeros among them.
 constexpr float kKvTiny = 8.673617379884035e-19f;   // 2^-60
 
+constexpr int kKvMaxHeads = 65535;   // kv heads of a call
+
 constexpr float kInt8Max = 127.f;
 constexpr float kE4m3Max = 448.f;
 

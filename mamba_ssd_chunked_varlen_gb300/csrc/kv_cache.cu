@@ -34,7 +34,7 @@ ssd_status_t kv_check(KvView *c, const void *k_cache, const void *v_cache, const
     if (table_stride < table_width)
         return SSD_ERR_INVALID_ARG;
     if (total_len > INT32_MAX / 2 || batch > INT32_MAX / 2 || num_pages > INT32_MAX / 2 / nheads_kv ||
-        static_cast<int64_t>(table_width) * page_size > INT32_MAX / 2 || nheads_kv > 65535)
+        static_cast<int64_t>(table_width) * page_size > INT32_MAX / 2 || nheads_kv > kKvMaxHeads)
         return SSD_ERR_UNSUPPORTED;
     if (total_len > 0 && batch > 0) {
         if (!qsl || !kv_lens || (table_width > 0 && !block_table))

@@ -134,3 +134,10 @@ def test_softmax_scale_that_overflows_is_refused(scale):
     p = ctypes.c_void_p(1 << 12)
     assert lib.attn(p, None, p, p, p, None, None, p, p, p, 10, 2, 4, 2, 64, 8, 16, 4, 4, 0, 0, 0, scale, 0,
                     p, 1 << 40, None, None) == 1
+
+
+def test_workspace_size_of_unsupported_heads():
+    """A number of kv heads that the calls refuse has no workspace."""
+    ws = attention.ssd_attn_varlen_workspace_size
+    assert ws(10, 2, 65535, 65535, 64) > 0
+    assert ws(10, 2, 65536, 65536, 64) == 0
