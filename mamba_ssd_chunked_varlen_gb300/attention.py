@@ -99,6 +99,8 @@ def _refuse(f, k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, blo
         raise ValueError("a bfloat16 cache has no scales")
     _tensor(query_start_loc, "query_start_loc", f.i32, device)
     _tensor(kv_lens, "kv_lens", f.i32, device)
+    if query_start_loc.dim() != 1 or query_start_loc.shape[0] < 1:
+        raise ValueError("query_start_loc must have shape (batch + 1,)")
     batch = query_start_loc.shape[0] - 1
     if kv_lens.shape != (batch,):
         raise ValueError(f"kv_lens must have shape ({batch},)")

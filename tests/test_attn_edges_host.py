@@ -141,3 +141,18 @@ def test_workspace_size_of_unsupported_heads():
     ws = attention.ssd_attn_varlen_workspace_size
     assert ws(10, 2, 65535, 65535, 64) > 0
     assert ws(10, 2, 65536, 65536, 64) == 0
+
+
+@pytest.mark.parametrize("name,make", [
+    ("qsl", lambda: torch.zeros((), dtype=torch.int32)), ("qsl", lambda: torch.zeros(0, dtype=torch.int32)),
+    ("qsl", lambda: torch.zeros(3, 1, dtype=torch.int32)), ("qsl", lambda: torch.zeros(2, dtype=torch.int32)),
+    ("qsl", lambda: torch.zeros(3, dtype=torch.int64)), ("lens", lambda: torch.zeros((), dtype=torch.int32)),
+    ("lens", lambda: torch.zeros(3, dtype=torch.int32)), ("lens", lambda: torch.zeros(4, dtype=torch.int32)[::2]),
+    ("table", lambda: torch.zeros(2, dtype=torch.int32)), ("table", lambda: torch.zeros(3, 3, dtype=torch.int32)),
+    ("table", lambda: torch.zeros((), dtype=torch.int32)), ("table", lambda: torch.zeros(3, 2, dtype=torch.int32).T)])
+def test_shapes_of_the_batch_are_refused(no_launch, name, make):
+    a = batch_of()
+    a[name] = on_device(make())
+    for call in calls(a):
+        with pytest.raises(ValueError):
+            call()
