@@ -176,8 +176,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tensormap(&tmX);
         ptx::prefetch_tensormap(&tmS);
     }
-    // with the block table the block-map kernel has completed (the chunk-state
-    // CTAs read it before letting later kernels launch)
+    // the block-map kernel has long ended where there is a block table (the chunk-state
+    // CTAs read it before letting later kernels launch), but only this grid's own wait
+    // makes the table visible here
+    if (p.table != nullptr)
+        pdl_wait();
     const BlockInfo bi = p.table != nullptr ? lookup_block(p, blk)
                                             : map_block<kThreads>(p, blk, scratch, nullptr);
     // Every CTA waits for the previous grid before it leaves (those without an
