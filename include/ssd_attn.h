@@ -32,7 +32,9 @@
  * scale = a / M, with M = 127 (int8, ties to even) or 448 (fp8 e4m3, its own
  * rounding to nearest even).  A row that holds an infinity or a NaN gets codes
  * 0 and scale NaN: it reads back as NaN, and so is every attention row that
- * sees it, and no other.
+ * sees it, and no other.  A cache filled in another way may have scales of any
+ * finite value, or NaN; e4m3's NaN codes may lie only in rows that no sequence
+ * holds.
  *
  * Conventions are those of ssd_scan.h: device pointers owned by the caller,
  * asynchronous on `stream`, SSD_OK or a status with nothing launched.  Errors
@@ -70,7 +72,8 @@ typedef enum {
  *              a fused projection; strides multiples of 8, 16-byte aligned
  *
  * Supported: head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; at most
- * 65,535 kv heads.  Cache pointers 16-byte aligned.  Two rows of one call must not share a cache row. */
+ * 65,535 kv heads.  Cache pointers 16-byte aligned.  Two rows of one call must
+ * not share a cache row. */
 SSD_API ssd_status_t ssd_kv_cache_write(
     const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
     const int32_t *query_start_loc, const int32_t *kv_lens, const int32_t *block_table,
@@ -104,7 +107,13 @@ SSD_API size_t ssd_attn_varlen_workspace_size(int64_t total_len, int32_t batch, 
  *   S_j = softmax_scale * q_i . k_j   for i - window < j <= i (all j <= i with window 0)
  *   o_i = sum_j exp(S_j) v_j / sum_j exp(S_j),   lse_i = ln sum_j exp(S_j)
  *
- * A row that sees no key gets o = 0 and lse = -infinity.
+ * A row that sees no key gets o = 0 and lse = -infinity.  Keys that the mask hides
+ * do not count, whatever they hold.  Over a bf16 cache an infinity in V is the
+ * result of the rows that see it (where its probability is too small for fp32
+ * it may be NaN), and NaN is NaN.  Probabilities are relative to a reference that
+ * may lag behind the maximum (by 2^16 at most), so that sums of p v pass through
+ * numbers larger than the result: values up to 2^80 in magnitude are safe at any
+ * length, larger ones may give infinities.
  *
  *   o, q       bf16 (total_len, nheads, head_dim), rows o_stride and q_stride
  *              elements apart (0: contiguous; multiples of 8); 16-byte aligned
@@ -115,8 +124,8 @@ SSD_API size_t ssd_attn_varlen_workspace_size(int64_t total_len, int32_t batch, 
  * Sums and softmax statistics are fp32; probabilities (times v's scale) enter the
  * product with v as one bf16 each, or as two where a sequence has at most 16 query
  * rows a kv head.  Supported as above, nheads a multiple of nheads_kv, at most 128
- * query heads a kv head; window >= 0; softmax_scale finite, and so
- * is its product with log2(e). */
+ * query heads a kv head; window >= 0 (one that no context can pass is none);
+ * softmax_scale finite, and so is its product with log2(e). */
 SSD_API ssd_status_t ssd_attn_varlen_fwd(
     void *o, float *lse, const void *q, const void *k_cache, const void *v_cache,
     const float *k_scale, const float *v_scale, const int32_t *query_start_loc,

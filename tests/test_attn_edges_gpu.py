@@ -191,3 +191,18 @@ def test_values_of_a_negligible_piece(kind, case):
         assert torch.isnan(o[:, :2]).all()
         o[:, :2] = clean[:, :2]
     assert torch.equal(o, clean) and (kind != "bf16" or torch.equal(lse, clean_lse))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_large_values(kind):
+    """Values of 2^79 while the scores grow from key to key, so that the reference lags behind
+    the maximum: the sums stay finite."""
+    import torch
+    b = Batch([(1, 900), (5, 500), (60, 700)], 4, 2, 64, 32, kind, seed=29)
+    for k, v in zip(b.k_seq, b.v_seq):
+        k.abs_().mul_(torch.linspace(0.0, 1.5, k.shape[0])[:, None, None]).copy_(k)
+        v.sign_().mul_(2.0 ** 79)
+    b.q.abs_()
+    b.fill()
+    o, lse = b.attend()
+    check_attend(b, o, lse, what="large")
