@@ -30,13 +30,14 @@
 // int8 keys, one token each: 137 us of the call's 149, for 639 MB, 4.7 TB/s, 69 % of the copy rate.  Each
 // scheduler has three warps, which wait for one another's widening and products
 // more than for memory (issue 51 %, integer pipe 56 %); more warps have too few
-// registers (12 warps of 168: 152 us a call, 14 of 144: 179, 16 of 128: 162).  Tiles
-// of 16 keys instead of 32: 160 us instead of 156.
+// registers (12 warps of 168: 152 us a call, 14 of 144: 179, 16 of 128: 162).  At
+// head_dim 128 the 168 do not quite suffice either: some 60 (bf16) to 230 bytes
+// a thread are spilled.  Tiles of 16 keys instead of 32: 160 us instead of 156.
 //
 // 8-bit codes are widened in registers, which is exact: K's to fp16 (the cheaper
 // way; a row of Q is scaled by a power of two to fit fp16's range, exact but for
-// elements below 2^-32 of the row's largest), V's to bf16, because a weight times
-// its key's scale needs the range.
+// elements below 2^-24 of the row's largest, which are off by 2^-32 of it at most), V's to
+// bf16, because a weight times its key's scale needs the range.
 #pragma once
 
 #include <cfloat>

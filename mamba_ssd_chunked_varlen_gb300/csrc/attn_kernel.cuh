@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *s_nonfinite = s_abort + 1;   // V rows of the current segment were cleaned
+    // infinities or NaN were taken out of some V tile: from then on the output of every
+    // segment looks its masked tiles over for what to add back
+    volatile int *s_nonfinite = s_abort + 1;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // the same in every lane
 
