@@ -193,6 +193,42 @@ def test_values_of_a_negligible_piece(kind, case):
     assert torch.equal(o, clean) and (kind != "bf16" or torch.equal(lse, clean_lse))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_more_sequences_than_the_plan_keeps_on_chip(kind):
+    """Over 4,096 sequences, of both kinds of unit, and more units of a kind than 1,024."""
+    lens = [(1, 1 + 5 * b % 60) for b in range(4300)] + [(20, 30), (0, 9), (3, 3)] * 20 + [(9, 140)]
+    b = Batch(lens, 2, 1, 64, 16, kind, seed=27).fill()
+    o, lse = b.attend()
+    check_attend(b, o, lse, what="many")
+    assert b.errors.item() == 0
+
+
+@pytest.mark.parametrize("kind,window", [("bf16", 0), ("int8", 0), ("fp8", 100)])
+def test_far_pages(kind, window):
+    """Pages past 2^31 elements into the cache."""
+    b = Batch([(1, 700), (40, 300), (5, 90)], 4, 2, 64, 256, kind, seed=28)
+    page = 256 * 2 * 64
+    b.pages = (1 << 31) // page + 8
+    near = b.table_cpu < 1 << 30
+    b.table_cpu = b.table_cpu.where(~near, b.pages - 1 - b.table_cpu)
+    b.block_table.copy_(b.table_cpu)
+    b.k_cache = b.k_cache.new_zeros((b.pages, 2, 256, 64))
+    b.v_cache = b.k_cache.clone()
+    if kind != "bf16":
+        b.k_scale = b.k_scale.new_zeros((b.pages, 2, 256))
+        b.v_scale = b.k_scale.clone()
+    b.fill()
+    o, lse = b.attend(window=window)
+    # (the pages in use alone, counted from the first of them)
+    low = b.pages - 8 - 1
+    for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        if getattr(b, name) is not None:
+            setattr(b, name, getattr(b, name)[low:].clone())
+    b.table_cpu = b.table_cpu.where(~near, b.table_cpu - low)
+    check_attend(b, o, lse, window=window, what="far")
+    assert b.errors.item() == 0
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_large_values(kind):
     """Values of 2^79 while the scores grow from key to key, so that the reference lags behind
