@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(Cfg<kType, kDim>::kThreads, 1)
                         ptx::fence_proxy_async_smem();
                     }
                     const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
+                    __syncwarp();        // the lanes' zeros, before the arrival that lets them be read
                     if (lane == 0)
                         ptx::mbar_arrive_expect_tx(bars + kScFull + slot, n * 2 * bytes);
                     __syncwarp();

@@ -242,3 +242,20 @@ def test_large_values(kind):
     b.fill()
     o, lse = b.attend()
     check_attend(b, o, lse, what="large")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_without_a_page(kind):
+    """Whole key tiles whose pages are out of range read as zeros, one after the other and between
+    tiles that are there."""
+    from mamba_ssd_chunked_varlen_gb300 import attention
+    b = Batch([(40, 1500), (2, 600)], 4, 2, 64, 32, kind, seed=33).fill()
+    ks, vs = b.stored()
+    for seq, lo, hi in ((0, 128, 640), (0, 768, 896), (0, 1024, 1280), (1, 0, 256)):
+        b.block_table[seq, lo // 32:hi // 32] = b.pages
+        ks[seq][lo:hi] = 0.0
+        vs[seq][lo:hi] = 0.0
+    for _ in range(5):
+        o, lse = b.attend()
+        check_attend(b, o, lse, what="no page", stored=(ks, vs))
+    assert b.errors.item() == attention.DEVERR_BAD_PAGE
