@@ -1,0 +1,76 @@
+/*
+ * ssd_layers.h -- C ABI of the operators around the scan (ssd_scan.h) and the
+ * attention (ssd_attn.h) in a hybrid model's layers: the short causal
+ * convolution before a scan, the selective scan whose step and decay are each
+ * channel's own, the root-mean-square norm, and rotary positions.
+ *
+ * They take the ragged batch of those two:
+ *
+ *   query_start_loc   int32 (batch + 1): the new tokens of sequence b are rows
+ *                     [qsl[b], qsl[b+1]) of the token-major tensors.  qsl[0] is
+ *                     0; qsl[batch] may be less than total_len (a padded batch):
+ *                     rows behind the last sequence are neither used nor written
+ *   has_initial_state uint8 (batch) or NULL (all false); nonzero = true
+ *   cache_indices     uint32 (batch): pool slot of sequence b.  SSD_NO_SLOT is
+ *                     none: the state starts at zero and is not kept.  Other
+ *                     sequences' slots must be distinct
+ *
+ * Only the pool slots that cache_indices names are written, each with the state
+ * after its sequence's last token, also for a sequence of length 0 (its initial
+ * state, or zeros).
+ *
+ * Token-major tensors have rows a stride of their own apart, in elements
+ * (0: contiguous), at least the row and a multiple of 8; they are 16-byte aligned.
+ * Outputs must not overlap inputs where it is not said that they may.
+ *
+ * Conventions are those of ssd_scan.h: device pointers owned by the caller,
+ * asynchronous on `stream`, SSD_OK or a status with nothing launched.  Errors
+ * that only the device can see are OR-ed into `errors` (device memory, or NULL),
+ * which the library never clears:
+ *
+ *   SSD_DEVERR_BAD_QUERY_START_LOC  qsl[0] != 0, decreasing, or above total_len: a
+ *                     sequence with such a bound is skipped, the rows that no good
+ *                     sequence holds and the skipped sequences' slots are
+ *                     unspecified (no other memory is touched)
+ *   SSD_DEVERR_BAD_CACHE_INDEX      cache_indices[b] >= max_slots and not
+ *                     SSD_NO_SLOT: taken for SSD_NO_SLOT
+ */
+#ifndef SSD_LAYERS_H_
+#define SSD_LAYERS_H_
+
+#include "ssd_attn.h"
+#include "ssd_scan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SSD_NO_SLOT 0xffffffffu
+
+/* The short causal convolution of every channel, for prompts and single tokens:
+ *
+ *   y[t,c] = act(bias[c] + sum_{j < width} weight[c,j] u[t - (width-1) + j, c])
+ *
+ * with u = x in the sequence and, before its first token, the last inputs that
+ * its slot holds (zeros without has_initial_state); act is silu, v / (1 + e^-v),
+ * or nothing.  The slot gets the last width - 1 inputs.
+ *
+ *   y, x       bf16 (total_len, channels), rows y_stride and x_stride apart, e.g.
+ *              column slices of a fused projection
+ *   weight     fp32 (channels, width);  bias fp32 (channels) or NULL (zeros)
+ *   conv_pool  bf16 (max_slots, width - 1, channels): the oldest input first
+ *
+ * Supported: width 2, 3 or 4; channels a multiple of 8, at most 2^20.  Sums are
+ * fp32, y is rounded once. */
+SSD_API ssd_status_t ssd_causal_conv_varlen_fwd(
+    void *y, const void *x, const float *weight, const float *bias, void *conv_pool,
+    const int32_t *query_start_loc, const uint8_t *has_initial_state,
+    const uint32_t *cache_indices, int64_t total_len, int32_t batch, int32_t channels,
+    int32_t width, int64_t max_slots, int64_t y_stride, int64_t x_stride, int32_t silu,
+    uint32_t *errors, ssd_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSD_LAYERS_H_ */

@@ -1,10 +1,10 @@
 """GB300-native (sm_103a) Mamba-2 SSD varlen forward prefill scan.
 
 The compute path is the CUDA library libssd_scan.so (C ABI in
-include/ssd_scan.h and include/ssd_attn.h); ``binding`` (the scan) and
-``attention`` (the paged key/value cache and the attention over it, for the
-attention layers of a hybrid model) are its thin Python front ends and
-``workloads`` the seeded synthetic inputs.
+include/ssd_scan.h, include/ssd_attn.h and include/ssd_layers.h); ``binding`` (the
+scan), ``attention`` (the paged key/value cache and the attention over it, for the
+attention layers of a hybrid model) and ``layers`` (what stands around the two) are
+its thin Python front ends and ``workloads`` the seeded synthetic inputs.
 """
 from .attention import (  # noqa: F401
     alloc_attn_workspace,
@@ -37,3 +37,4 @@ from .binding import (  # noqa: F401
     ssd_scan_varlen_workspace_size,
     status_string,
 )
+from .layers import ssd_causal_conv_varlen_fwd  # noqa: F401

@@ -3,7 +3,8 @@
 Each translation unit under csrc/ is compiled in parallel with nvcc
 (-gencode arch=compute_103a,code=sm_103a, -lineinfo, static CUDA runtime)
 and linked into one shared library exporting the C ABI of
-include/ssd_scan.h and include/ssd_attn.h.  Only nvcc and a host compiler are needed; no GPU.
+include/ssd_scan.h, include/ssd_attn.h and include/ssd_layers.h.  Only nvcc and a host
+compiler are needed; no GPU.
 """
 from __future__ import annotations
 

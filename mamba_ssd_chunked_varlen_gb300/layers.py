@@ -1,0 +1,155 @@
+"""Python binding of the C ABI in include/ssd_layers.h (ctypes): the operators
+around the scan and the attention in a hybrid model's layers.
+
+Argument marshalling only, as in ``binding``: the work runs in the CUDA kernels
+of libssd_scan.so on torch's current stream (or `stream`), and there is no CPU
+fallback.  Calls run on the device of their tensors.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import binding
+from .binding import SSD_OK, SSDError
+
+# Every symbol include/ssd_layers.h declares.
+EXPORTED_SYMBOLS = (
+    "ssd_causal_conv_varlen_fwd",
+)
+
+NO_SLOT = 0xffffffff   # SSD_NO_SLOT (-1 in an int32 tensor of cache_indices)
+
+_fn = None
+
+
+class _Functions:
+    def __init__(self):
+        import torch
+        lib = binding.library()
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        self.conv = lib.ssd_causal_conv_varlen_fwd
+        self.conv.restype = ctypes.c_int
+        self.conv.argtypes = [vp] * 8 + [i64, i32, i32, i32, i64, i64, i64, i32, vp, vp]
+        self.bf16, self.f32, self.i32, self.u32 = torch.bfloat16, torch.float32, torch.int32, torch.uint32
+        self.u8, self.bool = torch.uint8, torch.bool
+        # the current stream's handle alone, where torch has that (an order of
+        # magnitude less time than a Stream object)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _functions() -> _Functions:
+    global _fn
+    if _fn is None:
+        _fn = _Functions()
+    return _fn
+
+
+def _call(f, fn, what: str, device: int, stream, *args):
+    """Call into the library on the tensors' device and stream."""
+    if f.current_device() != device:
+        import torch
+        with torch.cuda.device(device):
+            return _call(f, fn, what, device, stream, *args)
+    st = fn(*args, f.raw_stream(device) if stream is None else stream.cuda_stream)
+    if st != SSD_OK:
+        raise SSDError(st, what)
+
+
+def _device(t, what: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _ptr(t, what: str, dtype, shape, device: int):
+    """Pointer of a contiguous tensor of exactly that type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must have dtype {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    raise ValueError(f"{what} must be on device {device}, got {t.device}")
+
+
+def _rows(t, what: str, dtype, shape, device: int):
+    """Pointer and row pitch (elements) of a token-major tensor whose rows are
+    contiguous and do not overlap (an expanded tensor's do: its pitch of 0 would say
+    "contiguous" in the C ABI)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on device {device}, got {t.device}")
+    row = 1
+    stride = t.stride()
+    for d in range(len(shape) - 1, 0, -1):
+        if stride[d] != row and shape[d] != 1:
+            raise ValueError(f"{what}: each token's row must be contiguous")
+        row *= shape[d]
+    if shape[0] <= 1:
+        return t.data_ptr(), row
+    if stride[0] < row:
+        raise ValueError(f"{what}: tokens' rows must not overlap (an expanded tensor has to be "
+                         "made contiguous)")
+    return t.data_ptr(), stride[0]
+
+
+def _errors(f, errors, device: int):
+    if errors is None:
+        return None
+    if errors.numel() < 1 or errors.dtype not in (f.i32, f.u32):
+        raise ValueError("errors must be an int32 or uint32 tensor of one element")
+    if errors.get_device() != device:
+        raise ValueError(f"errors must be on device {device}, got {errors.device}")
+    return errors.data_ptr()
+
+
+def _slots(f, query_start_loc, has_initial_state, cache_indices, device: int):
+    """Pointers of the batch and its slots, and the batch size."""
+    if query_start_loc.dim() != 1 or query_start_loc.shape[0] < 1:
+        raise ValueError("query_start_loc must have shape (batch + 1,)")
+    batch = query_start_loc.shape[0] - 1
+    has = None
+    if has_initial_state is not None:
+        has = _ptr(has_initial_state, "has_initial_state",
+                   f.bool if has_initial_state.dtype is f.bool else f.u8, (batch,), device)
+    return (_ptr(query_start_loc, "query_start_loc", f.i32, (batch + 1,), device), has,
+            _ptr(cache_indices, "cache_indices", f.u32 if cache_indices.dtype is f.u32 else f.i32,
+                 (batch,), device)), batch
+
+
+def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, has_initial_state,
+                               cache_indices, *, silu: bool = True, errors=None, stream=None) -> None:
+    """The short causal convolution of every channel, for prompts and single tokens,
+    with the last inputs of every sequence kept in a pool of slots.
+
+    y, x (rows, channels) bf16, each row contiguous, any row pitch that is a
+    multiple of 8 elements; weight (channels, width) fp32, width 2 to 4; bias
+    (channels,) fp32 or None; conv_pool (slots, width - 1, channels) bf16, updated
+    in place; query_start_loc (batch + 1,) int32; has_initial_state (batch,)
+    uint8/bool or None; cache_indices (batch,) int32/uint32 (same bits; -1 is no
+    slot); silu: y is silu of the sum.  errors: an int32 tensor of one element that
+    collects the SSD_DEVERR_* flags, or None."""
+    f = _functions()
+    device = _device(x, "x")
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must have shape (rows, channels) and weight (channels, width)")
+    shape = x.shape
+    total, channels = shape
+    width = weight.shape[1]
+    slots, batch = _slots(f, query_start_loc, has_initial_state, cache_indices, device)
+    py, sy = _rows(y, "y", f.bf16, shape, device)
+    px, sx = _rows(x, "x", f.bf16, shape, device)
+    max_slots = conv_pool.shape[0]
+    _call(f, f.conv, "ssd_causal_conv_varlen_fwd", device, stream,
+          py, px, _ptr(weight, "weight", f.f32, (channels, width), device),
+          None if bias is None else _ptr(bias, "bias", f.f32, (channels,), device),
+          _ptr(conv_pool, "conv_pool", f.bf16, (max_slots, width - 1, channels), device),
+          *slots, total, batch, channels, width, max_slots, sy, sx, bool(silu),
+          _errors(f, errors, device))
