@@ -69,6 +69,30 @@ SSD_API ssd_status_t ssd_causal_conv_varlen_fwd(
     int32_t width, int64_t max_slots, int64_t y_stride, int64_t x_stride, int32_t silu,
     uint32_t *errors, ssd_stream_t stream);
 
+/* Root-mean-square norm over groups of dim / ngroups columns.  For each row and group
+ *
+ *   y = s weight / sqrt(mean s^2 + eps)
+ *
+ * with s = x, or x + residual, which is written back to residual (rounded to
+ * bf16; the norm is that of the sum before), or x silu(gate).
+ *
+ *   x          bf16 (rows, dim);  gate, residual likewise or NULL, not both
+ *   weight     fp32 (dim) or NULL (ones)
+ *   y          (rows, dim) in bf16, or in 8-bit codes (out_type, ssd_kv_type_t); in
+ *              bf16 it may be x or gate itself
+ *   scale      fp32 (rows, ngroups) with 8-bit codes, else NULL: an element stands
+ *              for code * scale.  Codes and scales are those that ssd_attn.h defines
+ *              for cache rows, of each row's groups: a group with an infinity or a
+ *              NaN gets codes 0 and scale NaN
+ *
+ * Rows are any multiple of 8 elements apart that is not below dim.  Supported: dim /
+ * ngroups a multiple of 8, at most 32,768; eps from 2^-80 to 1.  s has to stay in
+ * fp32's range (its square need not).  All in fp32, rounded once. */
+SSD_API ssd_status_t ssd_rms_norm_fwd(
+    void *y, float *scale, const void *x, void *residual, const void *gate, const float *weight,
+    int64_t rows, int32_t dim, int32_t ngroups, int32_t out_type, float eps, int64_t y_stride,
+    int64_t x_stride, int64_t residual_stride, int64_t gate_stride, ssd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

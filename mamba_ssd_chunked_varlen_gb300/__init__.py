@@ -37,4 +37,7 @@ from .binding import (  # noqa: F401
     ssd_scan_varlen_workspace_size,
     status_string,
 )
-from .layers import ssd_causal_conv_varlen_fwd  # noqa: F401
+from .layers import (  # noqa: F401
+    ssd_causal_conv_varlen_fwd,
+    ssd_rms_norm_fwd,
+)

@@ -8,6 +8,7 @@
 
 #include "../../include/ssd_layers.h"
 #include "attn_common.cuh"
+#include "rows.cuh"
 #include "ssd_device.cuh"
 
 namespace ssd {
@@ -69,32 +70,10 @@ __device__ __forceinline__ int warp_last_start(const int32_t *qsl, int batch, in
     return lo;
 }
 
-// Eight bf16 values as fp32.
-__device__ __forceinline__ void widen8(const uint4 &r, float (&x)[8])
-{
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-__device__ __forceinline__ uint4 round8(const float (&x)[8])
-{
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7]));
-}
-
 // v / (1 + e^-v).  (e^-v may overflow: v / infinity is the right zero.)
 __device__ __forceinline__ float silu_f32(float v)
 {
     return __fdividef(v, 1.f + __expf(-v));
-}
-
-inline bool layer_sizes(int64_t total_len, int32_t batch, int64_t max_slots)
-{
-    return total_len >= 0 && batch >= 0 && max_slots >= 0;
 }
 
 // What every call with slots checks of them (total_len may be 0: slots are written all the same).

@@ -15,6 +15,7 @@ from .binding import SSD_OK, SSDError
 # Every symbol include/ssd_layers.h declares.
 EXPORTED_SYMBOLS = (
     "ssd_causal_conv_varlen_fwd",
+    "ssd_rms_norm_fwd",
 )
 
 NO_SLOT = 0xffffffff   # SSD_NO_SLOT (-1 in an int32 tensor of cache_indices)
@@ -30,6 +31,10 @@ class _Functions:
         self.conv = lib.ssd_causal_conv_varlen_fwd
         self.conv.restype = ctypes.c_int
         self.conv.argtypes = [vp] * 8 + [i64, i32, i32, i32, i64, i64, i64, i32, vp, vp]
+        self.norm = lib.ssd_rms_norm_fwd
+        self.norm.restype = ctypes.c_int
+        self.norm.argtypes = [vp] * 6 + [i64, i32, i32, i32, ctypes.c_float] + [i64] * 4 + [vp]
+        self.types = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
         self.bf16, self.f32, self.i32, self.u32 = torch.bfloat16, torch.float32, torch.int32, torch.uint32
         self.u8, self.bool = torch.uint8, torch.bool
         # the current stream's handle alone, where torch has that (an order of
@@ -153,3 +158,34 @@ def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, h
           _ptr(conv_pool, "conv_pool", f.bf16, (max_slots, width - 1, channels), device),
           *slots, total, batch, channels, width, max_slots, sy, sx, bool(silu),
           _errors(f, errors, device))
+
+
+def ssd_rms_norm_fwd(y, x, weight, *, residual=None, gate=None, scale=None, ngroups: int = 1,
+                     eps: float = 1e-5, stream=None) -> None:
+    """Root-mean-square norm over each row's groups of dim / ngroups columns, of
+    x, of x + residual (updated in place) or of x silu(gate).
+
+    x, residual, gate (rows, dim) bf16, each row contiguous, any row pitch that is a
+    multiple of 8 elements; weight (dim,) fp32 or None; y (rows, dim) bf16 (it may
+    be x or gate), or float8_e4m3fn or int8 codes with scale (rows, ngroups) fp32."""
+    f = _functions()
+    device = _device(x, "x")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x must have shape (rows, dim)")
+    rows, dim = shape
+    kind = f.types.get(y.dtype)
+    if kind is None:
+        raise ValueError(f"y must be bfloat16, float8_e4m3fn or int8, got {y.dtype}")
+    if (kind != 0) != (scale is not None):
+        raise ValueError("8-bit codes need a scale" if kind else "a bfloat16 output has no scale")
+    if ngroups < 1 or dim % ngroups:
+        raise ValueError(f"ngroups must divide {dim}, got {ngroups}")
+    py, sy = _rows(y, "y", y.dtype, shape, device)
+    px, sx = _rows(x, "x", f.bf16, shape, device)
+    pr, sr = (None, 0) if residual is None else _rows(residual, "residual", f.bf16, shape, device)
+    pg, sg = (None, 0) if gate is None else _rows(gate, "gate", f.bf16, shape, device)
+    _call(f, f.norm, "ssd_rms_norm_fwd", device, stream, py,
+          None if scale is None else _ptr(scale, "scale", f.f32, (rows, ngroups), device), px, pr, pg,
+          None if weight is None else _ptr(weight, "weight", f.f32, (dim,), device),
+          rows, dim, ngroups, kind, eps, sy, sx, sr, sg)

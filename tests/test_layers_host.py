@@ -64,3 +64,25 @@ def test_binding_refuses_cpu_tensors(lib):
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         layers.ssd_causal_conv_varlen_fwd(x, x, torch.zeros(64, 4), None, x.view(1, 2, 64), i, None, i[:1])
+
+
+def _norm(lib, **over):
+    a = dict(y=A, scale=None, x=A, residual=None, gate=None, weight=A, rows=4, dim=64, groups=1, kind=0,
+             eps=1e-5, ys=0, xs=0, rs=0, gs=0) | over
+    return lib.ssd_rms_norm_fwd(
+        _vp(a["y"]), _vp(a["scale"]), _vp(a["x"]), _vp(a["residual"]), _vp(a["gate"]), _vp(a["weight"]),
+        a["rows"], a["dim"], a["groups"], a["kind"], a["eps"], a["ys"], a["xs"], a["rs"], a["gs"], None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(rows=-1), 1), (dict(dim=0), 1), (dict(groups=0), 1), (dict(groups=3), 1), (dict(kind=3), 1),
+    (dict(kind=-1), 1), (dict(eps=0.0), 1), (dict(eps=-1.0), 1), (dict(eps=2.0), 1),
+    (dict(eps=float("nan")), 1), (dict(y=None), 1), (dict(x=None), 1), (dict(kind=1), 1),
+    (dict(kind=2), 1), (dict(scale=A), 1), (dict(residual=A, gate=A), 1), (dict(x=A + 8), 1),
+    (dict(y=A + 8), 1), (dict(residual=A + 2), 1), (dict(gate=A + 4), 1), (dict(weight=A + 4), 1),
+    (dict(ys=56), 1), (dict(xs=68), 1), (dict(rs=8), 1), (dict(gs=65), 1),
+    (dict(groups=16), 2), (dict(dim=60), 2), (dict(dim=32768 + 8), 2), (dict(rows=1 << 31), 2),
+    (dict(rows=1 << 29, dim=64 * 64, groups=64), 2), (dict(rows=0, y=None, x=None), 0),
+])
+def test_norm_refuses(lib, over, status):
+    assert _norm(lib, **over) == status
