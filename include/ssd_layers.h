@@ -93,6 +93,51 @@ SSD_API ssd_status_t ssd_rms_norm_fwd(
     int64_t rows, int32_t dim, int32_t ngroups, int32_t out_type, float eps, int64_t y_stride,
     int64_t x_stride, int64_t residual_stride, int64_t gate_stride, ssd_stream_t stream);
 
+/* Rotary positions.  The first rotary_dim elements of a head are pairs (a, b), element
+ * i with rotary_dim / 2 + i, or neighbours 2 i and 2 i + 1 (interleaved); pair i of
+ * the token at position p becomes
+ *
+ *   a' = magnitude (a cos(p f_i) - b sin(p f_i)),  b' = magnitude (b cos(p f_i) + a sin(p f_i))
+ *
+ * and the rest of the head stays.  Frequencies are a table of turns: f_i / (2 pi)
+ * as a 64-bit binary fraction, so that p f_i modulo a turn is one integer product,
+ * exact at any position; ssd_rope_table makes it.  Scaled frequencies (for contexts
+ * longer than a model was trained on) are other values of f_i and magnitude.
+ *
+ *   turns      uint64 (rotary_dim / 2), device memory
+ *   kv_lens    int32 (batch), as in ssd_attn.h: row t of sequence b is its token
+ *              kv_lens[b] - qsl[b+1] + t.  Rows at a negative position are padding:
+ *              neither used nor written, like rows that no sequence holds
+ *
+ * Supported: rotary_dim a multiple of 16, at most head_dim; head_dim 64 or 128. */
+
+/* Host only: turns[i] = frequencies[i] / (2 pi) 2^64, rounded, for n frequencies in
+ * radians per position, each at least 0 and below 2 pi (else SSD_ERR_INVALID_ARG). */
+SSD_API ssd_status_t ssd_rope_table(uint64_t *turns, const double *frequencies, int32_t n);
+
+/* Rotates the new tokens' queries and keys, or one of them (the other's pointers
+ * NULL): q and q_out bf16 (total_len, nheads, head_dim), k and k_out bf16 (total_len,
+ * nheads_kv, head_dim).  An output may be its input, at the same stride.  The cosine,
+ * the sine and the products are fp32, outputs are rounded once. */
+SSD_API ssd_status_t ssd_rope_varlen_fwd(
+    void *q_out, const void *q, void *k_out, const void *k, const uint64_t *turns,
+    const int32_t *query_start_loc, const int32_t *kv_lens, int64_t total_len, int32_t batch,
+    int32_t nheads, int32_t nheads_kv, int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+    float magnitude, int64_t q_out_stride, int64_t q_stride, int64_t k_out_stride,
+    int64_t k_stride, uint32_t *errors, ssd_stream_t stream);
+
+/* ssd_rope_varlen_fwd of q and k and ssd_kv_cache_write of the rotated k and of v in
+ * one launch: what the attention needs of a projection's output.  The rotated k is
+ * quantised from fp32.  Arguments as for these two; query_start_loc as above. */
+SSD_API ssd_status_t ssd_rope_kv_cache_write(
+    void *q_out, const void *q, const void *k, const void *v, const uint64_t *turns,
+    void *k_cache, void *v_cache, float *k_scale, float *v_scale, const int32_t *query_start_loc,
+    const int32_t *kv_lens, const int32_t *block_table, int64_t total_len, int32_t batch,
+    int32_t nheads, int32_t nheads_kv, int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+    float magnitude, int64_t num_pages, int32_t page_size, int32_t table_width,
+    int64_t table_stride, int32_t cache_type, int64_t q_out_stride, int64_t q_stride,
+    int64_t k_stride, int64_t v_stride, uint32_t *errors, ssd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,6 +38,10 @@ from .binding import (  # noqa: F401
     status_string,
 )
 from .layers import (  # noqa: F401
+    alloc_rope_table,
+    rope_frequencies,
     ssd_causal_conv_varlen_fwd,
     ssd_rms_norm_fwd,
+    ssd_rope_kv_cache_write,
+    ssd_rope_varlen_fwd,
 )

@@ -9,13 +9,18 @@ from __future__ import annotations
 
 import ctypes
 
-from . import binding
+import math
+
+from . import attention, binding
 from .binding import SSD_OK, SSDError
 
 # Every symbol include/ssd_layers.h declares.
 EXPORTED_SYMBOLS = (
     "ssd_causal_conv_varlen_fwd",
     "ssd_rms_norm_fwd",
+    "ssd_rope_table",
+    "ssd_rope_varlen_fwd",
+    "ssd_rope_kv_cache_write",
 )
 
 NO_SLOT = 0xffffffff   # SSD_NO_SLOT (-1 in an int32 tensor of cache_indices)
@@ -34,9 +39,20 @@ class _Functions:
         self.norm = lib.ssd_rms_norm_fwd
         self.norm.restype = ctypes.c_int
         self.norm.argtypes = [vp] * 6 + [i64, i32, i32, i32, ctypes.c_float] + [i64] * 4 + [vp]
+        self.rope_table = lib.ssd_rope_table
+        self.rope_table.restype = ctypes.c_int
+        self.rope_table.argtypes = [vp, vp, i32]
+        # total_len, batch, nheads, nheads_kv, head_dim, rotary_dim, interleaved, magnitude
+        rotary = [i64, i32, i32, i32, i32, i32, i32, ctypes.c_float]
+        self.rope = lib.ssd_rope_varlen_fwd
+        self.rope.restype = ctypes.c_int
+        self.rope.argtypes = [vp] * 7 + rotary + [i64] * 4 + [vp, vp]
+        self.rope_write = lib.ssd_rope_kv_cache_write
+        self.rope_write.restype = ctypes.c_int
+        self.rope_write.argtypes = ([vp] * 12 + rotary + [i64, i32, i32, i64, i32] + [i64] * 4 + [vp, vp])
         self.types = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
         self.bf16, self.f32, self.i32, self.u32 = torch.bfloat16, torch.float32, torch.int32, torch.uint32
-        self.u8, self.bool = torch.uint8, torch.bool
+        self.u8, self.bool, self.i64 = torch.uint8, torch.bool, torch.int64
         # the current stream's handle alone, where torch has that (an order of
         # magnitude less time than a Stream object)
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -189,3 +205,127 @@ def ssd_rms_norm_fwd(y, x, weight, *, residual=None, gate=None, scale=None, ngro
           None if scale is None else _ptr(scale, "scale", f.f32, (rows, ngroups), device), px, pr, pg,
           None if weight is None else _ptr(weight, "weight", f.f32, (dim,), device),
           rows, dim, ngroups, kind, eps, sy, sx, sr, sg)
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     original_len: int = 8192, low_turns: float = 1.0, high_turns: float = 32.0):
+    """Frequencies (radians per position, rotary_dim / 2 of them, in 64 bits) and the
+    magnitude for alloc_rope_table and the rotary calls.
+
+    f_i = base^(-2 i / rotary_dim), for contexts `factor` times original_len changed by
+    `scaling`:
+
+      "none"        as they are
+      "linear"      all divided by factor
+      "base"        the base times factor^(rotary_dim / (rotary_dim - 2)): the highest stays,
+                    the lowest is divided by factor
+      "ramp"        divided where a pair makes at most low_turns turns in original_len
+                    positions, kept from high_turns on, blended linearly in the pair's
+                    index between; magnitude 0.1 ln(factor) + 1
+      "wavelength"  the same blended linearly in the number of turns; magnitude 1"""
+    if rotary_dim < 4 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and at least 4, got {rotary_dim}")
+    if not (base > 1.0 and math.isfinite(base) and factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("base must be above 1 and factor at least 1")
+    half = rotary_dim // 2
+    if scaling == "base":
+        base *= factor ** (rotary_dim / (rotary_dim - 2))
+    f = [base ** (-i / half) for i in range(half)]
+    if scaling in ("none", "base"):
+        return f, 1.0
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling not in ("ramp", "wavelength"):
+        raise ValueError(f"scaling must be none, linear, base, ramp or wavelength, got {scaling!r}")
+    if not 0.0 < low_turns < high_turns or original_len < 1:
+        raise ValueError("0 < low_turns < high_turns and original_len >= 1 are needed")
+    if scaling == "ramp":
+        def pair_of(turns):    # the (fractional) pair that makes so many turns in original_len positions
+            return half * math.log(original_len / (turns * 2 * math.pi)) / math.log(base)
+        low = max(math.floor(pair_of(high_turns)), 0)
+        high = min(math.ceil(pair_of(low_turns)), half - 1)
+        keep = [1.0 - min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) for i in range(half)]
+    else:
+        keep = [min(max((x * original_len / (2 * math.pi) - low_turns) / (high_turns - low_turns), 0.0), 1.0)
+                for x in f]
+    return ([x / factor * (1.0 - k) + x * k for x, k in zip(f, keep)],
+            0.1 * math.log(factor) + 1.0 if scaling == "ramp" else 1.0)
+
+
+def alloc_rope_table(frequencies, device="cuda"):
+    """The table of turns that the rotary calls take: an int64 tensor of one element per
+    frequency (the bits of the C ABI's uint64)."""
+    import torch
+    values = [float(x) for x in frequencies]
+    if not values:
+        raise ValueError("at least one frequency is needed")
+    turns = (ctypes.c_uint64 * len(values))()
+    st = _functions().rope_table(turns, (ctypes.c_double * len(values))(*values), len(values))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_rope_table")
+    return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _rotary(f, table, device: int):
+    if table.dim() != 1:
+        raise ValueError("table must have shape (rotary_dim / 2,)")
+    return _ptr(table, "table", f.i64, table.shape, device), 2 * table.shape[0]
+
+
+def _heads(out, x, what: str, f, device: int):
+    if x.dim() != 3:
+        raise ValueError(f"{what} must have shape (rows, heads, head_dim)")
+    shape = x.shape
+    return *_rows(out, f"{what}_out", f.bf16, shape, device), *_rows(x, what, f.bf16, shape, device), shape
+
+
+def ssd_rope_varlen_fwd(q_out, q, k_out, k, table, query_start_loc, kv_lens, *, interleaved: bool = False,
+                        magnitude: float = 1.0, errors=None, stream=None) -> None:
+    """Rotate the new tokens' queries and keys by their positions (k and k_out may
+    both be None, or q and q_out).
+
+    q_out, q (rows, nheads, head_dim) and k_out, k (rows, nheads_kv, head_dim) bf16, each
+    row contiguous, any row pitch that is a multiple of 8 elements, an output may be
+    its input; table: alloc_rope_table's, of rotary_dim / 2 pairs; query_start_loc
+    (batch + 1,) and kv_lens (batch,) int32 as for ssd_kv_cache_write; interleaved: pairs
+    of neighbours and not of halves."""
+    f = _functions()
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
+        raise ValueError("q and q_out, or k and k_out, or both are needed")
+    device = _device(k if q is None else q, "k" if q is None else "q")
+    turns, rotary_dim = _rotary(f, table, device)
+    batch = query_start_loc.shape[0] - 1
+    qo = qi = ko = ki = None
+    sqo = sq = sko = sk = heads = heads_kv = 0
+    if q is not None:
+        qo, sqo, qi, sq, (total, heads, dim) = _heads(q_out, q, "q", f, device)
+    if k is not None:
+        ko, sko, ki, sk, shape = _heads(k_out, k, "k", f, device)
+        if q is not None and (shape[0] != total or shape[2] != dim):
+            raise ValueError(f"k must have shape ({total}, nheads_kv, {dim}), got {tuple(shape)}")
+        total, heads_kv, dim = shape
+    _call(f, f.rope, "ssd_rope_varlen_fwd", device, stream, qo, qi, ko, ki, turns,
+          _ptr(query_start_loc, "query_start_loc", f.i32, (batch + 1,), device),
+          _ptr(kv_lens, "kv_lens", f.i32, (batch,), device), total, batch, heads, heads_kv, dim, rotary_dim,
+          bool(interleaved), magnitude, sqo, sq, sko, sk, _errors(f, errors, device))
+
+
+def ssd_rope_kv_cache_write(q_out, q, k, v, table, k_cache, v_cache, k_scale, v_scale, query_start_loc,
+                            kv_lens, block_table, *, interleaved: bool = False, magnitude: float = 1.0,
+                            errors=None, stream=None) -> None:
+    """Rotate the new tokens' queries into q_out, and write their rotated keys and their
+    values into the paged cache, in one launch: ssd_rope_varlen_fwd and
+    ssd_kv_cache_write, with their arguments."""
+    f = _functions()
+    ptrs, batch, heads_kv, dim, sizes, pe, device = attention._cache(
+        attention._functions(), k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, block_table,
+        errors)
+    turns, rotary_dim = _rotary(f, table, device)
+    qo, sqo, qi, sq, shape = _heads(q_out, q, "q", f, device)
+    total, heads, _ = shape
+    if shape[2] != dim:
+        raise ValueError(f"q must have shape (rows, nheads, {dim}), got {tuple(shape)}")
+    pk, sk = _rows(k, "k", f.bf16, (total, heads_kv, dim), device)
+    pv, sv = _rows(v, "v", f.bf16, (total, heads_kv, dim), device)
+    _call(f, f.rope_write, "ssd_rope_kv_cache_write", device, stream, qo, qi, pk, pv, turns, *ptrs, total,
+          batch, heads, heads_kv, dim, rotary_dim, bool(interleaved), magnitude, *sizes, sqo, sq, sk, sv, pe)

@@ -86,3 +86,104 @@ def _norm(lib, **over):
 ])
 def test_norm_refuses(lib, over, status):
     assert _norm(lib, **over) == status
+
+
+ROPE = dict(qo=A, q=A, ko=A, k=A, v=A, turns=A, qsl=A, kv_lens=A, total=10, batch=2, heads=4, kv_heads=2, dim=64,
+            part=64, inter=0, m=1.0, qos=0, qs=0, kos=0, ks=0, vs=0, k_cache=A, v_cache=A, k_scale=None,
+            v_scale=None, table=A, pages=8, page=16, width=4, stride=4, kind=0)
+
+
+def _rope(lib, **over):
+    a = ROPE | over
+    return lib.ssd_rope_varlen_fwd(
+        _vp(a["qo"]), _vp(a["q"]), _vp(a["ko"]), _vp(a["k"]), _vp(a["turns"]), _vp(a["qsl"]), _vp(a["kv_lens"]),
+        a["total"], a["batch"], a["heads"], a["kv_heads"], a["dim"], a["part"], a["inter"], a["m"], a["qos"],
+        a["qs"], a["kos"], a["ks"], None, None)
+
+
+def _rope_write(lib, **over):
+    a = ROPE | over
+    return lib.ssd_rope_kv_cache_write(
+        _vp(a["qo"]), _vp(a["q"]), _vp(a["k"]), _vp(a["v"]), _vp(a["turns"]), _vp(a["k_cache"]), _vp(a["v_cache"]),
+        _vp(a["k_scale"]), _vp(a["v_scale"]), _vp(a["qsl"]), _vp(a["kv_lens"]), _vp(a["table"]), a["total"],
+        a["batch"], a["heads"], a["kv_heads"], a["dim"], a["part"], a["inter"], a["m"], a["pages"], a["page"],
+        a["width"], a["stride"], a["kind"], a["qos"], a["qs"], a["ks"], a["vs"], None, None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(total=-1), 1), (dict(batch=-1), 1), (dict(dim=0), 1), (dict(heads=-1), 1), (dict(part=0), 1),
+    (dict(part=80), 1), (dict(m=float("nan")), 1), (dict(m=float("inf")), 1), (dict(turns=None), 1),
+    (dict(turns=A + 4), 1), (dict(q=None), 1), (dict(qo=None), 1), (dict(k=None), 1), (dict(qsl=None), 1),
+    (dict(kv_lens=None), 1), (dict(q=A + 8), 1), (dict(qo=A + 2), 1), (dict(k=A + 8), 1), (dict(qs=248), 1),
+    (dict(qos=260), 1), (dict(ks=8), 1), (dict(part=8), 2), (dict(part=24), 2), (dict(dim=96), 2),
+    (dict(total=1 << 31), 2), (dict(heads=1 << 16), 2), (dict(kv_heads=1 << 16), 2),
+    (dict(total=0, q=None, k=None, v=None), 0),
+])
+def test_rope_refuses(lib, over, status):
+    assert _rope(lib, **over) == status
+    assert _rope_write(lib, **over) == status
+
+
+def test_rope_refuses_more(lib):
+    assert _rope(lib, ko=None) == 1
+    assert _rope(lib, ko=A + 4) == 1
+    assert _rope(lib, kos=120) == 1
+    assert _rope(lib, heads=0, kv_heads=0) == 1
+    assert _rope(lib, batch=0) == 0                  # a padded batch without sequences
+    assert _rope_write(lib, batch=0) == 0
+    for over, status in ((dict(v=None), 1), (dict(v=A + 8), 1), (dict(vs=120), 1), (dict(heads=0), 1),
+                         (dict(kv_heads=0), 1), (dict(k_cache=None), 1), (dict(table=None), 1), (dict(kind=1), 1),
+                         (dict(kind=3), 1), (dict(page=48), 2), (dict(stride=3), 1), (dict(pages=0), 1)):
+        assert _rope_write(lib, **over) == status, over
+
+
+def test_rope_table_refuses(lib):
+    for f in (-1.0, 6.3, float("nan"), float("inf")):
+        with pytest.raises(binding.SSDError):
+            layers.alloc_rope_table([1.0, f], "cpu")
+    with pytest.raises(ValueError):
+        layers.alloc_rope_table([], "cpu")
+    assert lib.ssd_rope_table(None, None, 0) == 0
+    assert lib.ssd_rope_table(None, None, 1) == 1
+    assert lib.ssd_rope_table(None, None, -1) == 1
+
+
+def test_rope_frequencies():
+    import math
+    f = layers.rope_frequencies
+    plain, m = f(64, 10000.0)
+    assert m == 1.0 and len(plain) == 32 and plain[0] == 1.0
+    assert math.isclose(plain[31], 10000.0 ** (-62 / 64), rel_tol=1e-12)
+    assert f(64, scaling="linear", factor=4.0) == ([x / 4.0 for x in plain], 1.0)
+    based, m = f(64, scaling="base", factor=4.0)
+    assert m == 1.0 and based[0] == 1.0 and math.isclose(based[31], plain[31] / 4.0, rel_tol=1e-12)
+    for scaling, low, high in (("ramp", 1.0, 32.0), ("wavelength", 1.0, 4.0)):
+        got, m = f(64, scaling=scaling, factor=8.0, original_len=2048, low_turns=low, high_turns=high)
+        assert m == (0.1 * math.log(8.0) + 1.0 if scaling == "ramp" else 1.0)
+        for x, y in zip(plain, got):
+            turns = x * 2048 / (2 * math.pi)
+            assert x / 8.0 * (1 - 1e-12) <= y <= x
+            if turns >= 2 * high:
+                assert y == x
+            if turns <= low / 2:
+                assert math.isclose(y, x / 8.0, rel_tol=1e-12)
+        assert f(64, scaling=scaling, factor=1.0)[0] == pytest.approx(plain, rel=1e-12)
+    for bad in (dict(rotary_dim=63), dict(rotary_dim=2), dict(rotary_dim=64, base=1.0),
+                dict(rotary_dim=64, factor=0.5), dict(rotary_dim=64, scaling="other"),
+                dict(rotary_dim=64, scaling="ramp", low_turns=4.0, high_turns=2.0)):
+        with pytest.raises(ValueError):
+            f(**bad)
+
+
+def test_rope_binding_refuses(lib):
+    import torch
+    q = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    table = layers.alloc_rope_table([1.0] * 32, "cpu")
+    assert table.dtype == torch.int64 and table.shape == (32,)
+    with pytest.raises(ValueError):
+        layers.ssd_rope_varlen_fwd(None, None, None, None, table, i, i[:1])
+    with pytest.raises(ValueError):
+        layers.ssd_rope_varlen_fwd(q, q, None, q, table, i, i[:1])
+    with pytest.raises(ValueError):
+        layers.ssd_rope_varlen_fwd(q, q, None, None, table, i, i[:1])     # CPU tensors
