@@ -69,6 +69,50 @@ SSD_API ssd_status_t ssd_causal_conv_varlen_fwd(
     int32_t width, int64_t max_slots, int64_t y_stride, int64_t x_stride, int32_t silu,
     uint32_t *errors, ssd_stream_t stream);
 
+/* The selective scan whose step and decay are each channel's own, for prompts and single
+ * tokens.  For every channel c and state n:
+ *
+ *   d_t = softplus(dt[t,c] + dt_bias[c])      (plain dt + dt_bias when dt_softplus == 0)
+ *   h_n = exp(d_t A[c,n]) h_n + d_t x[t,c] B[t,n]
+ *   y[t,c] = (sum_n C[t,n] h_n + D[c] x[t,c]) silu(z[t,c])
+ *
+ * from the slot's states, or zeros, at each sequence's start (the scan of ssd_scan.h has
+ * one step and decay per head).
+ *
+ *   y, x, dt, z  bf16 (total_len, channels);  z NULL: no gate
+ *   B, C         bf16 (total_len, dstate)
+ *   A            fp32 (channels, dstate);  D, dt_bias fp32 (channels) or NULL (zeros)
+ *   ssm_pool     (max_slots, channels, dstate), fp32, or bf16: widened when read, rounded
+ *                when written (pool_type)
+ *   strides      of the token-major tensors, or NULL: all contiguous
+ *   workspace    at least ssd_selective_scan_varlen_workspace_size bytes, 256-byte aligned;
+ *                needs no initialisation; one call at a time per workspace
+ *
+ * Supported: dstate 8, 16, 32 or 64; channels a multiple of 8, at most 2^20.  States and
+ * sums are fp32, y is rounded once. */
+typedef enum {
+    SSD_POOL_FP32 = 0,
+    SSD_POOL_BF16 = 1
+} ssd_pool_type_t;
+
+typedef struct {
+    int64_t y, x, dt, B, C, z;   /* elements between consecutive tokens; 0: contiguous */
+} ssd_selective_strides_t;
+
+/* Bytes of device scratch that the call needs for these sizes, and enough for every call
+ * that is not larger in any of them; 0 when they are invalid or unsupported. */
+SSD_API size_t ssd_selective_scan_varlen_workspace_size(int64_t total_len, int32_t batch,
+                                                        int32_t channels, int32_t dstate);
+
+SSD_API ssd_status_t ssd_selective_scan_varlen_fwd(
+    void *y, const void *x, const void *dt, const float *A, const void *B, const void *C,
+    const float *D, const void *z, const float *dt_bias, void *ssm_pool,
+    const int32_t *query_start_loc, const uint8_t *has_initial_state,
+    const uint32_t *cache_indices, int64_t total_len, int32_t batch, int32_t channels,
+    int32_t dstate, int64_t max_slots, int32_t pool_type, int32_t dt_softplus,
+    const ssd_selective_strides_t *strides, void *workspace, size_t workspace_bytes,
+    uint32_t *errors, ssd_stream_t stream);
+
 /* Root-mean-square norm over groups of dim / ngroups columns.  For each row and group
  *
  *   y = s weight / sqrt(mean s^2 + eps)

@@ -39,9 +39,12 @@ from .binding import (  # noqa: F401
 )
 from .layers import (  # noqa: F401
     alloc_rope_table,
+    alloc_selective_scan_workspace,
     rope_frequencies,
     ssd_causal_conv_varlen_fwd,
     ssd_rms_norm_fwd,
     ssd_rope_kv_cache_write,
     ssd_rope_varlen_fwd,
+    ssd_selective_scan_varlen_fwd,
+    ssd_selective_scan_varlen_workspace_size,
 )

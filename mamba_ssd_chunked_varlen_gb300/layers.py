@@ -17,6 +17,8 @@ from .binding import SSD_OK, SSDError
 # Every symbol include/ssd_layers.h declares.
 EXPORTED_SYMBOLS = (
     "ssd_causal_conv_varlen_fwd",
+    "ssd_selective_scan_varlen_workspace_size",
+    "ssd_selective_scan_varlen_fwd",
     "ssd_rms_norm_fwd",
     "ssd_rope_table",
     "ssd_rope_varlen_fwd",
@@ -28,6 +30,11 @@ NO_SLOT = 0xffffffff   # SSD_NO_SLOT (-1 in an int32 tensor of cache_indices)
 _fn = None
 
 
+class SelectiveStrides(ctypes.Structure):
+    """ssd_selective_strides_t: elements between consecutive tokens (0: contiguous)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("y", "x", "dt", "B", "C", "z")]
+
+
 class _Functions:
     def __init__(self):
         import torch
@@ -36,6 +43,13 @@ class _Functions:
         self.conv = lib.ssd_causal_conv_varlen_fwd
         self.conv.restype = ctypes.c_int
         self.conv.argtypes = [vp] * 8 + [i64, i32, i32, i32, i64, i64, i64, i32, vp, vp]
+        self.scan_workspace_size = lib.ssd_selective_scan_varlen_workspace_size
+        self.scan_workspace_size.restype = sz
+        self.scan_workspace_size.argtypes = [i64, i32, i32, i32]
+        self.scan = lib.ssd_selective_scan_varlen_fwd
+        self.scan.restype = ctypes.c_int
+        self.scan.argtypes = ([vp] * 13 + [i64, i32, i32, i32, i64, i32, i32]
+                              + [ctypes.POINTER(SelectiveStrides), vp, sz, vp, vp])
         self.norm = lib.ssd_rms_norm_fwd
         self.norm.restype = ctypes.c_int
         self.norm.argtypes = [vp] * 6 + [i64, i32, i32, i32, ctypes.c_float] + [i64] * 4 + [vp]
@@ -173,6 +187,61 @@ def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, h
           None if bias is None else _ptr(bias, "bias", f.f32, (channels,), device),
           _ptr(conv_pool, "conv_pool", f.bf16, (max_slots, width - 1, channels), device),
           *slots, total, batch, channels, width, max_slots, sy, sx, bool(silu),
+          _errors(f, errors, device))
+
+
+def ssd_selective_scan_varlen_workspace_size(total_len: int, batch: int, channels: int, dstate: int) -> int:
+    return int(_functions().scan_workspace_size(total_len, batch, channels, dstate))
+
+
+def alloc_selective_scan_workspace(total_len: int, batch: int, channels: int, dstate: int, device="cuda"):
+    """A uint8 torch tensor of the size the C ABI asks for; it serves every call of at
+    most these sizes."""
+    import torch
+    n = ssd_selective_scan_varlen_workspace_size(total_len, batch, channels, dstate)
+    if n == 0:
+        raise SSDError(2, "ssd_selective_scan_varlen_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def ssd_selective_scan_varlen_fwd(y, x, dt, A, B, C, D, z, dt_bias, ssm_pool, query_start_loc,
+                                  has_initial_state, cache_indices, *, dt_softplus: bool = True,
+                                  workspace=None, errors=None, stream=None) -> None:
+    """The selective scan whose step and decay are each channel's own, for prompts and
+    single tokens.
+
+    y, x, dt (rows, channels) and z (the gate) likewise or None, B, C (rows, dstate) bf16,
+    each row contiguous, any row pitch that is a multiple of 8 elements; A (channels,
+    dstate) fp32; D, dt_bias (channels,) fp32 or None; ssm_pool (slots, channels, dstate)
+    fp32 or bf16, updated in place; the batch and errors as for
+    ssd_causal_conv_varlen_fwd; workspace: a uint8 tensor of at least
+    ssd_selective_scan_varlen_workspace_size bytes (alloc_selective_scan_workspace)."""
+    f = _functions()
+    device = _device(x, "x")
+    if x.dim() != 2 or A.dim() != 2:
+        raise ValueError("x must have shape (rows, channels) and A (channels, dstate)")
+    shape = x.shape
+    total, channels = shape
+    dstate = A.shape[1]
+    if workspace is None:
+        raise ValueError("workspace is required (see alloc_selective_scan_workspace)")
+    slots, batch = _slots(f, query_start_loc, has_initial_state, cache_indices, device)
+    py, sy = _rows(y, "y", f.bf16, shape, device)
+    px, sx = _rows(x, "x", f.bf16, shape, device)
+    pd, sd = _rows(dt, "dt", f.bf16, shape, device)
+    pb, sb = _rows(B, "B", f.bf16, (total, dstate), device)
+    pc, sc = _rows(C, "C", f.bf16, (total, dstate), device)
+    pz, sz = (None, 0) if z is None else _rows(z, "z", f.bf16, shape, device)
+    bf16 = ssm_pool.dtype is f.bf16
+    max_slots = ssm_pool.shape[0]
+    _call(f, f.scan, "ssd_selective_scan_varlen_fwd", device, stream, py, px, pd,
+          _ptr(A, "A", f.f32, (channels, dstate), device), pb, pc,
+          None if D is None else _ptr(D, "D", f.f32, (channels,), device), pz,
+          None if dt_bias is None else _ptr(dt_bias, "dt_bias", f.f32, (channels,), device),
+          _ptr(ssm_pool, "ssm_pool", f.bf16 if bf16 else f.f32, (max_slots, channels, dstate), device),
+          *slots, total, batch, channels, dstate, max_slots, bf16, bool(dt_softplus),
+          ctypes.byref(SelectiveStrides(sy, sx, sd, sb, sc, sz)),
+          _ptr(workspace, "workspace", f.u8, (workspace.numel(),), device), workspace.numel(),
           _errors(f, errors, device))
 
 

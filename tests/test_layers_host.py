@@ -187,3 +187,45 @@ def test_rope_binding_refuses(lib):
         layers.ssd_rope_varlen_fwd(q, q, None, q, table, i, i[:1])
     with pytest.raises(ValueError):
         layers.ssd_rope_varlen_fwd(q, q, None, None, table, i, i[:1])     # CPU tensors
+
+
+def _scan(lib, **over):
+    a = dict(y=A, x=A, dt=A, A=A, B=A, C=A, D=None, z=None, bias=None, pool=A, qsl=A, has=None, slots=A,
+             total=10, batch=2, channels=64, dstate=16, max_slots=4, pool_type=0, strides={}, ws=A,
+             wsb=1 << 40) | over
+    return lib.ssd_selective_scan_varlen_fwd(
+        _vp(a["y"]), _vp(a["x"]), _vp(a["dt"]), _vp(a["A"]), _vp(a["B"]), _vp(a["C"]), _vp(a["D"]), _vp(a["z"]),
+        _vp(a["bias"]), _vp(a["pool"]), _vp(a["qsl"]), _vp(a["has"]), _vp(a["slots"]), a["total"], a["batch"],
+        a["channels"], a["dstate"], a["max_slots"], a["pool_type"], 1,
+        None if a["strides"] is None else ctypes.byref(layers.SelectiveStrides(**a["strides"])), _vp(a["ws"]),
+        a["wsb"], None, None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(total=-1), 1), (dict(batch=-1), 1), (dict(max_slots=-1), 1), (dict(channels=0), 1),
+    (dict(dstate=0), 1), (dict(pool_type=2), 1), (dict(pool_type=-1), 1), (dict(y=None), 1), (dict(x=None), 1),
+    (dict(dt=None), 1), (dict(A=None), 1), (dict(B=None), 1), (dict(C=None), 1), (dict(pool=None), 1),
+    (dict(qsl=None), 1), (dict(slots=None), 1), (dict(x=A + 8), 1), (dict(y=A + 2), 1), (dict(dt=A + 2), 1),
+    (dict(z=A + 8), 1), (dict(B=A + 8), 1), (dict(C=A + 4), 1), (dict(A=A + 4), 1), (dict(pool=A + 8), 1),
+    (dict(strides=dict(x=56)), 1), (dict(strides=dict(y=68)), 1), (dict(strides=dict(dt=65)), 1),
+    (dict(strides=dict(B=8)), 1), (dict(strides=dict(C=20)), 1), (dict(strides=dict(z=-64)), 1),
+    (dict(channels=60), 2), (dict(channels=(1 << 20) + 8), 2), (dict(dstate=4), 2), (dict(dstate=24), 2),
+    (dict(dstate=128), 2), (dict(total=1 << 31), 2), (dict(batch=(1 << 31) - 1), 2),
+    (dict(ws=None), 3), (dict(ws=A + 16), 3), (dict(wsb=16), 3),
+    (dict(batch=0), 0), (dict(batch=0, strides=None, ws=None), 0),
+])
+def test_scan_refuses(lib, over, status):
+    assert _scan(lib, **over) == status
+
+
+def test_scan_workspace_size(lib):
+    size = layers.ssd_selective_scan_varlen_workspace_size
+    assert size(0, 0, 8, 8) > 0 and size(1, 1, 64, 16) > 0
+    for bad in ((-1, 1, 64, 16), (1, -1, 64, 16), (1, 1, 60, 16), (1, 1, 64, 12), (1, 1, 0, 16), (1 << 31, 1, 64, 16)):
+        assert size(*bad) == 0
+    # enough for every call that is not larger in any size
+    sizes = [(t, b, c, n) for t in (1, 1000, 100000) for b in (1, 64) for c in (8, 1024, 16384) for n in (8, 64)]
+    for big in sizes:
+        for small in sizes:
+            if all(x <= y for x, y in zip(small, big)):
+                assert size(*small) <= size(*big), (small, big)
