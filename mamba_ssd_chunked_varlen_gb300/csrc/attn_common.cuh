@@ -10,13 +10,16 @@
 
 namespace ssd {
 
-// Launches a kernel that begins with pdl_wait() ahead of its predecessor's end.
+// Launches a kernel that begins with pdl_wait() ahead of its predecessor's end, with so
+// many bytes of dynamic shared memory.
 template <typename... Args>
-inline cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args)
+inline cudaError_t launch_pdl_smem(void (*fn)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                   Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -24,6 +27,11 @@ inline cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaS
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+template <typename... Args>
+inline cudaError_t launch_pdl(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args)
+{
+    return launch_pdl_smem(fn, grid, threads, 0, stream, args...);
 }
 
 // Smallest row maximum that a quantised row is scaled by: M / a and a / M stay

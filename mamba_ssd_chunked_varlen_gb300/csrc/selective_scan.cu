@@ -10,13 +10,17 @@
 // multiply-adds (fma.rn.f32x2) at 2, so that both pipes are about equally loaded and
 // the kernel is written to issue as little else as it can.
 //
-// A channel is N / 8 lanes of eight states, kept as pairs of fp32.  A warp is 32 N / 8
-// channels on its own; its CTA shares the tokens' B and C, widened to fp32 in shared
-// memory.  Tokens go in groups of eight: each of a channel's lanes makes the steps of
-// its share of them and hands them over by shuffles, and gets the sums of its share
-// back from a reduction that halves the sums as it halves the lanes.
+// A channel is N / 8 lanes of eight states; a warp is 256 / N channels on its own.  Tokens
+// go in groups of eight, and in a group in pairs: a pair's arguments, inputs and sums are
+// two fp32 each in one instruction, the states take the two one after the other.  Each of a
+// channel's lanes makes the steps of its share of a group's tokens, a group ahead, and
+// hands them over by shuffles; its share of the sums comes back from a reduction that
+// halves the sums as it halves the lanes.  The CTA copies blocks of 16 tokens to shared
+// memory two blocks ahead and lays their B and C out in fp32, a pair's two values side by
+// side, so that a lane reads four operands at once.
 #include <algorithm>
 
+#include "attn_ptx.cuh"
 #include "layer_common.cuh"
 
 namespace ssd {
@@ -26,7 +30,9 @@ constexpr int kScanWarps = 4;
 constexpr int kScanThreads = kScanWarps * 32;
 constexpr int kStates = 8;            // states of a lane
 constexpr int kGroup = 8;             // tokens of a group
-constexpr int kBlock = 32;            // tokens whose B and C are in shared memory at once
+constexpr int kBlock = 16;            // tokens of a block
+constexpr int kStages = 3;            // blocks in shared memory
+constexpr int kShort = 7;             // tokens of a sequence that goes without shared memory
 
 struct SelParams {
     SlotBatch s;
@@ -40,46 +46,12 @@ struct SelParams {
 };
 
 // ---------------------------------------------------------------- arithmetic
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two fp32 values in one register pair.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 pack2(float a, float b)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(F2 a, float &x, float &y)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // max(v, 0) + log(1 + e^-|v|).  With e = e^-|v| in (0, 1], log(1 + e) = e P(e), P of degree
 // 9 fitted to log(1 + e) / e (relative error 5e-9, 1.6e-7 with fp32's roundings): small
 // steps keep their relative precision.
 __device__ __forceinline__ float step_of(float v)
 {
-    const float e = ex2(-1.4426950408889634f * fabsf(v));
+    const float e = ptx::ex2(-1.4426950408889634f * fabsf(v));
     float p = -0.0032440251670777798f;
     p = fmaf(p, e, 0.01985146291553974f);
     p = fmaf(p, e, -0.05695953220129013f);
@@ -93,98 +65,114 @@ __device__ __forceinline__ float step_of(float v)
     return fmaf(p, e, fmaxf(v, 0.f));
 }
 
+// ---------------------------------------------------------------- copies
+// 16 bytes from global to shared memory without registers; zeros where there is no source.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 // ---------------------------------------------------------------- pool
 template <bool kBf16>
-__device__ __forceinline__ void load_states(const void *pool, int64_t at, F2 (&h)[kStates / 2])
+__device__ __forceinline__ void load_states(const void *pool, int64_t at, float (&h)[kStates])
 {
-    float v[8];
     if constexpr (kBf16) {
-        widen8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pool) + at), v);
+        widen8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pool) + at), h);
     } else {
-        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(static_cast<const float *>(pool) + at);
-        *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(static_cast<const float *>(pool) + at + 4);
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(pool) + at);
+        *reinterpret_cast<float4 *>(h) = src[0];
+        *reinterpret_cast<float4 *>(h + 4) = src[1];
     }
-#pragma unroll
-    for (int k = 0; k < kStates / 2; ++k)
-        h[k] = pack2(v[2 * k], v[2 * k + 1]);
 }
 
 template <bool kBf16>
-__device__ __forceinline__ void store_states(void *pool, int64_t at, const F2 (&h)[kStates / 2])
+__device__ __forceinline__ void store_states(void *pool, int64_t at, const float (&h)[kStates])
 {
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < kStates / 2; ++k)
-        unpack2(h[k], v[2 * k], v[2 * k + 1]);
     if constexpr (kBf16) {
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(pool) + at) = round8(v);
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(pool) + at) = round8(h);
     } else {
-        *reinterpret_cast<float4 *>(static_cast<float *>(pool) + at) = *reinterpret_cast<const float4 *>(v);
-        *reinterpret_cast<float4 *>(static_cast<float *>(pool) + at + 4) = *reinterpret_cast<const float4 *>(v + 4);
+        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(pool) + at);
+        dst[0] = make_float4(h[0], h[1], h[2], h[3]);
+        dst[1] = make_float4(h[4], h[5], h[6], h[7]);
     }
 }
 
-// ---------------------------------------------------------------- a sequence
+// ---------------------------------------------------------------- lanes
+// Shared memory of a CTA.  Rows are padded so that the lanes of a warp that read
+// several tokens at once find them in different banks.
 template <int N>
 struct SelShared {
-    float B[2][kBlock][N], C[2][kBlock][N];
+    static constexpr int kLanes = N / kStates;                  // lanes of a channel
+    static constexpr int kChannels = 32 / kLanes;               // channels of a warp
+    static constexpr int kCols = kScanWarps * kChannels;        // of the CTA
+    static constexpr int kPitch = kCols + (kLanes == 2 ? 16 : 8);
+    struct Block {
+        __nv_bfloat16 x[kBlock][kPitch], dt[kBlock][kPitch], z[kBlock][kPitch], B[kBlock][N], C[kBlock][N];
+    };
+    Block block[kStages];
+    __nv_bfloat16 y[2][kBlock][kPitch];
+    // per pair of tokens, [chunk][part]: two states of a part for the two tokens
+    float4 B[2][kBlock / 2][kStates / 2][kLanes], C[2][kBlock / 2][kStates / 2][kLanes];
 };
 
-// What one lane holds of its channel.
-template <int N>
+// What a lane holds of its channel.
 struct SelLane {
-    static constexpr int kLanes = N / kStates;       // lanes of a channel
-    static constexpr int kChannels = 32 / kLanes;    // channels of a warp
-    static constexpr int kMine = kGroup / kLanes;    // tokens of a group that a lane makes the steps of
-
-    const SelParams &p;
-    int part, in_warp, ch;                           // states' part, channel in the warp, channel
-    bool valid;
-    F2 a[kStates / 2], h[kStates / 2];               // A log2(e), the states
+    float h[kStates];
+    float a[kStates];          // A log2(e)
     float D, bias;
+    bool softplus;
 
-    // one token: B and C in shared memory from this lane's part on; returns sum C h of the part
-    __device__ __forceinline__ float token(float dt, float u, const float *B, const float *C)
+    __device__ __forceinline__ float step(__nv_bfloat16 raw) const
     {
-        const F2 dt2 = pack2(dt, dt), u2 = pack2(u, u);
-        F2 sum = pack2(0.f, 0.f);
+        const float v = __bfloat162float(raw) + bias, d = step_of(v);
+        return softplus ? d : v;
+    }
+
+    // The states over a pair of tokens, whose steps are dt, inputs (before B) u; B and C of
+    // the lane's states are kStride float4 apart.  Returns the pair's sums of C h.
+    template <int kStride>
+    __device__ __forceinline__ uint64_t pair(uint64_t dt, uint64_t u, const float4 *B, const float4 *C)
+    {
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < kStates / 2; k += 2) {
-            const float4 b = *reinterpret_cast<const float4 *>(B + 2 * k);
-            const float4 c = *reinterpret_cast<const float4 *>(C + 2 * k);
+        for (int k = 0; k < kStates / 2; ++k) {
+            const float4 b = B[k * kStride], c = C[k * kStride];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float e0, e1;
-                unpack2(mul2(dt2, a[k + i]), e0, e1);
-                const F2 in = mul2(u2, i ? pack2(b.z, b.w) : pack2(b.x, b.y));
-                h[k + i] = fma2(pack2(ex2(e0), ex2(e1)), h[k + i], in);
-                sum = fma2(h[k + i], i ? pack2(c.z, c.w) : pack2(c.x, c.y), sum);
+                float e0, e1, in0, in1;
+                ptx::unpack2(ptx::mul2(dt, ptx::pack2(a[2 * k + i], a[2 * k + i])), e0, e1);
+                ptx::unpack2(ptx::mul2(u, i ? ptx::pack2(b.z, b.w) : ptx::pack2(b.x, b.y)), in0, in1);
+                const float first = fmaf(ptx::ex2(e0), h[2 * k + i], in0);
+                h[2 * k + i] = fmaf(ptx::ex2(e1), first, in1);
+                sum[i] = ptx::fma2(ptx::pack2(first, h[2 * k + i]), i ? ptx::pack2(c.z, c.w) : ptx::pack2(c.x, c.y),
+                                   sum[i]);
             }
         }
-        float s0, s1;
-        unpack2(sum, s0, s1);
-        return s0 + s1;
+        return ptx::add2(sum[0], sum[1]);
     }
 
-    __device__ __forceinline__ float step(const __nv_bfloat16 raw) const
+    // One token, B and C of the lane's states in bf16; returns the sum of C h.
+    __device__ __forceinline__ float token(float dt, float u, const uint4 &braw, const uint4 &craw)
     {
-        const float v = __bfloat162float(raw) + bias;
-        return p.softplus ? step_of(v) : v;
-    }
-
-    __device__ __forceinline__ void put(int64_t t, float sum, float x, const __nv_bfloat16 z)
-    {
-        float v = fmaf(D, x, sum);
-        if (p.z)
-            v *= silu_f32(__bfloat162float(z));
-        if (valid)
-            p.y[t * p.y_stride + ch] = __float2bfloat16_rn(v);
+        float b[8], c[8], sum = 0.f;
+        widen8(braw, b);
+        widen8(craw, c);
+#pragma unroll
+        for (int n = 0; n < kStates; ++n) {
+            h[n] = fmaf(ptx::ex2(dt * a[n]), h[n], u * b[n]);
+            sum = fmaf(h[n], c[n], sum);
+        }
+        return sum;
     }
 };
 
-// Sums over a channel's lanes of kLanes tokens at once: lane part gets token part's.
+// Sums over a channel's lanes of kLanes tokens at once: lane `part` gets token part's.
 template <int kLanes, int kChannels>
-__device__ __forceinline__ float reduce_tokens(float (&v)[kLanes], int part)
+__device__ __forceinline__ float reduce_tokens(float *v, int part)
 {
 #pragma unroll
     for (int n = kLanes / 2; n >= 1; n /= 2) {
@@ -198,143 +186,245 @@ __device__ __forceinline__ float reduce_tokens(float (&v)[kLanes], int part)
     return v[0];
 }
 
-template <int N, bool kBf16>
+template <int N, bool kBf16, bool kGate>
 __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __grid_constant__ SelParams p)
 {
-    using Lane = SelLane<N>;
-    constexpr int kLanes = Lane::kLanes, kChannels = Lane::kChannels, kMine = Lane::kMine;
-    __shared__ alignas(16) SelShared<N> s;
+    using Shared = SelShared<N>;
+    constexpr int kLanes = Shared::kLanes, kChannels = Shared::kChannels, kCols = Shared::kCols;
+    constexpr int kMine = kGroup / kLanes;           // tokens of a group that a lane makes the steps of
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared &s = *reinterpret_cast<Shared *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
-    Lane me{p, lane / kChannels, lane % kChannels};
-    me.ch = (tile * kScanWarps + warp) * kChannels + me.in_warp;
-    me.valid = me.ch < p.channels;
-    const int ch = me.valid ? me.ch : 0;      // (the other lanes follow a channel that is there)
+    const int part = lane / kChannels, in_warp = lane % kChannels, col = warp * kChannels + in_warp;
+    const int b = blockIdx.x / p.tiles, col0 = blockIdx.x % p.tiles * kCols;
+    const bool valid = col0 + col < p.channels;
+    const int ch = valid ? col0 + col : 0;    // (the other lanes follow a channel that is there)
     pdl_wait();
     int32_t begin, end;
     if (!seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, begin, end))
         return;
     const int64_t slot = seq_slot(p.s, b);
     const bool has = slot >= 0 && p.s.has_init && p.s.has_init[b];
-    const int64_t at = (slot * p.channels + ch) * N + me.part * kStates;
+    const int64_t at = (slot * p.channels + ch) * N + part * kStates;
+
+    // copies of a block's rows, 16 bytes at a time
+    constexpr int kRowLoads = kCols / 8, kBcLoads = N / 8;
+    auto fetch = [&](int t0) {
+        typename Shared::Block &dst = s.block[(t0 - begin) / kBlock % kStages];
 #pragma unroll
-    for (int k = 0; k < kStates / 2; ++k)
-        me.h[k] = pack2(0.f, 0.f);
+        for (int i0 = 0; i0 < kBlock * kRowLoads; i0 += kScanThreads) {
+            const int i = i0 + threadIdx.x, row = i / kRowLoads, c = i % kRowLoads * 8;
+            if (kBlock * kRowLoads % kScanThreads == 0 || i < kBlock * kRowLoads) {
+                const bool there = t0 + row < end && col0 + c < p.channels;
+                const int64_t t = there ? t0 + row : begin;
+                const int from = there ? col0 + c : 0;
+                copy16(&dst.x[row][c], p.x + t * p.x_stride + from, there);
+                copy16(&dst.dt[row][c], p.dt + t * p.dt_stride + from, there);
+                if constexpr (kGate)
+                    copy16(&dst.z[row][c], p.z + t * p.z_stride + from, there);
+            }
+        }
+#pragma unroll
+        for (int i0 = 0; i0 < 2 * kBlock * kBcLoads; i0 += kScanThreads) {
+            const int i = i0 + threadIdx.x, row = i / kBcLoads % kBlock, c = i % kBcLoads * 8;
+            if (2 * kBlock * kBcLoads % kScanThreads == 0 || i < 2 * kBlock * kBcLoads) {
+                const bool there = t0 + row < end, is_c = i >= kBlock * kBcLoads;
+                const int64_t t = there ? t0 + row : begin;
+                copy16(is_c ? &dst.C[row][c] : &dst.B[row][c],
+                       (is_c ? p.C + t * p.c_stride : p.B + t * p.b_stride) + c, there);
+            }
+        }
+        copies_commit();
+    };
+    const bool staged = end - begin > kShort;
+    if (staged) {
+        fetch(begin);
+        if (begin + kBlock < end)
+            fetch(begin + kBlock);
+    }
+    SelLane me;
+#pragma unroll
+    for (int n = 0; n < kStates; ++n)
+        me.h[n] = 0.f;
     if (has)
         load_states<kBf16>(p.pool, at, me.h);
-    {
-        const float *A = p.A + static_cast<int64_t>(ch) * N + me.part * kStates;
 #pragma unroll
-        for (int k = 0; k < kStates / 2; ++k) {
-            const float2 v = __ldg(reinterpret_cast<const float2 *>(A) + k);
-            me.a[k] = pack2(v.x * 1.4426950408889634f, v.y * 1.4426950408889634f);
-        }
+    for (int n = 0; n < kStates; n += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + static_cast<int64_t>(ch) * N + part * kStates + n));
+        me.a[n] = v.x * 1.4426950408889634f;
+        me.a[n + 1] = v.y * 1.4426950408889634f;
+        me.a[n + 2] = v.z * 1.4426950408889634f;
+        me.a[n + 3] = v.w * 1.4426950408889634f;
     }
     me.D = p.D ? p.D[ch] : 0.f;
     me.bias = p.dt_bias ? p.dt_bias[ch] : 0.f;
+    me.softplus = p.softplus;
+    auto output = [&](float sum, float x, __nv_bfloat16 z) {
+        float v = fmaf(me.D, x, sum);
+        if constexpr (kGate)
+            v *= silu_f32(__bfloat162float(z));
+        return __float2bfloat16_rn(v);
+    };
+    const __nv_bfloat16 none = __float2bfloat16_rn(0.f);
 
-    // B and C of a block: one load of eight values at a time
-    constexpr int kLoads = (2 * kBlock * N / 8 + kScanThreads - 1) / kScanThreads;
-    uint4 bc[kLoads];
-    auto fetch = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = i * kScanThreads + threadIdx.x, row = at / (N / 8) % kBlock, col = at % (N / 8) * 8;
-            const bool is_c = at >= kBlock * N / 8;
-            bc[i] = make_uint4(0, 0, 0, 0);
-            if (at < 2 * kBlock * N / 8 && t0 + row < end)
-                bc[i] = *reinterpret_cast<const uint4 *>(
-                    (is_c ? p.C + (t0 + row) * p.c_stride : p.B + (t0 + row) * p.b_stride) + col);
-        }
-    };
-    auto stage = [&](int buffer) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = i * kScanThreads + threadIdx.x, row = at / (N / 8) % kBlock, col = at % (N / 8) * 8;
-            if (at < 2 * kBlock * N / 8) {
-                float v[8];
-                widen8(bc[i], v);
-                float *dst = (at >= kBlock * N / 8 ? s.C[buffer][row] : s.B[buffer][row]) + col;
-                *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(v);
-                *reinterpret_cast<float4 *>(dst + 4) = *reinterpret_cast<const float4 *>(v + 4);
-            }
-        }
-    };
-    const __nv_bfloat16 *px = p.x + ch, *pd = p.dt + ch, *pz = p.z ? p.z + ch : nullptr;
-    // x, dt and z of the lane's tokens of a group
-    __nv_bfloat16 x[kMine], d[kMine], z[kMine];
-    auto load_group = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int64_t t = t0 + i * kLanes + me.part;
-            x[i] = d[i] = z[i] = __float2bfloat16_rn(0.f);
-            if (t0 + kGroup <= end) {
-                x[i] = px[t * p.x_stride];
-                d[i] = pd[t * p.dt_stride];
-                if (pz)
-                    z[i] = pz[t * p.z_stride];
-            }
-        }
-    };
-
-    load_group(begin);
-    fetch(begin);
-    int buffer = 0;
-    for (int t0 = begin; t0 < end; t0 += kBlock, buffer ^= 1) {
-        stage(buffer);
-        if (t0 + kBlock < end)
-            fetch(t0 + kBlock);
-        __syncthreads();   // (a warp that is ahead writes the other buffer)
-        const float *B = s.B[buffer][0] + me.part * kStates, *C = s.C[buffer][0] + me.part * kStates;
-        const int n = min(kBlock, end - t0);
-        int g = 0;
-        for (; g + kGroup <= n; g += kGroup) {
-            float dt[kMine], u[kMine], xs[kMine];
-            __nv_bfloat16 zs[kMine];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                xs[i] = __bfloat162float(x[i]);
-                zs[i] = z[i];
-                dt[i] = me.step(d[i]);
-                u[i] = dt[i] * xs[i];
-            }
-            load_group(t0 + g + kGroup);
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                float sums[kLanes];
-#pragma unroll
-                for (int j = 0; j < kLanes; ++j) {
-                    const int from = j * kChannels + me.in_warp, row = (g + i * kLanes + j) * N;
-                    const float dj = kLanes == 1 ? dt[i] : __shfl_sync(0xffffffffu, dt[i], from);
-                    const float uj = kLanes == 1 ? u[i] : __shfl_sync(0xffffffffu, u[i], from);
-                    sums[j] = me.token(dj, uj, B + row, C + row);
-                }
-                me.put(t0 + g + i * kLanes + me.part, reduce_tokens<kLanes, kChannels>(sums, me.part), xs[i], zs[i]);
-            }
-        }
-        for (; g < n; ++g) {      // the last tokens, fewer than a group
-            const int64_t t = t0 + g;
-            const float xt = __bfloat162float(px[t * p.x_stride]), dt = me.step(pd[t * p.dt_stride]);
-            float sum = me.token(dt, dt * xt, B + g * N, C + g * N);
+    if (!staged) {
+        // a few tokens: straight from global memory
+        for (int t = begin; t < end; ++t) {
+            const __nv_bfloat16 z = kGate ? p.z[t * p.z_stride + ch] : none;
+            const float x = __bfloat162float(p.x[t * p.x_stride + ch]), dt = me.step(p.dt[t * p.dt_stride + ch]);
+            float sum = me.token(dt, dt * x,
+                                 *reinterpret_cast<const uint4 *>(p.B + t * p.b_stride + part * kStates),
+                                 *reinterpret_cast<const uint4 *>(p.C + t * p.c_stride + part * kStates));
 #pragma unroll
             for (int o = kChannels; o < 32; o <<= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (me.part == 0)
-                me.put(t, sum, xt, pz ? pz[t * p.z_stride] : __float2bfloat16_rn(0.f));
+            if (part == 0 && valid)
+                p.y[t * p.y_stride + ch] = output(sum, x, z);
+        }
+        if (slot >= 0 && valid)
+            store_states<kBf16>(p.pool, at, me.h);
+        return;
+    }
+
+    // B and C of a block in fp32, pair by pair
+    auto lay_out = [&](int k) {
+        const typename Shared::Block &src = s.block[k % kStages];
+        constexpr int kItems = kBlock / 2 * (N / 2);
+#pragma unroll
+        for (int i0 = 0; i0 < kItems; i0 += kScanThreads) {
+            const int i = i0 + threadIdx.x;
+            if (kItems % kScanThreads == 0 || i < kItems) {
+                const int pair = i / (N / 2), n = i % (N / 2) * 2, to_part = n / kStates, chunk = n % kStates / 2;
+                auto two = [&](const __nv_bfloat16 (*v)[N]) {
+                    const uint32_t t0 = *reinterpret_cast<const uint32_t *>(&v[2 * pair][n]);
+                    const uint32_t t1 = *reinterpret_cast<const uint32_t *>(&v[2 * pair + 1][n]);
+                    return make_float4(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16),
+                                       __uint_as_float(t0 & 0xffff0000u), __uint_as_float(t1 & 0xffff0000u));
+                };
+                s.B[k & 1][pair][chunk][to_part] = two(src.B);
+                s.C[k & 1][pair][chunk][to_part] = two(src.C);
+            }
+        }
+    };
+    // y of block k from shared memory, 16 bytes at a time
+    auto write_out = [&](int k) {
+        const int t0 = begin + k * kBlock;
+#pragma unroll
+        for (int i0 = 0; i0 < kBlock * kRowLoads; i0 += kScanThreads) {
+            const int i = i0 + threadIdx.x, row = i / kRowLoads, c = i % kRowLoads * 8;
+            if ((kBlock * kRowLoads % kScanThreads == 0 || i < kBlock * kRowLoads) && t0 + row < end &&
+                col0 + c < p.channels)
+                *reinterpret_cast<uint4 *>(p.y + (t0 + row) * p.y_stride + col0 + c) =
+                    *reinterpret_cast<const uint4 *>(&s.y[k & 1][row][c]);
+        }
+    };
+    // the steps of the lane's tokens of a group
+    float dt[kMine], u[kMine], x[kMine];
+    __nv_bfloat16 z[kMine];
+    auto steps = [&](const typename Shared::Block &src, int row0, float (&dt)[kMine], float (&u)[kMine],
+                     float (&x)[kMine], __nv_bfloat16 (&z)[kMine]) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int row = row0 + i * kLanes + part;
+            x[i] = __bfloat162float(src.x[row][col]);
+            z[i] = kGate ? src.z[row][col] : none;
+            dt[i] = me.step(src.dt[row][col]);
+            u[i] = dt[i] * x[i];
+        }
+    };
+
+    copies_wait();
+    __syncthreads();
+    lay_out(0);
+    steps(s.block[0], 0, dt, u, x, z);
+    const int blocks = (end - begin + kBlock - 1) / kBlock;
+    for (int k = 0; k < blocks; ++k) {
+        // block k + 1 has arrived for everybody, and nobody reads blocks and y of k - 1 any more
+        copies_wait();
+        __syncthreads();
+        const int t0 = begin + k * kBlock, n = min(kBlock, end - t0);
+        if (t0 + 2 * kBlock < end)
+            fetch(t0 + 2 * kBlock);
+        if (k > 0)
+            write_out(k - 1);
+        if (k + 1 < blocks)
+            lay_out(k + 1);
+        const typename Shared::Block &now = s.block[k % kStages], &next = s.block[(k + 1) % kStages];
+        int g = 0;
+        for (; g + kGroup <= n; g += kGroup) {
+            // the next group's steps go between this one's (past the end they are not used)
+            float dt1[kMine], u1[kMine], x1[kMine];
+            __nv_bfloat16 z1[kMine];
+            const bool more = g + kGroup < kBlock;
+            steps(more ? now : next, more ? g + kGroup : 0, dt1, u1, x1, z1);
+            float sums[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; j += 2) {
+                uint64_t dt2, u2;
+                if constexpr (kLanes == 1) {
+                    dt2 = ptx::pack2(dt[j], dt[j + 1]);
+                    u2 = ptx::pack2(u[j], u[j + 1]);
+                } else {
+                    const int i = j / kLanes, from = j % kLanes * kChannels + in_warp;
+                    dt2 = ptx::pack2(__shfl_sync(0xffffffffu, dt[i], from),
+                                     __shfl_sync(0xffffffffu, dt[i], from + kChannels));
+                    u2 = ptx::pack2(__shfl_sync(0xffffffffu, u[i], from),
+                                    __shfl_sync(0xffffffffu, u[i], from + kChannels));
+                }
+                const int row = (g + j) / 2;
+                ptx::unpack2(me.pair<kLanes>(dt2, u2, &s.B[k & 1][row][0][part], &s.C[k & 1][row][0][part]), sums[j],
+                             sums[j + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const float sum = reduce_tokens<kLanes, kChannels>(sums + i * kLanes, part);
+                s.y[k & 1][g + i * kLanes + part][col] = output(sum, x[i], z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                dt[i] = dt1[i];
+                u[i] = u1[i];
+                x[i] = x1[i];
+                z[i] = z1[i];
+            }
+        }
+        for (; g < n; ++g) {      // the sequence's last tokens, fewer than a group
+            const float xt = __bfloat162float(now.x[g][col]), d = me.step(now.dt[g][col]);
+            float sum = me.token(d, d * xt, *reinterpret_cast<const uint4 *>(&now.B[g][part * kStates]),
+                                 *reinterpret_cast<const uint4 *>(&now.C[g][part * kStates]));
+#pragma unroll
+            for (int o = kChannels; o < 32; o <<= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (part == 0)
+                s.y[k & 1][g][col] = output(sum, xt, kGate ? now.z[g][col] : none);
         }
     }
-    if (slot >= 0 && me.valid)
+    __syncthreads();
+    write_out(blocks - 1);
+    if (slot >= 0 && valid)
         store_states<kBf16>(p.pool, at, me.h);
+}
+
+template <int N, bool kBf16, bool kGate>
+cudaError_t launch(SelParams &p, cudaStream_t stream)
+{
+    using Shared = SelShared<N>;
+    constexpr int kBytes = sizeof(Shared);
+    cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<N, kBf16, kGate>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess)
+        return e;
+    p.tiles = (p.channels + Shared::kCols - 1) / Shared::kCols;
+    return launch_pdl_smem(selective_scan_kernel<N, kBf16, kGate>, dim3(static_cast<unsigned>(p.tiles * p.s.batch)),
+                           kScanThreads, kBytes, stream, p);
 }
 
 template <int N>
 cudaError_t launch(SelParams &p, bool bf16, cudaStream_t stream)
 {
-    const int cols = kScanWarps * SelLane<N>::kChannels;
-    p.tiles = (p.channels + cols - 1) / cols;
-    const dim3 grid(static_cast<unsigned>(p.tiles * p.s.batch));
-    return bf16 ? launch_pdl(selective_scan_kernel<N, true>, grid, kScanThreads, stream, p)
-                : launch_pdl(selective_scan_kernel<N, false>, grid, kScanThreads, stream, p);
+    if (p.z)
+        return bf16 ? launch<N, true, true>(p, stream) : launch<N, false, true>(p, stream);
+    return bf16 ? launch<N, true, false>(p, stream) : launch<N, false, false>(p, stream);
 }
 
 bool sel_sizes(int64_t total_len, int32_t batch, int32_t channels, int32_t dstate)
