@@ -11,10 +11,10 @@
 // the kernel is written to issue as little else as it can.
 //
 // A channel is N / 8 lanes of eight states; a warp is 256 / N channels on its own.  Tokens
-// go in groups of eight, and in a group in pairs: a pair's arguments, inputs and sums are
-// two fp32 each in one instruction, the states take the two one after the other.  Each of a
-// channel's lanes makes the steps of its share of a group's tokens, a group ahead, and
-// hands them over by shuffles; its share of the sums comes back from a reduction that
+// go in pairs: a pair's arguments, inputs and sums are two fp32 each in one instruction,
+// the states take the two one after the other.  Each of a channel's lanes makes the
+// steps of its share of a group's pairs, a group ahead and two at a time as well, and hands
+// them over through shared memory; its share of the sums comes back from a reduction that
 // halves the sums as it halves the lanes.  The CTA copies blocks of 16 tokens to shared
 // memory two blocks ahead and lays their B and C out in fp32, a pair's two values side by
 // side, so that a lane reads four operands at once.
@@ -28,8 +28,6 @@ namespace {
 
 constexpr int kScanWarps = 4;
 constexpr int kScanThreads = kScanWarps * 32;
-constexpr int kStates = 8;            // states of a lane
-constexpr int kGroup = 8;             // tokens of a group
 constexpr int kBlock = 16;            // tokens of a block
 constexpr int kStages = 3;            // blocks in shared memory
 constexpr int kShort = 7;             // tokens of a sequence that goes without shared memory
@@ -42,28 +40,94 @@ struct SelParams {
     void *pool;
     int64_t y_stride, x_stride, dt_stride, b_stride, c_stride, z_stride;
     int32_t channels, tiles;          // tiles of a CTA's channels
-    int32_t softplus;
+    int32_t softplus, pool_bf16;
 };
 
 // ---------------------------------------------------------------- arithmetic
-// max(v, 0) + log(1 + e^-|v|).  With e = e^-|v| in (0, 1], log(1 + e) = e P(e), P of degree
-// 9 fitted to log(1 + e) / e (relative error 5e-9, 1.6e-7 with fp32's roundings): small
-// steps keep their relative precision.
+// A value twice.  (Volatile: made once and kept, not again at each use.)
+__device__ __forceinline__ uint64_t twice(float v)
+{
+    uint64_t r;
+    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
+}
+
+// log(1 + e) / e on [0, 1], degree 8: relative error 3e-8, 1.8e-7 with fp32's roundings.
+#define SSD_LOG1P_TERMS(F) \
+    F(0.0052326940931379795f) F(-0.029505237936973572f) F(0.07822595536708832f) F(-0.13663245737552643f) \
+    F(0.19106006622314453f) F(-0.2484298199415207f) F(0.3331909775733948f) F(-0.4999949336051941f) \
+    F(0.9999999403953552f)
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// softplus(v) = max(v, 0) + log(1 + e) with e = e^-|v| in (0, 1]: small steps keep their
+// relative precision.
 __device__ __forceinline__ float step_of(float v)
 {
-    const float e = ptx::ex2(-1.4426950408889634f * fabsf(v));
-    float p = -0.0032440251670777798f;
-    p = fmaf(p, e, 0.01985146291553974f);
-    p = fmaf(p, e, -0.05695953220129013f);
-    p = fmaf(p, e, 0.10603655129671097f);
-    p = fmaf(p, e, -0.15305592119693756f);
-    p = fmaf(p, e, 0.1967593878507614f);
-    p = fmaf(p, e, -0.24954134225845337f);
-    p = fmaf(p, e, 0.3332996368408203f);
-    p = fmaf(p, e, -0.4999990165233612f);
-    p = fmaf(p, e, 1.f);
+    const float e = ptx::ex2(-fabsf(v * kLog2e));
+    float p = 0.f;
+#define SSD_TERM(c) p = fmaf(p, e, c);
+    SSD_LOG1P_TERMS(SSD_TERM)
+#undef SSD_TERM
     return fmaf(p, e, fmaxf(v, 0.f));
 }
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What two tokens' steps and outputs need, each value twice.
+struct Pairwise {
+    uint64_t terms[9], log2e, bias, D;
+    bool softplus;
+
+    __device__ __forceinline__ void set(float bias_, float D_, bool softplus_)
+    {
+        int i = 0;
+#define SSD_TERM(c) terms[i++] = twice(c);
+        SSD_LOG1P_TERMS(SSD_TERM)
+#undef SSD_TERM
+        log2e = twice(kLog2e);
+        bias = twice(bias_);
+        D = twice(D_);
+        softplus = softplus_;
+    }
+
+    // steps of two raw values: step_of on each
+    __device__ __forceinline__ uint64_t steps(float raw0, float raw1) const
+    {
+        const uint64_t v = ptx::add2(ptx::pack2(raw0, raw1), bias);
+        float v0, v1, t0, t1, d0, d1;
+        ptx::unpack2(v, v0, v1);
+        ptx::unpack2(ptx::mul2(v, log2e), t0, t1);
+        const uint64_t e = ptx::pack2(ptx::ex2(-fabsf(t0)), ptx::ex2(-fabsf(t1)));
+        uint64_t p = ptx::fma2(terms[0], e, terms[1]);
+#pragma unroll
+        for (int i = 2; i < 9; ++i)
+            p = ptx::fma2(p, e, terms[i]);
+        ptx::unpack2(ptx::fma2(p, e, ptx::pack2(fmaxf(v0, 0.f), fmaxf(v1, 0.f))), d0, d1);
+        return ptx::pack2(softplus ? d0 : v0, softplus ? d1 : v1);
+    }
+
+    // two outputs of sums of C h, x and the gate
+    template <bool kGate>
+    __device__ __forceinline__ uint32_t outputs(uint64_t sum, uint64_t x, float z0, float z1) const
+    {
+        uint64_t v = ptx::fma2(D, x, sum);
+        if constexpr (kGate) {
+            float t0, t1, q0, q1;
+            ptx::unpack2(ptx::mul2(ptx::pack2(z0, z1), log2e), t0, t1);
+            ptx::unpack2(ptx::add2(ptx::pack2(ptx::ex2(-t0), ptx::ex2(-t1)), ptx::pack2(1.f, 1.f)), q0, q1);
+            v = ptx::mul2(ptx::mul2(v, ptx::pack2(z0, z1)), ptx::pack2(rcp(q0), rcp(q1)));
+        }
+        float v0, v1;
+        ptx::unpack2(v, v0, v1);
+        return pack_bf16(v0, v1);
+    }
+};
 
 // ---------------------------------------------------------------- copies
 // 16 bytes from global to shared memory without registers; zeros where there is no source.
@@ -76,35 +140,57 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool there)
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// ---------------------------------------------------------------- pool
-template <bool kBf16>
-__device__ __forceinline__ void load_states(const void *pool, int64_t at, float (&h)[kStates])
+// ---------------------------------------------------------------- states
+// 4 or 8 consecutive bf16 values as fp32.
+template <int kCount>
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16 *src, float (&v)[kCount])
 {
-    if constexpr (kBf16) {
-        widen8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pool) + at), h);
-    } else {
-        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(pool) + at);
-        *reinterpret_cast<float4 *>(h) = src[0];
-        *reinterpret_cast<float4 *>(h + 4) = src[1];
+#pragma unroll
+    for (int i = 0; i < kCount; i += 4) {
+        const uint2 r = *reinterpret_cast<const uint2 *>(src + i);
+        v[i] = __uint_as_float(r.x << 16);
+        v[i + 1] = __uint_as_float(r.x & 0xffff0000u);
+        v[i + 2] = __uint_as_float(r.y << 16);
+        v[i + 3] = __uint_as_float(r.y & 0xffff0000u);
     }
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void store_states(void *pool, int64_t at, const float (&h)[kStates])
+// kStates states (4 or 8) from the pool and into it.
+template <int kStates>
+__device__ __forceinline__ void load_states(const void *pool, bool bf16, int64_t at, float (&h)[kStates])
 {
-    if constexpr (kBf16) {
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(pool) + at) = round8(h);
-    } else {
-        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(pool) + at);
-        dst[0] = make_float4(h[0], h[1], h[2], h[3]);
-        dst[1] = make_float4(h[4], h[5], h[6], h[7]);
+    if (bf16) {
+        load_bf16(static_cast<const __nv_bfloat16 *>(pool) + at, h);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kStates; i += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(pool) + at + i);
+        h[i] = v.x;
+        h[i + 1] = v.y;
+        h[i + 2] = v.z;
+        h[i + 3] = v.w;
+    }
+}
+
+template <int kStates>
+__device__ __forceinline__ void store_states(void *pool, bool bf16, int64_t at, const float (&h)[kStates])
+{
+#pragma unroll
+    for (int i = 0; i < kStates; i += 4) {
+        if (bf16)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(pool) + at + i) =
+                make_uint2(pack_bf16(h[i], h[i + 1]), pack_bf16(h[i + 2], h[i + 3]));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(pool) + at + i) =
+                make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
     }
 }
 
 // ---------------------------------------------------------------- lanes
 // Shared memory of a CTA.  Rows are padded so that the lanes of a warp that read
 // several tokens at once find them in different banks.
-template <int N>
+template <int N, int kStates>
 struct SelShared {
     static constexpr int kLanes = N / kStates;                  // lanes of a channel
     static constexpr int kChannels = 32 / kLanes;               // channels of a warp
@@ -115,23 +201,18 @@ struct SelShared {
     };
     Block block[kStages];
     __nv_bfloat16 y[2][kBlock][kPitch];
+    // per warp, two groups: the steps and the inputs before B of a pair {d0, d1, u0, u1}
+    static constexpr int kGroup = kLanes == 8 ? 16 : 8;         // tokens of a group
+    float4 steps[2][kScanWarps][kGroup / 2][kChannels];
     // per pair of tokens, [chunk][part]: two states of a part for the two tokens
     float4 B[2][kBlock / 2][kStates / 2][kLanes], C[2][kBlock / 2][kStates / 2][kLanes];
 };
 
 // What a lane holds of its channel.
+template <int kStates>
 struct SelLane {
     float h[kStates];
-    float a[kStates];          // A log2(e)
-    float D, bias;
-    bool softplus;
-
-    __device__ __forceinline__ float step(__nv_bfloat16 raw) const
-    {
-        const float v = __bfloat162float(raw) + bias, d = step_of(v);
-        return softplus ? d : v;
-    }
-
+    uint64_t a[kStates];       // A log2(e), twice
     // The states over a pair of tokens, whose steps are dt, inputs (before B) u; B and C of
     // the lane's states are kStride float4 apart.  Returns the pair's sums of C h.
     template <int kStride>
@@ -144,7 +225,7 @@ struct SelLane {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float e0, e1, in0, in1;
-                ptx::unpack2(ptx::mul2(dt, ptx::pack2(a[2 * k + i], a[2 * k + i])), e0, e1);
+                ptx::unpack2(ptx::mul2(dt, a[2 * k + i]), e0, e1);
                 ptx::unpack2(ptx::mul2(u, i ? ptx::pack2(b.z, b.w) : ptx::pack2(b.x, b.y)), in0, in1);
                 const float first = fmaf(ptx::ex2(e0), h[2 * k + i], in0);
                 h[2 * k + i] = fmaf(ptx::ex2(e1), first, in1);
@@ -156,42 +237,50 @@ struct SelLane {
     }
 
     // One token, B and C of the lane's states in bf16; returns the sum of C h.
-    __device__ __forceinline__ float token(float dt, float u, const uint4 &braw, const uint4 &craw)
+    __device__ __forceinline__ float token(float dt, float u, const __nv_bfloat16 *B, const __nv_bfloat16 *C)
     {
-        float b[8], c[8], sum = 0.f;
-        widen8(braw, b);
-        widen8(craw, c);
+        float b[kStates], c[kStates], sum = 0.f;
+        load_bf16(B, b);
+        load_bf16(C, c);
 #pragma unroll
         for (int n = 0; n < kStates; ++n) {
-            h[n] = fmaf(ptx::ex2(dt * a[n]), h[n], u * b[n]);
+            float an, same;
+            ptx::unpack2(a[n], an, same);
+            h[n] = fmaf(ptx::ex2(dt * an), h[n], u * b[n]);
             sum = fmaf(h[n], c[n], sum);
         }
         return sum;
     }
 };
 
-// Sums over a channel's lanes of kLanes tokens at once: lane `part` gets token part's.
+// Sums over a channel's lanes of kLanes pairs at once: lane `part` gets pair part's.
 template <int kLanes, int kChannels>
-__device__ __forceinline__ float reduce_tokens(float *v, int part)
+__device__ __forceinline__ uint64_t reduce_pairs(uint64_t *v, int part)
 {
 #pragma unroll
     for (int n = kLanes / 2; n >= 1; n /= 2) {
         const bool upper = part & n;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, n * kChannels);
+            const uint64_t send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+            float s0, s1;
+            ptx::unpack2(send, s0, s1);
+            v[i] = ptx::add2(keep, ptx::pack2(__shfl_xor_sync(0xffffffffu, s0, n * kChannels),
+                                              __shfl_xor_sync(0xffffffffu, s1, n * kChannels)));
         }
     }
     return v[0];
 }
 
-template <int N, bool kBf16, bool kGate>
-__global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __grid_constant__ SelParams p)
+// (Two CTAs an SM asked for: without a number of them ptxas keeps to 80 registers and
+// orders the code for that, 560 us for two prompts of 9,763 tokens instead of 430.)
+template <int N, int kStates, bool kGate>
+__global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const __grid_constant__ SelParams p)
 {
-    using Shared = SelShared<N>;
+    using Shared = SelShared<N, kStates>;
     constexpr int kLanes = Shared::kLanes, kChannels = Shared::kChannels, kCols = Shared::kCols;
-    constexpr int kMine = kGroup / kLanes;           // tokens of a group that a lane makes the steps of
+    constexpr int kGroup = Shared::kGroup, kGroups = kBlock / kGroup;
+    constexpr int kMine = kGroup / 2 / kLanes;       // pairs of a group that a lane makes the steps of
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -242,25 +331,28 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __gr
         if (begin + kBlock < end)
             fetch(begin + kBlock);
     }
-    SelLane me;
+    SelLane<kStates> me;
 #pragma unroll
     for (int n = 0; n < kStates; ++n)
         me.h[n] = 0.f;
     if (has)
-        load_states<kBf16>(p.pool, at, me.h);
+        load_states(p.pool, p.pool_bf16, at, me.h);
 #pragma unroll
     for (int n = 0; n < kStates; n += 4) {
         const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + static_cast<int64_t>(ch) * N + part * kStates + n));
-        me.a[n] = v.x * 1.4426950408889634f;
-        me.a[n + 1] = v.y * 1.4426950408889634f;
-        me.a[n + 2] = v.z * 1.4426950408889634f;
-        me.a[n + 3] = v.w * 1.4426950408889634f;
+        me.a[n] = twice(v.x * kLog2e);
+        me.a[n + 1] = twice(v.y * kLog2e);
+        me.a[n + 2] = twice(v.z * kLog2e);
+        me.a[n + 3] = twice(v.w * kLog2e);
     }
-    me.D = p.D ? p.D[ch] : 0.f;
-    me.bias = p.dt_bias ? p.dt_bias[ch] : 0.f;
-    me.softplus = p.softplus;
+    const float D = p.D ? p.D[ch] : 0.f, bias = p.dt_bias ? p.dt_bias[ch] : 0.f;
+    // one token's step and output
+    auto step = [&](__nv_bfloat16 raw) {
+        const float v = __bfloat162float(raw) + bias;
+        return p.softplus ? step_of(v) : v;
+    };
     auto output = [&](float sum, float x, __nv_bfloat16 z) {
-        float v = fmaf(me.D, x, sum);
+        float v = fmaf(D, x, sum);
         if constexpr (kGate)
             v *= silu_f32(__bfloat162float(z));
         return __float2bfloat16_rn(v);
@@ -271,10 +363,9 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __gr
         // a few tokens: straight from global memory
         for (int t = begin; t < end; ++t) {
             const __nv_bfloat16 z = kGate ? p.z[t * p.z_stride + ch] : none;
-            const float x = __bfloat162float(p.x[t * p.x_stride + ch]), dt = me.step(p.dt[t * p.dt_stride + ch]);
+            const float x = __bfloat162float(p.x[t * p.x_stride + ch]), dt = step(p.dt[t * p.dt_stride + ch]);
             float sum = me.token(dt, dt * x,
-                                 *reinterpret_cast<const uint4 *>(p.B + t * p.b_stride + part * kStates),
-                                 *reinterpret_cast<const uint4 *>(p.C + t * p.c_stride + part * kStates));
+                                 p.B + t * p.b_stride + part * kStates, p.C + t * p.c_stride + part * kStates);
 #pragma unroll
             for (int o = kChannels; o < 32; o <<= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -282,7 +373,7 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __gr
                 p.y[t * p.y_stride + ch] = output(sum, x, z);
         }
         if (slot >= 0 && valid)
-            store_states<kBf16>(p.pool, at, me.h);
+            store_states(p.pool, p.pool_bf16, at, me.h);
         return;
     }
 
@@ -318,25 +409,66 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __gr
                     *reinterpret_cast<const uint4 *>(&s.y[k & 1][row][c]);
         }
     };
-    // the steps of the lane's tokens of a group
-    float dt[kMine], u[kMine], x[kMine];
-    __nv_bfloat16 z[kMine];
-    auto steps = [&](const typename Shared::Block &src, int row0, float (&dt)[kMine], float (&u)[kMine],
-                     float (&x)[kMine], __nv_bfloat16 (&z)[kMine]) {
+    // The lane's pairs of a group: tokens 2 (i kLanes + part) and the next of it.  Their steps
+    // go to the warp's shared memory, their x and z stay.
+    Pairwise two;
+    two.set(bias, D, p.softplus);
+    struct Kept {
+        uint64_t x[kMine];
+        float z[kGate ? 2 * kMine : 1];
+    };
+    auto make_steps = [&](const typename Shared::Block &src, int row0, float4 (&made)[kMine], Kept &keep) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int row = row0 + i * kLanes + part;
-            x[i] = __bfloat162float(src.x[row][col]);
-            z[i] = kGate ? src.z[row][col] : none;
-            dt[i] = me.step(src.dt[row][col]);
-            u[i] = dt[i] * x[i];
+            const int pair = i * kLanes + part, row = row0 + 2 * pair;
+            keep.x[i] = ptx::pack2(__bfloat162float(src.x[row][col]), __bfloat162float(src.x[row + 1][col]));
+            if constexpr (kGate) {
+                keep.z[2 * i] = __bfloat162float(src.z[row][col]);
+                keep.z[2 * i + 1] = __bfloat162float(src.z[row + 1][col]);
+            }
+            const uint64_t d = two.steps(__bfloat162float(src.dt[row][col]), __bfloat162float(src.dt[row + 1][col]));
+            float d0, d1, u0, u1;
+            ptx::unpack2(d, d0, d1);
+            ptx::unpack2(ptx::mul2(d, keep.x[i]), u0, u1);
+            made[i] = make_float4(d0, d1, u0, u1);
+        }
+    };
+    auto hand_over = [&](const float4 (&made)[kMine], float4 (&dst)[kGroup / 2][kChannels]) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            dst[i * kLanes + part][in_warp] = made[i];
+    };
+    // A group from row g of block k: its states and sums, and the y of the lane's pairs.
+    auto group = [&](int k, int g, const float4 (&src)[kGroup / 2][kChannels], const Kept &keep) {
+        uint32_t out[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            uint64_t sums[kLanes];
+#pragma unroll
+            for (int j = 0; j < kLanes; ++j) {
+                const int pair = i * kLanes + j, row = g / 2 + pair;
+                const float4 st = src[pair][in_warp];
+                sums[j] = me.template pair<kLanes>(ptx::pack2(st.x, st.y), ptx::pack2(st.z, st.w),
+                                                   &s.B[k & 1][row][0][part], &s.C[k & 1][row][0][part]);
+            }
+            out[i] = two.template outputs<kGate>(reduce_pairs<kLanes, kChannels>(sums, part), keep.x[i],
+                                                 keep.z[kGate ? 2 * i : 0], keep.z[kGate ? 2 * i + 1 : 0]);
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int row = g + 2 * (i * kLanes + part);
+            s.y[k & 1][row][col] = __ushort_as_bfloat16(static_cast<unsigned short>(out[i]));
+            s.y[k & 1][row + 1][col] = __ushort_as_bfloat16(static_cast<unsigned short>(out[i] >> 16));
         }
     };
 
     copies_wait();
     __syncthreads();
     lay_out(0);
-    steps(s.block[0], 0, dt, u, x, z);
+    Kept keep[2];
+    float4 made[kMine];
+    make_steps(s.block[0], 0, made, keep[0]);
+    hand_over(made, s.steps[0][warp]);
     const int blocks = (end - begin + kBlock - 1) / kBlock;
     for (int k = 0; k < blocks; ++k) {
         // block k + 1 has arrived for everybody, and nobody reads blocks and y of k - 1 any more
@@ -350,48 +482,30 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __gr
         if (k + 1 < blocks)
             lay_out(k + 1);
         const typename Shared::Block &now = s.block[k % kStages], &next = s.block[(k + 1) % kStages];
+        if (n == kBlock) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                // the next group's steps are made among this one's states, and stored behind
+                // them, where no load has to wait for them (past the end they are not used)
+                const int from = (kGroups == 1 ? k : i) & 1;
+                make_steps(i + 1 < kGroups ? now : next, (i + 1) % kGroups * kGroup, made,
+                           keep[kGroups == 1 ? 1 : (i + 1) & 1]);
+                group(k, i * kGroup, s.steps[from][warp], keep[kGroups == 1 ? 0 : i & 1]);
+                hand_over(made, s.steps[from ^ 1][warp]);
+                if constexpr (kGroups == 1)
+                    keep[0] = keep[1];
+                __syncwarp();
+            }
+            continue;
+        }
         int g = 0;
-        for (; g + kGroup <= n; g += kGroup) {
-            // the next group's steps go between this one's (past the end they are not used)
-            float dt1[kMine], u1[kMine], x1[kMine];
-            __nv_bfloat16 z1[kMine];
-            const bool more = g + kGroup < kBlock;
-            steps(more ? now : next, more ? g + kGroup : 0, dt1, u1, x1, z1);
-            float sums[kGroup];
-#pragma unroll
-            for (int j = 0; j < kGroup; j += 2) {
-                uint64_t dt2, u2;
-                if constexpr (kLanes == 1) {
-                    dt2 = ptx::pack2(dt[j], dt[j + 1]);
-                    u2 = ptx::pack2(u[j], u[j + 1]);
-                } else {
-                    const int i = j / kLanes, from = j % kLanes * kChannels + in_warp;
-                    dt2 = ptx::pack2(__shfl_sync(0xffffffffu, dt[i], from),
-                                     __shfl_sync(0xffffffffu, dt[i], from + kChannels));
-                    u2 = ptx::pack2(__shfl_sync(0xffffffffu, u[i], from),
-                                    __shfl_sync(0xffffffffu, u[i], from + kChannels));
-                }
-                const int row = (g + j) / 2;
-                ptx::unpack2(me.pair<kLanes>(dt2, u2, &s.B[k & 1][row][0][part], &s.C[k & 1][row][0][part]), sums[j],
-                             sums[j + 1]);
-            }
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const float sum = reduce_tokens<kLanes, kChannels>(sums + i * kLanes, part);
-                s.y[k & 1][g + i * kLanes + part][col] = output(sum, x[i], z[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                dt[i] = dt1[i];
-                u[i] = u1[i];
-                x[i] = x1[i];
-                z[i] = z1[i];
-            }
+        if (kGroups > 1 && n >= kGroup) {
+            group(k, 0, s.steps[0][warp], keep[0]);
+            g = kGroup;
         }
         for (; g < n; ++g) {      // the sequence's last tokens, fewer than a group
-            const float xt = __bfloat162float(now.x[g][col]), d = me.step(now.dt[g][col]);
-            float sum = me.token(d, d * xt, *reinterpret_cast<const uint4 *>(&now.B[g][part * kStates]),
-                                 *reinterpret_cast<const uint4 *>(&now.C[g][part * kStates]));
+            const float xt = __bfloat162float(now.x[g][col]), d = step(now.dt[g][col]);
+            float sum = me.token(d, d * xt, &now.B[g][part * kStates], &now.C[g][part * kStates]);
 #pragma unroll
             for (int o = kChannels; o < 32; o <<= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -402,29 +516,27 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(const __gr
     __syncthreads();
     write_out(blocks - 1);
     if (slot >= 0 && valid)
-        store_states<kBf16>(p.pool, at, me.h);
+        store_states(p.pool, p.pool_bf16, at, me.h);
 }
 
-template <int N, bool kBf16, bool kGate>
+template <int N, int kStates, bool kGate>
 cudaError_t launch(SelParams &p, cudaStream_t stream)
 {
-    using Shared = SelShared<N>;
+    using Shared = SelShared<N, kStates>;
     constexpr int kBytes = sizeof(Shared);
-    cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<N, kBf16, kGate>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<N, kStates, kGate>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess)
         return e;
     p.tiles = (p.channels + Shared::kCols - 1) / Shared::kCols;
-    return launch_pdl_smem(selective_scan_kernel<N, kBf16, kGate>, dim3(static_cast<unsigned>(p.tiles * p.s.batch)),
+    return launch_pdl_smem(selective_scan_kernel<N, kStates, kGate>, dim3(static_cast<unsigned>(p.tiles * p.s.batch)),
                            kScanThreads, kBytes, stream, p);
 }
 
-template <int N>
-cudaError_t launch(SelParams &p, bool bf16, cudaStream_t stream)
+template <int N, int kStates>
+cudaError_t launch(SelParams &p, cudaStream_t stream)
 {
-    if (p.z)
-        return bf16 ? launch<N, true, true>(p, stream) : launch<N, false, true>(p, stream);
-    return bf16 ? launch<N, true, false>(p, stream) : launch<N, false, false>(p, stream);
+    return p.z ? launch<N, kStates, true>(p, stream) : launch<N, kStates, false>(p, stream);
 }
 
 bool sel_sizes(int64_t total_len, int32_t batch, int32_t channels, int32_t dstate)
@@ -500,12 +612,13 @@ ssd_status_t ssd_selective_scan_varlen_fwd(
     p.z_stride = t.z;
     p.channels = channels;
     p.softplus = dt_softplus != 0;
-    const bool bf16 = pool_type == SSD_POOL_BF16;
+    constexpr int kStates = 8;
+    p.pool_bf16 = pool_type == SSD_POOL_BF16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dstate == 8    ? launch<8>(p, bf16, s)
-                          : dstate == 16 ? launch<16>(p, bf16, s)
-                          : dstate == 32 ? launch<32>(p, bf16, s)
-                                         : launch<64>(p, bf16, s);
+    const cudaError_t e = dstate == 8    ? launch<8, kStates>(p, s)
+                          : dstate == 16 ? launch<16, kStates>(p, s)
+                          : dstate == 32 ? launch<32, kStates>(p, s)
+                                         : launch<64, kStates>(p, s);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
