@@ -16,8 +16,16 @@
 // steps of its share of a group's pairs, a group ahead and two at a time as well, and hands
 // them over through shared memory; its share of the sums comes back from a reduction that
 // halves the sums as it halves the lanes.  The CTA copies blocks of 16 tokens to shared
-// memory two blocks ahead and lays their B and C out in fp32, a pair's two values side by
+// memory three blocks ahead and lays their B and C out in fp32, a pair's two values side by
 // side, so that a lane reads four operands at once.
+//
+// A sequence that would keep too few warps busy is cut into chunks (sel_chunk).  A first
+// kernel makes the states alone that each chunk but the last leads to from zero (the first:
+// from the sequence's own), and the sums of their steps; in the second a chunk joins what
+// lies before it, h = exp(A sum dt) h + the next chunk's own, and does its tokens.  One CTA
+// lists the chunks before, the long ones first.  Batches of single tokens, whose work is to
+// read and write the states, go to a kernel whose CTAs keep their tile's decays and have
+// the next sequences' states on their way.
 #include <algorithm>
 
 #include "attn_ptx.cuh"
@@ -29,8 +37,25 @@ namespace {
 constexpr int kScanWarps = 4;
 constexpr int kScanThreads = kScanWarps * 32;
 constexpr int kBlock = 16;            // tokens of a block
-constexpr int kStages = 3;            // blocks in shared memory
+constexpr int kStages = 4;            // blocks in shared memory
 constexpr int kShort = 7;             // tokens of a sequence that goes without shared memory
+
+constexpr int kStates = 8;            // states of a lane
+constexpr int kMinChunk = 64;         // tokens of a chunk at least
+constexpr int kFullWarps = 5000;      // warps that sel_chunk wants of a call's chunks
+constexpr int kFewWarps = 800;        // warps that leave a sequence whole (sel_cut)
+constexpr int kResident = 4;          // CTAs of an SM at most
+
+// A chunk k of a sequence, as a rule the whole sequence.
+struct alignas(32) SelUnit {
+    int32_t seq, begin, end;          // its tokens [begin, end)
+    int32_t k, ends;                  // index; where the ends of the sequence's chunks begin
+    int32_t cut, last, pad;           // whether the sequence is cut, whether it is its last
+};
+
+struct SelHeader {
+    int32_t units, ends;              // chunks; of them not the last of their sequence
+};
 
 struct SelParams {
     SlotBatch s;
@@ -38,10 +63,112 @@ struct SelParams {
     const __nv_bfloat16 *x, *dt, *B, *C, *z;
     const float *A, *D, *dt_bias;
     void *pool;
+    SelHeader *header;
+    SelUnit *units, *inner;           // the chunks, long ones first (null: each sequence is
+                                      // one, in order); the chunk before each end
+    float *ends, *sums;               // [end]: states and steps' sum of the chunk before it
+    float *firsts;                    // states that a cut sequence starts from, at its first end
     int64_t y_stride, x_stride, dt_stride, b_stride, c_stride, z_stride;
     int32_t channels, tiles;          // tiles of a CTA's channels
+    int32_t chunk, cut;               // smallest chunk, shortest sequence that is cut
     int32_t softplus, pool_bf16;
 };
+
+// ---------------------------------------------------------------- chunks
+// Tokens of the smallest chunk, as many as give kFullWarps warps over all tokens, and of
+// the shortest sequence that is cut.  Cutting makes the states of most tokens twice, which
+// costs about 0.7 of the whole again; a sequence alone takes 62 ns a token whatever its
+// warps, while they are fewer than the schedulers, and in chunks some 0.125 ns a token and
+// warp of the call.  (One sequence of 4,096 tokens, 2,048 channels: 263 us whole, 85 in
+// chunks; of 9,763 tokens, 8,192 channels: 604 and 585; two of them: 430 and 538.)
+inline int32_t sel_rounded(int64_t tokens)
+{
+    return static_cast<int32_t>(std::min<int64_t>((tokens + kBlock - 1) / kBlock * kBlock, INT32_MAX / 2));
+}
+inline int64_t sel_warp_tokens(int64_t total_len, int32_t channels, int32_t dstate)
+{
+    return total_len * ((static_cast<int64_t>(channels) * dstate + 32 * kStates - 1) / (32 * kStates));
+}
+inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
+{
+    return std::max(kMinChunk, sel_rounded((sel_warp_tokens(total_len, channels, dstate) + kFullWarps - 1) / kFullWarps));
+}
+inline int32_t sel_cut(int64_t total_len, int32_t channels, int32_t dstate)
+{
+    return std::max(2 * sel_chunk(total_len, channels, dstate),
+                    sel_rounded(sel_warp_tokens(total_len, channels, dstate) / kFewWarps));
+}
+
+// Lists the chunks: `count` of `len` tokens a sequence, the last one shorter.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanSizes = 16;        // sizes of chunks (powers of two) that are told apart
+
+__global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __grid_constant__ SelParams p)
+{
+    __shared__ int s_units[kPlanSizes], s_ends;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < kPlanSizes)
+        s_units[threadIdx.x] = 0;
+    if (threadIdx.x == 0)
+        s_ends = 0;
+    pdl_wait();
+    __syncthreads();
+    auto chunks = [&](int b, int32_t &begin, int32_t &end, int32_t &len, int &count) {
+        count = 0;
+        if (b >= p.s.batch || !seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, begin, end))
+            return 0;
+        len = end - begin;
+        count = 1;
+        if (len >= p.cut) {
+            const int32_t n = len / p.chunk;
+            len = ((len + n - 1) / n + kBlock - 1) / kBlock * kBlock;
+            count = (end - begin + len - 1) / len;
+        }
+        return kPlanSizes - 1 - min(kPlanSizes - 1, 31 - __clz(len | 1));      // long ones first
+    };
+    int32_t begin = 0, end = 0, len = 0;
+    int count;
+    for (int b = threadIdx.x; b < p.s.batch; b += kPlanThreads) {
+        const int size = chunks(b, begin, end, len, count);
+        if (count)
+            atomicAdd(&s_units[size], count);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int n = lane < kPlanSizes ? s_units[lane] : 0, upto = warp_inclusive_scan(n);
+        if (lane < kPlanSizes)
+            s_units[lane] = upto - n;
+        if (lane == 31)
+            p.header->units = upto;
+    }
+    __syncthreads();
+    for (int b0 = threadIdx.x - lane; b0 < p.s.batch; b0 += kPlanThreads) {
+        const int b = b0 + lane, size = chunks(b, begin, end, len, count);
+        int at = 0, ends = 0;
+        if (count) {
+            at = atomicAdd(&s_units[size], count);
+            if (count > 1)
+                ends = atomicAdd(&s_ends, count - 1);
+            else
+                p.units[at] = SelUnit{b, begin, end, 0, 0, 0, 1, 0};
+        }
+        for (uint32_t many = __ballot_sync(0xffffffffu, count > 1); many; many &= many - 1) {
+            const int from = __ffs(many) - 1;
+            const int n = __shfl_sync(0xffffffffu, count, from), first = __shfl_sync(0xffffffffu, begin, from);
+            const int behind = __shfl_sync(0xffffffffu, end, from), l = __shfl_sync(0xffffffffu, len, from);
+            const int u = __shfl_sync(0xffffffffu, at, from), e = __shfl_sync(0xffffffffu, ends, from);
+            for (int k = lane; k < n; k += 32) {
+                const SelUnit unit = {b0 + from, first + k * l, min(first + (k + 1) * l, behind), k, e, 1, k == n - 1, 0};
+                p.units[u + k] = unit;
+                if (k < n - 1)
+                    p.inner[e + k] = unit;
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        p.header->ends = s_ends;
+}
 
 // ---------------------------------------------------------------- arithmetic
 // A value twice.  (Volatile: made once and kept, not again at each use.)
@@ -138,25 +265,20 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool there)
                  : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
-// ---------------------------------------------------------------- states
-// 4 or 8 consecutive bf16 values as fp32.
-template <int kCount>
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16 *src, float (&v)[kCount])
+// Until all but the last kBehind groups of copies have arrived.
+template <int kBehind>
+__device__ __forceinline__ void copies_wait()
 {
-#pragma unroll
-    for (int i = 0; i < kCount; i += 4) {
-        const uint2 r = *reinterpret_cast<const uint2 *>(src + i);
-        v[i] = __uint_as_float(r.x << 16);
-        v[i + 1] = __uint_as_float(r.x & 0xffff0000u);
-        v[i + 2] = __uint_as_float(r.y << 16);
-        v[i + 3] = __uint_as_float(r.y & 0xffff0000u);
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBehind) : "memory");
 }
 
-// kStates states (4 or 8) from the pool and into it.
-template <int kStates>
+// ---------------------------------------------------------------- states
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16 *src, float (&v)[kStates])
+{
+    widen8(*reinterpret_cast<const uint4 *>(src), v);
+}
+
+// A lane's states from the pool and into it.
 __device__ __forceinline__ void load_states(const void *pool, bool bf16, int64_t at, float (&h)[kStates])
 {
     if (bf16) {
@@ -173,7 +295,6 @@ __device__ __forceinline__ void load_states(const void *pool, bool bf16, int64_t
     }
 }
 
-template <int kStates>
 __device__ __forceinline__ void store_states(void *pool, bool bf16, int64_t at, const float (&h)[kStates])
 {
 #pragma unroll
@@ -190,7 +311,7 @@ __device__ __forceinline__ void store_states(void *pool, bool bf16, int64_t at, 
 // ---------------------------------------------------------------- lanes
 // Shared memory of a CTA.  Rows are padded so that the lanes of a warp that read
 // several tokens at once find them in different banks.
-template <int N, int kStates>
+template <int N>
 struct SelShared {
     static constexpr int kLanes = N / kStates;                  // lanes of a channel
     static constexpr int kChannels = 32 / kLanes;               // channels of a warp
@@ -209,19 +330,37 @@ struct SelShared {
 };
 
 // What a lane holds of its channel.
-template <int kStates>
 struct SelLane {
     float h[kStates];
     uint64_t a[kStates];       // A log2(e), twice
+
+    __device__ __forceinline__ void load_decays(const float *A)
+    {
+#pragma unroll
+        for (int n = 0; n < kStates; n += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(A + n));
+            a[n] = twice(v.x * kLog2e);
+            a[n + 1] = twice(v.y * kLog2e);
+            a[n + 2] = twice(v.z * kLog2e);
+            a[n + 3] = twice(v.w * kLog2e);
+        }
+    }
+    __device__ __forceinline__ float decay(int n) const
+    {
+        float v, same;
+        ptx::unpack2(a[n], v, same);
+        return v;
+    }
+
     // The states over a pair of tokens, whose steps are dt, inputs (before B) u; B and C of
-    // the lane's states are kStride float4 apart.  Returns the pair's sums of C h.
-    template <int kStride>
+    // the lane's states are kStride float4 apart.  Returns the pair's sums of C h (kOut).
+    template <int kStride, bool kOut>
     __device__ __forceinline__ uint64_t pair(uint64_t dt, uint64_t u, const float4 *B, const float4 *C)
     {
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < kStates / 2; ++k) {
-            const float4 b = B[k * kStride], c = C[k * kStride];
+            const float4 b = B[k * kStride], c = kOut ? C[k * kStride] : make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float e0, e1, in0, in1;
@@ -229,8 +368,9 @@ struct SelLane {
                 ptx::unpack2(ptx::mul2(u, i ? ptx::pack2(b.z, b.w) : ptx::pack2(b.x, b.y)), in0, in1);
                 const float first = fmaf(ptx::ex2(e0), h[2 * k + i], in0);
                 h[2 * k + i] = fmaf(ptx::ex2(e1), first, in1);
-                sum[i] = ptx::fma2(ptx::pack2(first, h[2 * k + i]), i ? ptx::pack2(c.z, c.w) : ptx::pack2(c.x, c.y),
-                                   sum[i]);
+                if constexpr (kOut)
+                    sum[i] = ptx::fma2(ptx::pack2(first, h[2 * k + i]),
+                                       i ? ptx::pack2(c.z, c.w) : ptx::pack2(c.x, c.y), sum[i]);
             }
         }
         return ptx::add2(sum[0], sum[1]);
@@ -244,9 +384,7 @@ struct SelLane {
         load_bf16(C, c);
 #pragma unroll
         for (int n = 0; n < kStates; ++n) {
-            float an, same;
-            ptx::unpack2(a[n], an, same);
-            h[n] = fmaf(ptx::ex2(dt * an), h[n], u * b[n]);
+            h[n] = fmaf(ptx::ex2(dt * decay(n)), h[n], u * b[n]);
             sum = fmaf(h[n], c[n], sum);
         }
         return sum;
@@ -272,33 +410,26 @@ __device__ __forceinline__ uint64_t reduce_pairs(uint64_t *v, int part)
     return v[0];
 }
 
-// (Two CTAs an SM asked for: without a number of them ptxas keeps to 80 registers and
-// orders the code for that, 560 us for two prompts of 9,763 tokens instead of 430.)
-template <int N, int kStates, bool kGate>
-__global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const __grid_constant__ SelParams p)
+// Tokens [begin, end) of one sequence by a CTA: the lane's states over them and, with
+// kOut, their y; else the sum of the channel's steps in `total`.
+template <int N, bool kGate, bool kOut>
+__device__ __forceinline__ void sel_tokens(const SelParams &p, SelShared<N> &s, SelLane &me, int begin, int end,
+                                           int col0, float D, float bias, float &total)
 {
-    using Shared = SelShared<N, kStates>;
+    using Shared = SelShared<N>;
     constexpr int kLanes = Shared::kLanes, kChannels = Shared::kChannels, kCols = Shared::kCols;
     constexpr int kGroup = Shared::kGroup, kGroups = kBlock / kGroup;
     constexpr int kMine = kGroup / 2 / kLanes;       // pairs of a group that a lane makes the steps of
-    extern __shared__ __align__(16) uint8_t smem[];
-    Shared &s = *reinterpret_cast<Shared *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = lane / kChannels, in_warp = lane % kChannels, col = warp * kChannels + in_warp;
-    const int b = blockIdx.x / p.tiles, col0 = blockIdx.x % p.tiles * kCols;
-    const bool valid = col0 + col < p.channels;
-    const int ch = valid ? col0 + col : 0;    // (the other lanes follow a channel that is there)
-    pdl_wait();
-    int32_t begin, end;
-    if (!seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, begin, end))
-        return;
-    const int64_t slot = seq_slot(p.s, b);
-    const bool has = slot >= 0 && p.s.has_init && p.s.has_init[b];
-    const int64_t at = (slot * p.channels + ch) * N + part * kStates;
 
     // copies of a block's rows, 16 bytes at a time
-    constexpr int kRowLoads = kCols / 8, kBcLoads = N / 8;
+    constexpr int kRowLoads = kCols / 8, kBcLoads = N / 8, kBc = kOut ? 2 : 1;
     auto fetch = [&](int t0) {
+        if (t0 >= end) {      // (groups are counted)
+            copies_commit();
+            return;
+        }
         typename Shared::Block &dst = s.block[(t0 - begin) / kBlock % kStages];
 #pragma unroll
         for (int i0 = 0; i0 < kBlock * kRowLoads; i0 += kScanThreads) {
@@ -309,14 +440,14 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
                 const int from = there ? col0 + c : 0;
                 copy16(&dst.x[row][c], p.x + t * p.x_stride + from, there);
                 copy16(&dst.dt[row][c], p.dt + t * p.dt_stride + from, there);
-                if constexpr (kGate)
+                if constexpr (kGate && kOut)
                     copy16(&dst.z[row][c], p.z + t * p.z_stride + from, there);
             }
         }
 #pragma unroll
-        for (int i0 = 0; i0 < 2 * kBlock * kBcLoads; i0 += kScanThreads) {
+        for (int i0 = 0; i0 < kBc * kBlock * kBcLoads; i0 += kScanThreads) {
             const int i = i0 + threadIdx.x, row = i / kBcLoads % kBlock, c = i % kBcLoads * 8;
-            if (2 * kBlock * kBcLoads % kScanThreads == 0 || i < 2 * kBlock * kBcLoads) {
+            if (kBc * kBlock * kBcLoads % kScanThreads == 0 || i < kBc * kBlock * kBcLoads) {
                 const bool there = t0 + row < end, is_c = i >= kBlock * kBcLoads;
                 const int64_t t = there ? t0 + row : begin;
                 copy16(is_c ? &dst.C[row][c] : &dst.B[row][c],
@@ -325,27 +456,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
         }
         copies_commit();
     };
-    const bool staged = end - begin > kShort;
-    if (staged) {
-        fetch(begin);
-        if (begin + kBlock < end)
-            fetch(begin + kBlock);
-    }
-    SelLane<kStates> me;
 #pragma unroll
-    for (int n = 0; n < kStates; ++n)
-        me.h[n] = 0.f;
-    if (has)
-        load_states(p.pool, p.pool_bf16, at, me.h);
-#pragma unroll
-    for (int n = 0; n < kStates; n += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + static_cast<int64_t>(ch) * N + part * kStates + n));
-        me.a[n] = twice(v.x * kLog2e);
-        me.a[n + 1] = twice(v.y * kLog2e);
-        me.a[n + 2] = twice(v.z * kLog2e);
-        me.a[n + 3] = twice(v.w * kLog2e);
-    }
-    const float D = p.D ? p.D[ch] : 0.f, bias = p.dt_bias ? p.dt_bias[ch] : 0.f;
+    for (int k = 0; k + 1 < kStages; ++k)
+        fetch(begin + k * kBlock);
     // one token's step and output
     auto step = [&](__nv_bfloat16 raw) {
         const float v = __bfloat162float(raw) + bias;
@@ -358,24 +471,6 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
         return __float2bfloat16_rn(v);
     };
     const __nv_bfloat16 none = __float2bfloat16_rn(0.f);
-
-    if (!staged) {
-        // a few tokens: straight from global memory
-        for (int t = begin; t < end; ++t) {
-            const __nv_bfloat16 z = kGate ? p.z[t * p.z_stride + ch] : none;
-            const float x = __bfloat162float(p.x[t * p.x_stride + ch]), dt = step(p.dt[t * p.dt_stride + ch]);
-            float sum = me.token(dt, dt * x,
-                                 p.B + t * p.b_stride + part * kStates, p.C + t * p.c_stride + part * kStates);
-#pragma unroll
-            for (int o = kChannels; o < 32; o <<= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (part == 0 && valid)
-                p.y[t * p.y_stride + ch] = output(sum, x, z);
-        }
-        if (slot >= 0 && valid)
-            store_states(p.pool, p.pool_bf16, at, me.h);
-        return;
-    }
 
     // B and C of a block in fp32, pair by pair
     auto lay_out = [&](int k) {
@@ -393,7 +488,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
                                        __uint_as_float(t0 & 0xffff0000u), __uint_as_float(t1 & 0xffff0000u));
                 };
                 s.B[k & 1][pair][chunk][to_part] = two(src.B);
-                s.C[k & 1][pair][chunk][to_part] = two(src.C);
+                if constexpr (kOut)
+                    s.C[k & 1][pair][chunk][to_part] = two(src.C);
             }
         }
     };
@@ -415,14 +511,14 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
     two.set(bias, D, p.softplus);
     struct Kept {
         uint64_t x[kMine];
-        float z[kGate ? 2 * kMine : 1];
+        float z[kGate && kOut ? 2 * kMine : 1];
     };
     auto make_steps = [&](const typename Shared::Block &src, int row0, float4 (&made)[kMine], Kept &keep) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int pair = i * kLanes + part, row = row0 + 2 * pair;
             keep.x[i] = ptx::pack2(__bfloat162float(src.x[row][col]), __bfloat162float(src.x[row + 1][col]));
-            if constexpr (kGate) {
+            if constexpr (kGate && kOut) {
                 keep.z[2 * i] = __bfloat162float(src.z[row][col]);
                 keep.z[2 * i + 1] = __bfloat162float(src.z[row + 1][col]);
             }
@@ -441,6 +537,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
     // A group from row g of block k: its states and sums, and the y of the lane's pairs.
     auto group = [&](int k, int g, const float4 (&src)[kGroup / 2][kChannels], const Kept &keep) {
         uint32_t out[kMine];
+        uint64_t steps = 0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             uint64_t sums[kLanes];
@@ -448,21 +545,30 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
             for (int j = 0; j < kLanes; ++j) {
                 const int pair = i * kLanes + j, row = g / 2 + pair;
                 const float4 st = src[pair][in_warp];
-                sums[j] = me.template pair<kLanes>(ptx::pack2(st.x, st.y), ptx::pack2(st.z, st.w),
-                                                   &s.B[k & 1][row][0][part], &s.C[k & 1][row][0][part]);
+                sums[j] = me.template pair<kLanes, kOut>(ptx::pack2(st.x, st.y), ptx::pack2(st.z, st.w),
+                                                         &s.B[k & 1][row][0][part], &s.C[k & 1][row][0][part]);
+                if constexpr (!kOut)
+                    steps = ptx::add2(steps, ptx::pack2(st.x, st.y));
             }
-            out[i] = two.template outputs<kGate>(reduce_pairs<kLanes, kChannels>(sums, part), keep.x[i],
-                                                 keep.z[kGate ? 2 * i : 0], keep.z[kGate ? 2 * i + 1 : 0]);
+            if constexpr (kOut)
+                out[i] = two.template outputs<kGate>(reduce_pairs<kLanes, kChannels>(sums, part), keep.x[i],
+                                                     keep.z[kGate ? 2 * i : 0], keep.z[kGate ? 2 * i + 1 : 0]);
         }
+        if constexpr (kOut) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int row = g + 2 * (i * kLanes + part);
-            s.y[k & 1][row][col] = __ushort_as_bfloat16(static_cast<unsigned short>(out[i]));
-            s.y[k & 1][row + 1][col] = __ushort_as_bfloat16(static_cast<unsigned short>(out[i] >> 16));
+            for (int i = 0; i < kMine; ++i) {
+                const int row = g + 2 * (i * kLanes + part);
+                s.y[k & 1][row][col] = __ushort_as_bfloat16(static_cast<unsigned short>(out[i]));
+                s.y[k & 1][row + 1][col] = __ushort_as_bfloat16(static_cast<unsigned short>(out[i] >> 16));
+            }
+        } else {
+            float d0, d1;
+            ptx::unpack2(steps, d0, d1);
+            total += d0 + d1;
         }
     };
 
-    copies_wait();
+    copies_wait<kStages - 2>();
     __syncthreads();
     lay_out(0);
     Kept keep[2];
@@ -472,12 +578,11 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
     const int blocks = (end - begin + kBlock - 1) / kBlock;
     for (int k = 0; k < blocks; ++k) {
         // block k + 1 has arrived for everybody, and nobody reads blocks and y of k - 1 any more
-        copies_wait();
+        copies_wait<kStages - 3>();
         __syncthreads();
         const int t0 = begin + k * kBlock, n = min(kBlock, end - t0);
-        if (t0 + 2 * kBlock < end)
-            fetch(t0 + 2 * kBlock);
-        if (k > 0)
+        fetch(t0 + (kStages - 1) * kBlock);
+        if (kOut && k > 0)
             write_out(k - 1);
         if (k + 1 < blocks)
             lay_out(k + 1);
@@ -506,37 +611,372 @@ __global__ void __launch_bounds__(kScanThreads, 2) selective_scan_kernel(const _
         for (; g < n; ++g) {      // the sequence's last tokens, fewer than a group
             const float xt = __bfloat162float(now.x[g][col]), d = step(now.dt[g][col]);
             float sum = me.token(d, d * xt, &now.B[g][part * kStates], &now.C[g][part * kStates]);
+            if constexpr (kOut) {
+#pragma unroll
+                for (int o = kChannels; o < 32; o <<= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (part == 0)
+                    s.y[k & 1][g][col] = output(sum, xt, kGate ? now.z[g][col] : none);
+            } else {
+                total += d;
+            }
+        }
+    }
+    if constexpr (kOut) {
+        __syncthreads();
+        write_out(blocks - 1);
+    }
+}
+
+// A few tokens [begin, end) straight from global memory.
+template <int N, bool kGate>
+__device__ __forceinline__ void sel_few(const SelParams &p, SelLane &me, int begin, int end, int ch, bool valid,
+                                        float D, float bias)
+{
+    constexpr int kChannels = 32 / (N / kStates);
+    const int part = (threadIdx.x & 31) / kChannels;
+    for (int64_t t = begin; t < end; ++t) {
+        const float x = __bfloat162float(p.x[t * p.x_stride + ch]);
+        const float v = __bfloat162float(p.dt[t * p.dt_stride + ch]) + bias;
+        const float z = kGate ? __bfloat162float(p.z[t * p.z_stride + ch]) : 0.f;
+        const float dt = p.softplus ? step_of(v) : v;
+        float sum = me.token(dt, dt * x, p.B + t * p.b_stride + part * kStates,
+                             p.C + t * p.c_stride + part * kStates);
+#pragma unroll
+        for (int o = kChannels; o < 32; o <<= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        float y = fmaf(D, x, sum);
+        if constexpr (kGate)
+            y *= silu_f32(z);
+        if (part == 0 && valid)
+            p.y[t * p.y_stride + ch] = __float2bfloat16_rn(y);
+    }
+}
+
+// A tile of channels as one of its lanes sees it.
+template <int N>
+struct SelPlace {
+    int col0, ch, part;
+    bool valid;                               // (lanes past the last channel follow one that is there)
+    int64_t at, states;                       // the lane's states in a slot, those of a slot
+
+    __device__ __forceinline__ SelPlace(const SelParams &p, int tile)
+    {
+        constexpr int kChannels = SelShared<N>::kChannels;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        part = lane / kChannels;
+        col0 = tile * SelShared<N>::kCols;
+        ch = col0 + warp * kChannels + lane % kChannels;
+        valid = ch < p.channels;
+        ch = valid ? ch : 0;
+        states = static_cast<int64_t>(p.channels) * N;
+        at = static_cast<int64_t>(ch) * N + part * kStates;
+    }
+};
+
+// The states and the steps' sum of the chunk before an end.
+template <int N>
+__global__ void __launch_bounds__(kScanThreads, kResident) selective_states_kernel(const __grid_constant__ SelParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
+    const int64_t end = blockIdx.x / p.tiles;
+    pdl_wait();
+    if (end >= p.header->ends)
+        return;
+    const SelUnit u = p.inner[end];
+    SelLane me;
+    me.load_decays(p.A + me_at.at);
+#pragma unroll
+    for (int n = 0; n < kStates; ++n)
+        me.h[n] = 0.f;
+    if (u.k == 0) {
+        const int64_t slot = seq_slot(p.s, u.seq);
+        if (slot >= 0 && p.s.has_init && p.s.has_init[u.seq]) {
+            load_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
+            // (the slot is written by the sequence's last chunk, perhaps before its first
+            // one starts)
+            if (me_at.valid)
+                store_states(p.firsts, false, end * me_at.states + me_at.at, me.h);
+        }
+    }
+    float total = 0.f;
+    sel_tokens<N, false, false>(p, *reinterpret_cast<SelShared<N> *>(smem), me, u.begin, u.end, me_at.col0, 0.f,
+                                p.dt_bias ? p.dt_bias[me_at.ch] : 0.f, total);
+    if (!me_at.valid)
+        return;
+    store_states(p.ends, false, end * me_at.states + me_at.at, me.h);
+    if (me_at.part == 0)
+        p.sums[end * p.channels + me_at.ch] = total;
+}
+
+// The tokens of a chunk, as a rule of a whole sequence.  (With the CTAs of an SM asked for:
+// without, ptxas keeps to 80 registers and orders the code for that, 560 us for two
+// prompts of 9,763 tokens instead of 430.)
+template <int N, bool kGate>
+__global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel(const __grid_constant__ SelParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
+    const int unit = blockIdx.x / p.tiles;
+    pdl_wait();
+    SelUnit u = {unit, 0, 0, 0, 0, 0, 1, 0};
+    if (p.units) {
+        if (unit >= p.header->units)
+            return;
+        u = p.units[unit];
+    } else if (!seq_rows(p.s.qsl, p.s.total_len, p.s.errors, unit, u.begin, u.end)) {
+        return;
+    }
+    SelLane me;
+    me.load_decays(p.A + me_at.at);
+    const float D = p.D ? p.D[me_at.ch] : 0.f, bias = p.dt_bias ? p.dt_bias[me_at.ch] : 0.f;
+    const int64_t slot = seq_slot(p.s, u.seq);
+#pragma unroll
+    for (int n = 0; n < kStates; ++n)
+        me.h[n] = 0.f;
+    if (u.k > 0) {
+#pragma unroll 4
+        for (int64_t e = u.ends; e < u.ends + u.k; ++e) {
+            float own[kStates];
+            load_states(p.ends, false, e * me_at.states + me_at.at, own);
+            const float sum = p.sums[e * p.channels + me_at.ch];
+#pragma unroll
+            for (int n = 0; n < kStates; ++n)
+                me.h[n] = e == u.ends ? own[n] : fmaf(ptx::ex2(sum * me.decay(n)), me.h[n], own[n]);
+        }
+    } else if (slot >= 0 && p.s.has_init && p.s.has_init[u.seq]) {
+        if (u.cut)
+            load_states(p.firsts, false, u.ends * me_at.states + me_at.at, me.h);
+        else
+            load_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
+    }
+    float total = 0.f;
+    if (u.end - u.begin > kShort)
+        sel_tokens<N, kGate, true>(p, *reinterpret_cast<SelShared<N> *>(smem), me, u.begin, u.end, me_at.col0, D,
+                                   bias, total);
+    else
+        sel_few<N, kGate>(p, me, u.begin, u.end, me_at.ch, me_at.valid, D, bias);
+    if (u.last && slot >= 0 && me_at.valid)
+        store_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
+}
+
+// Single tokens, as a rule.  A CTA takes every `groups`-th sequence for its tile of channels;
+// kAhead - 1 sequences' states and first tokens are on their way while it works on one.  A
+// lane copies its own states.  (More tokens come straight from global memory.)
+constexpr int kAhead = 4;
+constexpr int kStepResident = 8;      // CTAs of an SM
+
+template <int N>
+struct SelStep {
+    struct Stage {
+        float4 state[kStates / 4][kScanThreads];
+        __nv_bfloat16 x[SelShared<N>::kCols], dt[SelShared<N>::kCols], z[SelShared<N>::kCols], B[N], C[N];
+        int64_t slot;
+        int32_t begin, end, has, good;
+    };
+    Stage stage[kAhead];
+};
+
+template <int N, bool kGate>
+__global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_kernel(const __grid_constant__ SelParams p)
+{
+    constexpr int kCols = SelShared<N>::kCols, kChannels = SelShared<N>::kChannels;
+    __shared__ alignas(16) SelStep<N> s;
+    const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
+    const int groups = gridDim.x / p.tiles, tid = threadIdx.x;
+    const int col = (tid >> 5) * kChannels + (tid & 31) % kChannels;
+    pdl_wait();
+    struct Meta {
+        int64_t slot;
+        int32_t begin, end, has, good;
+    };
+    auto meta = [&](int b) {
+        Meta m = {-1, 0, 0, 0, 0};
+        if (b < p.s.batch && seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, m.begin, m.end)) {
+            m.slot = seq_slot(p.s, b);
+            m.has = m.slot >= 0 && p.s.has_init && p.s.has_init[b];
+            m.good = 1;
+        }
+        return m;
+    };
+    auto fetch = [&](const Meta &m, typename SelStep<N>::Stage &to) {
+        if (m.has && me_at.valid) {
+            const int64_t at = m.slot * me_at.states + me_at.at;
+            if (p.pool_bf16) {
+                copy16(&to.state[0][tid], static_cast<const __nv_bfloat16 *>(p.pool) + at, true);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kStates / 4; ++i)
+                    copy16(&to.state[i][tid], static_cast<const float *>(p.pool) + at + 4 * i, true);
+            }
+        }
+        if (m.begin < m.end) {
+            // x, dt, z, B and C of the first token, 16 bytes a thread
+            const int64_t t = m.begin;
+            constexpr int kRow = kCols / 8, kBc = N / 8;
+            static_assert(3 * kRow + 2 * kBc <= kScanThreads);
+            const int what = tid / kRow, c = tid % kRow * 8;
+            if (what < (kGate ? 3 : 2)) {
+                const bool there = me_at.col0 + c < p.channels;
+                const int from = there ? me_at.col0 + c : 0;
+                copy16(what == 0 ? &to.x[c] : what == 1 ? &to.dt[c] : &to.z[c],
+                       (what == 0 ? p.x + t * p.x_stride : what == 1 ? p.dt + t * p.dt_stride : p.z + t * p.z_stride) +
+                           from, there);
+            } else if (const int i = tid - 3 * kRow; i >= 0 && i < 2 * kBc) {
+                copy16(i < kBc ? &to.B[8 * i] : &to.C[8 * (i - kBc)],
+                       i < kBc ? p.B + t * p.b_stride + 8 * i : p.C + t * p.c_stride + 8 * (i - kBc), true);
+            }
+        }
+        if (tid == 0) {
+            to.slot = m.slot;
+            to.begin = m.begin;
+            to.end = m.end;
+            to.has = m.has;
+            to.good = m.good;
+        }
+        copies_commit();
+    };
+    SelLane me;
+    me.load_decays(p.A + me_at.at);
+    const float D = p.D ? p.D[me_at.ch] : 0.f, bias = p.dt_bias ? p.dt_bias[me_at.ch] : 0.f;
+    int b = blockIdx.x / p.tiles;
+#pragma unroll
+    for (int i = 0; i + 1 < kAhead; ++i)
+        fetch(meta(b + i * groups), s.stage[i]);
+    Meta next = meta(b + (kAhead - 1) * groups);
+    for (int i = 0; b < p.s.batch; b += groups, i = (i + 1) % kAhead) {
+        copies_wait<kAhead - 2>();
+        __syncthreads();      // also: everybody is done with the stage that is filled next
+        fetch(next, s.stage[(i + kAhead - 1) % kAhead]);
+        next = meta(b + kAhead * groups);
+        const typename SelStep<N>::Stage &now = s.stage[i];
+        if (!now.good)
+            continue;
+#pragma unroll
+        for (int n = 0; n < kStates; ++n)
+            me.h[n] = 0.f;
+        if (now.has && me_at.valid) {
+            if (p.pool_bf16) {
+                widen8(*reinterpret_cast<const uint4 *>(&now.state[0][tid]), me.h);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kStates; k += 4) {
+                    const float4 v = now.state[k / 4][tid];
+                    me.h[k] = v.x;
+                    me.h[k + 1] = v.y;
+                    me.h[k + 2] = v.z;
+                    me.h[k + 3] = v.w;
+                }
+            }
+        }
+        if (now.begin < now.end) {
+            const float x = __bfloat162float(now.x[col]), v = __bfloat162float(now.dt[col]) + bias;
+            const float dt = p.softplus ? step_of(v) : v;
+            float sum = me.token(dt, dt * x, &now.B[me_at.part * kStates], &now.C[me_at.part * kStates]);
 #pragma unroll
             for (int o = kChannels; o < 32; o <<= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (part == 0)
-                s.y[k & 1][g][col] = output(sum, xt, kGate ? now.z[g][col] : none);
+            float y = fmaf(D, x, sum);
+            if constexpr (kGate)
+                y *= silu_f32(__bfloat162float(now.z[col]));
+            if (me_at.part == 0 && me_at.valid)
+                p.y[now.begin * p.y_stride + me_at.ch] = __float2bfloat16_rn(y);
+            if (now.begin + 1 < now.end)
+                sel_few<N, kGate>(p, me, now.begin + 1, now.end, me_at.ch, me_at.valid, D, bias);
         }
+        if (now.slot >= 0 && me_at.valid)
+            store_states(p.pool, p.pool_bf16, now.slot * me_at.states + me_at.at, me.h);
     }
-    __syncthreads();
-    write_out(blocks - 1);
-    if (slot >= 0 && valid)
-        store_states(p.pool, p.pool_bf16, at, me.h);
 }
 
-template <int N, int kStates, bool kGate>
+// Ends of chunks of a call, at most: a cut sequence's chunks are no shorter than sel_chunk,
+// and its last is no end.
+int64_t sel_ends(int64_t total_len, int32_t chunk) { return total_len / chunk; }
+
+struct SelLayout {
+    size_t units, inner, ends, firsts, sums, total;
+};
+SelLayout sel_layout(int64_t total_len, int32_t batch, int32_t channels, int32_t dstate, int64_t ends)
+{
+    SelLayout L;
+    size_t off = (sizeof(SelHeader) + 255) & ~size_t{255};
+    auto take = [&](int64_t bytes) {
+        const size_t at = off;
+        off = (off + static_cast<size_t>(bytes) + 255) & ~size_t{255};
+        return at;
+    };
+    const int64_t states = static_cast<int64_t>(channels) * dstate * 4;
+    L.units = take((ends + batch) * static_cast<int64_t>(sizeof(SelUnit)));
+    L.inner = take(ends * static_cast<int64_t>(sizeof(SelUnit)));
+    L.ends = take(ends * states);
+    L.firsts = take(ends * states);
+    L.sums = take(ends * channels * 4);
+    L.total = off;
+    return L;
+}
+
+// Bytes for these sizes and all that are not larger: sel_chunk gives at most kFullWarps /
+// warps ends, with channels dstate / 256 warps at least, and none below kMinChunk.
+size_t sel_bytes(int64_t total_len, int32_t batch, int32_t channels, int32_t dstate)
+{
+    const int64_t states = static_cast<int64_t>(channels) * dstate, ends = total_len / kMinChunk;
+    const int64_t held = std::min<int64_t>(ends * states, int64_t{kFullWarps} * 32 * kStates);
+    return static_cast<size_t>(held * (4 + 4) + held / kStates * 4 +
+                               (2 * std::min<int64_t>(ends, kFullWarps) + batch) * static_cast<int64_t>(sizeof(SelUnit)) +
+                               6 * 256 + sizeof(SelHeader));
+}
+
+template <int N, bool kGate>
 cudaError_t launch(SelParams &p, cudaStream_t stream)
 {
-    using Shared = SelShared<N, kStates>;
+    using Shared = SelShared<N>;
     constexpr int kBytes = sizeof(Shared);
-    const cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<N, kStates, kGate>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (e != cudaSuccess)
-        return e;
     p.tiles = (p.channels + Shared::kCols - 1) / Shared::kCols;
-    return launch_pdl_smem(selective_scan_kernel<N, kStates, kGate>, dim3(static_cast<unsigned>(p.tiles * p.s.batch)),
-                           kScanThreads, kBytes, stream, p);
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+        return cudaErrorInvalidDevice;
+    // two tokens a sequence on average: most are alone (96 tokens of 96 sequences, 8,192
+    // channels: SEE us, in the other kernel SEE)
+    if (p.s.total_len <= 2 * static_cast<int64_t>(p.s.batch)) {
+        const int64_t groups = std::min<int64_t>(p.s.batch, (int64_t{kStepResident} * sms + p.tiles - 1) / p.tiles);
+        return launch_pdl(selective_step_kernel<N, kGate>, dim3(static_cast<unsigned>(p.tiles * groups)), kScanThreads,
+                          stream, p);
+    }
+    // A call of fewer tokens has no sequence that is cut, and of one of several sequences with
+    // warps for two thirds of the schedulers each, cutting gains 5 % at best, but the list, the
+    // idle CTAs and the other order of the rest cost more (two prompts of 9,763 tokens, 8,192
+    // channels: 473 us instead of 440).
+    const int64_t warps = (static_cast<int64_t>(p.channels) * N + 32 * kStates - 1) / (32 * kStates);
+    const bool may_cut = p.s.total_len >= p.cut && (p.s.batch == 1 || 3 * warps < 8 * sms);
+    const int64_t ends = may_cut ? sel_ends(p.s.total_len, p.chunk) : 0;
+    if (!ends)
+        p.cut = INT32_MAX;
+    const int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
+    const bool listed = ends || whole > int64_t{kResident} * sms;
+    cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<N, kGate>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (listed && e == cudaSuccess)
+        e = launch_pdl(selective_plan_kernel, dim3(1), kPlanThreads, stream, p);
+    if (ends && e == cudaSuccess) {
+        e = cudaFuncSetAttribute(selective_states_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        if (e == cudaSuccess)
+            e = launch_pdl_smem(selective_states_kernel<N>, dim3(static_cast<unsigned>(p.tiles * ends)), kScanThreads,
+                                kBytes, stream, p);
+    }
+    if (!listed)
+        p.units = nullptr;
+    if (e == cudaSuccess)
+        e = launch_pdl_smem(selective_scan_kernel<N, kGate>, dim3(static_cast<unsigned>(p.tiles * ends + whole)),
+                            kScanThreads, kBytes, stream, p);
+    return e;
 }
 
-template <int N, int kStates>
+template <int N>
 cudaError_t launch(SelParams &p, cudaStream_t stream)
 {
-    return p.z ? launch<N, kStates, true>(p, stream) : launch<N, kStates, false>(p, stream);
+    return p.z ? launch<N, true>(p, stream) : launch<N, false>(p, stream);
 }
 
 bool sel_sizes(int64_t total_len, int32_t batch, int32_t channels, int32_t dstate)
@@ -555,7 +995,9 @@ extern "C" {
 size_t ssd_selective_scan_varlen_workspace_size(int64_t total_len, int32_t batch, int32_t channels,
                                                 int32_t dstate)
 {
-    return ssd::sel_sizes(total_len, batch, channels, dstate) ? 256 : 0;
+    if (!ssd::sel_sizes(total_len, batch, channels, dstate))
+        return 0;
+    return ssd::sel_bytes(total_len, batch, channels, dstate);
 }
 
 ssd_status_t ssd_selective_scan_varlen_fwd(
@@ -612,13 +1054,22 @@ ssd_status_t ssd_selective_scan_varlen_fwd(
     p.z_stride = t.z;
     p.channels = channels;
     p.softplus = dt_softplus != 0;
-    constexpr int kStates = 8;
     p.pool_bf16 = pool_type == SSD_POOL_BF16;
+    p.chunk = sel_chunk(total_len, channels, dstate);
+    p.cut = sel_cut(total_len, channels, dstate);
+    const SelLayout L = sel_layout(total_len, batch, channels, dstate, sel_ends(total_len, p.chunk));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.header = reinterpret_cast<SelHeader *>(ws);
+    p.units = reinterpret_cast<SelUnit *>(ws + L.units);
+    p.inner = reinterpret_cast<SelUnit *>(ws + L.inner);
+    p.ends = reinterpret_cast<float *>(ws + L.ends);
+    p.firsts = reinterpret_cast<float *>(ws + L.firsts);
+    p.sums = reinterpret_cast<float *>(ws + L.sums);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dstate == 8    ? launch<8, kStates>(p, s)
-                          : dstate == 16 ? launch<16, kStates>(p, s)
-                          : dstate == 32 ? launch<32, kStates>(p, s)
-                                         : launch<64, kStates>(p, s);
+    const cudaError_t e = dstate == 8    ? launch<8>(p, s)
+                          : dstate == 16 ? launch<16>(p, s)
+                          : dstate == 32 ? launch<32>(p, s)
+                                         : launch<64>(p, s);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

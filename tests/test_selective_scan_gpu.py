@@ -133,6 +133,17 @@ def test_against_the_recurrence(lens, dstate):
     check(Ragged(LENS[lens], seed=lens), 72, dstate, seed=lens)
 
 
+# sequences that are cut into chunks: of 64 tokens, the shortest there are, or more
+@pytest.mark.parametrize("lens,channels,dstate", [
+    ([128], 8, 8), ([127], 8, 16), ([129], 40, 16), ([1000], 8, 16), ([1000, 3, 700, 1, 129, 0, 128, 127], 72, 16),
+    ([64] * 9 + [192, 0, 193], 72, 32), ([1, 500, 1, 1, 300], 24, 64), ([1500], 1024, 16), ([700, 600], 2048, 16),
+    ([2000, 1500, 40, 1900], 264, 8),
+])
+def test_chunks(lens, channels, dstate):
+    check(Ragged(lens, seed=len(lens)), channels, dstate, seed=dstate, gate=dstate != 32)
+    check(Ragged(lens, seed=len(lens) + 1, rows=sum(lens) + 70, none=(0,)), channels, dstate, bf16=True)
+
+
 @pytest.mark.parametrize("channels", [8, 56, 64, 136, 520])
 @pytest.mark.parametrize("dstate", [8, 16, 32, 64])
 def test_channels(channels, dstate):
