@@ -88,8 +88,8 @@ SSD_API ssd_status_t ssd_causal_conv_varlen_fwd(
  *   workspace    at least ssd_selective_scan_varlen_workspace_size bytes, 256-byte aligned;
  *                needs no initialisation; one call at a time per workspace
  *
- * Supported: dstate 8, 16, 32 or 64; channels a multiple of 8, at most 2^20.  States and
- * sums are fp32, y is rounded once. */
+ * Supported: dstate 8, 16, 32 or 64; channels a multiple of 8, at most 2^20; strides below
+ * 2^31.  States and sums are fp32, y is rounded once. */
 typedef enum {
     SSD_POOL_FP32 = 0,
     SSD_POOL_BF16 = 1

@@ -27,6 +27,7 @@
 // read and write the states, go to a kernel whose CTAs keep their tile's decays and have
 // the next sequences' states on their way.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_ptx.cuh"
 #include "layer_common.cuh"
@@ -68,7 +69,7 @@ struct SelParams {
                                       // one, in order); the chunk before each end
     float *ends, *sums;               // [end]: states and steps' sum of the chunk before it
     float *firsts;                    // states that a cut sequence starts from, at its first end
-    int64_t y_stride, x_stride, dt_stride, b_stride, c_stride, z_stride;
+    int32_t y_stride, x_stride, dt_stride, b_stride, c_stride, z_stride;
     int32_t channels, tiles;          // tiles of a CTA's channels
     int32_t chunk, cut;               // smallest chunk, shortest sequence that is cut
     int32_t softplus, pool_bf16;
@@ -377,17 +378,21 @@ struct SelLane {
     }
 
     // One token, B and C of the lane's states in bf16; returns the sum of C h.
-    __device__ __forceinline__ float token(float dt, float u, const __nv_bfloat16 *B, const __nv_bfloat16 *C)
+    __device__ __forceinline__ float token(float dt, float u, const uint4 &B, const uint4 &C)
     {
         float b[kStates], c[kStates], sum = 0.f;
-        load_bf16(B, b);
-        load_bf16(C, c);
+        widen8(B, b);
+        widen8(C, c);
 #pragma unroll
         for (int n = 0; n < kStates; ++n) {
             h[n] = fmaf(ptx::ex2(dt * decay(n)), h[n], u * b[n]);
             sum = fmaf(h[n], c[n], sum);
         }
         return sum;
+    }
+    __device__ __forceinline__ float token(float dt, float u, const __nv_bfloat16 *B, const __nv_bfloat16 *C)
+    {
+        return token(dt, u, *reinterpret_cast<const uint4 *>(B), *reinterpret_cast<const uint4 *>(C));
     }
 };
 
@@ -501,7 +506,7 @@ __device__ __forceinline__ void sel_tokens(const SelParams &p, SelShared<N> &s, 
             const int i = i0 + threadIdx.x, row = i / kRowLoads, c = i % kRowLoads * 8;
             if ((kBlock * kRowLoads % kScanThreads == 0 || i < kBlock * kRowLoads) && t0 + row < end &&
                 col0 + c < p.channels)
-                *reinterpret_cast<uint4 *>(p.y + (t0 + row) * p.y_stride + col0 + c) =
+                *reinterpret_cast<uint4 *>(p.y + static_cast<int64_t>(t0 + row) * p.y_stride + col0 + c) =
                     *reinterpret_cast<const uint4 *>(&s.y[k & 1][row][c]);
         }
     };
@@ -658,7 +663,8 @@ template <int N>
 struct SelPlace {
     int col0, ch, part;
     bool valid;                               // (lanes past the last channel follow one that is there)
-    int64_t at, states;                       // the lane's states in a slot, those of a slot
+    int64_t at;                               // the lane's states in a slot
+    int64_t states;                           // those of a slot
 
     __device__ __forceinline__ SelPlace(const SelParams &p, int tile)
     {
@@ -669,7 +675,7 @@ struct SelPlace {
         ch = col0 + warp * kChannels + lane % kChannels;
         valid = ch < p.channels;
         ch = valid ? ch : 0;
-        states = static_cast<int64_t>(p.channels) * N;
+        states = static_cast<uint32_t>(p.channels) * N;
         at = static_cast<int64_t>(ch) * N + part * kStates;
     }
 };
@@ -761,132 +767,154 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel
         store_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
 }
 
-// Single tokens, as a rule.  A CTA takes every `groups`-th sequence for its tile of channels;
-// kAhead - 1 sequences' states and first tokens are on their way while it works on one.  A
-// lane copies its own states.  (More tokens come straight from global memory.)
-constexpr int kAhead = 4;
-constexpr int kStepResident = 8;      // CTAs of an SM
+// Single tokens, as a rule.  A CTA takes every `groups`-th sequence for its tile of channels
+// and looks kScanThreads of them up at once; its warps are on their own otherwise, each with
+// the states and first tokens of two sequences in registers, one on its way while it works
+// on the other.  (A sequence's further tokens come when they are due.)
+constexpr int kStepResident = 6;      // CTAs of an SM
+constexpr int kAhead = 2;             // sequences that a warp holds
 
-template <int N>
-struct SelStep {
-    struct Stage {
-        float4 state[kStates / 4][kScanThreads];
-        __nv_bfloat16 x[SelShared<N>::kCols], dt[SelShared<N>::kCols], z[SelShared<N>::kCols], B[N], C[N];
-        int64_t slot;
-        int32_t begin, end, has, good;
-    };
-    Stage stage[kAhead];
+struct alignas(16) SelSequence {
+    uint32_t slot;                    // or SSD_NO_SLOT
+    int32_t begin, tokens;            // (tokens < 0: its offsets are none)
+    int32_t has;                      // an initial state
 };
 
-template <int N, bool kGate>
+template <int N, bool kGate, bool kBf16>
 __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_kernel(const __grid_constant__ SelParams p)
 {
-    constexpr int kCols = SelShared<N>::kCols, kChannels = SelShared<N>::kChannels;
-    __shared__ alignas(16) SelStep<N> s;
+    constexpr int kChannels = SelShared<N>::kChannels;
+    __shared__ SelSequence s_seq[kScanThreads];
     const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
     const int groups = gridDim.x / p.tiles, tid = threadIdx.x;
-    const int col = (tid >> 5) * kChannels + (tid & 31) % kChannels;
     pdl_wait();
-    struct Meta {
-        int64_t slot;
-        int32_t begin, end, has, good;
+    struct Token {
+        uint4 B, C;
+        __nv_bfloat16 x, dt, z;
     };
-    auto meta = [&](int b) {
-        Meta m = {-1, 0, 0, 0, 0};
-        if (b < p.s.batch && seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, m.begin, m.end)) {
-            m.slot = seq_slot(p.s, b);
-            m.has = m.slot >= 0 && p.s.has_init && p.s.has_init[b];
-            m.good = 1;
-        }
-        return m;
+    const __nv_bfloat16 none = __float2bfloat16_rn(0.f);
+    auto load_token = [&](int64_t t) {
+        Token v;
+        v.x = p.x[t * p.x_stride + me_at.ch];
+        v.dt = p.dt[t * p.dt_stride + me_at.ch];
+        v.z = kGate ? p.z[t * p.z_stride + me_at.ch] : none;
+        v.B = *reinterpret_cast<const uint4 *>(p.B + t * p.b_stride + me_at.part * kStates);
+        v.C = *reinterpret_cast<const uint4 *>(p.C + t * p.c_stride + me_at.part * kStates);
+        return v;
     };
-    auto fetch = [&](const Meta &m, typename SelStep<N>::Stage &to) {
-        if (m.has && me_at.valid) {
-            const int64_t at = m.slot * me_at.states + me_at.at;
-            if (p.pool_bf16) {
-                copy16(&to.state[0][tid], static_cast<const __nv_bfloat16 *>(p.pool) + at, true);
-            } else {
+    constexpr int kLoads = kBf16 ? 1 : 2;     // of 16 bytes, of a lane's states
+    using Element = std::conditional_t<kBf16, __nv_bfloat16, float>;
+    Element *pool = static_cast<Element *>(p.pool) + me_at.at;
+    struct Item {
+        SelSequence q;
+        uint4 state[kLoads];
+        Token token;
+    };
+    auto load = [&](Item &it, int i, int count) {
+        it.q = i < count ? s_seq[i] : SelSequence{SSD_NO_SLOT, 0, -1, 0};
 #pragma unroll
-                for (int i = 0; i < kStates / 4; ++i)
-                    copy16(&to.state[i][tid], static_cast<const float *>(p.pool) + at + 4 * i, true);
-            }
-        }
-        if (m.begin < m.end) {
-            // x, dt, z, B and C of the first token, 16 bytes a thread
-            const int64_t t = m.begin;
-            constexpr int kRow = kCols / 8, kBc = N / 8;
-            static_assert(3 * kRow + 2 * kBc <= kScanThreads);
-            const int what = tid / kRow, c = tid % kRow * 8;
-            if (what < (kGate ? 3 : 2)) {
-                const bool there = me_at.col0 + c < p.channels;
-                const int from = there ? me_at.col0 + c : 0;
-                copy16(what == 0 ? &to.x[c] : what == 1 ? &to.dt[c] : &to.z[c],
-                       (what == 0 ? p.x + t * p.x_stride : what == 1 ? p.dt + t * p.dt_stride : p.z + t * p.z_stride) +
-                           from, there);
-            } else if (const int i = tid - 3 * kRow; i >= 0 && i < 2 * kBc) {
-                copy16(i < kBc ? &to.B[8 * i] : &to.C[8 * (i - kBc)],
-                       i < kBc ? p.B + t * p.b_stride + 8 * i : p.C + t * p.c_stride + 8 * (i - kBc), true);
-            }
-        }
-        if (tid == 0) {
-            to.slot = m.slot;
-            to.begin = m.begin;
-            to.end = m.end;
-            to.has = m.has;
-            to.good = m.good;
-        }
-        copies_commit();
+        for (int k = 0; k < kLoads; ++k)
+            it.state[k] = it.q.has ? reinterpret_cast<const uint4 *>(pool + it.q.slot * me_at.states)[k]
+                                   : make_uint4(0, 0, 0, 0);
+        if (it.q.tokens > 0)
+            it.token = load_token(it.q.begin);
     };
-    SelLane me;
-    me.load_decays(p.A + me_at.at);
+    uint64_t a[kStates / 2];                  // A log2(e), two states each
+#pragma unroll
+    for (int k = 0; k < kStates / 4; ++k) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + me_at.at) + k);
+        a[2 * k] = ptx::pack2(v.x * kLog2e, v.y * kLog2e);
+        a[2 * k + 1] = ptx::pack2(v.z * kLog2e, v.w * kLog2e);
+    }
     const float D = p.D ? p.D[me_at.ch] : 0.f, bias = p.dt_bias ? p.dt_bias[me_at.ch] : 0.f;
-    int b = blockIdx.x / p.tiles;
+    uint64_t h[kStates / 2];
+    auto step = [&](const Token &v, int64_t t) {
+        const float x = __bfloat162float(v.x), raw = __bfloat162float(v.dt) + bias;
+        const float dt = p.softplus ? step_of(raw) : raw, u = dt * x;
+        const uint64_t dt2 = ptx::pack2(dt, dt), u2 = ptx::pack2(u, u);
+        const uint32_t B[4] = {v.B.x, v.B.y, v.B.z, v.B.w}, C[4] = {v.C.x, v.C.y, v.C.z, v.C.w};
+        uint64_t sum2 = 0;
 #pragma unroll
-    for (int i = 0; i + 1 < kAhead; ++i)
-        fetch(meta(b + i * groups), s.stage[i]);
-    Meta next = meta(b + (kAhead - 1) * groups);
-    for (int i = 0; b < p.s.batch; b += groups, i = (i + 1) % kAhead) {
-        copies_wait<kAhead - 2>();
-        __syncthreads();      // also: everybody is done with the stage that is filled next
-        fetch(next, s.stage[(i + kAhead - 1) % kAhead]);
-        next = meta(b + kAhead * groups);
-        const typename SelStep<N>::Stage &now = s.stage[i];
-        if (!now.good)
-            continue;
+        for (int k = 0; k < kStates / 2; ++k) {
+            float e0, e1;
+            ptx::unpack2(ptx::mul2(dt2, a[k]), e0, e1);
+            const uint64_t b = ptx::pack2(__uint_as_float(B[k] << 16), __uint_as_float(B[k] & 0xffff0000u));
+            const uint64_t c = ptx::pack2(__uint_as_float(C[k] << 16), __uint_as_float(C[k] & 0xffff0000u));
+            h[k] = ptx::fma2(ptx::pack2(ptx::ex2(e0), ptx::ex2(e1)), h[k], ptx::mul2(u2, b));
+            sum2 = ptx::fma2(h[k], c, sum2);
+        }
+        float sum, other;
+        ptx::unpack2(sum2, sum, other);
+        sum += other;
 #pragma unroll
-        for (int n = 0; n < kStates; ++n)
-            me.h[n] = 0.f;
-        if (now.has && me_at.valid) {
-            if (p.pool_bf16) {
-                widen8(*reinterpret_cast<const uint4 *>(&now.state[0][tid]), me.h);
-            } else {
+        for (int o = kChannels; o < 32; o <<= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        float y = fmaf(D, x, sum);
+        if constexpr (kGate)
+            y *= silu_f32(__bfloat162float(v.z));
+        if (me_at.part == 0 && me_at.valid)
+            p.y[t * p.y_stride + me_at.ch] = __float2bfloat16_rn(y);
+    };
+    auto work = [&](const Item &it) {
+        if (it.q.tokens < 0)
+            return;
+        if constexpr (kBf16) {
+            const uint32_t w[4] = {it.state[0].x, it.state[0].y, it.state[0].z, it.state[0].w};
 #pragma unroll
-                for (int k = 0; k < kStates; k += 4) {
-                    const float4 v = now.state[k / 4][tid];
-                    me.h[k] = v.x;
-                    me.h[k + 1] = v.y;
-                    me.h[k + 2] = v.z;
-                    me.h[k + 3] = v.w;
-                }
+            for (int k = 0; k < 4; ++k)
+                h[k] = ptx::pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+        } else {
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                h[2 * k] = ptx::pack2(__uint_as_float(it.state[k].x), __uint_as_float(it.state[k].y));
+                h[2 * k + 1] = ptx::pack2(__uint_as_float(it.state[k].z), __uint_as_float(it.state[k].w));
             }
         }
-        if (now.begin < now.end) {
-            const float x = __bfloat162float(now.x[col]), v = __bfloat162float(now.dt[col]) + bias;
-            const float dt = p.softplus ? step_of(v) : v;
-            float sum = me.token(dt, dt * x, &now.B[me_at.part * kStates], &now.C[me_at.part * kStates]);
-#pragma unroll
-            for (int o = kChannels; o < 32; o <<= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            float y = fmaf(D, x, sum);
-            if constexpr (kGate)
-                y *= silu_f32(__bfloat162float(now.z[col]));
-            if (me_at.part == 0 && me_at.valid)
-                p.y[now.begin * p.y_stride + me_at.ch] = __float2bfloat16_rn(y);
-            if (now.begin + 1 < now.end)
-                sel_few<N, kGate>(p, me, now.begin + 1, now.end, me_at.ch, me_at.valid, D, bias);
+        if (it.q.tokens > 0) {
+            step(it.token, it.q.begin);
+            for (int i = 1; i < it.q.tokens; ++i)
+                step(load_token(it.q.begin + i), it.q.begin + i);
         }
-        if (now.slot >= 0 && me_at.valid)
-            store_states(p.pool, p.pool_bf16, now.slot * me_at.states + me_at.at, me.h);
+        if (it.q.slot == SSD_NO_SLOT || !me_at.valid)
+            return;
+        float v[kStates];
+#pragma unroll
+        for (int k = 0; k < kStates / 2; ++k)
+            ptx::unpack2(h[k], v[2 * k], v[2 * k + 1]);
+        Element *to = pool + it.q.slot * me_at.states;
+        if constexpr (kBf16) {
+            *reinterpret_cast<uint4 *>(to) = round8(v);
+        } else {
+            reinterpret_cast<float4 *>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    };
+    for (int b0 = blockIdx.x / p.tiles; b0 < p.s.batch; b0 += kScanThreads * groups) {
+        __syncthreads();      // everybody is done with the sequences before
+        const int count = min(kScanThreads, (p.s.batch - b0 + groups - 1) / groups);
+        if (tid < count) {
+            const int b = b0 + tid * groups;
+            int32_t begin, end;
+            SelSequence q = {SSD_NO_SLOT, 0, -1, 0};
+            if (seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, begin, end)) {
+                q.slot = static_cast<uint32_t>(seq_slot(p.s, b));
+                q.begin = begin;
+                q.tokens = end - begin;
+                q.has = q.slot != SSD_NO_SLOT && p.s.has_init && p.s.has_init[b];
+            }
+            s_seq[tid] = q;
+        }
+        __syncthreads();
+        Item item[kAhead];
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k)
+            load(item[k], k, count);
+        for (int i = 0; i < count; i += kAhead)
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                load(item[(k + kAhead - 1) % kAhead], i + k + kAhead - 1, count);
+                work(item[k]);
+            }
     }
 }
 
@@ -937,12 +965,12 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     if (cudaGetDevice(&device) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
         return cudaErrorInvalidDevice;
-    // two tokens a sequence on average: most are alone (96 tokens of 96 sequences, 8,192
-    // channels: SEE us, in the other kernel SEE)
+    // Two tokens a sequence on average: most are alone (96 tokens of 96 sequences, 8,192
+    // channels: 22 us, in the other kernel 48).  No more CTAs than are resident at once.
     if (p.s.total_len <= 2 * static_cast<int64_t>(p.s.batch)) {
-        const int64_t groups = std::min<int64_t>(p.s.batch, (int64_t{kStepResident} * sms + p.tiles - 1) / p.tiles);
-        return launch_pdl(selective_step_kernel<N, kGate>, dim3(static_cast<unsigned>(p.tiles * groups)), kScanThreads,
-                          stream, p);
+        const int64_t groups = std::min<int64_t>(p.s.batch, std::max(1, kStepResident * sms / p.tiles));
+        return launch_pdl(p.pool_bf16 ? selective_step_kernel<N, kGate, true> : selective_step_kernel<N, kGate, false>,
+                          dim3(static_cast<unsigned>(p.tiles * groups)), kScanThreads, stream, p);
     }
     // A call of fewer tokens has no sequence that is cut, and of one of several sequences with
     // warps for two thirds of the schedulers each, cutting gains 5 % at best, but the list, the
@@ -1025,6 +1053,8 @@ ssd_status_t ssd_selective_scan_varlen_fwd(
     if (!kv_pitch(&t.y, channels) || !kv_pitch(&t.x, channels) || !kv_pitch(&t.dt, channels) ||
         !kv_pitch(&t.z, channels) || !kv_pitch(&t.B, dstate) || !kv_pitch(&t.C, dstate))
         return SSD_ERR_INVALID_ARG;
+    if (std::max({t.y, t.x, t.dt, t.z, t.B, t.C}) > INT32_MAX)
+        return SSD_ERR_UNSUPPORTED;
     if (batch == 0)
         return SSD_OK;
     if (!A || (total_len > 0 && (!y || !x || !dt || !B || !C)) || (max_slots > 0 && !ssm_pool))
@@ -1046,12 +1076,12 @@ ssd_status_t ssd_selective_scan_varlen_fwd(
     p.D = D;
     p.dt_bias = dt_bias;
     p.pool = ssm_pool;
-    p.y_stride = t.y;
-    p.x_stride = t.x;
-    p.dt_stride = t.dt;
-    p.b_stride = t.B;
-    p.c_stride = t.C;
-    p.z_stride = t.z;
+    p.y_stride = static_cast<int32_t>(t.y);
+    p.x_stride = static_cast<int32_t>(t.x);
+    p.dt_stride = static_cast<int32_t>(t.dt);
+    p.b_stride = static_cast<int32_t>(t.B);
+    p.c_stride = static_cast<int32_t>(t.C);
+    p.z_stride = static_cast<int32_t>(t.z);
     p.channels = channels;
     p.softplus = dt_softplus != 0;
     p.pool_bf16 = pool_type == SSD_POOL_BF16;

@@ -112,9 +112,11 @@ def _ptr(t, what: str, dtype, shape, device: int):
 
 
 def _rows(t, what: str, dtype, shape, device: int):
-    """Pointer and row pitch (elements) of a token-major tensor whose rows are
-    contiguous and do not overlap (an expanded tensor's do: its pitch of 0 would say
-    "contiguous" in the C ABI)."""
+    """Pointer and row pitch (elements; 0: contiguous) of a token-major tensor whose rows
+    are contiguous and do not overlap (an expanded tensor's do: its pitch of 0 would
+    say "contiguous" in the C ABI)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr(), 0
     if t.dtype is not dtype:
         raise ValueError(f"{what} must have dtype {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -128,7 +130,7 @@ def _rows(t, what: str, dtype, shape, device: int):
             raise ValueError(f"{what}: each token's row must be contiguous")
         row *= shape[d]
     if shape[0] <= 1:
-        return t.data_ptr(), row
+        return t.data_ptr(), 0
     if stride[0] < row:
         raise ValueError(f"{what}: tokens' rows must not overlap (an expanded tensor has to be "
                          "made contiguous)")
@@ -138,7 +140,7 @@ def _rows(t, what: str, dtype, shape, device: int):
 def _errors(f, errors, device: int):
     if errors is None:
         return None
-    if errors.numel() < 1 or errors.dtype not in (f.i32, f.u32):
+    if (errors.dtype is not f.i32 and errors.dtype is not f.u32) or errors.numel() < 1:
         raise ValueError("errors must be an int32 or uint32 tensor of one element")
     if errors.get_device() != device:
         raise ValueError(f"errors must be on device {device}, got {errors.device}")
@@ -159,6 +161,35 @@ def _slots(f, query_start_loc, has_initial_state, cache_indices, device: int):
                  (batch,), device)), batch
 
 
+def _slots_fast(f, query_start_loc, has_initial_state, cache_indices, errors, device: int):
+    """Pointers of the batch, its slots and the errors, and the batch size; None where
+    anything is not as it should be (_slots and _errors say what).  One pass of cheap
+    tests: a step's calls are short."""
+    shape, dtype = query_start_loc.shape, cache_indices.dtype
+    if (len(shape) != 1 or shape[0] < 1 or query_start_loc.dtype is not f.i32
+            or query_start_loc.get_device() != device or not query_start_loc.is_contiguous()
+            or cache_indices.shape != (shape[0] - 1,) or (dtype is not f.i32 and dtype is not f.u32)
+            or cache_indices.get_device() != device or not cache_indices.is_contiguous()):
+        return None, 0
+    batch, has, pe = shape[0] - 1, None, None
+    if has_initial_state is not None:
+        dtype = has_initial_state.dtype
+        if (has_initial_state.shape != (batch,) or (dtype is not f.bool and dtype is not f.u8)
+                or has_initial_state.get_device() != device or not has_initial_state.is_contiguous()):
+            return None, 0
+        has = has_initial_state.data_ptr()
+    if errors is not None:
+        dtype = errors.dtype
+        if (dtype is not f.i32 and dtype is not f.u32) or errors.get_device() != device or errors.numel() < 1:
+            return None, 0
+        pe = errors.data_ptr()
+    return (query_start_loc.data_ptr(), has, cache_indices.data_ptr(), pe), batch
+
+
+def _vector(f, t, n: int, device: int) -> bool:
+    return t.dtype is f.f32 and t.shape == (n,) and t.get_device() == device and t.is_contiguous()
+
+
 def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, has_initial_state,
                                cache_indices, *, silu: bool = True, errors=None, stream=None) -> None:
     """The short causal convolution of every channel, for prompts and single tokens,
@@ -172,10 +203,26 @@ def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, h
     slot); silu: y is silu of the sum.  errors: an int32 tensor of one element that
     collects the SSD_DEVERR_* flags, or None."""
     f = _functions()
+    shape, wshape, bf16, f32 = x.shape, weight.shape, f.bf16, f.f32
+    device = x.get_device()
+    if len(shape) == 2 and len(wshape) == 2 and device >= 0:
+        total, channels = shape
+        width, max_slots = wshape[1], conv_pool.shape[0]
+        where, batch = _slots_fast(f, query_start_loc, has_initial_state, cache_indices, errors, device)
+        if (where is not None and x.dtype is bf16 and y.dtype is bf16 and y.shape == shape
+                and y.get_device() == device and x.is_contiguous() and y.is_contiguous()
+                and weight.dtype is f32 and wshape[0] == channels and weight.get_device() == device
+                and weight.is_contiguous() and conv_pool.dtype is bf16
+                and conv_pool.shape == (max_slots, width - 1, channels)
+                and conv_pool.get_device() == device and conv_pool.is_contiguous()
+                and (bias is None or _vector(f, bias, channels, device))):
+            return _call(f, f.conv, "ssd_causal_conv_varlen_fwd", device, stream, y.data_ptr(), x.data_ptr(),
+                         weight.data_ptr(), None if bias is None else bias.data_ptr(), conv_pool.data_ptr(),
+                         *where[:3], total, batch, channels, width, max_slots, 0, 0, bool(silu), where[3])
+    # rows with a pitch of their own, or something is wrong
     device = _device(x, "x")
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must have shape (rows, channels) and weight (channels, width)")
-    shape = x.shape
     total, channels = shape
     width = weight.shape[1]
     slots, batch = _slots(f, query_start_loc, has_initial_state, cache_indices, device)
@@ -217,14 +264,41 @@ def ssd_selective_scan_varlen_fwd(y, x, dt, A, B, C, D, z, dt_bias, ssm_pool, qu
     ssd_causal_conv_varlen_fwd; workspace: a uint8 tensor of at least
     ssd_selective_scan_varlen_workspace_size bytes (alloc_selective_scan_workspace)."""
     f = _functions()
+    if workspace is None:
+        raise ValueError("workspace is required (see alloc_selective_scan_workspace)")
+    shape, ashape, bf16, f32 = x.shape, A.shape, f.bf16, f.f32
+    device = x.get_device()
+    if len(shape) == 2 and len(ashape) == 2 and device >= 0:
+        total, channels = shape
+        dstate, max_slots, kind = ashape[1], ssm_pool.shape[0], ssm_pool.dtype
+        bc = (total, dstate)
+        where, batch = _slots_fast(f, query_start_loc, has_initial_state, cache_indices, errors, device)
+        if (where is not None and x.dtype is bf16 and y.dtype is bf16 and dt.dtype is bf16 and B.dtype is bf16
+                and C.dtype is bf16 and A.dtype is f32 and y.shape == shape and dt.shape == shape
+                and B.shape == bc and C.shape == bc and ashape[0] == channels
+                and y.get_device() == device and dt.get_device() == device and A.get_device() == device
+                and B.get_device() == device and C.get_device() == device
+                and x.is_contiguous() and y.is_contiguous() and dt.is_contiguous() and A.is_contiguous()
+                and B.is_contiguous() and C.is_contiguous()
+                and (z is None or (z.dtype is bf16 and z.shape == shape and z.get_device() == device
+                                   and z.is_contiguous()))
+                and (D is None or _vector(f, D, channels, device))
+                and (dt_bias is None or _vector(f, dt_bias, channels, device))
+                and (kind is f32 or kind is bf16) and ssm_pool.shape == (max_slots, channels, dstate)
+                and ssm_pool.get_device() == device and ssm_pool.is_contiguous()
+                and workspace.dtype is f.u8 and workspace.get_device() == device and workspace.is_contiguous()):
+            return _call(f, f.scan, "ssd_selective_scan_varlen_fwd", device, stream, y.data_ptr(), x.data_ptr(),
+                         dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+                         None if D is None else D.data_ptr(), None if z is None else z.data_ptr(),
+                         None if dt_bias is None else dt_bias.data_ptr(), ssm_pool.data_ptr(), *where[:3], total,
+                         batch, channels, dstate, max_slots, kind is bf16, bool(dt_softplus), None,
+                         workspace.data_ptr(), workspace.numel(), where[3])
+    # rows with a pitch of their own, or something is wrong
     device = _device(x, "x")
     if x.dim() != 2 or A.dim() != 2:
         raise ValueError("x must have shape (rows, channels) and A (channels, dstate)")
-    shape = x.shape
     total, channels = shape
     dstate = A.shape[1]
-    if workspace is None:
-        raise ValueError("workspace is required (see alloc_selective_scan_workspace)")
     slots, batch = _slots(f, query_start_loc, has_initial_state, cache_indices, device)
     py, sy = _rows(y, "y", f.bf16, shape, device)
     px, sx = _rows(x, "x", f.bf16, shape, device)
@@ -232,14 +306,13 @@ def ssd_selective_scan_varlen_fwd(y, x, dt, A, B, C, D, z, dt_bias, ssm_pool, qu
     pb, sb = _rows(B, "B", f.bf16, (total, dstate), device)
     pc, sc = _rows(C, "C", f.bf16, (total, dstate), device)
     pz, sz = (None, 0) if z is None else _rows(z, "z", f.bf16, shape, device)
-    bf16 = ssm_pool.dtype is f.bf16
-    max_slots = ssm_pool.shape[0]
+    max_slots, narrow = ssm_pool.shape[0], ssm_pool.dtype is f.bf16
     _call(f, f.scan, "ssd_selective_scan_varlen_fwd", device, stream, py, px, pd,
           _ptr(A, "A", f.f32, (channels, dstate), device), pb, pc,
           None if D is None else _ptr(D, "D", f.f32, (channels,), device), pz,
           None if dt_bias is None else _ptr(dt_bias, "dt_bias", f.f32, (channels,), device),
-          _ptr(ssm_pool, "ssm_pool", f.bf16 if bf16 else f.f32, (max_slots, channels, dstate), device),
-          *slots, total, batch, channels, dstate, max_slots, bf16, bool(dt_softplus),
+          _ptr(ssm_pool, "ssm_pool", f.bf16 if narrow else f.f32, (max_slots, channels, dstate), device),
+          *slots, total, batch, channels, dstate, max_slots, narrow, bool(dt_softplus),
           ctypes.byref(SelectiveStrides(sy, sx, sd, sb, sc, sz)),
           _ptr(workspace, "workspace", f.u8, (workspace.numel(),), device), workspace.numel(),
           _errors(f, errors, device))

@@ -210,7 +210,7 @@ def _scan(lib, **over):
     (dict(strides=dict(x=56)), 1), (dict(strides=dict(y=68)), 1), (dict(strides=dict(dt=65)), 1),
     (dict(strides=dict(B=8)), 1), (dict(strides=dict(C=20)), 1), (dict(strides=dict(z=-64)), 1),
     (dict(channels=60), 2), (dict(channels=(1 << 20) + 8), 2), (dict(dstate=4), 2), (dict(dstate=24), 2),
-    (dict(dstate=128), 2), (dict(total=1 << 31), 2), (dict(batch=(1 << 31) - 1), 2),
+    (dict(dstate=128), 2), (dict(strides=dict(dt=1 << 31)), 2), (dict(total=1 << 31), 2), (dict(batch=(1 << 31) - 1), 2),
     (dict(ws=None), 3), (dict(ws=A + 16), 3), (dict(wsb=16), 3),
     (dict(batch=0), 0), (dict(batch=0, strides=None, ws=None), 0),
 ])
