@@ -70,6 +70,14 @@ __device__ __forceinline__ int warp_last_start(const int32_t *qsl, int batch, in
     return lo;
 }
 
+// 1 / x, flushing results below 2^-126 to zero.
+__device__ __forceinline__ float rcp_f32(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // v / (1 + e^-v).  (e^-v may overflow: v / infinity is the right zero.)
 __device__ __forceinline__ float silu_f32(float v)
 {

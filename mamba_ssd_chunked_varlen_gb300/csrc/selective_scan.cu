@@ -200,13 +200,6 @@ __device__ __forceinline__ float step_of(float v)
     return fmaf(p, e, fmaxf(v, 0.f));
 }
 
-__device__ __forceinline__ float rcp(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // What two tokens' steps and outputs need, each value twice.
 struct Pairwise {
     uint64_t terms[9], log2e, bias, D;
@@ -249,7 +242,7 @@ struct Pairwise {
             float t0, t1, q0, q1;
             ptx::unpack2(ptx::mul2(ptx::pack2(z0, z1), log2e), t0, t1);
             ptx::unpack2(ptx::add2(ptx::pack2(ptx::ex2(-t0), ptx::ex2(-t1)), ptx::pack2(1.f, 1.f)), q0, q1);
-            v = ptx::mul2(ptx::mul2(v, ptx::pack2(z0, z1)), ptx::pack2(rcp(q0), rcp(q1)));
+            v = ptx::mul2(ptx::mul2(v, ptx::pack2(z0, z1)), ptx::pack2(rcp_f32(q0), rcp_f32(q1)));
         }
         float v0, v1;
         ptx::unpack2(v, v0, v1);
