@@ -11,9 +11,12 @@
 //
 // A warp takes a token: each lane two angles, which go through shared memory to the
 // lanes that need them and serve all heads.  A row is head_dim / 8 lanes of eight
-// elements, as in kv_cache.cu; a half's partner comes from another lane by shuffles.
+// elements, as in kv_cache.cu; a half's partner comes from another lane by shuffles.  Rows go
+// in steps of one tensor, so that only those that become codes are looked through for
+// their largest, and a step's loads are on their way while the one before is worked on.
 #include <cmath>
 
+#include "attn_ptx.cuh"
 #include "layer_common.cuh"
 
 namespace ssd {
@@ -29,7 +32,8 @@ struct RopeParams {
     const __nv_bfloat16 *q, *k, *v;
     const uint64_t *turns;
     int64_t q_out_stride, q_stride, k_out_stride, k_stride, v_stride;
-    int32_t heads, rows, part_rows;   // query heads; rows of a token, of them in one part
+    int32_t heads;                    // query heads
+    int32_t steps, part_steps;        // steps of a token, of them in one part
     int32_t part, half;               // rotated elements of a head, and half of them
     float magnitude;
 };
@@ -55,7 +59,7 @@ __device__ __forceinline__ int64_t position_of(const RopeParams &p, int b, int64
 template <bool kNeighbours>
 struct LaneTurns {
     static constexpr int kPairs = kNeighbours ? 4 : 8;
-    float cos[kPairs], sin[kPairs];
+    uint64_t cos[kPairs / 2], sin[kPairs / 2];
 
     // halves: the lower element's sine with its sign, a' = a cos - b sin
     __device__ __forceinline__ void load(const float2 *turn, int col, int half)
@@ -65,31 +69,42 @@ struct LaneTurns {
 #pragma unroll
         for (int i = 0; i < kPairs; i += 2) {
             const float4 two = *reinterpret_cast<const float4 *>(turn + at + i);
-            cos[i] = two.x;
-            sin[i] = sign * two.y;
-            cos[i + 1] = two.z;
-            sin[i + 1] = sign * two.w;
+            cos[i / 2] = ptx::pack2(two.x, two.z);
+            sin[i / 2] = ptx::pack2(sign * two.y, sign * two.w);
         }
     }
 
-    __device__ __forceinline__ void rotate(float (&x)[8], const float (&partner)[8]) const
+    // eight elements as pairs, and in the other layout those of the lane's partner
+    __device__ __forceinline__ void rotate(uint64_t (&x)[4], const uint64_t (&partner)[4]) const
     {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
+        for (int i = 0; i < 4; ++i) {
             if constexpr (kNeighbours) {
-                const float a = x[i], b = x[i + 1];
-                x[i] = a * cos[i / 2] - b * sin[i / 2];
-                x[i + 1] = b * cos[i / 2] + a * sin[i / 2];
+                float a, b, c0, c1, s0, s1;
+                ptx::unpack2(x[i], a, b);
+                ptx::unpack2(cos[i / 2], c0, c1);
+                ptx::unpack2(sin[i / 2], s0, s1);
+                const float c = i & 1 ? c1 : c0, s = i & 1 ? s1 : s0;
+                x[i] = ptx::pack2(a * c - b * s, b * c + a * s);
             } else {
-                x[i] = x[i] * cos[i] + partner[i] * sin[i];
-                x[i + 1] = x[i + 1] * cos[i + 1] + partner[i + 1] * sin[i + 1];
+                x[i] = ptx::fma2(x[i], cos[i], ptx::mul2(partner[i], sin[i]));
             }
         }
     }
 };
 
+__device__ __forceinline__ void widen_pairs(const uint4 &r, uint64_t (&x)[4])
+{
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = ptx::pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
+enum RopeTensor { kQ, kK, kV };
+
 template <int kType, int kDim, bool kNeighbours>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kRopeWarps * 32, 3) rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kLanes = kDim / 8;           // lanes of a row
     constexpr int kAtOnce = 32 / kLanes;       // rows of the warp's one load
@@ -106,21 +121,34 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
     if (t >= p.c.total_len)
         return;
     const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-    const int first = blockIdx.y * p.part_rows, last = min(first + p.part_rows, p.rows);
-    const int q_rows = p.heads, k_rows = q_rows + p.c.heads;   // rows of q, then of k, then of v
-    auto load = [&](int r) {
-        if (r >= last)
-            return make_uint4(0, 0, 0, 0);
-        const __nv_bfloat16 *src = r < q_rows   ? p.q + t * p.q_stride + static_cast<int64_t>(r) * kDim
-                                   : r < k_rows ? p.k + t * p.k_stride + static_cast<int64_t>(r - q_rows) * kDim
-                                                : p.v + t * p.v_stride + static_cast<int64_t>(r - k_rows) * kDim;
-        return *reinterpret_cast<const uint4 *>(src + col);
+    const int first = blockIdx.y * p.part_steps, last = min(first + p.part_steps, p.steps);
+    const int q_steps = (p.heads + kStep - 1) / kStep, k_steps = (p.c.heads + kStep - 1) / kStep;
+    const __nv_bfloat16 *q = p.q + t * p.q_stride + col, *k = p.k + t * p.k_stride + col;
+    const __nv_bfloat16 *v = p.v + t * p.v_stride + col;
+    // a step's tensor, its first row there, and the rows of the tensor
+    struct Step {
+        RopeTensor tensor;
+        int row, rows;
+    };
+    auto step_of = [&](int i) {
+        return i < q_steps             ? Step{kQ, i * kStep, p.heads}
+               : i < q_steps + k_steps ? Step{kK, (i - q_steps) * kStep, p.c.heads}
+                                       : Step{kV, (i - q_steps - k_steps) * kStep, p.c.heads};
+    };
+    auto load = [&](uint4 (&raw)[kRopeAhead], int at) {
+        const Step s = step_of(at);
+        const __nv_bfloat16 *src = s.tensor == kQ ? q : s.tensor == kK ? k : v;
+#pragma unroll
+        for (int i = 0; i < kRopeAhead; ++i) {
+            const int r = s.row + i * kAtOnce + sub;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (at < last && r < s.rows)
+                raw[i] = *reinterpret_cast<const uint4 *>(src + r * kDim);
+        }
     };
     // the rows do not depend on their position: the first ones are on their way
-    uint4 raw[kRopeAhead];
-#pragma unroll
-    for (int i = 0; i < kRopeAhead; ++i)
-        raw[i] = load(first + i * kAtOnce + sub);
+    uint4 raw[kRopeAhead], next[kRopeAhead];
+    load(raw, first);
 
     const int b = warp_last_start(p.c.qsl, p.c.batch, t);
     const int64_t pos = position_of<kType>(p, b, t);
@@ -134,75 +162,109 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
         sincospif(static_cast<float>(angle) * 0x1p-31f, &sin, &cos);
         s_turn[warp][i] = make_float2(cos * p.magnitude, sin * p.magnitude);
     }
-    int64_t page = -1;
+    int64_t cache_row = -1;                    // of head 0, further heads are a page apart
     if constexpr (kType != kRopeNone)
-        if (last > q_rows)
-            page = kv_page_of(p.c, b, static_cast<int32_t>(pos));
+        if (last > q_steps) {
+            const int64_t page = kv_page_of(p.c, b, static_cast<int32_t>(pos));
+            cache_row = page < 0 ? -1 : kv_row(p.c, page, 0, static_cast<int32_t>(pos));
+        }
     __syncwarp();
     LaneTurns<kNeighbours> turns;
     const bool turned = col < p.part;
     turns.load(s_turn[warp], turned ? col : 0, p.half);
     const int partner = kNeighbours || !turned ? lane : col < p.half ? lane + p.half / 8 : lane - p.half / 8;
 
-    for (int r0 = first; r0 < last; r0 += kStep) {
-        uint4 next[kRopeAhead];
+    auto rotated = [&](const uint4 &r, uint64_t (&x)[4]) {
+        widen_pairs(r, x);
+        uint64_t other[4] = {};
+        if constexpr (!kNeighbours) {
+            uint4 o;
+            o.x = __shfl_sync(0xffffffffu, r.x, partner);
+            o.y = __shfl_sync(0xffffffffu, r.y, partner);
+            o.z = __shfl_sync(0xffffffffu, r.z, partner);
+            o.w = __shfl_sync(0xffffffffu, r.w, partner);
+            widen_pairs(o, other);
+        }
+        if (turned)
+            turns.rotate(x, other);
+    };
+    auto round_pairs = [](const uint64_t (&x)[4]) {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < kRopeAhead; ++i)
-            next[i] = load(r0 + kStep + i * kAtOnce + sub);
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            ptx::unpack2(x[i], a, b);
+            w[i] = pack_bf16(a, b);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    // rows of q, or of k without a cache: rotated and stored
+    auto turn_rows = [&](__nv_bfloat16 *dst, int row, int rows) {
 #pragma unroll
         for (int i = 0; i < kRopeAhead; ++i) {
-            const int r = r0 + i * kAtOnce + sub;
-            float x[8], other[8];
-            widen8(raw[i], x);
-            if constexpr (!kNeighbours) {
-                uint4 o;
-                o.x = __shfl_sync(0xffffffffu, raw[i].x, partner);
-                o.y = __shfl_sync(0xffffffffu, raw[i].y, partner);
-                o.z = __shfl_sync(0xffffffffu, raw[i].z, partner);
-                o.w = __shfl_sync(0xffffffffu, raw[i].w, partner);
-                widen8(o, other);
-            }
-            if (turned && r < k_rows)
-                turns.rotate(x, other);
-            if (r < q_rows) {
-                if (r < last)
-                    *reinterpret_cast<uint4 *>(p.q_out + t * p.q_out_stride + static_cast<int64_t>(r) * kDim +
-                                               col) = round8(x);
-            } else if constexpr (kType == kRopeNone) {
-                if (r < last)
-                    *reinterpret_cast<uint4 *>(p.k_out + t * p.k_out_stride +
-                                               static_cast<int64_t>(r - q_rows) * kDim + col) = round8(x);
-            }
-            if constexpr (kType != kRopeNone) {
-                const bool is_v = r >= k_rows, put = r >= q_rows && r < last && page >= 0;
-                const int64_t row = kv_row(p.c, page, r - (is_v ? k_rows : q_rows), static_cast<int32_t>(pos));
-                if constexpr (kType == SSD_KV_BF16) {
-                    if (put)
-                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(is_v ? p.c.v : p.c.k) +
-                                                   row * kDim + col) = is_v ? raw[i] : round8(x);
-                } else {
-                    constexpr float kTop = kType == SSD_KV_INT8 ? kInt8Max : kE4m3Max;
-                    // magnitudes order as integers, infinities and NaN come last
-                    uint32_t top = 0;
+            if (row + i * kAtOnce >= rows)     // (the same in all lanes)
+                break;
+            uint64_t x[4];
+            rotated(raw[i], x);
+            const int r = row + i * kAtOnce + sub;
+            if (r < rows)
+                *reinterpret_cast<uint4 *>(dst + r * kDim) = round_pairs(x);
+        }
+    };
+    // rows of k, rotated, or of v into the cache
+    auto keep_rows = [&](bool is_v, int row, int rows) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+        for (int i = 0; i < kRopeAhead; ++i) {
+            if (row + i * kAtOnce >= rows)
+                break;
+            uint64_t x[4];
+            if (is_v)
+                widen_pairs(raw[i], x);
+            else
+                rotated(raw[i], x);
+            const int r = row + i * kAtOnce + sub;
+            const bool put = r < rows && cache_row >= 0;
+            const int64_t to = cache_row + (static_cast<int64_t>(r) << p.c.page_shift);
+            void *cache = is_v ? p.c.v : p.c.k;
+            if constexpr (kType == SSD_KV_BF16) {
+                if (put)
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(cache) + to * kDim + col) =
+                        is_v ? raw[i] : round_pairs(x);
+            } else if constexpr (kType != kRopeNone) {
+                constexpr float kTop = kType == SSD_KV_INT8 ? kInt8Max : kE4m3Max;
+                float f[8];
+                // magnitudes order as integers, infinities and NaN come last
+                uint32_t top = 0;
 #pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1)
-                        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    if (put) {
-                        const bool bad = top >= 0x7f800000u;
-                        const float a = fmaxf(__uint_as_float(top), kKvTiny);
-                        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? p.c.v : p.c.k) + row * kDim +
-                                                   col) =
-                            bad ? make_uint2(0, 0) : encode8<kType>(x, __fdiv_rn(kTop, a));
-                        if (col == 0)
-                            (is_v ? p.c.v_scale : p.c.k_scale)[row] =
-                                bad ? __int_as_float(0x7fffffff) : __fdiv_rn(a, kTop);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    ptx::unpack2(x[j], f[2 * j], f[2 * j + 1]);
+                    top = max(top, max(__float_as_uint(f[2 * j]) & 0x7fffffffu,
+                                       __float_as_uint(f[2 * j + 1]) & 0x7fffffffu));
+                }
+#pragma unroll
+                for (int o = 1; o < kLanes; o <<= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const bool bad = top >= 0x7f800000u;
+                const float a = fmaxf(__uint_as_float(top), kKvTiny);
+                if (put) {
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + to * kDim + col) =
+                        bad ? make_uint2(0, 0) : encode8<kType>(f, __fdiv_rn(kTop, a));
+                    if (col == 0)
+                        (is_v ? p.c.v_scale : p.c.k_scale)[to] =
+                            bad ? __int_as_float(0x7fffffff) : __fdiv_rn(a, kTop);
                 }
             }
         }
+    };
+    for (int at = first; at < last; ++at) {
+        load(next, at + 1);
+        const Step s = step_of(at);
+        if (s.tensor == kQ)
+            turn_rows(p.q_out + t * p.q_out_stride + col, s.row, s.rows);
+        else if constexpr (kType == kRopeNone)
+            turn_rows(p.k_out + t * p.k_out_stride + col, s.row, s.rows);
+        else
+            keep_rows(s.tensor == kV, s.row, s.rows);
 #pragma unroll
         for (int i = 0; i < kRopeAhead; ++i)
             raw[i] = next[i];
@@ -213,12 +275,12 @@ template <int kType>
 cudaError_t launch(RopeParams &p, int64_t total_len, bool neighbours, cudaStream_t stream)
 {
     // a warp takes all of a token's rows once that gives every SM 16 warps; few tokens
-    // are spread over warps, a load's rows each
-    const int step = 256 / p.c.dim * kRopeAhead;
-    const bool many = total_len >= 16 * 152;
-    p.part_rows = many ? p.rows : step;
+    // are spread over warps, a step each
+    const int step = 256 / p.c.dim * kRopeAhead, kv = (p.c.heads + step - 1) / step;
+    p.steps = (p.heads + step - 1) / step + (kType == kRopeNone ? kv : 2 * kv);
+    p.part_steps = total_len >= 16 * 152 ? p.steps : 1;
     const dim3 grid(static_cast<unsigned>((total_len + kRopeWarps - 1) / kRopeWarps),
-                    static_cast<unsigned>((p.rows + p.part_rows - 1) / p.part_rows));
+                    static_cast<unsigned>((p.steps + p.part_steps - 1) / p.part_steps));
     const int threads = kRopeWarps * 32;
     if (p.c.dim == 128)
         return neighbours ? launch_pdl(rope_kernel<kType, 128, true>, grid, threads, stream, p)
@@ -310,7 +372,6 @@ ssd_status_t ssd_rope_varlen_fwd(void *q_out, const void *q, void *k_out, const 
     p.k_out_stride = k_out_stride;
     p.k_stride = k_stride;
     p.heads = nheads;
-    p.rows = nheads + nheads_kv;
     const cudaError_t e =
         launch<kRopeNone>(p, total_len, interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
@@ -356,7 +417,6 @@ ssd_status_t ssd_rope_kv_cache_write(
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     p.heads = nheads;
-    p.rows = nheads + 2 * nheads_kv;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool near = interleaved != 0;
     const cudaError_t e = cache_type == SSD_KV_BF16       ? launch<SSD_KV_BF16>(p, total_len, near, s)
