@@ -130,8 +130,8 @@ SSD_API ssd_status_t ssd_selective_scan_varlen_fwd(
  *              NaN gets codes 0 and scale NaN
  *
  * Rows are any multiple of 8 elements apart that is not below dim.  Supported: dim /
- * ngroups a multiple of 8, at most 32,768; eps from 2^-80 to 1.  s has to stay in
- * fp32's range (its square need not).  All in fp32, rounded once. */
+ * ngroups a multiple of 8, at most 32,768; eps from 2^-80 to 1.  s, and with codes s
+ * weight, has to stay in fp32's range (the square need not).  All in fp32, rounded once. */
 SSD_API ssd_status_t ssd_rms_norm_fwd(
     void *y, float *scale, const void *x, void *residual, const void *gate, const float *weight,
     int64_t rows, int32_t dim, int32_t ngroups, int32_t out_type, float eps, int64_t y_stride,

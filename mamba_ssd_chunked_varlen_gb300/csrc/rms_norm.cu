@@ -6,13 +6,18 @@
 //
 // A segment is one row's group.  It is read once and stays in registers, eight values
 // a load, between the sum of squares, the largest magnitude and the output: memory
-// bounds it.
+// bounds it.  Segments of up to 1,024 columns are a warp's or less (eight lanes up to 64,
+// sixteen up to 128), longer ones a CTA's.  There, for codes, y is (s w) r with r = 1 /
+// sqrt(...): a product with r > 0 keeps the order of magnitudes through its rounding, so
+// that max|y| is max|s w| r, and one barrier serves the sum and the largest (4,093 rows of
+// 5,120 to int8: 29.1 us with two, 27.1 with one; a warp's weights would be registers that
+// it needs, 8,191 rows of 8 gated groups to int8: 73 us with them, 68 without).
 #include "layer_common.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kNormWarps = 4;        // segments of a CTA when a warp takes one
+constexpr int kNormThreads = 128;    // threads of a CTA that takes several segments
 constexpr int kNormMaxVecs = 4;      // loads of eight values that a thread holds
 
 enum NormInput { kPlain, kResidual, kGate };
@@ -28,62 +33,57 @@ struct NormParams {
     float eps;
 };
 
-// Sum of v and largest of m over a segment's threads: a warp, or all of the CTA's.
-template <bool kWarp>
-__device__ __forceinline__ float segment_sum(float v, float *scratch)
+// Sum of v and largest of m over a segment's kLanes lanes, or (0) all of the CTA's.
+template <int kLanes, bool kTop>
+__device__ __forceinline__ void reduce(float &v, uint32_t &m, float2 *scratch)
 {
+    constexpr int kWidth = kLanes ? kLanes : 32;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = kWidth / 2; o > 0; o >>= 1) {
         v += __shfl_xor_sync(0xffffffffu, v, o);
-    if constexpr (kWarp) {
-        return v;
-    } else {
+        if constexpr (kTop)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    if constexpr (kLanes == 0) {
         const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0)
-            scratch[threadIdx.x >> 5] = v;
+            scratch[threadIdx.x >> 5] = make_float2(v, __uint_as_float(m));
         __syncthreads();
-        v = lane < warps ? scratch[lane] : 0.f;
+        const float2 part = lane < warps ? scratch[lane] : make_float2(0.f, 0.f);
+        v = part.x;
+        m = __float_as_uint(part.y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
+        if constexpr (kTop)
+            m = __reduce_max_sync(0xffffffffu, m);
     }
 }
 
-template <bool kWarp>
-__device__ __forceinline__ uint32_t segment_max(uint32_t v, uint32_t *scratch)
+// kLanes: lanes of a segment, 0 for a CTA; kThreads: threads of a CTA at most.
+template <int kType, int kIn, int kVecs, int kLanes, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : kThreads == 128 ? 8 : kIn == kPlain && kType == SSD_KV_BF16 ? 3 : 2) norm_kernel(const __grid_constant__ NormParams p)
 {
-    v = __reduce_max_sync(0xffffffffu, v);
-    if constexpr (kWarp) {
-        return v;
-    } else {
-        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0)
-            scratch[threadIdx.x >> 5] = v;
-        __syncthreads();
-        return __reduce_max_sync(0xffffffffu, lane < warps ? scratch[lane] : 0u);
-    }
-}
-
-template <int kType, int kIn, int kVecs, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? kNormWarps * 32 : 1024) norm_kernel(const __grid_constant__ NormParams p)
-{
-    __shared__ float s_sum[2][32];
-    __shared__ uint32_t s_max[32];
-    const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, step = (kWarp ? 32 : blockDim.x) * 8;
-    const int64_t seg = kWarp ? static_cast<int64_t>(blockIdx.x) * kNormWarps + (threadIdx.x >> 5) : blockIdx.x;
+    constexpr bool kCodes = kType != SSD_KV_BF16, kEarly = kCodes && kLanes == 0;
+    __shared__ float2 s_part[2][32];
+    const int tid = kLanes ? threadIdx.x % (kLanes ? kLanes : 1) : threadIdx.x;
+    const int step = (kLanes ? kLanes : blockDim.x) * 8;
+    const int64_t seg = kLanes ? static_cast<int64_t>(blockIdx.x) * (kThreads / (kLanes ? kLanes : 1)) +
+                                     threadIdx.x / (kLanes ? kLanes : 1)
+                               : blockIdx.x;
     pdl_wait();
-    if (kWarp && seg >= p.segments)
-        return;
-    const int64_t row = seg / p.groups;
-    const int col0 = static_cast<int>(seg % p.groups) * p.cols;
-    float s[kVecs][8];
+    // (lanes without a segment go along: the others' shuffles name them)
+    const bool there = seg < p.segments;
+    const int64_t row = there ? seg / p.groups : 0;
+    const int col0 = there ? static_cast<int>(seg % p.groups) * p.cols : 0;
+    const int cols = there ? p.cols : 0;
+    float s[kVecs][8], w[kVecs][8];
     uint4 raw[kVecs], other[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
         const int c = v * step + tid * 8;
         raw[v] = other[v] = make_uint4(0, 0, 0, 0);
-        if (c < p.cols) {
+        if (c < cols) {
             raw[v] = *reinterpret_cast<const uint4 *>(p.x + row * p.x_stride + col0 + c);
             if constexpr (kIn == kResidual)
                 other[v] = *reinterpret_cast<const uint4 *>(p.residual + row * p.residual_stride + col0 + c);
@@ -91,7 +91,25 @@ __global__ void __launch_bounds__(kWarp ? kNormWarps * 32 : 1024) norm_kernel(co
                 other[v] = *reinterpret_cast<const uint4 *>(p.gate + row * p.gate_stride + col0 + c);
         }
     }
+    auto weights = [&](int v) {
+        const int c = v * step + tid * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 f = p.weight && c < cols
+                                 ? __ldg(reinterpret_cast<const float4 *>(p.weight + col0 + c) + i)
+                                 : make_float4(1.f, 1.f, 1.f, 1.f);
+            w[v][4 * i] = f.x;
+            w[v][4 * i + 1] = f.y;
+            w[v][4 * i + 2] = f.z;
+            w[v][4 * i + 3] = f.w;
+        }
+    };
+    if constexpr (kEarly)
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            weights(v);
     float sum = 0.f;
+    uint32_t top = 0;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
         widen8(raw[v], s[v]);
@@ -104,62 +122,80 @@ __global__ void __launch_bounds__(kWarp ? kNormWarps * 32 : 1024) norm_kernel(co
         }
         if constexpr (kIn == kResidual) {
             const int c = v * step + tid * 8;
-            if (c < p.cols)
+            if (c < cols)
                 *reinterpret_cast<uint4 *>(p.residual + row * p.residual_stride + col0 + c) = round8(s[v]);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 8; ++k) {
             sum = fmaf(s[v][k], s[v][k], sum);
+            if constexpr (kEarly)
+                top = max(top, __float_as_uint(s[v][k] * w[v][k]) & 0x7fffffffu);
+        }
     }
-    sum = segment_sum<kWarp>(sum, s_sum[0]);
+    reduce<kLanes, kEarly>(sum, top, s_part[0]);
     float r = rsqrtf(sum / static_cast<float>(p.cols) + p.eps);
-    if (!(sum < __int_as_float(0x7f800000))) {
+    // (all of a segment's threads take this way or none; in a warp of several segments
+    // all lanes do when one segment has to)
+    const bool again = !(sum < __int_as_float(0x7f800000));
+    if (kLanes ? __any_sync(0xffffffffu, again) : again) {
         // squares out of range (or infinities and NaN): once more on s 2^-80, where eps is
         // nothing beside the mean
+        const float by = again ? 0x1p-80f : 1.f;
         sum = 0.f;
+        top = 0;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                s[v][k] *= 0x1p-80f;
+                s[v][k] *= by;
                 sum = fmaf(s[v][k], s[v][k], sum);
+                if constexpr (kEarly)
+                    top = max(top, __float_as_uint(s[v][k] * w[v][k]) & 0x7fffffffu);
             }
-        sum = segment_sum<kWarp>(sum, s_sum[1]);
-        r = rsqrtf(sum / static_cast<float>(p.cols));
+        reduce<kLanes, kEarly>(sum, top, s_part[1]);
+        if (again)
+            r = rsqrtf(sum / static_cast<float>(p.cols));
     }
-    uint32_t top = 0;
+    if constexpr (!kCodes) {
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-        const int c = v * step + tid * 8;
-        float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-        if (p.weight && c < p.cols) {
-            *reinterpret_cast<float4 *>(w) = __ldg(reinterpret_cast<const float4 *>(p.weight + col0 + c));
-            *reinterpret_cast<float4 *>(w + 4) = __ldg(reinterpret_cast<const float4 *>(p.weight + col0 + c + 4));
-        }
+        for (int v = 0; v < kVecs; ++v) {
+            const int c = v * step + tid * 8;
+            weights(v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            s[v][k] = s[v][k] * r * w[k];
-            if constexpr (kType != SSD_KV_BF16)
-                top = max(top, c < p.cols ? __float_as_uint(s[v][k]) & 0x7fffffffu : 0u);
-        }
-        if constexpr (kType == SSD_KV_BF16) {
-            if (c < p.cols)
+            for (int k = 0; k < 8; ++k)
+                s[v][k] = s[v][k] * r * w[v][k];
+            if (c < cols)
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + row * p.y_stride + col0 + c) =
                     round8(s[v]);
         }
-    }
-    if constexpr (kType != SSD_KV_BF16) {
+    } else {
         constexpr float kTop = kType == SSD_KV_INT8 ? kInt8Max : kE4m3Max;
-        top = segment_max<kWarp>(top, s_max);
-        const bool bad = top >= 0x7f800000u;
-        const float a = fmaxf(__uint_as_float(top), kKvTiny);
-        const float inv = __fdiv_rn(kTop, a);
-        if (tid == 0)
+        if constexpr (!kEarly) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                weights(v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    s[v][k] = s[v][k] * r * w[v][k];
+                    top = max(top, v * step + tid * 8 < cols ? __float_as_uint(s[v][k]) & 0x7fffffffu : 0u);
+                }
+            }
+            float none = 0.f;
+            reduce<kLanes, true>(none, top, s_part[0]);
+        }
+        const float largest = kEarly ? __uint_as_float(top) * r : __uint_as_float(top);
+        const bool bad = !(largest < __int_as_float(0x7f800000));
+        const float a = fmaxf(largest, kKvTiny), inv = __fdiv_rn(kTop, a);
+        if (there && tid == 0)
             p.scale[seg] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(a, kTop);
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
             const int c = v * step + tid * 8;
-            if (c < p.cols)
+            if constexpr (kEarly)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    s[v][k] = s[v][k] * w[v][k] * r;
+            if (c < cols)
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + row * p.y_stride + col0 + c) =
                     bad ? make_uint2(0, 0) : encode8<kType>(s[v], inv);
         }
@@ -170,18 +206,24 @@ template <int kType, int kIn>
 cudaError_t launch(const NormParams &p, cudaStream_t stream)
 {
     const int loads = p.cols / 8;
-    // a warp a segment while its lanes hold four loads at most: no barrier
+    // up to a warp a segment while its lanes hold four loads at most: no barrier
     if (loads <= 4 * 32) {
-        const dim3 grid(static_cast<unsigned>((p.segments + kNormWarps - 1) / kNormWarps));
-        return loads <= 32   ? launch_pdl(norm_kernel<kType, kIn, 1, true>, grid, kNormWarps * 32, stream, p)
-               : loads <= 64 ? launch_pdl(norm_kernel<kType, kIn, 2, true>, grid, kNormWarps * 32, stream, p)
-                             : launch_pdl(norm_kernel<kType, kIn, 4, true>, grid, kNormWarps * 32, stream, p);
+        auto go = [&](auto kernel, int lanes) {
+            const int64_t each = kNormThreads / lanes;
+            return launch_pdl(kernel, dim3(static_cast<unsigned>((p.segments + each - 1) / each)), kNormThreads, stream,
+                              p);
+        };
+        return loads <= 8    ? go(norm_kernel<kType, kIn, 1, 8, kNormThreads>, 8)
+               : loads <= 16 ? go(norm_kernel<kType, kIn, 1, 16, kNormThreads>, 16)
+               : loads <= 32 ? go(norm_kernel<kType, kIn, 1, 32, kNormThreads>, 32)
+               : loads <= 64 ? go(norm_kernel<kType, kIn, 2, 32, kNormThreads>, 32)
+                             : go(norm_kernel<kType, kIn, 4, 32, kNormThreads>, 32);
     }
     const dim3 grid(static_cast<unsigned>(p.segments));
-    const int vecs = loads <= 2 * 1024 ? 2 : kNormMaxVecs;
+    const int vecs = loads <= 2 * 512 ? 2 : kNormMaxVecs;
     const int threads = (loads + 32 * vecs - 1) / (32 * vecs) * 32;
-    return vecs == 2 ? launch_pdl(norm_kernel<kType, kIn, 2, false>, grid, threads, stream, p)
-                     : launch_pdl(norm_kernel<kType, kIn, kNormMaxVecs, false>, grid, threads, stream, p);
+    return vecs == 2 ? launch_pdl(norm_kernel<kType, kIn, 2, 0, 512>, grid, threads, stream, p)
+                     : launch_pdl(norm_kernel<kType, kIn, kNormMaxVecs, 0, 1024>, grid, threads, stream, p);
 }
 
 template <int kType>

@@ -409,16 +409,19 @@ def alloc_rope_table(frequencies, device="cuda"):
 
 
 def _rotary(f, table, device: int):
-    if table.dim() != 1:
+    shape = table.shape
+    if len(shape) != 1:
         raise ValueError("table must have shape (rotary_dim / 2,)")
-    return _ptr(table, "table", f.i64, table.shape, device), 2 * table.shape[0]
+    return _ptr(table, "table", f.i64, shape, device), 2 * shape[0]
 
 
-def _heads(out, x, what: str, f, device: int):
-    if x.dim() != 3:
-        raise ValueError(f"{what} must have shape (rows, heads, head_dim)")
-    shape = x.shape
-    return *_rows(out, f"{what}_out", f.bf16, shape, device), *_rows(x, what, f.bf16, shape, device), shape
+def _same_rows(out, x, what: str, f, shape, device: int):
+    """Pointers and pitches of an output and its input, of shape (rows, heads, head_dim)."""
+    bf16 = f.bf16
+    if (out.dtype is bf16 and x.dtype is bf16 and out.shape == shape and out.get_device() == device
+            and x.get_device() == device and out.is_contiguous() and x.is_contiguous()):
+        return out.data_ptr(), 0, x.data_ptr(), 0
+    return *_rows(out, f"{what}_out", bf16, shape, device), *_rows(x, what, bf16, shape, device)
 
 
 def ssd_rope_varlen_fwd(q_out, q, k_out, k, table, query_start_loc, kv_lens, *, interleaved: bool = False,
@@ -436,16 +439,23 @@ def ssd_rope_varlen_fwd(q_out, q, k_out, k, table, query_start_loc, kv_lens, *, 
         raise ValueError("q and q_out, or k and k_out, or both are needed")
     device = _device(k if q is None else q, "k" if q is None else "q")
     turns, rotary_dim = _rotary(f, table, device)
+    if query_start_loc.dim() != 1 or query_start_loc.shape[0] < 1:
+        raise ValueError("query_start_loc must have shape (batch + 1,)")
     batch = query_start_loc.shape[0] - 1
     qo = qi = ko = ki = None
     sqo = sq = sko = sk = heads = heads_kv = 0
+    for t, what in ((q, "q"), (k, "k")):
+        if t is not None and t.dim() != 3:
+            raise ValueError(f"{what} must have shape (rows, heads, head_dim)")
     if q is not None:
-        qo, sqo, qi, sq, (total, heads, dim) = _heads(q_out, q, "q", f, device)
+        total, heads, dim = q.shape
+        qo, sqo, qi, sq = _same_rows(q_out, q, "q", f, q.shape, device)
     if k is not None:
-        ko, sko, ki, sk, shape = _heads(k_out, k, "k", f, device)
+        shape = k.shape
         if q is not None and (shape[0] != total or shape[2] != dim):
             raise ValueError(f"k must have shape ({total}, nheads_kv, {dim}), got {tuple(shape)}")
         total, heads_kv, dim = shape
+        ko, sko, ki, sk = _same_rows(k_out, k, "k", f, shape, device)
     _call(f, f.rope, "ssd_rope_varlen_fwd", device, stream, qo, qi, ko, ki, turns,
           _ptr(query_start_loc, "query_start_loc", f.i32, (batch + 1,), device),
           _ptr(kv_lens, "kv_lens", f.i32, (batch,), device), total, batch, heads, heads_kv, dim, rotary_dim,
@@ -463,11 +473,13 @@ def ssd_rope_kv_cache_write(q_out, q, k, v, table, k_cache, v_cache, k_scale, v_
         attention._functions(), k_cache, v_cache, k_scale, v_scale, query_start_loc, kv_lens, block_table,
         errors)
     turns, rotary_dim = _rotary(f, table, device)
-    qo, sqo, qi, sq, shape = _heads(q_out, q, "q", f, device)
-    total, heads, _ = shape
-    if shape[2] != dim:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"q must have shape (rows, nheads, {dim}), got {tuple(shape)}")
-    pk, sk = _rows(k, "k", f.bf16, (total, heads_kv, dim), device)
-    pv, sv = _rows(v, "v", f.bf16, (total, heads_kv, dim), device)
+    total, heads, _ = shape
+    qo, sqo, qi, sq = _same_rows(q_out, q, "q", f, shape, device)
+    kv = (total, heads_kv, dim)
+    pk, sk = _rows(k, "k", f.bf16, kv, device)
+    pv, sv = _rows(v, "v", f.bf16, kv, device)
     _call(f, f.rope_write, "ssd_rope_kv_cache_write", device, stream, qo, qi, pk, pv, turns, *ptrs, total,
           batch, heads, heads_kv, dim, rotary_dim, bool(interleaved), magnitude, *sizes, sqo, sq, sk, sv, pe)
