@@ -44,7 +44,6 @@ constexpr int kShort = 7;             // tokens of a sequence that goes without 
 constexpr int kStates = 8;            // states of a lane
 constexpr int kMinChunk = 64;         // tokens of a chunk at least
 constexpr int kFullWarps = 5000;      // warps that sel_chunk wants of a call's chunks
-constexpr int kFewWarps = 800;        // warps that leave a sequence whole (sel_cut)
 constexpr int kResident = 4;          // CTAs of an SM at most
 
 // A chunk k of a sequence, as a rule the whole sequence.
@@ -71,66 +70,116 @@ struct SelParams {
     float *firsts;                    // states that a cut sequence starts from, at its first end
     int32_t y_stride, x_stride, dt_stride, b_stride, c_stride, z_stride;
     int32_t channels, tiles;          // tiles of a CTA's channels
-    int32_t chunk, cut;               // smallest chunk, shortest sequence that is cut
+    int32_t chunk, warps;             // smallest chunk (0: nothing is cut), warps of a sequence
     int32_t softplus, pool_bf16;
 };
 
 // ---------------------------------------------------------------- chunks
-// Tokens of the smallest chunk, as many as give kFullWarps warps over all tokens, and of
-// the shortest sequence that is cut.  Cutting makes the states of most tokens twice, which
-// costs about 0.7 of the whole again; a sequence alone takes 62 ns a token whatever its
-// warps, while they are fewer than the schedulers, and in chunks some 0.125 ns a token and
-// warp of the call.  (One sequence of 4,096 tokens, 2,048 channels: 263 us whole, 85 in
-// chunks; of 9,763 tokens, 8,192 channels: 604 and 585; two of them: 430 and 538.)
-inline int32_t sel_rounded(int64_t tokens)
+// Warps of a sequence, and tokens of the smallest chunk: as many as give kFullWarps warps
+// over all tokens.
+inline int64_t sel_warps(int32_t channels, int32_t dstate)
 {
-    return static_cast<int32_t>(std::min<int64_t>((tokens + kBlock - 1) / kBlock * kBlock, INT32_MAX / 2));
-}
-inline int64_t sel_warp_tokens(int64_t total_len, int32_t channels, int32_t dstate)
-{
-    return total_len * ((static_cast<int64_t>(channels) * dstate + 32 * kStates - 1) / (32 * kStates));
+    return (static_cast<int64_t>(channels) * dstate + 32 * kStates - 1) / (32 * kStates);
 }
 inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 {
-    return std::max(kMinChunk, sel_rounded((sel_warp_tokens(total_len, channels, dstate) + kFullWarps - 1) / kFullWarps));
-}
-inline int32_t sel_cut(int64_t total_len, int32_t channels, int32_t dstate)
-{
-    return std::max(2 * sel_chunk(total_len, channels, dstate),
-                    sel_rounded(sel_warp_tokens(total_len, channels, dstate) / kFewWarps));
+    const int64_t tokens = (total_len * sel_warps(channels, dstate) + kFullWarps - 1) / kFullWarps;
+    return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(kMinChunk, (tokens + kBlock - 1) / kBlock * kBlock),
+                                                  INT32_MAX / 2));
 }
 
-// Lists the chunks: `count` of `len` tokens a sequence, the last one shorter.
+// What a call takes, in ns, whose sequences of some length on are cut: its longest whole
+// sequence, or all of its tokens.  Measured: a token of a whole sequence 80, whatever its
+// warps, while they find room; a token and warp of a whole sequence 0.086, of a cut one
+// (whose states are made twice) 0.115; the additional kernel 6,000.  (One sequence of 4,096
+// tokens, 2,048 channels: 263 us whole, 78 cut; of 9,763 tokens, 8,192 channels: 604 and 575;
+// two prompts of 9,763 tokens: 431 and 540.)
+__device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int warps)
+{
+    return fmaxf(80.f * longest, (0.086f * whole + 0.115f * cut) * warps) + (cut > 0 ? 6000.f : 0.f);
+}
+
+// Lists the chunks: `count` of `len` tokens a sequence, the last one shorter.  Which lengths
+// are cut is up to sel_cost, by powers of two.
 constexpr int kPlanThreads = 512;
-constexpr int kPlanSizes = 16;        // sizes of chunks (powers of two) that are told apart
+constexpr int kPlanSizes = 16;        // powers of two that are told apart
+
+__device__ __forceinline__ int sel_size(int32_t len) { return min(kPlanSizes - 1, 31 - __clz(len | 1)); }
 
 __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __grid_constant__ SelParams p)
 {
-    __shared__ int s_units[kPlanSizes], s_ends;
+    __shared__ int s_units[kPlanSizes], s_tokens[kPlanSizes], s_longest[kPlanSizes], s_ends, s_cut;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x < kPlanSizes)
+    if (threadIdx.x < kPlanSizes) {
         s_units[threadIdx.x] = 0;
-    if (threadIdx.x == 0)
+        s_tokens[threadIdx.x] = 0;
+        s_longest[threadIdx.x] = 0;
+    }
+    if (threadIdx.x == 0) {
         s_ends = 0;
+        s_cut = INT32_MAX;
+    }
     pdl_wait();
     __syncthreads();
-    auto chunks = [&](int b, int32_t &begin, int32_t &end, int32_t &len, int &count) {
+    // the thread's first sequence stays in registers, as a rule there are no others
+    int32_t begin0 = 0, end0 = -1;
+    if (threadIdx.x < p.s.batch && !seq_rows(p.s.qsl, p.s.total_len, p.s.errors, threadIdx.x, begin0, end0))
+        end0 = -1;
+    auto rows = [&](int b, int32_t &begin, int32_t &end) {
+        begin = begin0;
+        end = end0;
+        return b < kPlanThreads ? end0 >= 0
+                                : b < p.s.batch && seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, begin, end);
+    };
+    int32_t begin, end, len = 0;
+    if (p.chunk) {
+        bool bad = false;
+        for (int b = threadIdx.x; b < p.s.batch; b += kPlanThreads) {
+            if (!rows(b, begin, end)) {
+                bad = true;
+                continue;
+            }
+            atomicAdd(&s_tokens[sel_size(end - begin)], end - begin);
+            atomicMax(&s_longest[sel_size(end - begin)], end - begin);
+        }
+        // (with offsets that fall, the sequences may come to more than the workspace is for)
+        if (!__syncthreads_or(bad) && threadIdx.x == 0) {
+            int whole = 0, cut = 0;
+            for (int i = 0; i < kPlanSizes; ++i) {
+                whole += s_tokens[i];
+                if (i > 0)
+                    s_longest[i] = max(s_longest[i], s_longest[i - 1]);
+            }
+            float best = sel_cost(s_longest[kPlanSizes - 1], whole, 0, p.warps);
+            for (int i = kPlanSizes - 1; i >= 0 && 2 << i > 2 * p.chunk; --i) {
+                whole -= s_tokens[i];
+                cut += s_tokens[i];
+                const float cost = sel_cost(i > 0 ? s_longest[i - 1] : 0, whole, cut, p.warps);
+                if (cost < best) {
+                    best = cost;
+                    s_cut = max(1 << i, 2 * p.chunk);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    const int32_t shortest = s_cut;
+    auto chunks = [&](int b, int &count) {
         count = 0;
-        if (b >= p.s.batch || !seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, begin, end))
+        if (!rows(b, begin, end))
             return 0;
         len = end - begin;
         count = 1;
-        if (len >= p.cut) {
+        if (len >= shortest) {
             const int32_t n = len / p.chunk;
             len = ((len + n - 1) / n + kBlock - 1) / kBlock * kBlock;
             count = (end - begin + len - 1) / len;
         }
-        return kPlanSizes - 1 - min(kPlanSizes - 1, 31 - __clz(len | 1));      // long ones first
+        return kPlanSizes - 1 - sel_size(len);      // long ones first
     };
-    int32_t begin = 0, end = 0, len = 0;
     int count;
     for (int b = threadIdx.x; b < p.s.batch; b += kPlanThreads) {
-        const int size = chunks(b, begin, end, len, count);
+        const int size = chunks(b, count);
         if (count)
             atomicAdd(&s_units[size], count);
     }
@@ -144,7 +193,7 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
     }
     __syncthreads();
     for (int b0 = threadIdx.x - lane; b0 < p.s.batch; b0 += kPlanThreads) {
-        const int b = b0 + lane, size = chunks(b, begin, end, len, count);
+        const int b = b0 + lane, size = chunks(b, count);
         int at = 0, ends = 0;
         if (count) {
             at = atomicAdd(&s_units[size], count);
@@ -965,15 +1014,14 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
         return launch_pdl(p.pool_bf16 ? selective_step_kernel<N, kGate, true> : selective_step_kernel<N, kGate, false>,
                           dim3(static_cast<unsigned>(p.tiles * groups)), kScanThreads, stream, p);
     }
-    // A call of fewer tokens has no sequence that is cut, and of one of several sequences with
-    // warps for two thirds of the schedulers each, cutting gains 5 % at best, but the list, the
-    // idle CTAs and the other order of the rest cost more (two prompts of 9,763 tokens, 8,192
-    // channels: 473 us instead of 440).
-    const int64_t warps = (static_cast<int64_t>(p.channels) * N + 32 * kStates - 1) / (32 * kStates);
-    const bool may_cut = p.s.total_len >= p.cut && (p.s.batch == 1 || 3 * warps < 8 * sms);
+    // Calls of few tokens are not cut, and neither are those of several sequences that have
+    // warps for two thirds of the schedulers each: cutting gains 5 % at best, but the list,
+    // the idle CTAs and the other order of the rest cost more (two prompts of 9,763 tokens,
+    // 8,192 channels: 473 us instead of 440).
+    const bool may_cut = p.s.total_len >= 2 * int64_t{p.chunk} && (p.s.batch == 1 || 3 * p.warps < 8 * sms);
     const int64_t ends = may_cut ? sel_ends(p.s.total_len, p.chunk) : 0;
-    if (!ends)
-        p.cut = INT32_MAX;
+    if (!may_cut)
+        p.chunk = 0;
     const int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
     const bool listed = ends || whole > int64_t{kResident} * sms;
     cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<N, kGate>,
@@ -1079,7 +1127,7 @@ ssd_status_t ssd_selective_scan_varlen_fwd(
     p.softplus = dt_softplus != 0;
     p.pool_bf16 = pool_type == SSD_POOL_BF16;
     p.chunk = sel_chunk(total_len, channels, dstate);
-    p.cut = sel_cut(total_len, channels, dstate);
+    p.warps = static_cast<int32_t>(sel_warps(channels, dstate));
     const SelLayout L = sel_layout(total_len, batch, channels, dstate, sel_ends(total_len, p.chunk));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.header = reinterpret_cast<SelHeader *>(ws);
