@@ -1,15 +1,21 @@
-"""One block of a hybrid model served with continuous batching: a Mamba-2 scan
-layer and an attention layer on the same ragged batch.
+"""One block of a hybrid model served with continuous batching: a scan layer and an
+attention layer on the same ragged batch.
 
 Every step takes the new tokens of all running sequences, prompts and single
 tokens alike, as one batch described by ``query_start_loc``:
 
-    scan layer       ssd_scan_varlen_fwd_strided  on column views of a projection,
-                     recurrent states in a pool of slots
-    attention layer  ssd_kv_cache_write  k and v of the new tokens into pages
-                     ssd_attn_varlen_fwd  the new tokens over the whole context
+    scan layer       ssd_rms_norm_fwd             the layer's input
+                     ssd_causal_conv_varlen_fwd   columns of a projection, the last
+                     inputs in a pool of slots
+                     ssd_scan_varlen_fwd_strided  on column views of the result,
+                     recurrent states in a pool of slots; or, with a step and decays of
+                     each channel's own, ssd_selective_scan_varlen_fwd
+                     ssd_rms_norm_fwd             the gated output, in groups
+    attention layer  ssd_rms_norm_fwd             its input, with the residual's addition
+                     ssd_rope_kv_cache_write      q, and k and v into pages, rotated
+                     ssd_attn_varlen_fwd          the new tokens over the whole context
 
-    python examples/hybrid_serving.py [--cache bfloat16|float8_e4m3fn|int8]
+    python examples/hybrid_serving.py [--cache bfloat16|float8_e4m3fn|int8] [--scan ssd|selective]
 
 The weights are random and the projections plain matrix products: what is shown
 is how the calls share a batch.
@@ -25,6 +31,8 @@ import mamba_ssd_chunked_varlen_gb300 as ssd  # noqa: E402
 
 HIDDEN = 512
 SCAN = dict(nheads=16, head_dim=64, ngroups=1, dstate=128, chunk_size=128)
+SELECTIVE = dict(channels=1024, dstate=16, step_rank=32)
+CONV, GROUPS = 4, 2     # the convolution's width, groups of the gated norm
 HEADS, KV_HEADS, DIM, PAGE = 16, 4, 128, 16
 
 
@@ -47,23 +55,41 @@ class Pages:
 
 class HybridBlock:
     def __init__(self, slots=8, max_tokens=1024, max_context=1024, cache=torch.bfloat16, seed=0,
-                 device="cuda"):
+                 device="cuda", scan="ssd"):
         g = torch.Generator().manual_seed(seed)
 
         def weight(n, m):
             return (torch.randn(n, m, generator=g) / n ** 0.5).bfloat16().to(device)
 
+        def near_one(*shape):
+            return torch.rand(shape, generator=g).add(0.5).to(device)
+
         inner, gn = SCAN["nheads"] * SCAN["head_dim"], SCAN["ngroups"] * SCAN["dstate"]
-        self.scan_cols = [inner, gn, gn, SCAN["nheads"]]             # x, B, C, dt
+        self.selective = scan == "selective"
+        n = SCAN["nheads"]
+        if self.selective:
+            inner, d, rank = SELECTIVE["channels"], SELECTIVE["dstate"], SELECTIVE["step_rank"]
+            self.conv_cols = [inner]
+            self.scan_cols = [inner, inner]                          # z, x
+            self.step_in, self.step_out = weight(inner, rank + 2 * d), weight(rank, inner)
+            self.A, n = -near_one(inner, d) * torch.arange(1, d + 1, device=device), inner
+        else:
+            self.conv_cols = [inner, gn, gn]                         # x, B, C
+            self.scan_cols = [inner, sum(self.conv_cols), n]         # z, the convolution's, dt
+            self.A = -near_one(n)
+        self.D = torch.ones(n, device=device)
+        self.dt_bias = torch.full((n,), -2.0, device=device)
+        self.conv_weight, self.conv_bias = near_one(sum(self.conv_cols), CONV) - 0.9, None
+        self.norms = near_one(HIDDEN), near_one(inner), near_one(HIDDEN)
         self.attn_cols = [HEADS * DIM, KV_HEADS * DIM, KV_HEADS * DIM]
         self.scan_in, self.scan_out = weight(HIDDEN, sum(self.scan_cols)), weight(inner, HIDDEN)
         self.attn_in, self.attn_out = weight(HIDDEN, sum(self.attn_cols)), weight(HEADS * DIM, HIDDEN)
-        n = SCAN["nheads"]
-        self.A = -torch.rand(n, generator=g).add(0.5).to(device)
-        self.D = torch.ones(n, device=device)
-        self.dt_bias = torch.full((n,), -2.0, device=device)
+        frequencies, self.magnitude = ssd.rope_frequencies(DIM)
+        self.turns = ssd.alloc_rope_table(frequencies, device)
         # what a server keeps: the states, the pages, the workspaces, one word of errors
-        self.states = torch.zeros(slots, n, SCAN["head_dim"], SCAN["dstate"], device=device)
+        self.conv_states = torch.zeros(slots, CONV - 1, sum(self.conv_cols), dtype=torch.bfloat16, device=device)
+        state = (inner, SELECTIVE["dstate"]) if self.selective else (n, SCAN["head_dim"], SCAN["dstate"])
+        self.states = torch.zeros(slots, *state, device=device)
         width = (max_context + PAGE - 1) // PAGE
         self.pages = Pages(slots * width, slots, width)
         shape = (slots * width, KV_HEADS, PAGE, DIM)
@@ -73,8 +99,11 @@ class HybridBlock:
         self.k_scale = torch.zeros(shape[:3], device=device) if quantised else None
         self.v_scale = self.k_scale.clone() if quantised else None
         self.errors = torch.zeros(1, dtype=torch.int32, device=device)
-        self.scan_ws = ssd.alloc_workspace(max_tokens, slots, n, SCAN["head_dim"], SCAN["ngroups"],
-                                           SCAN["dstate"], SCAN["chunk_size"], device=device)
+        if self.selective:
+            self.scan_ws = ssd.alloc_selective_scan_workspace(max_tokens, slots, *state, device=device)
+        else:
+            self.scan_ws = ssd.alloc_workspace(max_tokens, slots, n, SCAN["head_dim"], SCAN["ngroups"],
+                                               SCAN["dstate"], SCAN["chunk_size"], device=device)
         self.attn_ws = ssd.alloc_attn_workspace(max_tokens, slots, HEADS, KV_HEADS, DIM, device=device)
         self.lens = [0] * slots
         self.device = device
@@ -101,27 +130,54 @@ class HybridBlock:
         kv_lens = torch.tensor([self.lens[s] for s in slots], **i32)
         block_table = self.pages.rows(slots, device)
         self.batch = query_start_loc, kv_lens, block_table
+        where = (query_start_loc, torch.tensor([not f for f in fresh], device=device),
+                 torch.tensor(slots, **i32))
 
-        # ---- the scan layer: column views of one projection
-        x, B, C, dt = (h @ self.scan_in).split(self.scan_cols, 1)
-        y = torch.empty(total, SCAN["nheads"], SCAN["head_dim"], dtype=torch.bfloat16, device=device)
-        ssd.ssd_scan_varlen_fwd_strided(
-            y, x.unflatten(1, (SCAN["nheads"], -1)), dt, self.A, B.unflatten(1, (SCAN["ngroups"], -1)),
-            C.unflatten(1, (SCAN["ngroups"], -1)), self.D, self.dt_bias, self.states, query_start_loc,
-            torch.tensor([not f for f in fresh], device=device), torch.tensor(slots, **i32),
-            chunk_size=SCAN["chunk_size"], workspace=self.scan_ws)
-        h = h + y.flatten(1) @ self.scan_out
+        # ---- the scan layer: column views of one projection, the gate first
+        residual, normed = h.clone(), torch.empty_like(h)
+        ssd.ssd_rms_norm_fwd(normed, h, self.norms[0])
+        z, x, *dt = (normed @ self.scan_in).split(self.scan_cols, 1)
+        mixed = torch.empty(total, sum(self.conv_cols), dtype=torch.bfloat16, device=device)
+        ssd.ssd_causal_conv_varlen_fwd(mixed, x, self.conv_weight, self.conv_bias, self.conv_states, *where,
+                                       errors=self.errors)
+        y = torch.empty(total, z.shape[1], dtype=torch.bfloat16, device=device)
+        if self.selective:
+            self.scan_selective(y, mixed, where)
+        else:
+            self.scan_heads(y, mixed, dt[0], where)
+        ssd.ssd_rms_norm_fwd(y, y, self.norms[1], gate=z, ngroups=GROUPS)
 
-        # ---- the attention layer: the new keys and values first, then the queries
-        q, k, v = (h @ self.attn_in).split(self.attn_cols, 1)
-        q = q.unflatten(1, (HEADS, DIM))
+        # ---- the attention layer: the new keys and values with the queries' rotation first
+        ssd.ssd_rms_norm_fwd(normed, y @ self.scan_out, self.norms[2], residual=residual)
+        q, k, v = (normed @ self.attn_in).split(self.attn_cols, 1)
         k, v = (t.unflatten(1, (KV_HEADS, DIM)) for t in (k, v))
-        ssd.ssd_kv_cache_write(k, v, *self.cache, *self.batch, errors=self.errors)
+        plain, q = q.unflatten(1, (HEADS, DIM)), torch.empty(total, HEADS, DIM, dtype=torch.bfloat16, device=device)
+        ssd.ssd_rope_kv_cache_write(q, plain, k, v, self.turns, *self.cache, *self.batch,
+                                    magnitude=self.magnitude, errors=self.errors)
         o = torch.empty(total, HEADS, DIM, dtype=torch.bfloat16, device=device)
         ssd.ssd_attn_varlen_fwd(o, None, q, *self.cache, *self.batch, softmax_scale=DIM ** -0.5,
                                 workspace=self.attn_ws, errors=self.errors)
         self.last = q, o
-        return h + o.flatten(1) @ self.attn_out
+        return residual + o.flatten(1) @ self.attn_out
+
+    def scan_heads(self, y, mixed, dt, where):
+        """The scan whose step and decay are each head's."""
+        x, B, C = mixed.split(self.conv_cols, 1)
+        ssd.ssd_scan_varlen_fwd_strided(
+            y.unflatten(1, (SCAN["nheads"], -1)), x.unflatten(1, (SCAN["nheads"], -1)), dt, self.A,
+            B.unflatten(1, (SCAN["ngroups"], -1)), C.unflatten(1, (SCAN["ngroups"], -1)), self.D, self.dt_bias,
+            self.states, *where, chunk_size=SCAN["chunk_size"], workspace=self.scan_ws)
+
+    def scan_selective(self, y, x, where):
+        """The scan whose step and decays are each channel's, made from x."""
+        rank, d = SELECTIVE["step_rank"], SELECTIVE["dstate"]
+        step, B, C = (x @ self.step_in).split([rank, d, d], 1)
+        ssd.ssd_selective_scan_varlen_fwd(y, x, step @ self.step_out, self.A, B, C, self.D, None, self.dt_bias,
+                                          self.states, *where, workspace=self.scan_ws, errors=self.errors)
+
+    def flags(self):
+        """The device-side errors of all calls so far."""
+        return int(self.errors) | (0 if self.selective else ssd.ssd_scan_varlen_read_errors(self.scan_ws))
 
     def contexts(self):
         """The last step's contexts as the cache has them: k, v (tokens, kv heads, dim)
@@ -149,13 +205,14 @@ def serve(block, steps=12, seed=1):
 def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     p.add_argument("--cache", default="bfloat16", choices=("bfloat16", "float8_e4m3fn", "int8"))
+    p.add_argument("--scan", default="ssd", choices=("ssd", "selective"))
     p.add_argument("--steps", type=int, default=12)
     a = p.parse_args()
-    block = HybridBlock(cache=getattr(torch, a.cache))
+    block = HybridBlock(cache=getattr(torch, a.cache), scan=a.scan)
     for i, (batch, out) in enumerate(serve(block, a.steps)):
         print(f"step {i}: {sum(n for _, n in batch)} new tokens of {len(batch)} sequences, "
               f"contexts {[block.lens[s] for s, _ in batch]}, rms {out.float().pow(2).mean().sqrt().item():.3f}")
-    flags = int(block.errors) | ssd.ssd_scan_varlen_read_errors(block.scan_ws)
+    flags = block.flags()
     print(f"device error flags: {flags:#x}")
     return 1 if flags else 0
 

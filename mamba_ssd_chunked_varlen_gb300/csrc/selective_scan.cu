@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "attn_ptx.cuh"
+#include "kernels.cuh"
 #include "layer_common.cuh"
 
 namespace ssd {
@@ -1024,12 +1025,12 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
         p.chunk = 0;
     const int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
     const bool listed = ends || whole > int64_t{kResident} * sms;
-    cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<N, kGate>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    static SmemOptIn s_scan, s_states;
+    cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(selective_scan_kernel<N, kGate>), s_scan);
     if (listed && e == cudaSuccess)
         e = launch_pdl(selective_plan_kernel, dim3(1), kPlanThreads, stream, p);
     if (ends && e == cudaSuccess) {
-        e = cudaFuncSetAttribute(selective_states_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        e = ensure_max_smem(reinterpret_cast<const void *>(selective_states_kernel<N>), s_states);
         if (e == cudaSuccess)
             e = launch_pdl_smem(selective_states_kernel<N>, dim3(static_cast<unsigned>(p.tiles * ends)), kScanThreads,
                                 kBytes, stream, p);

@@ -208,3 +208,25 @@ def test_far_rows():
     near_x, near_y = x.contiguous(), torch.empty(n, 64, dtype=torch.bfloat16, device="cuda")
     pkg.ssd_causal_conv_varlen_fwd(near_y, near_x, weight, None, pool, *where)
     assert same_bits(y, near_y)
+
+
+def test_far_slots():
+    """A slot past 2^31 elements."""
+    import torch
+    import mamba_ssd_chunked_varlen_gb300 as pkg
+    channels = 1 << 20
+    slots = (1 << 31) // (3 * channels) + 3
+    pool = torch.zeros(slots, 3, channels, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, old = (torch.randn(n, channels, generator=g, device="cuda").bfloat16() for n in (2, 3))
+    weight = torch.randn(channels, 4, generator=g, device="cuda")
+    where = torch.tensor([0, 2], dtype=torch.int32, device="cuda"), torch.tensor([True], device="cuda")
+    out = []
+    for p, slot in ((pool, slots - 1), (torch.zeros(1, 3, channels, dtype=torch.bfloat16, device="cuda"), 0)):
+        p[slot] = old
+        y = torch.empty_like(x)
+        pkg.ssd_causal_conv_varlen_fwd(y, x, weight, None, p, *where,
+                                       torch.tensor([slot], dtype=torch.int32, device="cuda"))
+        out.append((y, p[slot]))
+    assert same_bits(out[0][0], out[1][0]) and same_bits(out[0][1], out[1][1])
+    assert not pool[:-1].any()

@@ -239,6 +239,64 @@ def test_device_side_errors():
     assert same_bits(other, pool) and same_bits(z[:8], y[:8]) and same_bits(z[13:], y[13:])
 
 
+def test_offsets_that_fall_are_not_cut():
+    """Sequences that come to far more tokens than there are rows: flagged, and nothing but
+    the rows and the named slots is touched."""
+    import torch
+    from mamba_ssd_chunked_varlen_gb300 import binding
+    n = 2000
+    r = Ragged([n] + [0] * 41, seed=11)
+    r.query_start_loc.copy_(torch.tensor([0, n] * 21 + [n]))
+    v = make(r, 24, 16, 11)
+    size = 1 << 20
+    wide = torch.full((size + (1 << 16),), 77, dtype=torch.uint8, device="cuda")
+    y, pool = torch.empty_like(v["x"]), v["pool"].clone()
+    import mamba_ssd_chunked_varlen_gb300 as pkg
+    need = pkg.ssd_selective_scan_varlen_workspace_size(n, 42, 24, 16)
+    assert need <= size
+    call(r, v, y, pool, workspace=wide[:need])
+    assert r.errors.item() == binding.DEVERR_BAD_QUERY_START_LOC
+    assert (wide[need:] == 77).all()
+    rest = [s for s in range(r.slots) if s not in r.slot]
+    assert same_bits(pool[rest], v["pool"][rest])
+
+
+def test_workspace_is_not_overrun():
+    """Cut sequences of many sizes with a workspace of exactly the size asked for."""
+    import torch
+    import mamba_ssd_chunked_varlen_gb300 as pkg
+    for lens, channels, dstate in (([3000], 8, 8), ([900, 3000, 40], 264, 16), ([2500], 2048, 16),
+                                   ([1000] * 3, 72, 64)):
+        r = Ragged(lens, seed=12)
+        v = make(r, channels, dstate, 12)
+        need = pkg.ssd_selective_scan_varlen_workspace_size(r.rows, len(lens), channels, dstate)
+        wide = torch.full((need + (1 << 16),), 77, dtype=torch.uint8, device="cuda")
+        y, pool = torch.empty_like(v["x"]), v["pool"].clone()
+        call(r, v, y, pool, workspace=wide[:need])
+        assert (wide[need:] == 77).all() and r.errors.item() == 0
+
+
+def test_far_slots():
+    """A slot past 2^31 elements, of single tokens and of a prompt that is cut."""
+    import torch
+    channels, dstate = 1 << 16, 16
+    slots = (1 << 31) // (channels * dstate) + 3
+    pool = torch.zeros(slots, channels, dstate, dtype=torch.bfloat16, device="cuda")
+    for lens in ([1], [300]):
+        r = Ragged(lens, seed=13)
+        v = make(r, channels, dstate, 13, bf16=True)
+        r.has_initial_state[:] = True
+        y, small = torch.empty_like(v["x"]), v["pool"].clone()
+        call(r, v, y, small)
+        slot = int(r.slot[0])
+        pool[-1] = v["pool"][slot]
+        r.cache_indices[0] = slots - 1
+        z = torch.empty_like(y)
+        call(r, v, z, pool)
+        assert same_bits(z, y) and same_bits(pool[-1], small[slot])
+        assert not pool[:-1].any()
+
+
 def test_stream_and_graph():
     import torch
     import mamba_ssd_chunked_varlen_gb300 as pkg
