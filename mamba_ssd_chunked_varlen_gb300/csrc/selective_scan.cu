@@ -40,7 +40,7 @@ constexpr int kScanWarps = 4;
 constexpr int kScanThreads = kScanWarps * 32;
 constexpr int kBlock = 16;            // tokens of a block
 constexpr int kStages = 4;            // blocks in shared memory
-constexpr int kShort = 7;             // tokens of a sequence that goes without shared memory
+constexpr int kFew = 8;               // tokens of a sequence that goes without shared memory
 
 constexpr int kStates = 8;            // states of a lane
 constexpr int kMinChunk = 64;         // tokens of a chunk at least
@@ -72,6 +72,7 @@ struct SelParams {
     int32_t y_stride, x_stride, dt_stride, b_stride, c_stride, z_stride;
     int32_t channels, tiles;          // tiles of a CTA's channels
     int32_t chunk, warps;             // smallest chunk (0: nothing is cut), warps of a sequence
+    int32_t few;                      // tokens of the sequences that the kernel of few takes
     int32_t softplus, pool_bf16;
 };
 
@@ -100,8 +101,8 @@ __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int w
     return fmaxf(80.f * longest, (0.086f * whole + 0.115f * cut) * warps) + (cut > 0 ? 6000.f : 0.f);
 }
 
-// Lists the chunks: `count` of `len` tokens a sequence, the last one shorter.  Which lengths
-// are cut is up to sel_cost, by powers of two.
+// Lists the chunks of the sequences of more than p.few tokens: `count` of `len` tokens a
+// sequence, the last one shorter.  Which lengths are cut is up to sel_cost, by powers of two.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanSizes = 16;        // powers of two that are told apart
 
@@ -140,6 +141,8 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
                 bad = true;
                 continue;
             }
+            if (end - begin <= p.few)
+                continue;
             atomicAdd(&s_tokens[sel_size(end - begin)], end - begin);
             atomicMax(&s_longest[sel_size(end - begin)], end - begin);
         }
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
     const int32_t shortest = s_cut;
     auto chunks = [&](int b, int &count) {
         count = 0;
-        if (!rows(b, begin, end))
+        if (!rows(b, begin, end) || end - begin <= p.few)
             return 0;
         len = end - begin;
         count = 1;
@@ -774,7 +777,7 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel
         if (unit >= p.header->units)
             return;
         u = p.units[unit];
-    } else if (!seq_rows(p.s.qsl, p.s.total_len, p.s.errors, unit, u.begin, u.end)) {
+    } else if (!seq_rows(p.s.qsl, p.s.total_len, p.s.errors, unit, u.begin, u.end) || u.end - u.begin <= p.few) {
         return;
     }
     SelLane me;
@@ -801,7 +804,7 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel
             load_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
     }
     float total = 0.f;
-    if (u.end - u.begin > kShort)
+    if (u.end - u.begin > kFew)
         sel_tokens<N, kGate, true>(p, *reinterpret_cast<SelShared<N> *>(smem), me, u.begin, u.end, me_at.col0, D,
                                    bias, total);
     else
@@ -810,16 +813,16 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel
         store_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
 }
 
-// Single tokens, as a rule.  A CTA takes every `groups`-th sequence for its tile of channels
-// and looks kScanThreads of them up at once; its warps are on their own otherwise, each with
-// the states and first tokens of two sequences in registers, one on its way while it works
-// on the other.  (A sequence's further tokens come when they are due.)
+// Sequences of at most p.few tokens, single ones as a rule.  A CTA takes every `groups`-th
+// sequence for its tile of channels and looks kScanThreads of them up at once; its warps
+// are on their own otherwise, each with the states and first tokens of kAhead sequences in
+// registers, on their way while it works on one.
 constexpr int kStepResident = 6;      // CTAs of an SM
 constexpr int kAhead = 2;             // sequences that a warp holds
 
 struct alignas(16) SelSequence {
     uint32_t slot;                    // or SSD_NO_SLOT
-    int32_t begin, tokens;            // (tokens < 0: its offsets are none)
+    int32_t begin, tokens;            // (tokens < 0: not this kernel's, or its offsets are none)
     int32_t has;                      // an initial state
 };
 
@@ -915,6 +918,8 @@ __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_ke
         }
         if (it.q.tokens > 0) {
             step(it.token, it.q.begin);
+            // (loading a further token ahead would cost registers that the others need: 96
+            // single tokens 28 us instead of 22)
             for (int i = 1; i < it.q.tokens; ++i)
                 step(load_token(it.q.begin + i), it.q.begin + i);
         }
@@ -942,8 +947,8 @@ __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_ke
             if (seq_rows(p.s.qsl, p.s.total_len, p.s.errors, b, begin, end)) {
                 q.slot = static_cast<uint32_t>(seq_slot(p.s, b));
                 q.begin = begin;
-                q.tokens = end - begin;
-                q.has = q.slot != SSD_NO_SLOT && p.s.has_init && p.s.has_init[b];
+                q.tokens = end - begin <= p.few ? end - begin : -1;
+                q.has = q.tokens >= 0 && q.slot != SSD_NO_SLOT && p.s.has_init && p.s.has_init[b];
             }
             s_seq[tid] = q;
         }
@@ -1008,12 +1013,22 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     if (cudaGetDevice(&device) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
         return cudaErrorInvalidDevice;
-    // Two tokens a sequence on average: most are alone (96 tokens of 96 sequences, 8,192
-    // channels: 22 us, in the other kernel 48).  No more CTAs than are resident at once.
-    if (p.s.total_len <= 2 * static_cast<int64_t>(p.s.batch)) {
+    // Where most sequences have few tokens, those have a kernel of their own, without shared
+    // memory or a list (96 of two tokens, 8,192 channels: 44 us with both kernels, 63 in the other
+    // one alone; 24 sequences of 72 tokens on average, twenty of them of one: 69.5 and 65.9).  It
+    // takes all of them, whatever their lengths, when there are no more tokens than sequences,
+    // and a lone one if it is that short.  No more CTAs than are resident at once.
+    const bool alone = p.s.total_len <= p.s.batch || (p.s.batch == 1 && p.s.total_len <= kFew);
+    p.few = alone ? INT32_MAX
+            : p.s.batch > 1 && p.s.total_len <= int64_t{kFew} * p.s.batch ? kFew
+                                                                          : -1;
+    if (p.few >= 0) {
         const int64_t groups = std::min<int64_t>(p.s.batch, std::max(1, kStepResident * sms / p.tiles));
-        return launch_pdl(p.pool_bf16 ? selective_step_kernel<N, kGate, true> : selective_step_kernel<N, kGate, false>,
-                          dim3(static_cast<unsigned>(p.tiles * groups)), kScanThreads, stream, p);
+        const cudaError_t e =
+            launch_pdl(p.pool_bf16 ? selective_step_kernel<N, kGate, true> : selective_step_kernel<N, kGate, false>,
+                       dim3(static_cast<unsigned>(p.tiles * groups)), kScanThreads, stream, p);
+        if (e != cudaSuccess || alone)
+            return e;
     }
     // Calls of few tokens are not cut, and neither are those of several sequences that have
     // warps for two thirds of the schedulers each: cutting gains 5 % at best, but the list,

@@ -144,6 +144,35 @@ def test_chunks(lens, channels, dstate):
     check(Ragged(lens, seed=len(lens) + 1, rows=sum(lens) + 70, none=(0,)), channels, dstate, bf16=True)
 
 
+# batches of few tokens with a longer sequence, and of more sequences than a plan's or a CTA's
+# threads
+@pytest.mark.parametrize("lens", [[1, 8, 9, 2, 40, 0, 1, 1, 1], [8] * 5, [9, 8, 7, 1, 1], [3] * 70 + [200] + [1] * 30,
+                                  [0] * 30 + [25], [3] * 600 + [150, 0, 1, 9], [1, 20] * 300])
+def test_few_tokens(lens):
+    check(Ragged(lens, seed=len(lens)), 24, 16, seed=3)
+    check(Ragged(lens, seed=len(lens), none=(1, len(lens) - 1)), 40, 8, seed=4, bf16=True, gate=False)
+
+
+def test_more_sequences_than_are_looked_up_at_once():
+    """1,100 single tokens, then 1,100 of up to two, in one call and in parts: the same bits."""
+    import torch
+    n, channels, dstate = 1100, 2048, 64
+    for lens in ([1] * n, [1, 2] * (n // 2), [1, 0, 1, 2] * (n // 4)):
+        r = Ragged(lens, seed=14)
+        v = make(r, channels, dstate, 14, bf16=True)
+        y, pool = torch.empty_like(v["x"]), v["pool"].clone()
+        call(r, v, y, pool)
+        z, other = torch.empty_like(y), v["pool"].clone()
+        for lo in range(0, n, 220):
+            rows = slice(int(r.start[lo]), int(r.start[lo + 220]))
+            part = Ragged(lens[lo:lo + 220], seed=14)
+            part.slots = r.slots
+            part.cache_indices.copy_(r.cache_indices[lo:lo + 220])
+            part.has_initial_state.copy_(r.has_initial_state[lo:lo + 220])
+            call(part, {k: t[rows] if k in ("x", "dt", "B", "C", "z") else t for k, t in v.items()}, z[rows], other)
+        assert same_bits(z, y) and same_bits(other, pool) and r.errors.item() == 0
+
+
 @pytest.mark.parametrize("channels", [8, 56, 64, 136, 520])
 @pytest.mark.parametrize("dstate", [8, 16, 32, 64])
 def test_channels(channels, dstate):
