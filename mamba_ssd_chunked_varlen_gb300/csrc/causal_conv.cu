@@ -172,7 +172,29 @@ __global__ void __launch_bounds__(kConvWarps * 32, 7) conv_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j + 1 < kWidth; ++j)
             shift_in(in, before[j]);
+        if (rows == 0xffffffffu) {
+            // all of the tile's rows, as a rule: no tests, addresses go by steps
+            const __nv_bfloat16 *xp = p.x + (t0 + kConvAhead) * p.x_stride + c;
+            __nv_bfloat16 *yp = p.y + t0 * p.y_stride + c;
 #pragma unroll 2
+            for (int i0 = 0; i0 < kConvRows; i0 += kConvAhead) {
+                if (i0 + kConvAhead < kConvRows) {
+#pragma unroll
+                    for (int i = 0; i < kConvAhead; ++i) {
+                        next[i] = *reinterpret_cast<const uint2 *>(xp);
+                        xp += p.x_stride;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kConvAhead; ++i) {
+                    shift_in(in, raw[i]);
+                    *reinterpret_cast<uint2 *>(yp) = w.template row<kSilu>(in);
+                    yp += p.y_stride;
+                    raw[i] = next[i];
+                }
+            }
+            return;
+        }
         for (int i0 = 0; i0 < kConvRows; i0 += kConvAhead) {
             fetch(next, i0 + kConvAhead);
 #pragma unroll
