@@ -15,9 +15,9 @@
 // the states take the two one after the other.  Each of a channel's lanes makes the
 // steps of its share of a group's pairs, a group ahead and two at a time as well, and hands
 // them over through shared memory; its share of the sums comes back from a reduction that
-// halves the sums as it halves the lanes.  The CTA copies blocks of 16 tokens to shared
-// memory three blocks ahead and lays their B and C out in fp32, a pair's two values side by
-// side, so that a lane reads four operands at once.
+// halves the sums as it halves the lanes.  The CTA copies blocks of 16 or 32 tokens to
+// shared memory two or three blocks ahead and lays their B and C out in fp32, a pair's two
+// values side by side, so that a lane reads four operands at once.
 //
 // A sequence that would keep too few warps busy is cut into chunks (sel_chunk).  A first
 // kernel makes the states alone that each chunk but the last leads to from zero (the first:
@@ -38,8 +38,7 @@ namespace {
 
 constexpr int kScanWarps = 4;
 constexpr int kScanThreads = kScanWarps * 32;
-constexpr int kBlock = 16;            // tokens of a block
-constexpr int kStages = 4;            // blocks in shared memory
+constexpr int kChunkStep = 16;        // chunks are multiples of so many tokens
 constexpr int kFew = 8;               // tokens of a sequence that goes without shared memory
 
 constexpr int kStates = 8;            // states of a lane
@@ -86,8 +85,8 @@ inline int64_t sel_warps(int32_t channels, int32_t dstate)
 inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 {
     const int64_t tokens = (total_len * sel_warps(channels, dstate) + kFullWarps - 1) / kFullWarps;
-    return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(kMinChunk, (tokens + kBlock - 1) / kBlock * kBlock),
-                                                  INT32_MAX / 2));
+    const int64_t steps = (tokens + kChunkStep - 1) / kChunkStep;
+    return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(kMinChunk, steps * kChunkStep), INT32_MAX / 2));
 }
 
 // What a call takes, in ns, whose sequences of some length on are cut: its longest whole
@@ -95,7 +94,7 @@ inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 // warps, while they find room; a token and warp of a whole sequence 0.086, of a cut one
 // (whose states are made twice) 0.115; the additional kernel 6,000.  (One sequence of 4,096
 // tokens, 2,048 channels: 263 us whole, 78 cut; of 9,763 tokens, 8,192 channels: 604 and 575;
-// two prompts of 9,763 tokens: 431 and 540.)
+// two prompts of 9,763 tokens: 407 and 540.)
 __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int warps)
 {
     return fmaxf(80.f * longest, (0.086f * whole + 0.115f * cut) * warps) + (cut > 0 ? 6000.f : 0.f);
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
         count = 1;
         if (len >= shortest) {
             const int32_t n = len / p.chunk;
-            len = ((len + n - 1) / n + kBlock - 1) / kBlock * kBlock;
+            len = ((len + n - 1) / n + kChunkStep - 1) / kChunkStep * kChunkStep;
             count = (end - begin + len - 1) / len;
         }
         return kPlanSizes - 1 - sel_size(len);      // long ones first
@@ -358,8 +357,9 @@ __device__ __forceinline__ void store_states(void *pool, bool bf16, int64_t at, 
 // ---------------------------------------------------------------- lanes
 // Shared memory of a CTA.  Rows are padded so that the lanes of a warp that read
 // several tokens at once find them in different banks.
-template <int N>
+template <int N, int kBlock>
 struct SelShared {
+    static constexpr int kStages = kBlock == 16 ? 4 : 3;        // blocks
     static constexpr int kLanes = N / kStates;                  // lanes of a channel
     static constexpr int kChannels = 32 / kLanes;               // channels of a warp
     static constexpr int kCols = kScanWarps * kChannels;        // of the CTA
@@ -463,13 +463,14 @@ __device__ __forceinline__ uint64_t reduce_pairs(uint64_t *v, int part)
 
 // Tokens [begin, end) of one sequence by a CTA: the lane's states over them and, with
 // kOut, their y; else the sum of the channel's steps in `total`.
-template <int N, bool kGate, bool kOut>
-__device__ __forceinline__ void sel_tokens(const SelParams &p, SelShared<N> &s, SelLane &me, int begin, int end,
+template <int N, bool kGate, bool kOut, int kBlock>
+__device__ __forceinline__ void sel_tokens(const SelParams &p, SelShared<N, kBlock> &s, SelLane &me, int begin, int end,
                                            int col0, float D, float bias, float &total)
 {
-    using Shared = SelShared<N>;
+    using Shared = SelShared<N, kBlock>;
     constexpr int kLanes = Shared::kLanes, kChannels = Shared::kChannels, kCols = Shared::kCols;
-    constexpr int kGroup = Shared::kGroup, kGroups = kBlock / kGroup;
+    constexpr int kGroup = Shared::kGroup, kGroups = kBlock / kGroup, kStages = Shared::kStages;
+    static_assert(kGroups == 1 || kGroups % 2 == 0);
     constexpr int kMine = kGroup / 2 / kLanes;       // pairs of a group that a lane makes the steps of
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = lane / kChannels, in_warp = lane % kChannels, col = warp * kChannels + in_warp;
@@ -655,10 +656,14 @@ __device__ __forceinline__ void sel_tokens(const SelParams &p, SelShared<N> &s, 
             continue;
         }
         int g = 0;
-        if (kGroups > 1 && n >= kGroup) {
-            group(k, 0, s.steps[0][warp], keep[0]);
-            g = kGroup;
-        }
+        if constexpr (kGroups > 1)
+            for (int from = 0; g + kGroup <= n; g += kGroup, from ^= 1) {
+                make_steps(now, g + kGroup, made, keep[1]);
+                group(k, g, s.steps[from][warp], keep[0]);
+                hand_over(made, s.steps[from ^ 1][warp]);
+                keep[0] = keep[1];
+                __syncwarp();
+            }
         for (; g < n; ++g) {      // the sequence's last tokens, fewer than a group
             const float xt = __bfloat162float(now.x[g][col]), d = step(now.dt[g][col]);
             float sum = me.token(d, d * xt, &now.B[g][part * kStates], &now.C[g][part * kStates]);
@@ -714,10 +719,10 @@ struct SelPlace {
 
     __device__ __forceinline__ SelPlace(const SelParams &p, int tile)
     {
-        constexpr int kChannels = SelShared<N>::kChannels;
+        constexpr int kChannels = SelShared<N, 16>::kChannels;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         part = lane / kChannels;
-        col0 = tile * SelShared<N>::kCols;
+        col0 = tile * SelShared<N, 16>::kCols;
         ch = col0 + warp * kChannels + lane % kChannels;
         valid = ch < p.channels;
         ch = valid ? ch : 0;
@@ -753,7 +758,7 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_states_kern
         }
     }
     float total = 0.f;
-    sel_tokens<N, false, false>(p, *reinterpret_cast<SelShared<N> *>(smem), me, u.begin, u.end, me_at.col0, 0.f,
+    sel_tokens<N, false, false>(p, *reinterpret_cast<SelShared<N, 16> *>(smem), me, u.begin, u.end, me_at.col0, 0.f,
                                 p.dt_bias ? p.dt_bias[me_at.ch] : 0.f, total);
     if (!me_at.valid)
         return;
@@ -764,8 +769,8 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_states_kern
 
 // The tokens of a chunk, as a rule of a whole sequence.  (With the CTAs of an SM asked for:
 // without, ptxas keeps to 80 registers and orders the code for that, 560 us for two
-// prompts of 9,763 tokens instead of 430.)
-template <int N, bool kGate>
+// prompts of 9,763 tokens instead of 430, with blocks of 16 tokens.)
+template <int N, bool kGate, int kBlock>
 __global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel(const __grid_constant__ SelParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -805,7 +810,7 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel
     }
     float total = 0.f;
     if (u.end - u.begin > kFew)
-        sel_tokens<N, kGate, true>(p, *reinterpret_cast<SelShared<N> *>(smem), me, u.begin, u.end, me_at.col0, D,
+        sel_tokens<N, kGate, true>(p, *reinterpret_cast<SelShared<N, kBlock> *>(smem), me, u.begin, u.end, me_at.col0, D,
                                    bias, total);
     else
         sel_few<N, kGate>(p, me, u.begin, u.end, me_at.ch, me_at.valid, D, bias);
@@ -829,7 +834,7 @@ struct alignas(16) SelSequence {
 template <int N, bool kGate, bool kBf16>
 __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_kernel(const __grid_constant__ SelParams p)
 {
-    constexpr int kChannels = SelShared<N>::kChannels;
+    constexpr int kChannels = SelShared<N, 16>::kChannels;
     __shared__ SelSequence s_seq[kScanThreads];
     const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
     const int groups = gridDim.x / p.tiles, tid = threadIdx.x;
@@ -1006,9 +1011,8 @@ size_t sel_bytes(int64_t total_len, int32_t batch, int32_t channels, int32_t dst
 template <int N, bool kGate>
 cudaError_t launch(SelParams &p, cudaStream_t stream)
 {
-    using Shared = SelShared<N>;
-    constexpr int kBytes = sizeof(Shared);
-    p.tiles = (p.channels + Shared::kCols - 1) / Shared::kCols;
+    constexpr int kCols = SelShared<N, 16>::kCols, kBytes = sizeof(SelShared<N, 16>);
+    p.tiles = (p.channels + kCols - 1) / kCols;
     int device = 0, sms = 0;
     if (cudaGetDevice(&device) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
@@ -1033,15 +1037,27 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     // Calls of few tokens are not cut, and neither are those of several sequences that have
     // warps for two thirds of the schedulers each: cutting gains 5 % at best, but the list,
     // the idle CTAs and the other order of the rest cost more (two prompts of 9,763 tokens,
-    // 8,192 channels: 473 us instead of 440).
+    // 8,192 channels: 473 us instead of 430).
     const bool may_cut = p.s.total_len >= 2 * int64_t{p.chunk} && (p.s.batch == 1 || 3 * p.warps < 8 * sms);
     const int64_t ends = may_cut ? sel_ends(p.s.total_len, p.chunk) : 0;
     if (!may_cut)
         p.chunk = 0;
     const int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
     const bool listed = ends || whole > int64_t{kResident} * sms;
-    static SmemOptIn s_scan, s_states;
-    cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(selective_scan_kernel<N, kGate>), s_scan);
+    static SmemOptIn s_scan, s_long, s_states;
+    // At most two CTAs an SM: blocks of 32 tokens, fewer barriers for more shared memory (two
+    // prompts of 9,763 tokens, 8,192 channels: 429 us with 16, 405 with 32; with four CTAs an
+    // SM, 8 of 1,000 tokens and 5,120 channels: 214 and 227).
+    if (!listed && whole <= 2 * sms) {
+        constexpr int kLong = sizeof(SelShared<N, 32>);
+        p.units = nullptr;
+        const cudaError_t e =
+            ensure_max_smem(reinterpret_cast<const void *>(selective_scan_kernel<N, kGate, 32>), s_long);
+        return e != cudaSuccess ? e
+                                : launch_pdl_smem(selective_scan_kernel<N, kGate, 32>, dim3(static_cast<unsigned>(whole)),
+                                                  kScanThreads, kLong, stream, p);
+    }
+    cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(selective_scan_kernel<N, kGate, 16>), s_scan);
     if (listed && e == cudaSuccess)
         e = launch_pdl(selective_plan_kernel, dim3(1), kPlanThreads, stream, p);
     if (ends && e == cudaSuccess) {
@@ -1053,7 +1069,7 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     if (!listed)
         p.units = nullptr;
     if (e == cudaSuccess)
-        e = launch_pdl_smem(selective_scan_kernel<N, kGate>, dim3(static_cast<unsigned>(p.tiles * ends + whole)),
+        e = launch_pdl_smem(selective_scan_kernel<N, kGate, 16>, dim3(static_cast<unsigned>(p.tiles * ends + whole)),
                             kScanThreads, kBytes, stream, p);
     return e;
 }

@@ -146,6 +146,15 @@ def test_chunks(lens, channels, dstate):
 
 # batches of few tokens with a longer sequence, and of more sequences than a plan's or a CTA's
 # threads
+@pytest.mark.parametrize("lens", [[101, 60], [32, 128], [15, 161], [200, 0], [50, 33, 101, 17]])
+@pytest.mark.parametrize("dstate", [8, 16, 32, 64])
+def test_many_channels_in_whole_sequences(lens, dstate):
+    """So many warps a sequence that nothing is cut: two sequences are two CTAs an SM at
+    most, four of them more."""
+    check(Ragged(lens, seed=dstate), 104_960 // dstate, dstate, seed=len(lens), gate=dstate != 8,
+          bf16=dstate == 32)
+
+
 @pytest.mark.parametrize("lens", [[1, 8, 9, 2, 40, 0, 1, 1, 1], [8] * 5, [9, 8, 7, 1, 1], [3] * 70 + [200] + [1] * 30,
                                   [0] * 30 + [25], [3] * 600 + [150, 0, 1, 9], [1, 20] * 300])
 def test_few_tokens(lens):
