@@ -60,9 +60,17 @@ __device__ __forceinline__ void reduce(float &v, uint32_t &m, float2 *scratch)
     }
 }
 
+// CTAs of an SM that registers are to be left for.
+template <int kType, int kIn>
+constexpr int norm_resident(int threads)
+{
+    return threads == 1024 ? 1 : threads == kNormThreads ? 8 : kIn == kPlain && kType == SSD_KV_BF16 ? 3 : 2;
+}
+
 // kLanes: lanes of a segment, 0 for a CTA; kThreads: threads of a CTA at most.
 template <int kType, int kIn, int kVecs, int kLanes, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : kThreads == 128 ? 8 : kIn == kPlain && kType == SSD_KV_BF16 ? 3 : 2) norm_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(kThreads, norm_resident<kType, kIn>(kThreads))
+norm_kernel(const __grid_constant__ NormParams p)
 {
     constexpr bool kCodes = kType != SSD_KV_BF16, kEarly = kCodes && kLanes == 0;
     __shared__ float2 s_part[2][32];

@@ -205,7 +205,7 @@ def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, h
     f = _functions()
     shape, wshape, bf16, f32 = x.shape, weight.shape, f.bf16, f.f32
     device = x.get_device()
-    if len(shape) == 2 and len(wshape) == 2 and device >= 0:
+    if len(shape) == 2 and len(wshape) == 2 and conv_pool.dim() == 3 and device >= 0:
         total, channels = shape
         width, max_slots = wshape[1], conv_pool.shape[0]
         where, batch = _slots_fast(f, query_start_loc, has_initial_state, cache_indices, errors, device)
@@ -221,8 +221,9 @@ def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, h
                          *where[:3], total, batch, channels, width, max_slots, 0, 0, bool(silu), where[3])
     # rows with a pitch of their own, or something is wrong
     device = _device(x, "x")
-    if x.dim() != 2 or weight.dim() != 2:
-        raise ValueError("x must have shape (rows, channels) and weight (channels, width)")
+    if x.dim() != 2 or weight.dim() != 2 or conv_pool.dim() != 3:
+        raise ValueError("x must have shape (rows, channels), weight (channels, width) and conv_pool "
+                         "(slots, width - 1, channels)")
     total, channels = shape
     width = weight.shape[1]
     slots, batch = _slots(f, query_start_loc, has_initial_state, cache_indices, device)
@@ -268,7 +269,7 @@ def ssd_selective_scan_varlen_fwd(y, x, dt, A, B, C, D, z, dt_bias, ssm_pool, qu
         raise ValueError("workspace is required (see alloc_selective_scan_workspace)")
     shape, ashape, bf16, f32 = x.shape, A.shape, f.bf16, f.f32
     device = x.get_device()
-    if len(shape) == 2 and len(ashape) == 2 and device >= 0:
+    if len(shape) == 2 and len(ashape) == 2 and ssm_pool.dim() == 3 and device >= 0:
         total, channels = shape
         dstate, max_slots, kind = ashape[1], ssm_pool.shape[0], ssm_pool.dtype
         bc = (total, dstate)
@@ -295,8 +296,9 @@ def ssd_selective_scan_varlen_fwd(y, x, dt, A, B, C, D, z, dt_bias, ssm_pool, qu
                          workspace.data_ptr(), workspace.numel(), where[3])
     # rows with a pitch of their own, or something is wrong
     device = _device(x, "x")
-    if x.dim() != 2 or A.dim() != 2:
-        raise ValueError("x must have shape (rows, channels) and A (channels, dstate)")
+    if x.dim() != 2 or A.dim() != 2 or ssm_pool.dim() != 3:
+        raise ValueError("x must have shape (rows, channels), A (channels, dstate) and ssm_pool "
+                         "(slots, channels, dstate)")
     total, channels = shape
     dstate = A.shape[1]
     slots, batch = _slots(f, query_start_loc, has_initial_state, cache_indices, device)
@@ -325,7 +327,8 @@ def ssd_rms_norm_fwd(y, x, weight, *, residual=None, gate=None, scale=None, ngro
 
     x, residual, gate (rows, dim) bf16, each row contiguous, any row pitch that is a
     multiple of 8 elements; weight (dim,) fp32 or None; y (rows, dim) bf16 (it may
-    be x or gate), or float8_e4m3fn or int8 codes with scale (rows, ngroups) fp32."""
+    be x or gate), or float8_e4m3fn or int8 codes with scale (rows, ngroups) fp32; eps
+    from 2^-80 to 1."""
     f = _functions()
     device = _device(x, "x")
     shape = x.shape
