@@ -834,28 +834,39 @@ struct alignas(16) SelSequence {
 template <int N, bool kGate, bool kBf16>
 __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_kernel(const __grid_constant__ SelParams p)
 {
-    constexpr int kChannels = SelShared<N, 16>::kChannels;
+    // Neighbouring lanes are a channel's, and a load of theirs takes what lies side by side: 16
+    // bytes of states each, four fp32 or eight bf16.
+    constexpr int kLanes = N / kStates;
+    constexpr int kLoads = kBf16 ? 1 : 2;     // of 16 bytes, of a lane's states
     __shared__ SelSequence s_seq[kScanThreads];
-    const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
+    const int part = threadIdx.x % kLanes;
+    const int there = static_cast<int>(blockIdx.x % p.tiles) * SelShared<N, 16>::kCols + threadIdx.x / kLanes;
+    const bool valid = there < p.channels;    // (lanes past the last channel follow one that is there)
+    const int ch = valid ? there : 0;
+    const int64_t states = static_cast<int64_t>(p.channels) * N;
+    // the first state of the lane's four with index i
+    auto four = [&](int i) { return kBf16 ? part * kStates + 4 * i : (i * kLanes + part) * 4; };
     const int groups = gridDim.x / p.tiles, tid = threadIdx.x;
     pdl_wait();
     struct Token {
-        uint4 B, C;
+        uint2 B[2], C[2];
         __nv_bfloat16 x, dt, z;
     };
     const __nv_bfloat16 none = __float2bfloat16_rn(0.f);
     auto load_token = [&](int64_t t) {
         Token v;
-        v.x = p.x[t * p.x_stride + me_at.ch];
-        v.dt = p.dt[t * p.dt_stride + me_at.ch];
-        v.z = kGate ? p.z[t * p.z_stride + me_at.ch] : none;
-        v.B = *reinterpret_cast<const uint4 *>(p.B + t * p.b_stride + me_at.part * kStates);
-        v.C = *reinterpret_cast<const uint4 *>(p.C + t * p.c_stride + me_at.part * kStates);
+        v.x = p.x[t * p.x_stride + ch];
+        v.dt = p.dt[t * p.dt_stride + ch];
+        v.z = kGate ? p.z[t * p.z_stride + ch] : none;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v.B[i] = *reinterpret_cast<const uint2 *>(p.B + t * p.b_stride + four(i));
+            v.C[i] = *reinterpret_cast<const uint2 *>(p.C + t * p.c_stride + four(i));
+        }
         return v;
     };
-    constexpr int kLoads = kBf16 ? 1 : 2;     // of 16 bytes, of a lane's states
     using Element = std::conditional_t<kBf16, __nv_bfloat16, float>;
-    Element *pool = static_cast<Element *>(p.pool) + me_at.at;
+    Element *pool = static_cast<Element *>(p.pool) + static_cast<int64_t>(ch) * N;
     struct Item {
         SelSequence q;
         uint4 state[kLoads];
@@ -865,7 +876,7 @@ __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_ke
         it.q = i < count ? s_seq[i] : SelSequence{SSD_NO_SLOT, 0, -1, 0};
 #pragma unroll
         for (int k = 0; k < kLoads; ++k)
-            it.state[k] = it.q.has ? reinterpret_cast<const uint4 *>(pool + it.q.slot * me_at.states)[k]
+            it.state[k] = it.q.has ? *reinterpret_cast<const uint4 *>(pool + it.q.slot * states + four(k))
                                    : make_uint4(0, 0, 0, 0);
         if (it.q.tokens > 0)
             it.token = load_token(it.q.begin);
@@ -873,17 +884,18 @@ __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_ke
     uint64_t a[kStates / 2];                  // A log2(e), two states each
 #pragma unroll
     for (int k = 0; k < kStates / 4; ++k) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + me_at.at) + k);
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + static_cast<int64_t>(ch) * N + four(k)));
         a[2 * k] = ptx::pack2(v.x * kLog2e, v.y * kLog2e);
         a[2 * k + 1] = ptx::pack2(v.z * kLog2e, v.w * kLog2e);
     }
-    const float D = p.D ? p.D[me_at.ch] : 0.f, bias = p.dt_bias ? p.dt_bias[me_at.ch] : 0.f;
+    const float D = p.D ? p.D[ch] : 0.f, bias = p.dt_bias ? p.dt_bias[ch] : 0.f;
     uint64_t h[kStates / 2];
     auto step = [&](const Token &v, int64_t t) {
         const float x = __bfloat162float(v.x), raw = __bfloat162float(v.dt) + bias;
         const float dt = p.softplus ? step_of(raw) : raw, u = dt * x;
         const uint64_t dt2 = ptx::pack2(dt, dt), u2 = ptx::pack2(u, u);
-        const uint32_t B[4] = {v.B.x, v.B.y, v.B.z, v.B.w}, C[4] = {v.C.x, v.C.y, v.C.z, v.C.w};
+        const uint32_t B[4] = {v.B[0].x, v.B[0].y, v.B[1].x, v.B[1].y};
+        const uint32_t C[4] = {v.C[0].x, v.C[0].y, v.C[1].x, v.C[1].y};
         uint64_t sum2 = 0;
 #pragma unroll
         for (int k = 0; k < kStates / 2; ++k) {
@@ -898,13 +910,13 @@ __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_ke
         ptx::unpack2(sum2, sum, other);
         sum += other;
 #pragma unroll
-        for (int o = kChannels; o < 32; o <<= 1)
+        for (int o = 1; o < kLanes; o <<= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
         float y = fmaf(D, x, sum);
         if constexpr (kGate)
             y *= silu_f32(__bfloat162float(v.z));
-        if (me_at.part == 0 && me_at.valid)
-            p.y[t * p.y_stride + me_at.ch] = __float2bfloat16_rn(y);
+        if (part == 0 && valid)
+            p.y[t * p.y_stride + ch] = __float2bfloat16_rn(y);
     };
     auto work = [&](const Item &it) {
         if (it.q.tokens < 0)
@@ -928,18 +940,18 @@ __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_ke
             for (int i = 1; i < it.q.tokens; ++i)
                 step(load_token(it.q.begin + i), it.q.begin + i);
         }
-        if (it.q.slot == SSD_NO_SLOT || !me_at.valid)
+        if (it.q.slot == SSD_NO_SLOT || !valid)
             return;
         float v[kStates];
 #pragma unroll
         for (int k = 0; k < kStates / 2; ++k)
             ptx::unpack2(h[k], v[2 * k], v[2 * k + 1]);
-        Element *to = pool + it.q.slot * me_at.states;
+        Element *to = pool + it.q.slot * states;
         if constexpr (kBf16) {
-            *reinterpret_cast<uint4 *>(to) = round8(v);
+            *reinterpret_cast<uint4 *>(to + four(0)) = round8(v);
         } else {
-            reinterpret_cast<float4 *>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4 *>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<float4 *>(to + four(0)) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(to + four(1)) = make_float4(v[4], v[5], v[6], v[7]);
         }
     };
     for (int b0 = blockIdx.x / p.tiles; b0 < p.s.batch; b0 += kScanThreads * groups) {
