@@ -14,6 +14,7 @@
 // elements, as in kv_cache.cu; a half's partner comes from another lane by shuffles.  Rows go
 // in steps of one tensor, so that only those that become codes are looked through for
 // their largest, and a step's loads are on their way while the one before is worked on.
+#include <algorithm>
 #include <cmath>
 
 #include "attn_ptx.cuh"
@@ -22,7 +23,8 @@
 namespace ssd {
 namespace {
 
-constexpr int kRopeWarps = 8;         // tokens of a CTA
+constexpr int kRopeWarps = 4;         // tokens of a CTA
+constexpr int kRopeResident = 6;      // CTAs of an SM
 constexpr int kRopeAhead = 4;         // rows that a lane has in flight
 constexpr int kRopeNone = -1;         // cache type of the call without a cache
 
@@ -104,7 +106,7 @@ __device__ __forceinline__ void widen_pairs(const uint4 &r, uint64_t (&x)[4])
 enum RopeTensor { kQ, kK, kV };
 
 template <int kType, int kDim, bool kNeighbours>
-__global__ void __launch_bounds__(kRopeWarps * 32, 3) rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeResident) rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int kLanes = kDim / 8;           // lanes of a row
     constexpr int kAtOnce = 32 / kLanes;       // rows of the warp's one load
@@ -274,11 +276,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 3) rope_kernel(const __grid_c
 template <int kType>
 cudaError_t launch(RopeParams &p, int64_t total_len, bool neighbours, cudaStream_t stream)
 {
-    // a warp takes all of a token's rows once that gives every SM 16 warps; few tokens
-    // are spread over warps, a step each
+    // a warp takes about three of a token's steps once that gives every SM 16 warps: enough for
+    // the next one's loads to be ahead, and for a last wave that is not long (7,787 tokens of 32 and
+    // 8 heads of 128 to int8, six steps, with the reading back: 49 us whole, 45.6 in two parts, 47
+    // in three); few tokens are spread over warps, a step each
     const int step = 256 / p.c.dim * kRopeAhead, kv = (p.c.heads + step - 1) / step;
     p.steps = (p.heads + step - 1) / step + (kType == kRopeNone ? kv : 2 * kv);
-    p.part_steps = total_len >= 16 * 152 ? p.steps : 1;
+    const int parts = std::max(1, (p.steps + 1) / 3);
+    p.part_steps = total_len >= 16 * 152 ? (p.steps + parts - 1) / parts : 1;
     const dim3 grid(static_cast<unsigned>((total_len + kRopeWarps - 1) / kRopeWarps),
                     static_cast<unsigned>((p.steps + p.part_steps - 1) / p.part_steps));
     const int threads = kRopeWarps * 32;
