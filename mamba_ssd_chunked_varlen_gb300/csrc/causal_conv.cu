@@ -11,15 +11,20 @@
 // are of, and leaves out the first W - 1 tokens of each sequence; or it takes one
 // sequence, does those first tokens and moves its slot on.  So a slot is read and
 // written by one warp alone, and a batch of single tokens is all of the second kind.
+//
+// Width 4 with silu: four prompts of 22,500 tokens in all, 10,240 channels, 138 us, 98 % of the
+// measured copy rate (with four rows ahead and seven CTAs of four warps 142 us, eight channels
+// a lane 160); 100 single tokens and 156 of up to 127, 4,352 channels, 33.4 us.
 #include "attn_ptx.cuh"
 #include "layer_common.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kConvWarps = 4;         // warps of a CTA
+constexpr int kConvWarps = 2;         // warps of a CTA
+constexpr int kConvResident = 12;     // CTAs of an SM
 constexpr int kConvRows = 32;         // rows of a tile (the bits of a mask)
-constexpr int kConvAhead = 4;         // rows that a warp loads at once, one such step ahead
+constexpr int kConvAhead = 8;         // rows that a warp loads at once, one such step ahead
 
 struct ConvParams {
     SlotBatch s;
@@ -132,7 +137,7 @@ __device__ __forceinline__ void shift_in(Four (&in)[kWidth], const uint2 &raw)
 }
 
 template <int kWidth, bool kSilu>
-__global__ void __launch_bounds__(kConvWarps * 32, 7) conv_kernel(const __grid_constant__ ConvParams p)
+__global__ void __launch_bounds__(kConvWarps * 32, kConvResident) conv_kernel(const __grid_constant__ ConvParams p)
 {
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvWarps + (threadIdx.x >> 5);
