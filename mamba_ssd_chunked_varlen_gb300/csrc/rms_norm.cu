@@ -12,6 +12,8 @@
 // that max|y| is max|s w| r, and one barrier serves the sum and the largest (4,093 rows of
 // 5,120 to int8: 29.1 us with two, 27.1 with one; a warp's weights would be registers that
 // it needs, 8,191 rows of 8 gated groups to int8: 73 us with them, 68 without).
+#include <algorithm>
+
 #include "layer_common.cuh"
 
 namespace ssd {
@@ -28,7 +30,7 @@ struct NormParams {
     const __nv_bfloat16 *x, *gate;
     __nv_bfloat16 *residual;
     const float *weight;
-    int64_t segments, y_stride, x_stride, residual_stride, gate_stride;
+    int64_t rows, segments, y_stride, x_stride, residual_stride, gate_stride;
     int32_t groups, cols;            // columns of a group
     float eps;
 };
@@ -60,16 +62,16 @@ __device__ __forceinline__ void reduce(float &v, uint32_t &m, float2 *scratch)
     }
 }
 
-// CTAs of an SM that registers are to be left for.
-template <int kType, int kIn>
-constexpr int norm_resident(int threads)
-{
-    return threads == 1024 ? 1 : threads == kNormThreads ? 8 : kIn == kPlain && kType == SSD_KV_BF16 ? 3 : 2;
-}
+// Whether a CTA takes row after row of its group, whose weights it keeps, with the next row's
+// loads ahead.  (8,191 rows of 8,192 columns, a row a CTA against rows in turn: plain to int8 65
+// and 47 us, gated to bf16 65 and 61, to int8 89 and 85, with a residual to int8 80 and 76; but to
+// bf16 with a residual 78 and 88, as three CTAs of 40 registers a thread load more than two of 64.)
+constexpr bool norm_in_turn(int type, int in) { return type != SSD_KV_BF16 || in != kResidual; }
 
-// kLanes: lanes of a segment, 0 for a CTA; kThreads: threads of a CTA at most.
-template <int kType, int kIn, int kVecs, int kLanes, int kThreads>
-__global__ void __launch_bounds__(kThreads, norm_resident<kType, kIn>(kThreads))
+// kLanes: lanes of a segment, 0 for a CTA; kThreads: threads of a CTA at most; kResident: CTAs of
+// so many threads that an SM's registers are to suffice for.
+template <int kType, int kIn, int kVecs, int kLanes, int kThreads, int kResident>
+__global__ void __launch_bounds__(kThreads, kResident)
 norm_kernel(const __grid_constant__ NormParams p)
 {
     constexpr bool kCodes = kType != SSD_KV_BF16, kEarly = kCodes && kLanes == 0;
@@ -210,6 +212,124 @@ norm_kernel(const __grid_constant__ NormParams p)
     }
 }
 
+// The same for a group's rows one after the other: blockIdx.x % groups is the CTA's group.  (One
+// barrier a row: its scratch is another one than the row's before.)
+template <int kType, int kIn, int kThreads, int kResident>
+__global__ void __launch_bounds__(kThreads, kResident) norm_rows_kernel(const __grid_constant__ NormParams p)
+{
+    constexpr bool kCodes = kType != SSD_KV_BF16;
+    constexpr int kVecs = 2;
+    __shared__ float2 s_part[3][32];
+    const int step = blockDim.x * 8, group = static_cast<int>(blockIdx.x % p.groups), row_step = gridDim.x / p.groups;
+    const int col0 = group * p.cols;
+    pdl_wait();
+    float s[kVecs][8], w[kVecs][8];
+    uint4 raw[kVecs], other[kVecs];
+    const int at0 = col0 + threadIdx.x * 8;
+    auto load = [&](int64_t row) {
+        const __nv_bfloat16 *x = p.x + row * p.x_stride + at0;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            const int c = v * step + threadIdx.x * 8;
+            raw[v] = other[v] = make_uint4(0, 0, 0, 0);
+            if (c < p.cols && row < p.rows) {
+                raw[v] = *reinterpret_cast<const uint4 *>(x + v * step);
+                if constexpr (kIn == kResidual)
+                    other[v] = *reinterpret_cast<const uint4 *>(p.residual + row * p.residual_stride + col0 + c);
+                if constexpr (kIn == kGate)
+                    other[v] = *reinterpret_cast<const uint4 *>(p.gate + row * p.gate_stride + col0 + c);
+            }
+        }
+    };
+    int64_t row = blockIdx.x / p.groups;
+    load(row);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        const int c = v * step + threadIdx.x * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 f = p.weight && c < p.cols
+                                 ? __ldg(reinterpret_cast<const float4 *>(p.weight + col0 + c) + i)
+                                 : make_float4(1.f, 1.f, 1.f, 1.f);
+            w[v][4 * i] = f.x;
+            w[v][4 * i + 1] = f.y;
+            w[v][4 * i + 2] = f.z;
+            w[v][4 * i + 3] = f.w;
+        }
+    }
+    for (int turn = 0; row < p.rows; row += row_step, turn ^= 1) {
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            widen8(raw[v], s[v]);
+            if constexpr (kIn != kPlain) {
+                float o[8];
+                widen8(other[v], o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    s[v][k] = kIn == kResidual ? s[v][k] + o[k] : s[v][k] * silu_f32(o[k]);
+            }
+        }
+        load(row + row_step);
+        float sum = 0.f;
+        uint32_t top = 0;
+        auto add = [&](int v) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sum = fmaf(s[v][k], s[v][k], sum);
+                if constexpr (kCodes)
+                    top = max(top, __float_as_uint(s[v][k] * w[v][k]) & 0x7fffffffu);
+            }
+        };
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            const int c = v * step + threadIdx.x * 8;
+            if (kIn == kResidual && c < p.cols)
+                *reinterpret_cast<uint4 *>(p.residual + row * p.residual_stride + col0 + c) = round8(s[v]);
+            add(v);
+        }
+        reduce<0, kCodes>(sum, top, s_part[turn]);
+        float r = rsqrtf(sum / static_cast<float>(p.cols) + p.eps);
+        if (!(sum < __int_as_float(0x7f800000))) {     // (the same in all threads; as above)
+            sum = 0.f;
+            top = 0;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    s[v][k] *= 0x1p-80f;
+                add(v);
+            }
+            reduce<0, kCodes>(sum, top, s_part[2]);
+            r = rsqrtf(sum / static_cast<float>(p.cols));
+        }
+        float inv = 0.f;
+        bool bad = false;
+        if constexpr (kCodes) {
+            constexpr float kTop = kType == SSD_KV_INT8 ? kInt8Max : kE4m3Max;
+            const float largest = __uint_as_float(top) * r, a = fmaxf(largest, kKvTiny);
+            bad = !(largest < __int_as_float(0x7f800000));
+            inv = __fdiv_rn(kTop, a);
+            if (threadIdx.x == 0)
+                p.scale[row * p.groups + group] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(a, kTop);
+        }
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            const int c = v * step + threadIdx.x * 8;
+            const int64_t at = row * p.y_stride + col0 + c;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                s[v][k] = kCodes ? s[v][k] * w[v][k] * r : s[v][k] * r * w[v][k];
+            if (c < p.cols) {
+                if constexpr (kCodes)
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + at) =
+                        bad ? make_uint2(0, 0) : encode8<kType>(s[v], inv);
+                else
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + at) = round8(s[v]);
+            }
+        }
+    }
+}
+
 template <int kType, int kIn>
 cudaError_t launch(const NormParams &p, cudaStream_t stream)
 {
@@ -221,17 +341,33 @@ cudaError_t launch(const NormParams &p, cudaStream_t stream)
             return launch_pdl(kernel, dim3(static_cast<unsigned>((p.segments + each - 1) / each)), kNormThreads, stream,
                               p);
         };
-        return loads <= 8    ? go(norm_kernel<kType, kIn, 1, 8, kNormThreads>, 8)
-               : loads <= 16 ? go(norm_kernel<kType, kIn, 1, 16, kNormThreads>, 16)
-               : loads <= 32 ? go(norm_kernel<kType, kIn, 1, 32, kNormThreads>, 32)
-               : loads <= 64 ? go(norm_kernel<kType, kIn, 2, 32, kNormThreads>, 32)
-                             : go(norm_kernel<kType, kIn, 4, 32, kNormThreads>, 32);
+        return loads <= 8    ? go(norm_kernel<kType, kIn, 1, 8, kNormThreads, 8>, 8)
+               : loads <= 16 ? go(norm_kernel<kType, kIn, 1, 16, kNormThreads, 8>, 16)
+               : loads <= 32 ? go(norm_kernel<kType, kIn, 1, 32, kNormThreads, 8>, 32)
+               : loads <= 64 ? go(norm_kernel<kType, kIn, 2, 32, kNormThreads, 8>, 32)
+                             : go(norm_kernel<kType, kIn, 4, 32, kNormThreads, 8>, 32);
     }
-    const dim3 grid(static_cast<unsigned>(p.segments));
-    const int vecs = loads <= 2 * 512 ? 2 : kNormMaxVecs;
+    constexpr bool kInTurn = norm_in_turn(kType, kIn);
+    const int vecs = loads <= 2 * (kInTurn ? 1024 : 512) ? 2 : kNormMaxVecs;
     const int threads = (loads + 32 * vecs - 1) / (32 * vecs) * 32;
-    return vecs == 2 ? launch_pdl(norm_kernel<kType, kIn, 2, 0, 512>, grid, threads, stream, p)
-                     : launch_pdl(norm_kernel<kType, kIn, kNormMaxVecs, 0, 1024>, grid, threads, stream, p);
+    if constexpr (kInTurn)
+        if (vecs == 2) {
+            // as many CTAs as 64 registers a thread leave room for, each with rows of one group
+            int device = 0, sms = 0;
+            if (cudaGetDevice(&device) != cudaSuccess ||
+                cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+                return cudaErrorInvalidDevice;
+            const int64_t resident = static_cast<int64_t>(1024 / threads) * sms;
+            const int64_t each = std::min(std::max<int64_t>(1, resident / p.groups), p.rows);
+            const dim3 grid(static_cast<unsigned>(each * p.groups));
+            return threads <= 512 ? launch_pdl(norm_rows_kernel<kType, kIn, 512, 2>, grid, threads, stream, p)
+                                  : launch_pdl(norm_rows_kernel<kType, kIn, 1024, 1>, grid, threads, stream, p);
+        }
+    const dim3 grid(static_cast<unsigned>(p.segments));
+    if constexpr (!kInTurn)
+        if (vecs == 2)
+            return launch_pdl(norm_kernel<kType, kIn, 2, 0, 512, 3>, grid, threads, stream, p);
+    return launch_pdl(norm_kernel<kType, kIn, kNormMaxVecs, 0, 1024, 1>, grid, threads, stream, p);
 }
 
 template <int kType>
@@ -271,7 +407,7 @@ extern "C" ssd_status_t ssd_rms_norm_fwd(
         return SSD_ERR_INVALID_ARG;
     const NormParams p = {y, scale, static_cast<const __nv_bfloat16 *>(x),
                           static_cast<const __nv_bfloat16 *>(gate), static_cast<__nv_bfloat16 *>(residual),
-                          weight, rows * ngroups, y_stride, x_stride, residual_stride, gate_stride,
+                          weight, rows, rows * ngroups, y_stride, x_stride, residual_stride, gate_stride,
                           ngroups, cols, eps};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = out_type == SSD_KV_BF16       ? launch_in<SSD_KV_BF16>(p, s)

@@ -139,6 +139,33 @@ def test_ranges(kind, cols):
     run(9, cols, kind, residual=True, change=change)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("rows,groups,cols", [(701, 3, 1040), (1500, 1, 1096), (333, 1, 16384), (160, 5, 8200), (3, 200, 1032)])
+def test_rows_in_turn(kind, rows, groups, cols):
+    """More rows than CTAs at once, more groups than these, and rows of infinities, NaN and
+    squares out of range between others."""
+    def change(x, r):
+        for at, value in ((5, float("inf")), (rows // 2, 3.0e38), (rows // 2 + 1, 2.0e38), (rows - 2, float("nan"))):
+            if 0 <= at < rows:
+                x[at, at % cols] = value
+    run(rows, groups * cols, kind, groups, gate=True, seed=rows)
+    run(rows, groups * cols, kind, groups, residual=groups == 1, seed=rows, change=change if rows > 100 else None)
+
+
+@pytest.mark.parametrize("gate", [False, True])
+def test_rows_in_turn_in_place(gate):
+    import torch
+    import mamba_ssd_chunked_varlen_gb300 as pkg
+    x, z = torch.randn(2, 1100, 2 * 1160, device="cuda").bfloat16().unbind()
+    w = torch.randn(2 * 1160, device="cuda")
+    y = torch.empty_like(x)
+    pkg.ssd_rms_norm_fwd(y, x, w, gate=z if gate else None, ngroups=2)
+    for take in range(1 + gate):
+        args = [x.clone(), z.clone()]
+        pkg.ssd_rms_norm_fwd(args[take], args[0], w, gate=args[1] if gate else None, ngroups=2)
+        assert same_bits(args[take], y)
+
+
 def test_in_place():
     """y may be x or the gate."""
     import torch
