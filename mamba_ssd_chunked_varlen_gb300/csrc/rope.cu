@@ -14,6 +14,11 @@
 // elements, as in kv_cache.cu; a half's partner comes from another lane by shuffles.  Rows go
 // in steps of one tensor, so that only those that become codes are looked through for
 // their largest, and a step's loads are on their way while the one before is worked on.
+//
+// Memory bounds rows of bf16 (9,000 tokens of 16 and 16 heads of 64, 73 MB, 13.4 us, 80 % of the
+// measured copy rate with the launch; 64 and 64 heads of 128 98 %), instructions those
+// that become codes (7,787 tokens of 32 and 8 heads of 128 to int8 33 us, 176 MB: a q row's
+// lane issues 34, a k or v row's 66, and a token's angle and place 540 a warp).
 #include <algorithm>
 #include <cmath>
 

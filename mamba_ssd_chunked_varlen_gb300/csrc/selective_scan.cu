@@ -94,7 +94,7 @@ inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 // warps, while they find room; a token and warp of a whole sequence 0.086, of a cut one
 // (whose states are made twice) 0.115; the additional kernel 6,000.  (One sequence of 4,096
 // tokens, 2,048 channels: 263 us whole, 78 cut; of 9,763 tokens, 8,192 channels: 604 and 575;
-// two prompts of 9,763 tokens: 407 and 540.)
+// two prompts of 9,763 tokens in all: 407 and 540.)
 __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int warps)
 {
     return fmaxf(80.f * longest, (0.086f * whole + 0.115f * cut) * warps) + (cut > 0 ? 6000.f : 0.f);
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_states_kern
 
 // The tokens of a chunk, as a rule of a whole sequence.  (With the CTAs of an SM asked for:
 // without, ptxas keeps to 80 registers and orders the code for that, 560 us for two
-// prompts of 9,763 tokens instead of 430, with blocks of 16 tokens.)
+// prompts of 9,763 tokens in all instead of 430, with blocks of 16 tokens.)
 template <int N, bool kGate, int kBlock>
 __global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel(const __grid_constant__ SelParams p)
 {
@@ -1030,7 +1030,7 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
         return cudaErrorInvalidDevice;
     // Where most sequences have few tokens, those have a kernel of their own, without shared
-    // memory or a list (96 of two tokens, 8,192 channels: 44 us with both kernels, 63 in the other
+    // memory or a list (96 of two tokens, 8,192 channels: 39 us with both kernels, 63 in the other
     // one alone; 24 sequences of 72 tokens on average, twenty of them of one: 69.5 and 65.9).  It
     // takes all of them, whatever their lengths, when there are no more tokens than sequences,
     // and a lone one if it is that short.  No more CTAs than are resident at once.
@@ -1048,8 +1048,8 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     }
     // Calls of few tokens are not cut, and neither are those of several sequences that have
     // warps for two thirds of the schedulers each: cutting gains 5 % at best, but the list,
-    // the idle CTAs and the other order of the rest cost more (two prompts of 9,763 tokens,
-    // 8,192 channels: 473 us instead of 430).
+    // the idle CTAs and the other order of the rest cost more (two prompts of 9,763 tokens
+    // in all, 8,192 channels: 473 us instead of 430).
     const bool may_cut = p.s.total_len >= 2 * int64_t{p.chunk} && (p.s.batch == 1 || 3 * p.warps < 8 * sms);
     const int64_t ends = may_cut ? sel_ends(p.s.total_len, p.chunk) : 0;
     if (!may_cut)
@@ -1058,7 +1058,7 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     const bool listed = ends || whole > int64_t{kResident} * sms;
     static SmemOptIn s_scan, s_long, s_states;
     // At most two CTAs an SM: blocks of 32 tokens, fewer barriers for more shared memory (two
-    // prompts of 9,763 tokens, 8,192 channels: 429 us with 16, 405 with 32; with four CTAs an
+    // prompts of 9,763 tokens in all, 8,192 channels: 429 us with 16, 407 with 32; with four CTAs an
     // SM, 8 of 1,000 tokens and 5,120 channels: 214 and 227).
     if (!listed && whole <= 2 * sms) {
         constexpr int kLong = sizeof(SelShared<N, 32>);
