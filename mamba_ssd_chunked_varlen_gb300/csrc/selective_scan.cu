@@ -93,8 +93,8 @@ inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 // sequence, or all of its tokens.  Measured: a token of a whole sequence 80, whatever its
 // warps, while they find room; a token and warp of a whole sequence 0.086, of a cut one
 // (whose states are made twice) 0.115; the additional kernel 6,000.  (One sequence of 4,096
-// tokens, 2,048 channels: 263 us whole, 78 cut; of 9,763 tokens, 8,192 channels: 604 and 575;
-// two prompts of 9,763 tokens in all: 407 and 540.)
+// tokens, 2,048 channels: 263 us whole, 79 cut; of 9,763 tokens, 8,192 channels: 604 and 565;
+// two prompts of 9,763 tokens in all: 399 and 540.)
 __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int warps)
 {
     return fmaxf(80.f * longest, (0.086f * whole + 0.115f * cut) * warps) + (cut > 0 ? 6000.f : 0.f);
@@ -370,7 +370,7 @@ struct SelShared {
     Block block[kStages];
     __nv_bfloat16 y[2][kBlock][kPitch];
     // per warp, two groups: the steps and the inputs before B of a pair {d0, d1, u0, u1}
-    static constexpr int kGroup = kLanes == 8 ? 16 : 8;         // tokens of a group
+    static constexpr int kGroup = kLanes == 8 || kBlock == 32 ? 16 : 8;              // tokens of a group
     float4 steps[2][kScanWarps][kGroup / 2][kChannels];
     // per pair of tokens, [chunk][part]: two states of a part for the two tokens
     float4 B[2][kBlock / 2][kStates / 2][kLanes], C[2][kBlock / 2][kStates / 2][kLanes];
@@ -733,7 +733,7 @@ struct SelPlace {
 
 // The states and the steps' sum of the chunk before an end.
 template <int N>
-__global__ void __launch_bounds__(kScanThreads, kResident) selective_states_kernel(const __grid_constant__ SelParams p)
+__global__ void __launch_bounds__(kScanThreads, 3) selective_states_kernel(const __grid_constant__ SelParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
@@ -769,9 +769,11 @@ __global__ void __launch_bounds__(kScanThreads, kResident) selective_states_kern
 
 // The tokens of a chunk, as a rule of a whole sequence.  (With the CTAs of an SM asked for:
 // without, ptxas keeps to 80 registers and orders the code for that, 560 us for two
-// prompts of 9,763 tokens in all instead of 430, with blocks of 16 tokens.)
+// prompts of 9,763 tokens in all instead of 430, with blocks of 16 tokens.  Three asked for and
+// not the four that there are as a rule, which it orders worse: 8 of 1,000 tokens and 5,120
+// channels 211 us instead of 216.)
 template <int N, bool kGate, int kBlock>
-__global__ void __launch_bounds__(kScanThreads, kResident) selective_scan_kernel(const __grid_constant__ SelParams p)
+__global__ void __launch_bounds__(kScanThreads, kBlock == 32 ? 2 : 3) selective_scan_kernel(const __grid_constant__ SelParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
@@ -1058,7 +1060,7 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     const bool listed = ends || whole > int64_t{kResident} * sms;
     static SmemOptIn s_scan, s_long, s_states;
     // At most two CTAs an SM: blocks of 32 tokens, fewer barriers for more shared memory (two
-    // prompts of 9,763 tokens in all, 8,192 channels: 429 us with 16, 407 with 32; with four CTAs an
+    // prompts of 9,763 tokens in all, 8,192 channels: 429 us with 16, 399 with 32; with four CTAs an
     // SM, 8 of 1,000 tokens and 5,120 channels: 214 and 227).
     if (!listed && whole <= 2 * sms) {
         constexpr int kLong = sizeof(SelShared<N, 32>);
