@@ -12,9 +12,9 @@
 // sequence, does those first tokens and moves its slot on.  So a slot is read and
 // written by one warp alone, and a batch of single tokens is all of the second kind.
 //
-// Width 4 with silu: four prompts of 22,500 tokens in all, 10,240 channels, 138 us, 98 % of the
+// Width 4 with silu: four prompts of 22,500 tokens in all, 10,240 channels, 137.5 us, 98 % of the
 // measured copy rate (with four rows ahead and seven CTAs of four warps 142 us, eight channels
-// a lane 160); 100 single tokens and 156 of up to 127, 4,352 channels, 33.4 us.
+// a lane 160); 100 single tokens and 156 of up to 127, 4,352 channels, 33.1 us.
 #include "attn_ptx.cuh"
 #include "layer_common.cuh"
 
@@ -22,7 +22,7 @@ namespace ssd {
 namespace {
 
 constexpr int kConvWarps = 2;         // warps of a CTA
-constexpr int kConvResident = 12;     // CTAs of an SM
+constexpr int kConvResident = 11;     // CTAs of an SM
 constexpr int kConvRows = 32;         // rows of a tile (the bits of a mask)
 constexpr int kConvAhead = 8;         // rows that a warp loads at once, one such step ahead
 
