@@ -20,9 +20,11 @@
 // values side by side, so that a lane reads four operands at once.
 //
 // A sequence that would keep too few warps busy is cut into chunks (sel_chunk).  A first
-// kernel makes the states alone that each chunk but the last leads to from zero (the first:
-// from the sequence's own), and the sums of their steps; in the second a chunk joins what
-// lies before it, h = exp(A sum dt) h + the next chunk's own, and does its tokens.  One CTA
+// kernel does the first chunks, and makes the states alone that each further one but the last
+// leads to from zero, and the sums of their steps; in the second a chunk joins what lies
+// before it, h = exp(A sum dt) h + the next chunk's own, and does its tokens.  (With the first
+// chunks in the second kernel, too, and smallest chunks of 64: 20 single tokens and 4 of 427 on
+// average, 4,096 channels 63 us instead of 62, one of 9,763 and 8,192 565 and 532.)  One CTA
 // lists the chunks before, the long ones first.  Batches of single tokens, whose work is to
 // read and write the states, go to a kernel whose CTAs keep their tile's decays and have
 // the next sequences' states on their way.
@@ -42,7 +44,7 @@ constexpr int kChunkStep = 16;        // chunks are multiples of so many tokens
 constexpr int kFew = 8;               // tokens of a sequence that goes without shared memory
 
 constexpr int kStates = 8;            // states of a lane
-constexpr int kMinChunk = 64;         // tokens of a chunk at least
+constexpr int kMinChunk = 48;         // tokens of a chunk at least
 constexpr int kFullWarps = 5000;      // warps that sel_chunk wants of a call's chunks
 constexpr int kResident = 4;          // CTAs of an SM at most
 
@@ -64,15 +66,15 @@ struct SelParams {
     const float *A, *D, *dt_bias;
     void *pool;
     SelHeader *header;
-    SelUnit *units, *inner;           // the chunks, long ones first (null: each sequence is
-                                      // one, in order); the chunk before each end
+    SelUnit *units, *later;           // whole sequences and chunks with an end, long ones first (null:
+                                      // all are whole, in order); the chunk behind each end
     float *ends, *sums;               // [end]: states and steps' sum of the chunk before it
-    float *firsts;                    // states that a cut sequence starts from, at its first end
     int32_t y_stride, x_stride, dt_stride, b_stride, c_stride, z_stride;
     int32_t channels, tiles;          // tiles of a CTA's channels
     int32_t chunk, warps;             // smallest chunk (0: nothing is cut), warps of a sequence
     int32_t few;                      // tokens of the sequences that the kernel of few takes
     int32_t softplus, pool_bf16;
+    int32_t behind;                   // `units` are the chunks behind ends
 };
 
 // ---------------------------------------------------------------- chunks
@@ -92,8 +94,8 @@ inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 // What a call takes, in ns, whose sequences of some length on are cut: its longest whole
 // sequence, or all of its tokens.  Measured: a token of a whole sequence 80, whatever its
 // warps, while they find room; a token and warp of a whole sequence 0.086, of a cut one
-// (whose states are made twice) 0.115; the additional kernel 6,000.  (One sequence of 4,096
-// tokens, 2,048 channels: 263 us whole, 79 cut; of 9,763 tokens, 8,192 channels: 604 and 565;
+// (most of whose states are made twice) 0.115; the additional kernel 6,000.  (One sequence of 4,096
+// tokens, 2,048 channels: 263 us whole, 79 cut; of 9,763 tokens, 8,192 channels: 604 and 532;
 // two prompts of 9,763 tokens in all: 399 and 540.)
 __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int warps)
 {
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
     for (int b = threadIdx.x; b < p.s.batch; b += kPlanThreads) {
         const int size = chunks(b, count);
         if (count)
-            atomicAdd(&s_units[size], count);
+            atomicAdd(&s_units[size], max(1, count - 1));
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
         const int b = b0 + lane, size = chunks(b, count);
         int at = 0, ends = 0;
         if (count) {
-            at = atomicAdd(&s_units[size], count);
+            at = atomicAdd(&s_units[size], max(1, count - 1));
             if (count > 1)
                 ends = atomicAdd(&s_ends, count - 1);
             else
@@ -212,9 +214,10 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
             const int u = __shfl_sync(0xffffffffu, at, from), e = __shfl_sync(0xffffffffu, ends, from);
             for (int k = lane; k < n; k += 32) {
                 const SelUnit unit = {b0 + from, first + k * l, min(first + (k + 1) * l, behind), k, e, 1, k == n - 1, 0};
-                p.units[u + k] = unit;
                 if (k < n - 1)
-                    p.inner[e + k] = unit;
+                    p.units[u + k] = unit;
+                if (k > 0)
+                    p.later[e + k - 1] = unit;
             }
         }
     }
@@ -731,47 +734,38 @@ struct SelPlace {
     }
 };
 
-// The states and the steps' sum of the chunk before an end.
-template <int N>
-__global__ void __launch_bounds__(kScanThreads, 3) selective_states_kernel(const __grid_constant__ SelParams p)
+// A whole sequence, or the first chunk of a cut one: from the slot's states; these go to the slot,
+// or to the chunk's end.
+template <int N, bool kGate>
+__device__ __forceinline__ void sel_first(const SelParams &p, const SelPlace<N> &me_at, SelShared<N, 16> &s,
+                                          const SelUnit &u)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
-    const int64_t end = blockIdx.x / p.tiles;
-    pdl_wait();
-    if (end >= p.header->ends)
-        return;
-    const SelUnit u = p.inner[end];
     SelLane me;
     me.load_decays(p.A + me_at.at);
+    const float D = p.D ? p.D[me_at.ch] : 0.f, bias = p.dt_bias ? p.dt_bias[me_at.ch] : 0.f;
+    const int64_t slot = seq_slot(p.s, u.seq);
 #pragma unroll
     for (int n = 0; n < kStates; ++n)
         me.h[n] = 0.f;
-    if (u.k == 0) {
-        const int64_t slot = seq_slot(p.s, u.seq);
-        if (slot >= 0 && p.s.has_init && p.s.has_init[u.seq]) {
-            load_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
-            // (the slot is written by the sequence's last chunk, perhaps before its first
-            // one starts)
-            if (me_at.valid)
-                store_states(p.firsts, false, end * me_at.states + me_at.at, me.h);
-        }
-    }
+    if (slot >= 0 && p.s.has_init && p.s.has_init[u.seq])
+        load_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
     float total = 0.f;
-    sel_tokens<N, false, false>(p, *reinterpret_cast<SelShared<N, 16> *>(smem), me, u.begin, u.end, me_at.col0, 0.f,
-                                p.dt_bias ? p.dt_bias[me_at.ch] : 0.f, total);
+    if (u.end - u.begin > kFew)
+        sel_tokens<N, kGate, true>(p, s, me, u.begin, u.end, me_at.col0, D, bias, total);
+    else
+        sel_few<N, kGate>(p, me, u.begin, u.end, me_at.ch, me_at.valid, D, bias);
     if (!me_at.valid)
         return;
-    store_states(p.ends, false, end * me_at.states + me_at.at, me.h);
-    if (me_at.part == 0)
-        p.sums[end * p.channels + me_at.ch] = total;
+    if (u.cut)
+        store_states(p.ends, false, u.ends * me_at.states + me_at.at, me.h);
+    else if (slot >= 0)
+        store_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
 }
 
-// The tokens of a chunk, as a rule of a whole sequence.  (With the CTAs of an SM asked for:
-// without, ptxas keeps to 80 registers and orders the code for that, 560 us for two
-// prompts of 9,763 tokens in all instead of 430, with blocks of 16 tokens.  Three asked for and
-// not the four that there are as a rule, which it orders worse: 8 of 1,000 tokens and 5,120
-// channels 211 us instead of 216.)
+// The tokens of a whole sequence, or of a chunk that is not its sequence's first.  (With the CTAs
+// of an SM asked for: without, ptxas keeps to 80 registers and orders the code for that, 560 us
+// for two prompts of 9,763 tokens in all instead of 430, with blocks of 16 tokens.  Three asked
+// for and not the four that there are as a rule, which it orders worse.)
 template <int N, bool kGate, int kBlock>
 __global__ void __launch_bounds__(kScanThreads, kBlock == 32 ? 2 : 3) selective_scan_kernel(const __grid_constant__ SelParams p)
 {
@@ -781,7 +775,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlock == 32 ? 2 : 3) selective_
     pdl_wait();
     SelUnit u = {unit, 0, 0, 0, 0, 0, 1, 0};
     if (p.units) {
-        if (unit >= p.header->units)
+        if (unit >= (p.behind ? p.header->ends : p.header->units))
             return;
         u = p.units[unit];
     } else if (!seq_rows(p.s.qsl, p.s.total_len, p.s.errors, unit, u.begin, u.end) || u.end - u.begin <= p.few) {
@@ -805,10 +799,7 @@ __global__ void __launch_bounds__(kScanThreads, kBlock == 32 ? 2 : 3) selective_
                 me.h[n] = e == u.ends ? own[n] : fmaf(ptx::ex2(sum * me.decay(n)), me.h[n], own[n]);
         }
     } else if (slot >= 0 && p.s.has_init && p.s.has_init[u.seq]) {
-        if (u.cut)
-            load_states(p.firsts, false, u.ends * me_at.states + me_at.at, me.h);
-        else
-            load_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
+        load_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
     }
     float total = 0.f;
     if (u.end - u.begin > kFew)
@@ -818,6 +809,39 @@ __global__ void __launch_bounds__(kScanThreads, kBlock == 32 ? 2 : 3) selective_
         sel_few<N, kGate>(p, me, u.begin, u.end, me_at.ch, me_at.valid, D, bias);
     if (u.last && slot >= 0 && me_at.valid)
         store_states(p.pool, p.pool_bf16, slot * me_at.states + me_at.at, me.h);
+}
+
+// Whole sequences and chunks: first ones, and of those between the first and the last the states
+// from zero and the steps' sum alone.
+template <int N, bool kGate>
+__global__ void __launch_bounds__(kScanThreads, kResident) selective_first_kernel(const __grid_constant__ SelParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    auto &shared = *reinterpret_cast<SelShared<N, 16> *>(smem);
+    const SelPlace<N> me_at(p, blockIdx.x % p.tiles);
+    const int unit = blockIdx.x / p.tiles;
+    pdl_wait();
+    if (unit >= p.header->units)
+        return;
+    const SelUnit u = p.units[unit];
+    if (u.k == 0) {
+        sel_first<N, kGate>(p, me_at, shared, u);
+        return;
+    }
+    SelLane me;
+    me.load_decays(p.A + me_at.at);
+#pragma unroll
+    for (int n = 0; n < kStates; ++n)
+        me.h[n] = 0.f;
+    float total = 0.f;
+    sel_tokens<N, false, false>(p, shared, me, u.begin, u.end, me_at.col0, 0.f, p.dt_bias ? p.dt_bias[me_at.ch] : 0.f,
+                                total);
+    if (!me_at.valid)
+        return;
+    const int64_t end = u.ends + u.k;
+    store_states(p.ends, false, end * me_at.states + me_at.at, me.h);
+    if (me_at.part == 0)
+        p.sums[end * p.channels + me_at.ch] = total;
 }
 
 // Sequences of at most p.few tokens, single ones as a rule.  A CTA takes every `groups`-th
@@ -986,11 +1010,11 @@ __global__ void __launch_bounds__(kScanThreads, kStepResident) selective_step_ke
 }
 
 // Ends of chunks of a call, at most: a cut sequence's chunks are no shorter than sel_chunk,
-// and its last is no end.
+// and its last has no end.
 int64_t sel_ends(int64_t total_len, int32_t chunk) { return total_len / chunk; }
 
 struct SelLayout {
-    size_t units, inner, ends, firsts, sums, total;
+    size_t units, later, ends, sums, total;
 };
 SelLayout sel_layout(int64_t total_len, int32_t batch, int32_t channels, int32_t dstate, int64_t ends)
 {
@@ -1003,9 +1027,8 @@ SelLayout sel_layout(int64_t total_len, int32_t batch, int32_t channels, int32_t
     };
     const int64_t states = static_cast<int64_t>(channels) * dstate * 4;
     L.units = take((ends + batch) * static_cast<int64_t>(sizeof(SelUnit)));
-    L.inner = take(ends * static_cast<int64_t>(sizeof(SelUnit)));
+    L.later = take(ends * static_cast<int64_t>(sizeof(SelUnit)));
     L.ends = take(ends * states);
-    L.firsts = take(ends * states);
     L.sums = take(ends * channels * 4);
     L.total = off;
     return L;
@@ -1017,7 +1040,7 @@ size_t sel_bytes(int64_t total_len, int32_t batch, int32_t channels, int32_t dst
 {
     const int64_t states = static_cast<int64_t>(channels) * dstate, ends = total_len / kMinChunk;
     const int64_t held = std::min<int64_t>(ends * states, int64_t{kFullWarps} * 32 * kStates);
-    return static_cast<size_t>(held * (4 + 4) + held / kStates * 4 +
+    return static_cast<size_t>(held * 4 + held / kStates * 4 +
                                (2 * std::min<int64_t>(ends, kFullWarps) + batch) * static_cast<int64_t>(sizeof(SelUnit)) +
                                6 * 256 + sizeof(SelHeader));
 }
@@ -1058,34 +1081,30 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
         p.chunk = 0;
     const int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
     const bool listed = ends || whole > int64_t{kResident} * sms;
-    static SmemOptIn s_scan, s_long, s_states;
+    static SmemOptIn s_scan, s_long, s_first;
+    auto go = [&](auto kernel, SmemOptIn &opted, int64_t ctas, int bytes) {
+        const cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(kernel), opted);
+        return e != cudaSuccess ? e
+                                : launch_pdl_smem(kernel, dim3(static_cast<unsigned>(ctas)), kScanThreads, bytes, stream, p);
+    };
+    if (listed) {
+        cudaError_t e = launch_pdl(selective_plan_kernel, dim3(1), kPlanThreads, stream, p);
+        if (e == cudaSuccess)
+            e = ends ? go(selective_first_kernel<N, kGate>, s_first, p.tiles * ends + whole, kBytes)
+                     : go(selective_scan_kernel<N, kGate, 16>, s_scan, whole, kBytes);
+        if (e == cudaSuccess && ends) {
+            p.units = p.later;
+            p.behind = 1;
+            e = go(selective_scan_kernel<N, kGate, 16>, s_scan, p.tiles * ends, kBytes);
+        }
+        return e;
+    }
     // At most two CTAs an SM: blocks of 32 tokens, fewer barriers for more shared memory (two
     // prompts of 9,763 tokens in all, 8,192 channels: 429 us with 16, 399 with 32; with four CTAs an
     // SM, 8 of 1,000 tokens and 5,120 channels: 214 and 227).
-    if (!listed && whole <= 2 * sms) {
-        constexpr int kLong = sizeof(SelShared<N, 32>);
-        p.units = nullptr;
-        const cudaError_t e =
-            ensure_max_smem(reinterpret_cast<const void *>(selective_scan_kernel<N, kGate, 32>), s_long);
-        return e != cudaSuccess ? e
-                                : launch_pdl_smem(selective_scan_kernel<N, kGate, 32>, dim3(static_cast<unsigned>(whole)),
-                                                  kScanThreads, kLong, stream, p);
-    }
-    cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(selective_scan_kernel<N, kGate, 16>), s_scan);
-    if (listed && e == cudaSuccess)
-        e = launch_pdl(selective_plan_kernel, dim3(1), kPlanThreads, stream, p);
-    if (ends && e == cudaSuccess) {
-        e = ensure_max_smem(reinterpret_cast<const void *>(selective_states_kernel<N>), s_states);
-        if (e == cudaSuccess)
-            e = launch_pdl_smem(selective_states_kernel<N>, dim3(static_cast<unsigned>(p.tiles * ends)), kScanThreads,
-                                kBytes, stream, p);
-    }
-    if (!listed)
-        p.units = nullptr;
-    if (e == cudaSuccess)
-        e = launch_pdl_smem(selective_scan_kernel<N, kGate, 16>, dim3(static_cast<unsigned>(p.tiles * ends + whole)),
-                            kScanThreads, kBytes, stream, p);
-    return e;
+    p.units = nullptr;
+    return whole <= 2 * sms ? go(selective_scan_kernel<N, kGate, 32>, s_long, whole, sizeof(SelShared<N, 32>))
+                            : go(selective_scan_kernel<N, kGate, 16>, s_scan, whole, kBytes);
 }
 
 template <int N>
@@ -1178,9 +1197,8 @@ ssd_status_t ssd_selective_scan_varlen_fwd(
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.header = reinterpret_cast<SelHeader *>(ws);
     p.units = reinterpret_cast<SelUnit *>(ws + L.units);
-    p.inner = reinterpret_cast<SelUnit *>(ws + L.inner);
+    p.later = reinterpret_cast<SelUnit *>(ws + L.later);
     p.ends = reinterpret_cast<float *>(ws + L.ends);
-    p.firsts = reinterpret_cast<float *>(ws + L.firsts);
     p.sums = reinterpret_cast<float *>(ws + L.sums);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = dstate == 8    ? launch<8>(p, s)
