@@ -148,23 +148,33 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
             atomicMax(&s_longest[sel_size(end - begin)], end - begin);
         }
         // (with offsets that fall, the sequences may come to more than the workspace is for)
-        if (!__syncthreads_or(bad) && threadIdx.x == 0) {
-            int whole = 0, cut = 0;
-            for (int i = 0; i < kPlanSizes; ++i) {
-                whole += s_tokens[i];
-                if (i > 0)
-                    s_longest[i] = max(s_longest[i], s_longest[i - 1]);
+        if (!__syncthreads_or(bad) && threadIdx.x < 32) {
+            // a lane is a size; what a call takes with all from that size on cut
+            const int tokens = lane < kPlanSizes ? s_tokens[lane] : 0;
+            int upto = warp_inclusive_scan(tokens), longest = lane < kPlanSizes ? s_longest[lane] : 0;
+            const int all = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+            for (int o = 1; o < kPlanSizes; o <<= 1) {
+                const int other = __shfl_up_sync(0xffffffffu, longest, o);
+                longest = max(longest, lane >= o ? other : 0);
             }
-            float best = sel_cost(s_longest[kPlanSizes - 1], whole, 0, p.warps);
-            for (int i = kPlanSizes - 1; i >= 0 && 2 << i > 2 * p.chunk; --i) {
-                whole -= s_tokens[i];
-                cut += s_tokens[i];
-                const float cost = sel_cost(i > 0 ? s_longest[i - 1] : 0, whole, cut, p.warps);
-                if (cost < best) {
+            const float whole = sel_cost(__shfl_sync(0xffffffffu, longest, kPlanSizes - 1), all, 0, p.warps);
+            int below = __shfl_up_sync(0xffffffffu, longest, 1);
+            below = lane > 0 ? below : 0;
+            upto -= tokens;
+            float best = lane < kPlanSizes && 2 << lane > 2 * p.chunk ? sel_cost(below, upto, all - upto, p.warps) : whole;
+            int size = lane;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const float cost = __shfl_xor_sync(0xffffffffu, best, o);
+                const int other = __shfl_xor_sync(0xffffffffu, size, o);
+                if (cost < best || (cost == best && other > size)) {
                     best = cost;
-                    s_cut = max(1 << i, 2 * p.chunk);
+                    size = other;
                 }
             }
+            if (lane == 0 && best < whole)
+                s_cut = max(1 << size, 2 * p.chunk);
         }
         __syncthreads();
     }
