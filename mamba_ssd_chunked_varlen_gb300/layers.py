@@ -366,7 +366,9 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "
                     the lowest is divided by factor
       "ramp"        divided where a pair makes at most low_turns turns in original_len
                     positions, kept from high_turns on, blended linearly in the pair's
-                    index between; magnitude 0.1 ln(factor) + 1
+                    index between (from whole index to whole index, outwards, within 0 and
+                    rotary_dim - 1: the ramp may end behind the last pair); magnitude
+                    0.1 ln(factor) + 1
       "wavelength"  the same blended linearly in the number of turns; magnitude 1"""
     if rotary_dim < 4 or rotary_dim % 2:
         raise ValueError(f"rotary_dim must be even and at least 4, got {rotary_dim}")
@@ -388,8 +390,10 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "
         def pair_of(turns):    # the (fractional) pair that makes so many turns in original_len positions
             return half * math.log(original_len / (turns * 2 * math.pi)) / math.log(base)
         low = max(math.floor(pair_of(high_turns)), 0)
-        high = min(math.ceil(pair_of(low_turns)), half - 1)
-        keep = [1.0 - min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) for i in range(half)]
+        high = min(math.ceil(pair_of(low_turns)), rotary_dim - 1)
+        # (high <= 0: even the first pair makes at most low_turns)
+        keep = [1.0 - min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) if high > 0 else 0.0
+                for i in range(half)]
     else:
         keep = [min(max((x * original_len / (2 * math.pi) - low_turns) / (high_turns - low_turns), 0.0), 1.0)
                 for x in f]

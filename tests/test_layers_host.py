@@ -175,6 +175,36 @@ def test_rope_frequencies():
             f(**bad)
 
 
+@pytest.mark.parametrize("rotary_dim,base,original_len,low,high", [
+    (128, 1e4, 65536, 1.0, 32.0), (128, 1e4, 131072, 1.0, 32.0), (64, 1e4, 131072, 1.0, 32.0),
+    (64, 1e4, 1 << 24, 1.0, 32.0),               # the ramp's end behind rotary_dim - 1
+    (64, 1e4, 1 << 28, 1.0, 32.0),               # all pairs make more than high_turns
+    (128, 1e6, 32768, 1.0, 32.0), (64, 1e4, 8192, 1.0, 32.0), (32, 1e4, 8192, 0.5, 4.0),
+    (64, 1e4, 200, 1.0, 32.0), (64, 1e4, 6, 1.0, 32.0), (64, 1e4, 3, 1.0, 32.0),
+])
+def test_rope_ramp(rotary_dim, base, original_len, low, high):
+    """The share of the plain frequency by the definition, with the pairs' turns counted."""
+    import math
+    factor, half = 8.0, rotary_dim // 2
+    plain, _ = layers.rope_frequencies(rotary_dim, base)
+    got, _ = layers.rope_frequencies(rotary_dim, base, scaling="ramp", factor=factor, original_len=original_len,
+                                     low_turns=low, high_turns=high)
+
+    # pair i makes original_len base^(-i / half) / (2 pi) turns: where that is high, and low
+    def index(turns):
+        return half * math.log(original_len / (2 * math.pi * turns), base)
+    start, end = max(math.floor(index(high)), 0), min(math.ceil(index(low)), rotary_dim - 1)
+    for i, (x, y) in enumerate(zip(plain, got)):
+        turns = original_len * x / (2 * math.pi)
+        keep = (y / x * factor - 1.0) / (factor - 1.0)
+        if turns <= low:
+            assert keep == pytest.approx(0.0, abs=1e-12)
+        elif turns >= high:
+            assert keep == pytest.approx(1.0, abs=1e-12)
+        else:
+            assert keep == pytest.approx(min(max((end - i) / (end - start), 0.0), 1.0), abs=1e-9)
+
+
 def test_rope_binding_refuses(lib):
     import torch
     q = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
