@@ -105,9 +105,9 @@ __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int w
 // Lists the chunks of the sequences of more than p.few tokens: `count` of `len` tokens a
 // sequence, the last one shorter.  Which lengths are cut is up to sel_cost, by powers of two.
 constexpr int kPlanThreads = 512;
-constexpr int kPlanSizes = 16;        // powers of two that are told apart
+constexpr int kPlanSizes = 30;        // powers of two: all that a sequence's length can have
 
-__device__ __forceinline__ int sel_size(int32_t len) { return min(kPlanSizes - 1, 31 - __clz(len | 1)); }
+__device__ __forceinline__ int sel_size(int32_t len) { return 31 - __clz(len | 1); }
 
 __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __grid_constant__ SelParams p)
 {
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) selective_plan_kernel(const __gr
             int below = __shfl_up_sync(0xffffffffu, longest, 1);
             below = lane > 0 ? below : 0;
             upto -= tokens;
-            float best = lane < kPlanSizes && 2 << lane > 2 * p.chunk ? sel_cost(below, upto, all - upto, p.warps) : whole;
+            float best = lane < kPlanSizes && 1 << lane > p.chunk ? sel_cost(below, upto, all - upto, p.warps) : whole;
             int size = lane;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
