@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 
 from layer_helpers import Ragged, f64, near
-from test_selective_scan_gpu import call, scan_ref
+from test_selective_scan_gpu import call, make, scan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,72 @@ def test_sequences_past_the_largest_power_of_two():
         if hi == total:
             s = int(part.slot[0])
             near(f64(pool[int(r.slot[0])][some]), states[s], off[s] + 2.0 ** -60, "pool")
+
+
+def run(lens, channels, dstate, seed=0, **options):
+    """Rows and slots against the recurrence; the list in the workspace."""
+    import torch
+    import mamba_ssd_chunked_varlen_gb300 as pkg
+    r = Ragged(lens, seed=seed)
+    v = make(r, channels, dstate, seed, **options)
+    y, pool = torch.empty_like(v["x"]), v["pool"].clone()
+    workspace = pkg.alloc_selective_scan_workspace(r.rows, len(lens), channels, dstate)
+    workspace.zero_()
+    call(r, v, y, pool, workspace=workspace)
+    torch.cuda.synchronize()
+    ref = {k: None if t is None else f64(t) for k, t in v.items()}
+    want, bound, states, off = scan_ref(r, ref, f64(v["pool"]), True, pool.dtype == torch.bfloat16)
+    near(f64(y), want, bound, "y")
+    near(f64(pool), states, off, "pool")
+    assert r.errors.item() == 0
+    return listed(workspace)
+
+
+@pytest.mark.parametrize("n,ends", [(CHUNK - 1, 0), (CHUNK, 0), (CHUNK + 1, 0), (2 * CHUNK - 1, 0), (2 * CHUNK, 1),
+                                    (2 * CHUNK + 1, 1), (3 * CHUNK - 1, 1), (3 * CHUNK, 2), (3 * CHUNK + 1, 2),
+                                    (4 * CHUNK - 16, 2), (257, 4), (1000, 15)])
+@pytest.mark.parametrize("dstate", [8, 16, 64])
+def test_around_the_smallest_chunks(n, ends, dstate):
+    """Chunks are n / k tokens for k = floor(n / 48), rounded up to 16: 95 tokens are none, 96 two
+    of 48, 97 a chunk of 64 and one of 33, 1,000 fifteen of 64 and one of 40."""
+    k = max(1, n // CHUNK)
+    size = ((n + k - 1) // k + 15) // 16 * 16
+    assert ends == (0 if n < 2 * CHUNK else (n + size - 1) // size - 1)
+    assert run([n], 24, dstate, seed=n)[1] == ends
+    run([1, n, 0, n + 1, 3, n - 1], 24, dstate, seed=n, bf16=True, gate=False)
+
+
+@pytest.mark.parametrize("lens,units,ends", [
+    # 14 and 10 chunks that are not the last; the sequences of few tokens are another kernel's
+    ([1] * 600 + [900, 0, 2, 700] + [1] * 3, 24, 24),
+    # 46 and 17 of them, and 1,043 whole sequences
+    ([20] * 540 + [3000, 0, 9] + [30] * 500 + [1100, 7], 1106, 63),
+])
+def test_cut_sequences_behind_the_first_512(lens, units, ends):
+    """The list's threads keep their first sequence's offsets, and read those of further ones again."""
+    assert run(lens, 8, 16, seed=len(lens)) == (units, ends)
+
+
+def test_parts_equal_one_prompt_on_both_sides():
+    """A prompt in parts and single tokens, through its slot: states neither larger nor smaller."""
+    import torch
+    n = 375
+    r = Ragged([n], seed=7)
+    v = make(r, 136, 16, 7)
+    r.has_initial_state[:] = False
+    r.has[:] = False
+    y, pool = torch.empty_like(v["x"]), v["pool"].clone()
+    call(r, v, y, pool)
+    z, other = torch.empty_like(y), v["pool"].clone()
+    for lo, hi in zip([0, 1, 2, 35, 43, 300, 374], [1, 2, 35, 43, 300, 374, n]):
+        part = Ragged([hi - lo], seed=7)
+        part.has_initial_state[:] = lo > 0
+        call(part, {k: t[lo:hi] if k in ("x", "dt", "B", "C", "z") else t for k, t in v.items()}, z[lo:hi], other)
+    ref = {k: f64(t) for k, t in v.items()}
+    want, bound, states, off = scan_ref(r, ref, f64(v["pool"]), True, False)
+    # each is within the bound of the recurrence
+    for a, b in ((y, pool), (z, other)):
+        near(f64(a), want, bound, "y")
+        near(f64(b), states, off, "pool")
+    slot = int(r.slot[0])
+    assert np.abs(f64(other)[slot] - f64(pool)[slot]).max() <= 2 * off[slot].max()
