@@ -389,6 +389,14 @@ struct SelShared {
     float4 B[2][kBlock / 2][kStates / 2][kLanes], C[2][kBlock / 2][kStates / 2][kLanes];
 };
 
+// CTAs of an SM that have room for it, at most `most`.
+template <int N, int kBlock>
+constexpr int sel_resident(int most)
+{
+    const int room = (kMaxSmemPerBlock + 1024) / static_cast<int>(sizeof(SelShared<N, kBlock>) + 1024);
+    return room < most ? room : most;
+}
+
 // What a lane holds of its channel.
 struct SelLane {
     float h[kStates];
@@ -775,7 +783,7 @@ __device__ __forceinline__ void sel_first(const SelParams &p, const SelPlace<N> 
 // The tokens of a whole sequence, or of a chunk that is not its sequence's first.  (With the CTAs
 // of an SM asked for: without, ptxas keeps to 80 registers and orders the code for that, 560 us
 // for two prompts of 9,763 tokens in all instead of 430, with blocks of 16 tokens.  Three asked
-// for and not the four that there are as a rule, which it orders worse.)
+// for and not the four that there are from 16 states on, which it orders worse; with 8 there are two.)
 template <int N, bool kGate, int kBlock>
 __global__ void __launch_bounds__(kScanThreads, kBlock == 32 ? 2 : 3) selective_scan_kernel(const __grid_constant__ SelParams p)
 {
@@ -1090,7 +1098,7 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     if (!may_cut)
         p.chunk = 0;
     const int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
-    const bool listed = ends || whole > int64_t{kResident} * sms;
+    const bool listed = ends || whole > int64_t{sel_resident<N, 16>(kResident)} * sms;
     static SmemOptIn s_scan, s_long, s_first;
     auto go = [&](auto kernel, SmemOptIn &opted, int64_t ctas, int bytes) {
         const cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(kernel), opted);
@@ -1109,11 +1117,12 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
         }
         return e;
     }
-    // At most two CTAs an SM: blocks of 32 tokens, fewer barriers for more shared memory (two
-    // prompts of 9,763 tokens in all, 8,192 channels: 429 us with 16, 399 with 32; with four CTAs an
-    // SM, 8 of 1,000 tokens and 5,120 channels: 214 and 227).
+    // At most two CTAs an SM (one with 8 states, whose blocks of 32 leave no room for two): blocks of
+    // 32 tokens, fewer barriers for more shared memory (two prompts of 9,763 tokens in all, 8,192
+    // channels: 429 us with 16, 399 with 32; with four CTAs an SM, 8 of 1,000 tokens and 5,120
+    // channels: 214 and 227; two of 2,000 tokens, 16,384 channels of 8 states, 256 CTAs: 220 and 276).
     p.units = nullptr;
-    return whole <= 2 * sms ? go(selective_scan_kernel<N, kGate, 32>, s_long, whole, sizeof(SelShared<N, 32>))
+    return whole <= sel_resident<N, 32>(2) * sms ? go(selective_scan_kernel<N, kGate, 32>, s_long, whole, sizeof(SelShared<N, 32>))
                             : go(selective_scan_kernel<N, kGate, 16>, s_scan, whole, kBytes);
 }
 
