@@ -88,6 +88,10 @@ SSD_API ssd_status_t ssd_causal_conv_varlen_fwd(
  *   workspace    at least ssd_selective_scan_varlen_workspace_size bytes, 256-byte aligned;
  *                needs no initialisation; one call at a time per workspace
  *
+ * A call of exactly as many rows as sequences (total_len == batch) is taken for a step of single
+ * tokens: a longer sequence in it is right, but waits for memory at every token.  Batches padded
+ * with empty sequences that may hold prompts do better with any other number of rows.
+ *
  * Supported: dstate 8, 16, 32 or 64; channels a multiple of 8, at most 2^20; strides below
  * 2^31.  States and sums are fp32, y is rounded once. */
 typedef enum {

@@ -1073,14 +1073,17 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
         return cudaErrorInvalidDevice;
     // Where most sequences have few tokens, those have a kernel of their own, without shared
-    // memory or a list (96 of two tokens, 8,192 channels: 39 us with both kernels, 63 in the other
+    // memory or a list (96 of two tokens, 8,192 channels: 35.5 us with both kernels, 63 in the other
     // one alone; 24 sequences of 72 tokens on average, twenty of them of one: 69.5 and 65.9).  It
-    // takes all of them, whatever their lengths, when there are no more tokens than sequences,
-    // and a lone one if it is that short.  No more CTAs than are resident at once.
-    const bool alone = p.s.total_len <= p.s.batch || (p.s.batch == 1 && p.s.total_len <= kFew);
-    p.few = alone ? INT32_MAX
-            : p.s.batch > 1 && p.s.total_len <= int64_t{kFew} * p.s.batch ? kFew
-                                                                          : -1;
+    // takes all of them, whatever their lengths, when there are as many tokens as sequences, a step
+    // of single tokens (96 of them 22 us, 25 with both kernels).  Fewer tokens than sequences are a
+    // batch with empty ones, whose others may be long: one of 256 and 255 single tokens among 256
+    // empty ones, 2,048 channels, 199 us there and 46 with both.  No more CTAs than are resident at
+    // once.
+    const bool alone = p.s.total_len == p.s.batch || p.s.total_len <= kFew;
+    p.few = alone                                        ? INT32_MAX
+            : p.s.total_len <= int64_t{kFew} * p.s.batch ? kFew
+                                                         : -1;
     if (p.few >= 0) {
         const int64_t groups = std::min<int64_t>(p.s.batch, std::max(1, kStepResident * sms / p.tiles));
         const cudaError_t e =
@@ -1097,8 +1100,12 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     const int64_t ends = may_cut ? sel_ends(p.s.total_len, p.chunk) : 0;
     if (!may_cut)
         p.chunk = 0;
-    const int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
+    // (those of more than few tokens are not many; the list leaves the others out)
+    const int64_t most = p.few < 0 ? p.s.batch : std::min<int64_t>(p.s.batch, p.s.total_len / (p.few + 1));
+    int64_t whole = static_cast<int64_t>(p.tiles) * p.s.batch;
     const bool listed = ends || whole > int64_t{sel_resident<N, 16>(kResident)} * sms;
+    if (listed)
+        whole = p.tiles * most;
     static SmemOptIn s_scan, s_long, s_first;
     auto go = [&](auto kernel, SmemOptIn &opted, int64_t ctas, int bytes) {
         const cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(kernel), opted);
