@@ -288,7 +288,11 @@ cudaError_t launch(RopeParams &p, int64_t total_len, bool neighbours, cudaStream
     const int step = 256 / p.c.dim * kRopeAhead, kv = (p.c.heads + step - 1) / step;
     p.steps = (p.heads + step - 1) / step + (kType == kRopeNone ? kv : 2 * kv);
     const int parts = std::max(1, (p.steps + 1) / 3);
-    p.part_steps = total_len >= 16 * 152 ? (p.steps + parts - 1) / parts : 1;
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+        return cudaErrorInvalidDevice;
+    p.part_steps = total_len >= int64_t{16} * sms ? (p.steps + parts - 1) / parts : 1;
     const dim3 grid(static_cast<unsigned>((total_len + kRopeWarps - 1) / kRopeWarps),
                     static_cast<unsigned>((p.steps + p.part_steps - 1) / p.part_steps));
     const int threads = kRopeWarps * 32;
