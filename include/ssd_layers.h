@@ -31,7 +31,8 @@
  *   SSD_DEVERR_BAD_QUERY_START_LOC  qsl[0] != 0, decreasing, or above total_len: a
  *                     sequence with such a bound is skipped, the rows that no good
  *                     sequence holds and the skipped sequences' slots are
- *                     unspecified (no other memory is touched)
+ *                     unspecified; where offsets decrease, all rows and all named slots
+ *                     are (no other memory is touched)
  *   SSD_DEVERR_BAD_CACHE_INDEX      cache_indices[b] >= max_slots and not
  *                     SSD_NO_SLOT: taken for SSD_NO_SLOT
  */
@@ -53,7 +54,8 @@ extern "C" {
  *
  * with u = x in the sequence and, before its first token, the last inputs that
  * its slot holds (zeros without has_initial_state); act is silu, v / (1 + e^-v),
- * or nothing.  The slot gets the last width - 1 inputs.
+ * or nothing.  The slot gets the last width - 1 inputs.  (Here and below, silu of v < -87,
+ * smaller than 2e-36, is taken for 0.)
  *
  *   y, x       bf16 (total_len, channels), rows y_stride and x_stride apart, e.g.
  *              column slices of a fused projection

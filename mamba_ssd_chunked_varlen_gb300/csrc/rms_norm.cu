@@ -6,14 +6,21 @@
 //
 // A segment is one row's group.  It is read once and stays in registers, eight values
 // a load, between the sum of squares, the largest magnitude and the output: memory
-// bounds it.  Segments of up to 1,024 columns are a warp's or less (eight lanes up to 64,
-// sixteen up to 128), longer ones a CTA's.  There, for codes, y is (s w) r with r = 1 /
-// sqrt(...): a product with r > 0 keeps the order of magnitudes through its rounding, so
+// bounds it with a residual or to bf16.  Segments of up to 1,024 columns are a warp's or less
+// (eight lanes up to 64, sixteen up to 128), longer ones a CTA's.  There, for codes, y is (s w) r with
+// r = 1 / sqrt(...): a product with r > 0 keeps the order of magnitudes through its rounding, so
 // that max|y| is max|s w| r, and one barrier serves the sum and the largest (4,093 rows of
 // 5,120 to int8: 29.1 us with two, 27.1 with one, 25.8 with rows in turn; a warp's weights
 // would be registers that it needs, 8,191 rows of 8 gated groups to int8: 73 us with them, 68
 // without).  With a residual, 4,093 rows of 5,120 to bf16 take 26.9 us, 92 % of the measured copy
 // rate, to int8 25.8, 84 %; 8,191 rows of 8 gated groups to bf16 65, 90 %.
+//
+// Instructions bound codes without a residual (8,191 rows of 8,192 to int8: plain 47 us, 63 % of
+// the copy rate, gated 86, 57 %), and the 64 registers of a CTA of 1,024 threads those of more
+// than 16,384 columns, whose 32 values and 32 weights a thread do not fit: 360 to 400 bytes a thread
+// go to local memory and back (2,047 rows of 32,768 to int8: plain 89 us, 33 %, with a residual 132,
+// 52 %; to bf16, where the weights are loaded late and nothing spills, 60 and 87 us).  Rows in turn spill
+// 52 bytes to codes with a gate, 44 with a residual, 16 to bf16 with a gate.
 #include <algorithm>
 
 #include "layer_common.cuh"

@@ -92,11 +92,12 @@ inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 }
 
 // What a call takes, in ns, whose sequences of some length on are cut: its longest whole
-// sequence, or all of its tokens.  Measured: a token of a whole sequence 80, whatever its
-// warps, while they find room; a token and warp of a whole sequence 0.086, of a cut one
-// (most of whose states are made twice) 0.115; the additional kernel 6,000.  (One sequence of 4,096
-// tokens, 2,048 channels: 263 us whole, 79 cut; of 9,763 tokens, 8,192 channels: 604 and 532;
-// two prompts of 9,763 tokens in all: 399 and 540.)
+// sequence, or all of its tokens.  Measured, of 16 states: a token of a whole sequence 64 up to 4,096
+// channels, 90 of 8,192, taken as 80; a token and warp of a whole sequence 0.086, of a cut one (most
+// of whose states are made twice) 0.115; the additional kernel 6,000.  (Whole and cut, one
+// sequence of 4,096 tokens, 2,048 channels: 263 and 79 us; of 500 tokens, 8,192 channels: 52 and 42,
+// which 64 would leave whole; of 9,763 tokens: 604 in blocks of 32 and 532.  Two prompts of 9,763
+// tokens in all: 399 and 540.)
 __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int warps)
 {
     return fmaxf(80.f * longest, (0.086f * whole + 0.115f * cut) * warps) + (cut > 0 ? 6000.f : 0.f);
@@ -245,7 +246,9 @@ __device__ __forceinline__ uint64_t twice(float v)
     return r;
 }
 
-// log(1 + e) / e on [0, 1], degree 8: relative error 3e-8, 1.8e-7 with fp32's roundings.
+// log(1 + e) / e on [0, 1] by the polynomial of degree 8 whose largest relative error is smallest (by
+// Remez's exchange: 3.0e-8).  With its coefficients in fp32 6.4e-8, the last one's rounding for small
+// e; with fp32's operations log(1 + e) is off by 1.8e-7.
 #define SSD_LOG1P_TERMS(F) \
     F(0.0052326940931379795f) F(-0.029505237936973572f) F(0.07822595536708832f) F(-0.13663245737552643f) \
     F(0.19106006622314453f) F(-0.2484298199415207f) F(0.3331909775733948f) F(-0.4999949336051941f) \

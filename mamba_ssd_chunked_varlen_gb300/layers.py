@@ -200,8 +200,8 @@ def ssd_causal_conv_varlen_fwd(y, x, weight, bias, conv_pool, query_start_loc, h
     (channels,) fp32 or None; conv_pool (slots, width - 1, channels) bf16, updated
     in place; query_start_loc (batch + 1,) int32; has_initial_state (batch,)
     uint8/bool or None; cache_indices (batch,) int32/uint32 (same bits; -1 is no
-    slot); silu: y is silu of the sum.  errors: an int32 tensor of one element that
-    collects the SSD_DEVERR_* flags, or None."""
+    slot); silu: y is silu of the sum; y must not overlap x.  errors: an int32 tensor of one
+    element that collects the SSD_DEVERR_* flags, or None."""
     f = _functions()
     shape, wshape, bf16, f32 = x.shape, weight.shape, f.bf16, f.f32
     device = x.get_device()
@@ -262,8 +262,8 @@ def ssd_selective_scan_varlen_fwd(y, x, dt, A, B, C, D, z, dt_bias, ssm_pool, qu
     each row contiguous, any row pitch that is a multiple of 8 elements; A (channels,
     dstate) fp32; D, dt_bias (channels,) fp32 or None; ssm_pool (slots, channels, dstate)
     fp32 or bf16, updated in place; the batch and errors as for
-    ssd_causal_conv_varlen_fwd; workspace: a uint8 tensor of at least
-    ssd_selective_scan_varlen_workspace_size bytes (alloc_selective_scan_workspace)."""
+    ssd_causal_conv_varlen_fwd; y must not overlap another tensor; workspace: a uint8 tensor of
+    at least ssd_selective_scan_varlen_workspace_size bytes (alloc_selective_scan_workspace)."""
     f = _functions()
     if workspace is None:
         raise ValueError("workspace is required (see alloc_selective_scan_workspace)")
