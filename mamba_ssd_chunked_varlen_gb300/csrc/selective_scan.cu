@@ -24,8 +24,8 @@
 // leads to from zero, and the sums of their steps; in the second a chunk joins what lies
 // before it, h = exp(A sum dt) h + the next chunk's own, and does its tokens.  (With the first
 // chunks in the second kernel, too, and smallest chunks of 64: 20 single tokens and 4 of 427 on
-// average, 4,096 channels 63 us instead of 62, one of 9,763 and 8,192 565 and 532.)  One CTA
-// lists the chunks before, the long ones first.  Batches of single tokens, whose work is to
+// average, 4,096 channels 63 us instead of 62, one of 9,763 and 8,192, cut then, 565 and 532.)  One
+// CTA lists the chunks before, the long ones first.  Batches of single tokens, whose work is to
 // read and write the states, go to a kernel whose CTAs keep their tile's decays and have
 // the next sequences' states on their way.
 #include <algorithm>
@@ -95,9 +95,7 @@ inline int32_t sel_chunk(int64_t total_len, int32_t channels, int32_t dstate)
 // sequence, or all of its tokens.  Measured, of 16 states: a token of a whole sequence 64 up to 4,096
 // channels, 90 of 8,192, taken as 80; a token and warp of a whole sequence 0.086, of a cut one (most
 // of whose states are made twice) 0.115; the additional kernel 6,000.  (Whole and cut, one
-// sequence of 4,096 tokens, 2,048 channels: 263 and 79 us; of 500 tokens, 8,192 channels: 52 and 42,
-// which 64 would leave whole; of 9,763 tokens: 604 in blocks of 32 and 532.  Two prompts of 9,763
-// tokens in all: 399 and 540.)
+// sequence of 4,096 tokens, 2,048 channels: 263 and 79 us; of 500 tokens, 4,096 channels: 38 and 27.)
 __device__ __forceinline__ float sel_cost(int longest, int whole, int cut, int warps)
 {
     return fmaxf(80.f * longest, (0.086f * whole + 0.115f * cut) * warps) + (cut > 0 ? 6000.f : 0.f);
@@ -1095,11 +1093,13 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
         if (e != cudaSuccess || alone)
             return e;
     }
-    // Calls of few tokens are not cut, and neither are those of several sequences that have
-    // warps for two thirds of the schedulers each: cutting gains 5 % at best, but the list,
-    // the idle CTAs and the other order of the rest cost more (two prompts of 9,763 tokens
-    // in all, 8,192 channels: 473 us instead of 430).
-    const bool may_cut = p.s.total_len >= 2 * int64_t{p.chunk} && (p.s.batch == 1 || 3 * p.warps < 8 * sms);
+    // Calls of few tokens are not cut, and neither are those whose sequences have warps for two
+    // thirds of the schedulers each: whole, without the list, the idle CTAs and in blocks of 32 tokens,
+    // they take less as a rule (one of 500 and one of 9,763 tokens, 8,192 channels: 40 and 532 us
+    // cut, 30.5 and 505 whole; of 16,384 channels, which the list leaves whole: 71 and 1,206, without it
+    // 47 and 806; two prompts of 9,763 tokens in all, 8,192 channels: 473 and 430 then; but one of
+    // 9,763, 6,528 channels: 457 and 503).
+    const bool may_cut = p.s.total_len >= 2 * int64_t{p.chunk} && 3 * p.warps < 8 * sms;
     const int64_t ends = may_cut ? sel_ends(p.s.total_len, p.chunk) : 0;
     if (!may_cut)
         p.chunk = 0;

@@ -26,7 +26,7 @@ def test_sequences_past_the_largest_power_of_two():
     """So many tokens that the smallest chunk passes 2^15: the sequence is cut all the same."""
     import torch
     import mamba_ssd_chunked_varlen_gb300 as pkg
-    total, channels, dstate = 326_000, 2048, 64
+    total, channels, dstate = 430_000, 1536, 64
     assert total * (channels * dstate // 256) // 5000 > 1 << 15
     g = torch.Generator(device="cuda").manual_seed(1)
 
@@ -106,6 +106,13 @@ def test_cut_sequences_behind_the_first_512(lens, units, ends):
     assert run(lens, 8, 16, seed=len(lens)) == (units, ends)
 
 
+@pytest.mark.parametrize("channels,dstate,cut", [(6400, 16, True), (6528, 16, False), (1600, 64, True), (1664, 64, False)])
+def test_wide_sequences_are_not_cut(channels, dstate, cut):
+    """400 warps (of 256 states) are cut, 408 are more than two thirds of 152 SMs' schedulers: no list is
+    made, also for a lone sequence."""
+    assert run([400], channels, dstate, seed=channels) == ((6, 6) if cut else (0, 0))
+
+
 def test_parts_equal_one_prompt_on_both_sides():
     """A prompt in parts and single tokens, through its slot: states neither larger nor smaller."""
     import torch
@@ -133,7 +140,7 @@ def test_parts_equal_one_prompt_on_both_sides():
 
 def test_two_prompts_of_8_states_take_one_round():
     """256 CTAs with 8 states: two an SM with blocks of 16 tokens, one with those of 32.  They take less
-    than one and a half times what half of them take (1.33; 1.66 where they take two rounds)."""
+    than 1.75 times what half of them take, one an SM (220 and 142 us: 1.55; 275, 1.94, in two rounds)."""
     import torch
     import mamba_ssd_chunked_varlen_gb300 as pkg
     n, channels, dstate = 2000, 16384, 8
@@ -157,4 +164,4 @@ def test_two_prompts_of_8_states_take_one_round():
             torch.cuda.synchronize()
             best = min(best, a.elapsed_time(b) / 4)
         return best
-    assert time_of(2) < 1.5 * time_of(1)
+    assert time_of(2) < 1.75 * time_of(1)
