@@ -1132,8 +1132,9 @@ cudaError_t launch(SelParams &p, cudaStream_t stream)
     // channels: 429 us with 16, 399 with 32; with four CTAs an SM, 8 of 1,000 tokens and 5,120
     // channels: 214 and 227; two of 2,000 tokens, 16,384 channels of 8 states, 256 CTAs: 220 and 276).
     p.units = nullptr;
-    return whole <= sel_resident<N, 32>(2) * sms ? go(selective_scan_kernel<N, kGate, 32>, s_long, whole, sizeof(SelShared<N, 32>))
-                            : go(selective_scan_kernel<N, kGate, 16>, s_scan, whole, kBytes);
+    return whole <= sel_resident<N, 32>(2) * sms
+               ? go(selective_scan_kernel<N, kGate, 32>, s_long, whole, sizeof(SelShared<N, 32>))
+               : go(selective_scan_kernel<N, kGate, 16>, s_scan, whole, kBytes);
 }
 
 template <int N>
